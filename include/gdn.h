@@ -266,6 +266,162 @@ gdn_status gdn_kda_bwd(const gdn_problem *prob, const void *q, const void *k, co
                        void *dk, void *dv, float *dg, float *dbeta, void *workspace, size_t ws_bytes,
                        struct CUstream_st *stream);
 
+/*
+ * Element types of the entry points below (those above are BF16).
+ */
+#define GDN_BF16 0
+#define GDN_FP16 1
+#define GDN_FP32 2
+
+/*
+ * The recurrent form, for generation: N sequences take their next tokens on a pool of states.
+ * The operation is gdn_fwd's (gdn_step: one decay per value head, g [T][HV]) or gdn_kda_fwd's
+ * (gdn_kda_step: one per key channel, g [T][HV][128], of any steepness), token by token.
+ *   states     [slots][HV][128][128] FP32 (the layout of gdn_fwd_states' s_out: a prefill can write
+ *              into the pool), updated in place.
+ *   cu_seqlens_dev [N+1] int32: sequence n has the tokens cu[n] .. cu[n+1]-1, none or any number.
+ *              NULL: one token each (T == N).  There is no host copy: lengths may change between
+ *              replays of a captured graph.
+ *   slot_in    [N] int32: the slot each sequence starts from; -1: from the zero state.
+ *              NULL: sequence n's slot is n (slots >= N).
+ *   slot_out   [T] int32: the slot the state after each token goes to; -1: nowhere.  To verify
+ *              drafted tokens, give every token a slot and go on from the last accepted one's.
+ *              NULL: the state after a sequence's last token goes back to the slot it came from
+ *              (nowhere if that is -1).
+ *              A sequence reads its slot before it writes any, so its own slots may repeat; a slot
+ *              that one sequence writes must not be read or written by another in the same call.
+ *   q, k, v    token-major rows of 128 values per head (H, H, HV heads), heads contiguous, with
+ *              q_stride, k_stride, v_stride elements from token to token (0: contiguous), so that
+ *              they may be views of one packed row; o [T][HV][128] contiguous.  All four of type
+ *              `dtype`; strides and pointers in whole 16 bytes.
+ *   dev_err    a device int, zero at first; nonzero afterwards (gdn_device_status(dev_err) reads it):
+ *              GDN_ERR_DEVICE for a slot outside the pool or bad cu_seqlens.  A sequence with a bad
+ *              slot_in or bad bounds is skipped (its o rows keep what they held); a bad slot_out
+ *              is not written to.  The call never clears the word.
+ * The states are read once and written once per slot_out, whatever the number of tokens; sums and
+ * states are FP32.  Long prompts belong to gdn_fwd_states.
+ */
+typedef struct {
+    int64_t T;        /* tokens in all; 0 does nothing */
+    int32_t N;        /* sequences */
+    int32_t H;        /* query/key heads */
+    int32_t HV;       /* value heads, a multiple of H */
+    int32_t dk;       /* must be 128 */
+    int32_t dv;       /* must be 128 */
+    int32_t slots;    /* states in the pool */
+    float scale;      /* output scale */
+    int32_t l2norm;   /* non-zero: L2-normalise q and k inside the kernel */
+    int32_t dtype;    /* of q, k, v, o */
+    int64_t q_stride, k_stride, v_stride;
+} gdn_step_problem;
+gdn_status gdn_step(const gdn_step_problem *prob, const void *q, const void *k, const void *v,
+                    const float *g, const float *beta, const int32_t *cu_seqlens_dev,
+                    const int32_t *slot_in, const int32_t *slot_out, float *states, void *o,
+                    int32_t *dev_err, struct CUstream_st *stream);
+gdn_status gdn_kda_step(const gdn_step_problem *prob, const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, const int32_t *cu_seqlens_dev,
+                        const int32_t *slot_in, const int32_t *slot_out, float *states, void *o,
+                        int32_t *dev_err, struct CUstream_st *stream);
+
+/*
+ * gdn_conv1d_fwd for generation: the convolution + SiLU over the next tokens of N sequences, with
+ * the last W-1 rows of each kept in a pool of windows.
+ *   x, y       T rows of C channels, x_stride and y_stride elements apart (0: contiguous); y must
+ *              not overlap x;
+ *   w, b       [C][W] and [C] FP32, b may be NULL;
+ *   window     [slots][W-1][C], oldest row first, updated in place (not read with W = 1, may then
+ *              be NULL); the rows of a prompt's end, or zero rows where there are fewer;
+ *   dtype      of x, y and window; strides and pointers in whole 16 bytes.
+ * cu_seqlens_dev, slot_in (-1: zero rows), slot_out and dev_err are gdn_step's; a sequence with a
+ * bad slot_in is skipped.  1 <= W <= 4, C a multiple of 8.
+ */
+typedef struct {
+    int64_t T;
+    int32_t N;
+    int32_t C;
+    int32_t W;
+    int32_t slots;
+    int32_t dtype;
+    int64_t x_stride, y_stride;
+} gdn_conv_step_problem;
+gdn_status gdn_conv1d_step(const gdn_conv_step_problem *prob, const void *x, const float *w, const float *b,
+                           const int32_t *cu_seqlens_dev, const int32_t *slot_in, const int32_t *slot_out,
+                           void *window, void *y, int32_t *dev_err, struct CUstream_st *stream);
+
+/*
+ * The norm of q and k per head with the position rotation in the same pass, for layers that put them
+ * between the convolution and the rule (prob->l2norm is then 0 there), and its gradients.
+ * For each token at position p and each head's row x of D values:
+ *     x^ = x r,  r = 1 / sqrt(x.x / D + eps)  (GDN_NORM_RMS),  1 / sqrt(x.x + eps)  (GDN_NORM_L2),
+ *          1  (GDN_NORM_NONE)
+ *     z  = w x^                        (w [D] FP32, one for q and one for k; NULL: ones)
+ *     pair i < rot / 2 of z's first rot values, (a, b):
+ *     y  = m (a cos(p f_i) - b sin(p f_i),  b cos(p f_i) + a sin(p f_i));  the rest of z unchanged
+ * with pairs (z[i], z[i + rot/2]) (GDN_ROPE_HALF) or (z[2i], z[2i+1]) (GDN_ROPE_PAIRS).
+ *   freq       [rot/2] FP64 on the device: f in radians per position (gdn_rope_frequencies).  The
+ *              angle is reduced in 64-bit fixed point, so it is as exact at position 10^9 as at 1.
+ *   positions  [T] int32, p of each token; NULL: p counts from 0 in each of the N packed documents
+ *              of cu_seqlens_dev [N+1], or, where that is NULL too, p is the token's index.
+ *              Tokens outside cu_seqlens' range take the position from the nearest document.
+ *   strides    elements from token to token and from head to head (0: contiguous): q and k may be
+ *              views of a packed row.  q_* and k_* describe q, k and (backward) dq, dk; qo_* and ko_*
+ *              the outputs and (backward) dqo, dko.  The D values of a row are contiguous.
+ *   HQ, HK     heads, either may be 0 (its pointers are then unused).
+ * Forward: qo, ko; each may be its input (same strides).  Backward: dq, dk (each may be dqo, dko), and the
+ * weights' gradients dwq, dwk [D] FP32 (each NULL: not wanted; not NULL with its w NULL is allowed), summed
+ * over all tokens and heads in a fixed order.  x must be what the forward read.
+ * Any even rot <= D, any D <= 512, any alignment of at least the element's; sums in FP32.
+ * Rows whose values, strides and pointers are in whole 16 bytes take the fast kernels.
+ * gdn_qk_workspace_bytes: the backward's scratch (16-byte aligned), for the partial sums of dwq and dwk.
+ */
+#define GDN_ROPE_HALF 0
+#define GDN_ROPE_PAIRS 1
+#define GDN_NORM_NONE 0
+#define GDN_NORM_RMS 1
+#define GDN_NORM_L2 2
+typedef struct {
+    int64_t T;        /* tokens; 0 writes only zero dwq, dwk */
+    int32_t N;        /* documents of cu_seqlens_dev */
+    int32_t HQ, HK;   /* heads of q and k */
+    int32_t D;        /* values per head */
+    int32_t rot;      /* of them rotated: even, 0 .. D */
+    int32_t layout;   /* GDN_ROPE_* */
+    int32_t norm;     /* GDN_NORM_* */
+    int32_t dtype;    /* of q, k, the outputs and their gradients */
+    float eps;
+    float mscale;     /* m */
+    int64_t q_token, q_head, k_token, k_head;
+    int64_t qo_token, qo_head, ko_token, ko_head;
+} gdn_qk_problem;
+gdn_status gdn_qk_workspace_bytes(const gdn_qk_problem *prob, size_t *workspace_bytes);
+gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_problem *prob, const void *q, const void *k, const float *wq,
+                                const float *wk, const double *freq, const int32_t *positions,
+                                const int32_t *cu_seqlens_dev, void *qo, void *ko, struct CUstream_st *stream);
+gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_problem *prob, const void *q, const void *k, const float *wq,
+                                const float *wk, const double *freq, const int32_t *positions,
+                                const int32_t *cu_seqlens_dev, const void *dqo, const void *dko, void *dq,
+                                void *dk, float *dwq, float *dwk, void *workspace, size_t ws_bytes,
+                                struct CUstream_st *stream);
+
+/*
+ * The rotation's frequencies, on the host: f_i = base^(-2i/rot), i < rot/2, changed for contexts `factor`
+ * times longer than the trained `original` positions:
+ *   GDN_ROPE_PLAIN   as they are;
+ *   GDN_ROPE_LINEAR  f_i / factor (position interpolation, arXiv:2306.15595);
+ *   GDN_ROPE_BASE    with base factor^(rot/(rot-2)) times larger (the lowest frequency is divided by
+ *                    factor, the highest is kept; rot > 2);
+ *   GDN_ROPE_PARTS   by parts (YaRN, arXiv:2309.00071): pairs that turn more than `fast` times within
+ *                    `original` are kept, fewer than `slow` times divided by factor, a linear ramp over the pair
+ *                    index between; *mscale = 0.1 ln(factor) + 1 (1 otherwise).
+ * freq receives rot/2 values.
+ */
+#define GDN_ROPE_PLAIN 0
+#define GDN_ROPE_LINEAR 1
+#define GDN_ROPE_BASE 2
+#define GDN_ROPE_PARTS 3
+gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original,
+                                double fast, double slow, double *freq, float *mscale);
+
 /* Static description of a status code. */
 const char *gdn_status_string(gdn_status s);
 

@@ -24,8 +24,13 @@ EXPORTS = ("gdn_saved_bytes", "gdn_fwd", "gdn_bwd", "gdn_ckpt_fwd_bwd", "gdn_sta
            "gdn_device_status", "gdn_plan_segment_chunks", "gdn_chunk_table_offsets", "gdn_profile_enable",
            "gdn_profile_read", "gdn_fwd_noalloc", "gdn_fwd_states", "gdn_bwd_states", "gdn_conv1d_workspace_bytes",
            "gdn_conv1d_fwd", "gdn_conv1d_bwd", "gdn_backward_tape_offsets", "gdn_kda_saved_bytes", "gdn_kda_fwd",
-           "gdn_kda_bwd", "gdn_tensor_probe")
+           "gdn_kda_bwd", "gdn_tensor_probe", "gdn_step", "gdn_kda_step", "gdn_conv1d_step", "gdn_qk_workspace_bytes",
+           "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd", "gdn_rope_frequencies")
 SAVED_FULL, SAVED_REPLAY = 0, 1   # gdn_problem.saved_form
+BF16, FP16, FP32 = 0, 1, 2        # dtype of the step and q/k problems
+ROPE_HALF, ROPE_PAIRS = 0, 1      # gdn_qk_problem.layout
+NORM_NONE, NORM_RMS, NORM_L2 = 0, 1, 2   # gdn_qk_problem.norm
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3   # scalings of gdn_rope_frequencies
 
 
 class GDNError(RuntimeError):
@@ -47,6 +52,56 @@ class gdn_problem(ctypes.Structure):
 
 class gdn_conv_problem(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("C", ctypes.c_int32), ("W", ctypes.c_int32)]
+
+
+class gdn_step_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("H", ctypes.c_int32), ("HV", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("slots", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("l2norm", ctypes.c_int32), ("dtype", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class gdn_conv_step_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("C", ctypes.c_int32), ("W", ctypes.c_int32),
+                ("slots", ctypes.c_int32), ("dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64)]
+
+
+class gdn_qk_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("HQ", ctypes.c_int32), ("HK", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("mscale", ctypes.c_float),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("qo_token", ctypes.c_int64), ("qo_head", ctypes.c_int64),
+                ("ko_token", ctypes.c_int64), ("ko_head", ctypes.c_int64)]
+
+
+def _dtype(dtype) -> int:
+    """The library's number of an element type given as that number or as a torch dtype."""
+    if isinstance(dtype, int):
+        return dtype
+    return {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}[str(dtype)]
+
+
+def step_problem(T, N, H, HV, slots, scale=128 ** -0.5, l2norm=True, dtype=BF16, strides=(0, 0, 0), dk=128,
+                 dv=128) -> gdn_step_problem:
+    """strides: elements from token to token of q, k and v (0: contiguous)."""
+    return gdn_step_problem(int(T), int(N), int(H), int(HV), int(dk), int(dv), int(slots), float(scale),
+                            int(bool(l2norm)), _dtype(dtype), *(int(s) for s in strides))
+
+
+def conv_step_problem(T, N, C, slots, W=4, dtype=BF16, strides=(0, 0)) -> gdn_conv_step_problem:
+    """strides: elements from token to token of x and y (0: contiguous)."""
+    return gdn_conv_step_problem(int(T), int(N), int(C), int(W), int(slots), _dtype(dtype), int(strides[0]),
+                                 int(strides[1]))
+
+
+def qk_problem(T, HQ, HK, D=128, rot=None, layout=ROPE_HALF, norm=NORM_RMS, eps=1e-6, mscale=1.0, N=0, dtype=BF16,
+               q_strides=(0, 0), k_strides=(0, 0), qo_strides=(0, 0), ko_strides=(0, 0)) -> gdn_qk_problem:
+    """Strides: elements from token to token and from head to head (0: contiguous)."""
+    return gdn_qk_problem(int(T), int(N), int(HQ), int(HK), int(D), int(D if rot is None else rot), int(layout),
+                          int(norm), _dtype(dtype), float(eps), float(mscale),
+                          *(int(s) for pair in (q_strides, k_strides, qo_strides, ko_strides) for s in pair))
 
 
 def conv_problem(T, N, C, W=4) -> gdn_conv_problem:
@@ -92,6 +147,17 @@ def _load():
         getattr(L, name).restype = ctypes.c_int
     L.gdn_tensor_probe.argtypes = [ctypes.c_int32, vp, ctypes.POINTER(ctypes.c_double), vp]
     L.gdn_tensor_probe.restype = ctypes.c_int
+    sp, tp, np_ = (ctypes.POINTER(t) for t in (gdn_step_problem, gdn_conv_step_problem, gdn_qk_problem))
+    f64, f32p = ctypes.c_double, ctypes.POINTER(ctypes.c_float)
+    L.gdn_step.argtypes = L.gdn_kda_step.argtypes = [sp] + [vp] * 12
+    L.gdn_conv1d_step.argtypes = [tp] + [vp] * 10
+    L.gdn_qk_workspace_bytes.argtypes = [np_, ctypes.POINTER(sz)]
+    L.gdn_qk_norm_rope_fwd.argtypes = [np_] + [vp] * 10
+    L.gdn_qk_norm_rope_bwd.argtypes = [np_] + [vp] * 14 + [sz, vp]
+    L.gdn_rope_frequencies.argtypes = [ctypes.c_int32, f64, ctypes.c_int32, f64, f64, f64, f64, vp, f32p]
+    for name in ("gdn_step", "gdn_kda_step", "gdn_conv1d_step", "gdn_qk_workspace_bytes", "gdn_qk_norm_rope_fwd",
+                 "gdn_qk_norm_rope_bwd", "gdn_rope_frequencies"):
+        getattr(L, name).restype = ctypes.c_int
     L.gdn_profile_enable.argtypes = [ctypes.c_int]
     L.gdn_profile_enable.restype = None
     L.gdn_profile_read.argtypes = [ctypes.POINTER(gdn_kernel_stat), ctypes.c_int]
@@ -331,6 +397,69 @@ def gdn_conv1d_bwd(prob, x, w, b, cu_seqlens_dev, cu_seqlens_host, dy, dx, dw, d
                               ctypes.cast(_ptr(cu_seqlens_dev), ctypes.POINTER(ctypes.c_int32)), cup, _ptr(dy),
                               _ptr(dx), _ptr(dw), _ptr(db), _ptr(workspace), ws_bytes, _stream(stream)),
            "gdn_conv1d_bwd")
+
+
+def _step(entry, where, prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev, slot_in, slot_out, stream):
+    _check(entry(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens_dev),
+                 _ptr(slot_in), _ptr(slot_out), _ptr(states), _ptr(o), _ptr(dev_err), _stream(stream)), where)
+
+
+def gdn_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None,
+             stream=None):
+    """The recurrent form on a pool of states, FP32 [slots, HV, 128, 128]: N sequences take their next tokens; g, beta
+    FP32 [T, HV]; dev_err a device int32, zero at first; see include/gdn.h."""
+    _step(lib.gdn_step, "gdn_step", prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev, slot_in, slot_out,
+          stream)
+
+
+def gdn_kda_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None,
+                 stream=None):
+    """gdn_step with a log decay per key channel: g FP32 [T, HV, 128]; see include/gdn.h."""
+    _step(lib.gdn_kda_step, "gdn_kda_step", prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev, slot_in,
+          slot_out, stream)
+
+
+def gdn_conv1d_step(prob, x, w, b, window, y, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None, stream=None):
+    """The convolution + SiLU on a pool of windows [slots, W - 1, C]: x, y [T, C]; w [C, W], b [C] FP32; see
+    include/gdn.h."""
+    _check(lib.gdn_conv1d_step(ctypes.byref(prob), _ptr(x), _ptr(w), _ptr(b), _ptr(cu_seqlens_dev), _ptr(slot_in),
+                               _ptr(slot_out), _ptr(window), _ptr(y), _ptr(dev_err), _stream(stream)),
+           "gdn_conv1d_step")
+
+
+def gdn_qk_workspace_bytes(prob) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.gdn_qk_workspace_bytes(ctypes.byref(prob), ctypes.byref(n)), "gdn_qk_workspace_bytes")
+    return int(n.value)
+
+
+def gdn_qk_norm_rope_fwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, qo, ko, stream=None):
+    """The norm of q [T, HQ, D] and k [T, HK, D] per head with the position rotation: wq, wk FP32 [D] or None, freq FP64
+    [rot / 2], positions int32 [T] or None; see include/gdn.h."""
+    _check(lib.gdn_qk_norm_rope_fwd(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(freq),
+                                    _ptr(positions), _ptr(cu_seqlens_dev), _ptr(qo), _ptr(ko), _stream(stream)),
+           "gdn_qk_norm_rope_fwd")
+
+
+def gdn_qk_norm_rope_bwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, dqo, dko, dq, dk, dwq, dwk, workspace,
+                         ws_bytes=None, stream=None):
+    """Gradients of gdn_qk_norm_rope_fwd: dq, dk laid out as q, k; dwq, dwk FP32 [D] or None (the workspace is then not
+    needed); see include/gdn.h."""
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.gdn_qk_norm_rope_bwd(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(freq),
+                                    _ptr(positions), _ptr(cu_seqlens_dev), _ptr(dqo), _ptr(dko), _ptr(dq), _ptr(dk),
+                                    _ptr(dwq), _ptr(dwk), _ptr(workspace), ws_bytes, _stream(stream)),
+           "gdn_qk_norm_rope_bwd")
+
+
+def gdn_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=4096.0, fast=32.0, slow=1.0):
+    """(frequencies, mscale): FP64 numpy [rot / 2], radians per position, and the factor on cos and sin; see
+    include/gdn.h."""
+    freq, m = np.zeros(max(int(rot), 0) // 2, dtype=np.float64), ctypes.c_float(1.0)
+    _check(lib.gdn_rope_frequencies(int(rot), float(base), int(scaling), float(factor), float(original), float(fast),
+                                    float(slow), _ptr(freq), ctypes.byref(m)), "gdn_rope_frequencies")
+    return freq, m.value
 
 
 class Buffers:

@@ -288,7 +288,9 @@ static const char* const kKernelNames[K_NUM] = {
     "merge_kernel",       "fwd_scan_kernel",    "check_saved_kernel", "bwd_scan_kernel(walk)",
     "merge_bwd_kernel",   "bwd_scan_kernel",    "grad_kernel",        "passthrough_kernel",
     "conv_fwd_kernel",    "conv_bwd_kernel(+reduce)", "vnew_kernel",      "kda_prep_kernel",
-    "kda_out_kernel",     "kda_grad_kernel",    "walk_order_kernel"};
+    "kda_out_kernel",     "kda_grad_kernel",    "walk_order_kernel",
+    "step_kernel",        "kda_step_kernel",    "conv_step_kernel",   "qk_fwd_kernel",
+    "qk_bwd_kernel(+reduce)"};
 struct ProfRec {
   int id;
   cudaEvent_t e0, e1;

@@ -241,6 +241,7 @@ inline Tables tables_at(const Plan& P, uint8_t* ws) {
 gdn_status make_plan(const gdn_problem* p, const int32_t* cu, Plan* P);
 gdn_status make_kda_plan(const gdn_problem* p, const int32_t* cu, Plan* P);
 bool device_setup();
+int sm_count();   // SMs of the current device
 bool aligned16(const void* p);
 bool make_tmap(CUtensorMap* m, const void* base, int64_t T, int heads);
 // FP32 [T][heads][128] (the per-channel log decay g): boxes of 64 tokens x 128 channels of one head,

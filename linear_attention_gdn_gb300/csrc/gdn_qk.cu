@@ -1,0 +1,347 @@
+// gdn_qk.cu -- the norm of q and k per head with the position rotation in the same pass (forward),
+// and the host layer of both directions.
+//
+// Per row x of D values: r = 1 / sqrt(share x.x + eps), z = w x r, and each rotated pair of z turned by the
+// token's angle.  With the token's cos and sin and the weights folded into two coefficients a value,
+//   y[i] = r (x[i] (w[i] co[i]) + x[i'] (w[i'] si[i]))   (i' the partner of i),
+// a row costs one sum of squares, its partners and two multiply-adds a value.
+//
+// Fast kernel: bandwidth-bound, every value read and written once.  A row lies in L lanes of 8 values
+// (16-byte accesses for the 16-bit types); a CTA takes tiles of tokens, works out their angles together
+// into shared memory (each once, for all heads), and its groups of L lanes then walk runs of heads of one token, whose
+// coefficients stay in registers, QK_BATCH rows requested at a time.
+// The kernel for other rows (any alignment, odd D, rot not a multiple of 8 in the half layout) gives a
+// warp to each row and stages it in shared memory.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "gdn_prof.h"
+#include "gdn_qk.cuh"
+
+namespace gdn {
+
+template <typename E, int L, bool HALF>
+__global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
+  extern __shared__ __align__(16) uint8_t qk_smem[];
+  const int row_len = angle_row(a.rot), buf = a.tile * row_len;
+  uint64_t* step = reinterpret_cast<uint64_t*>(qk_smem);
+  float* angles = reinterpret_cast<float*>(step + row_len);   // two buffers of cos then sin
+  for (int i = threadIdx.x; i < a.rot / 2; i += QK_THREADS) step[i] = turn_step(a.freq[i]);
+  __syncthreads();
+  constexpr int GROUPS = QK_THREADS / L;
+  const int group = threadIdx.x / L, d0 = (threadIdx.x % L) * 8;
+  const int per_token = a.items[0] + a.items[1], n_items = a.tile * per_token;
+  HalfPartner<L> hp;
+  if (HALF) hp.setup(a.rot);
+  int doc = 0, flip = 0;
+  for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, flip ^= 1) {
+    float* cosv = angles + flip * 2 * buf;
+    float* sinv = cosv + buf;
+    fill_angles(a, step, tile, row_len, cosv, sinv, &doc);
+    __syncthreads();   // (the other buffer's readers are past the last tile's barrier)
+    for (int base = 0; base < n_items; base += GROUPS) {   // (uniform bounds: whole warps shuffle)
+      const int item = base + group, j = item / per_token, e = item - j * per_token;
+      const int64_t t = tile * a.tile + j;
+      const int which = e >= a.items[0];
+      const int h0 = (e - (which ? a.items[0] : 0)) * a.run;
+      const int heads = item < n_items && t < a.T && d0 < a.D ? min(a.run, a.heads[which] - h0) : 0;
+      const E* x = static_cast<const E*>(a.x[which]) + t * a.xt[which] + h0 * a.xh[which] + d0;
+      E* y = static_cast<E*>(a.out[which]) + t * a.yt[which] + h0 * a.yh[which] + d0;
+      float wc[8], ws[8];
+      {
+        float co[8], si[8], w[8], wp[8];
+        const int jj = item < n_items ? j : 0;
+        thread_angles<L, HALF>(a, cosv + jj * row_len, sinv + jj * row_len, row_len, co, si);
+        load_weights(a.w[which], d0, a.D, w);
+        Raw8<float> wr;
+        wr.put(w);
+        if (HALF) {
+          Raw8<float> pr;
+          hp.get(wr, &pr);
+          pr.get(wp);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) wp[i] = w[i ^ 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          wc[i] = w[i] * co[i];
+          ws[i] = wp[i] * si[i];
+        }
+      }
+      for (int u0 = 0; u0 < a.run; u0 += QK_BATCH) {
+        Raw8<E> raw[QK_BATCH];
+#pragma unroll
+        for (int u = 0; u < QK_BATCH; ++u) {
+          if (u0 + u < heads) raw[u].load(x + (u0 + u) * a.xh[which]);
+          else raw[u].zero();
+        }
+#pragma unroll
+        for (int u = 0; u < QK_BATCH; ++u) {
+          if (u0 + u >= a.run) break;
+          float v[8], p[8], ss = 0.f;
+          raw[u].get(v);
+          partner<L, HALF>(hp, a, raw[u], p);
+          float r = 1.f;
+          if (a.normed) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+            r = rsqrtf(fmaf(row_sum<L>(ss), a.share, a.eps));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = r * fmaf(p[i], ws[i], v[i] * wc[i]);
+          if (u0 + u < heads) {
+            raw[u].put(v);
+            raw[u].store(y + (u0 + u) * a.yh[which]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// rows of any kind: a warp per row
+template <typename E>
+__global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_fwd_row_kernel(const QkArgs a) {
+  __shared__ float rows[QK_ROW_WARPS][QK_MAXD];
+  const int lane = threadIdx.x & 31;
+  float* z = rows[threadIdx.x >> 5];
+  const int total = a.heads[0] + a.heads[1], half = a.rot / 2;
+  __shared__ uint64_t step[QK_MAXD / 2];
+  for (int i = threadIdx.x; i < half; i += QK_ROW_WARPS * 32) step[i] = turn_step(a.freq[i]);
+  __syncthreads();
+  int doc = 0;
+  const int64_t warps = (int64_t)gridDim.x * QK_ROW_WARPS;
+  for (int64_t row = (int64_t)blockIdx.x * QK_ROW_WARPS + (threadIdx.x >> 5); row < a.T * total; row += warps) {
+    const int64_t t = row / total;
+    const int e = (int)(row - t * total), which = e >= a.heads[0], h = e - (which ? a.heads[0] : 0);
+    const E* x = static_cast<const E*>(a.x[which]) + t * a.xt[which] + h * a.xh[which];
+    E* y = static_cast<E*>(a.out[which]) + t * a.yt[which] + h * a.yh[which];
+    float ss = 0.f;
+    for (int d = lane; d < a.D; d += 32) {
+      const float v = to_f32(x[d]);
+      ss = fmaf(v, v, ss);
+      z[d] = v * (a.w[which] ? a.w[which][d] : 1.f);
+    }
+    const float r = a.normed ? rsqrtf(fmaf(row_sum<32>(ss), a.share, a.eps)) : 1.f;
+    const int p = position_of(a, t, &doc);
+    __syncwarp();
+    for (int d = lane; d < a.D; d += 32) {
+      float v = z[d];
+      if (d < a.rot) {
+        const int f = a.half_layout ? (d < half ? d : d - half) : d >> 1;
+        const int other = a.half_layout ? (d < half ? d + half : d - half) : d ^ 1;
+        float c, s;
+        angle_cos_sin(step[f], p, a.mscale, &c, &s);
+        v = v * c + (d < other ? -z[other] : z[other]) * s;
+      }
+      y[d] = from_f32<E>(r * v);
+    }
+    __syncwarp();
+  }
+}
+
+template <typename E, int L>
+static void launch_fwd_rows(const QkArgs& a, int ctas, cudaStream_t s) {
+  const size_t smem = angle_smem(a.rot, a.tile);
+  if (a.half_layout) qk_fwd_kernel<E, L, true><<<ctas, QK_THREADS, smem, s>>>(a);
+  else qk_fwd_kernel<E, L, false><<<ctas, QK_THREADS, smem, s>>>(a);
+}
+template <typename E>
+static void launch_fwd(const QkArgs& a, bool fast, int ctas, cudaStream_t s) {
+  if (!fast) qk_fwd_row_kernel<E><<<ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
+  else if (a.D <= 64) launch_fwd_rows<E, 8>(a, ctas, s);
+  else if (a.D <= 128) launch_fwd_rows<E, 16>(a, ctas, s);
+  else launch_fwd_rows<E, 32>(a, ctas, s);
+}
+
+// ---------------------------------------------------------------------------
+// host layer
+// ---------------------------------------------------------------------------
+static gdn_status qk_check(const gdn_qk_problem* p) {
+  if (!p || p->T < 0 || p->N < 0 || p->HQ < 0 || p->HK < 0 || p->D < 1) return GDN_ERR_INVALID_ARG;
+  if (p->rot < 0 || p->rot > p->D || p->rot % 2 != 0) return GDN_ERR_INVALID_ARG;
+  if (p->layout != GDN_ROPE_HALF && p->layout != GDN_ROPE_PAIRS) return GDN_ERR_INVALID_ARG;
+  if (p->norm != GDN_NORM_NONE && p->norm != GDN_NORM_RMS && p->norm != GDN_NORM_L2) return GDN_ERR_INVALID_ARG;
+  if (p->dtype != GDN_BF16 && p->dtype != GDN_FP16 && p->dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.f)) return GDN_ERR_INVALID_ARG;
+  if (p->D > QK_MAXD || p->T > (int64_t)INT32_MAX / 2 || (int64_t)p->HQ + p->HK > 65536) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+static bool vectors(const void* p, int64_t token, int64_t head, int es) {
+  return ((uintptr_t)p & 15) == 0 && token * es % 16 == 0 && head * es % 16 == 0;
+}
+
+// the kernels' arguments, and whether the fast ones take the rows
+static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k, const float* wq, const float* wk,
+                          const double* freq, const int32_t* pos, const int32_t* cu, const void* inq, const void* ink,
+                          void* outq, void* outk, bool back, QkArgs* a, bool* fast) {
+  memset(a, 0, sizeof(*a));
+  const int es = elem_bytes(p->dtype);
+  const void* x[2] = {q, k};
+  const void* in[2] = {inq, ink};
+  void* out[2] = {outq, outk};
+  const int heads[2] = {p->HQ, p->HK};
+  const int64_t st[2][4] = {{p->q_token, p->q_head, p->qo_token, p->qo_head},
+                            {p->k_token, p->k_head, p->ko_token, p->ko_head}};
+  *fast = p->D % 8 == 0 && p->D <= QK_FAST_MAXD && (p->layout == GDN_ROPE_PAIRS || p->rot % 8 == 0);
+  for (int i = 0; i < 2; ++i) {
+    a->heads[i] = heads[i];
+    if (heads[i] == 0) continue;
+    if (!x[i] || !out[i] || (back && !in[i])) return GDN_ERR_INVALID_ARG;
+    if (((uintptr_t)x[i] | (uintptr_t)out[i] | (uintptr_t)in[i]) % es != 0) return GDN_ERR_INVALID_ARG;
+    for (int s = 0; s < 4; ++s)
+      if (st[i][s] < 0) return GDN_ERR_INVALID_ARG;
+    a->xh[i] = st[i][1] ? st[i][1] : p->D;
+    a->xt[i] = st[i][0] ? st[i][0] : a->xh[i] * heads[i];
+    a->yh[i] = st[i][3] ? st[i][3] : p->D;
+    a->yt[i] = st[i][2] ? st[i][2] : a->yh[i] * heads[i];
+    if ((heads[i] > 1 && (a->xh[i] < p->D || a->yh[i] < p->D)) || (p->T > 1 && (a->xt[i] < p->D || a->yt[i] < p->D)))
+      return GDN_ERR_INVALID_ARG;
+    a->x[i] = x[i];
+    a->in[i] = in[i];
+    a->out[i] = out[i];
+    *fast = *fast && vectors(x[i], a->xt[i], a->xh[i], es) &&
+            (back ? vectors(out[i], a->xt[i], a->xh[i], es) && vectors(in[i], a->yt[i], a->yh[i], es)
+                  : vectors(out[i], a->yt[i], a->yh[i], es));
+  }
+  if (p->rot > 0 && (!freq || ((uintptr_t)freq & 7) != 0)) return GDN_ERR_INVALID_ARG;
+  if (cu && p->N < 1) return GDN_ERR_INVALID_ARG;
+  a->w[0] = wq;
+  a->w[1] = wk;
+  a->freq = freq;
+  a->pos = pos;
+  a->cu = cu;
+  a->T = p->T;
+  a->N = p->N;
+  a->D = p->D;
+  a->rot = p->rot;
+  a->half_layout = p->layout == GDN_ROPE_HALF;
+  a->normed = p->norm != GDN_NORM_NONE;
+  a->share = p->norm == GDN_NORM_RMS ? 1.f / (float)p->D : p->norm == GDN_NORM_L2 ? 1.f : 0.f;
+  a->eps = p->eps;
+  a->mscale = p->mscale;
+  // Runs of up to 8 heads of a token use its coefficients again; shorter ones where the rows would
+  // not give every SM four CTAs' worth of groups.  A tile has tokens for every group of a CTA.
+  const int groups = QK_THREADS / (p->D <= 64 ? 8 : p->D <= 128 ? 16 : 32);
+  const int64_t want = (int64_t)sm_count() * 4 * groups;
+  for (a->run = 8; a->run > 1; a->run /= 2)
+    if (p->T * ((p->HQ + a->run - 1) / a->run + (p->HK + a->run - 1) / a->run) >= want) break;
+  for (int i = 0; i < 2; ++i) a->items[i] = (heads[i] + a->run - 1) / a->run;
+  const int per_token = std::max(1, a->items[0] + a->items[1]);
+  a->tile = std::max(1, std::min(QK_MAX_TILE, groups / per_token));
+  a->tiles = (p->T + a->tile - 1) / a->tile;
+  return GDN_OK;
+}
+
+static int row_ctas(const QkArgs& a) {
+  const int64_t rows = a.T * (a.heads[0] + a.heads[1]);
+  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + QK_ROW_WARPS - 1) / QK_ROW_WARPS,
+                                                     (int64_t)sm_count() * QK_CTAS * 2));
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_qk_workspace_bytes(const gdn_qk_problem* p, size_t* bytes) {
+  const gdn_status st = qk_check(p);
+  if (st != GDN_OK) return st;
+  if (!bytes) return GDN_ERR_INVALID_ARG;
+  *bytes = (size_t)sm_count() * QK_CTAS * 2 * p->D * sizeof(float);
+  return GDN_OK;
+}
+
+gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_problem* p, const void* q, const void* k, const float* wq,
+                                const float* wk, const double* freq, const int32_t* positions,
+                                const int32_t* cu_dev, void* qo, void* ko, struct CUstream_st* stream) {
+  gdn_status st = qk_check(p);
+  if (st != GDN_OK) return st;
+  if (p->T == 0 || p->HQ + p->HK == 0) return GDN_OK;
+  QkArgs a;
+  bool fast;
+  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, nullptr, nullptr, qo, ko, false, &a, &fast);
+  if (st != GDN_OK) return st;
+  const int ctas = fast ? (int)std::min<int64_t>(a.tiles, (int64_t)sm_count() * QK_CTAS) : row_ctas(a);
+  prof_begin(K_QK_FWD, stream);
+  switch (p->dtype) {
+    case GDN_BF16: launch_fwd<__nv_bfloat16>(a, fast, ctas, stream); break;
+    case GDN_FP16: launch_fwd<__half>(a, fast, ctas, stream); break;
+    default: launch_fwd<float>(a, fast, ctas, stream); break;
+  }
+  prof_end(K_QK_FWD, stream);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_problem* p, const void* q, const void* k, const float* wq,
+                                const float* wk, const double* freq, const int32_t* positions,
+                                const int32_t* cu_dev, const void* dqo, const void* dko, void* dq, void* dk,
+                                float* dwq, float* dwk, void* workspace, size_t ws_bytes,
+                                struct CUstream_st* stream) {
+  gdn_status st = qk_check(p);
+  if (st != GDN_OK) return st;
+  if ((dwq && ((uintptr_t)dwq & 3)) || (dwk && ((uintptr_t)dwk & 3))) return GDN_ERR_INVALID_ARG;
+  size_t need = 0;
+  gdn_qk_workspace_bytes(p, &need);
+  if ((dwq || dwk) && ws_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
+  if ((dwq || dwk) && !aligned16(workspace)) return GDN_ERR_INVALID_ARG;
+  if (p->T == 0 || p->HQ + p->HK == 0) {   // no rows: the weights' gradients are zero
+    if (dwq && cudaMemsetAsync(dwq, 0, sizeof(float) * p->D, stream) != cudaSuccess) return GDN_ERR_CUDA;
+    if (dwk && cudaMemsetAsync(dwk, 0, sizeof(float) * p->D, stream) != cudaSuccess) return GDN_ERR_CUDA;
+    return GDN_OK;
+  }
+  QkArgs a;
+  bool fast;
+  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, dqo, dko, dq, dk, true, &a, &fast);
+  if (st != GDN_OK) return st;
+  a.part = dwq || dwk ? static_cast<float*>(workspace) : nullptr;
+  const int ctas = fast ? (int)std::min<int64_t>(a.tiles, (int64_t)sm_count() * QK_BWD_CTAS)
+                        : std::min(row_ctas(a), sm_count() * QK_CTAS);
+  prof_begin(K_QK_BWD, stream);
+  launch_qk_bwd(a, p->dtype, fast, ctas, dwq, dwk, stream);
+  prof_end(K_QK_BWD, stream);
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original,
+                                double fast, double slow, double* freq, float* mscale) {
+  if (rot < 0 || rot % 2 != 0 || !(base > 0.0) || !std::isfinite(base) || !freq || !mscale) return GDN_ERR_INVALID_ARG;
+  if (scaling != GDN_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor))) return GDN_ERR_INVALID_ARG;
+  const double two_pi = 2.0 * std::acos(-1.0);
+  double low = 0.0, high = 0.0;
+  *mscale = 1.f;
+  switch (scaling) {
+    case GDN_ROPE_PLAIN:
+    case GDN_ROPE_LINEAR: break;
+    case GDN_ROPE_BASE:
+      if (rot <= 2) return GDN_ERR_INVALID_ARG;
+      base *= std::pow(factor, (double)rot / (rot - 2));
+      break;
+    case GDN_ROPE_PARTS:
+      if (!(original > 0.0) || !(slow > 0.0) || !(fast >= slow) || !std::isfinite(fast) || !std::isfinite(original) ||
+          base <= 1.0 || factor < 1.0)
+        return GDN_ERR_INVALID_ARG;
+      // the pair index whose frequency turns n times within the trained length
+      low = std::max(0.0, std::floor(rot * std::log(original / (fast * two_pi)) / (2.0 * std::log(base))));
+      high = std::min(rot - 1.0, std::ceil(rot * std::log(original / (slow * two_pi)) / (2.0 * std::log(base))));
+      *mscale = (float)(0.1 * std::log(factor) + 1.0);
+      break;
+    default: return GDN_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scaling == GDN_ROPE_LINEAR) f /= factor;
+    if (scaling == GDN_ROPE_PARTS) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 1e-3)));
+      f = f * (1.0 - ramp) + f / factor * ramp;
+    }
+    freq[i] = f;
+  }
+  return GDN_OK;
+}
+
+}  // extern "C"

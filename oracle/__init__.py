@@ -11,4 +11,6 @@ Modules:
   tables.py     brute-force enumeration of the varlen chunk tables
   conv1d.py     the short causal convolution + SiLU front, forward and backward
   kda.py        the per-channel-decay (KDA) recurrence, forward and backward
+  step.py       the recurrent form and the convolution on pools of states and windows
+  qk.py         the norm of q and k per head with the position rotation, forward and backward
 """
