@@ -399,32 +399,41 @@ def gdn_conv1d_bwd(prob, x, w, b, cu_seqlens_dev, cu_seqlens_host, dy, dx, dw, d
            "gdn_conv1d_bwd")
 
 
-def _step(entry, where, prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev, slot_in, slot_out, stream):
-    _check(entry(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens_dev),
-                 _ptr(slot_in), _ptr(slot_out), _ptr(states), _ptr(o), _ptr(dev_err), _stream(stream)), where)
+def _call(where, prob, pointers, stream, *size):
+    """One call of an entry point whose arguments are a problem, pointers, at most a size, and the stream.  A single token's
+    call is as short as its launch, so tensors' addresses go to ctypes as plain integers (None is NULL)."""
+    st = getattr(lib, where)(prob, *[x.data_ptr() if hasattr(x, "data_ptr") else _ptr(x) for x in pointers], *size,
+                             _raw_stream() if stream is None else _stream(stream))
+    if st != 0:
+        raise GDNError(st, where)
+
+
+def _raw_stream():
+    """Address of torch's current stream on the current device."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without the Stream object, where torch has it
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
 
 
 def gdn_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None,
              stream=None):
     """The recurrent form on a pool of states, FP32 [slots, HV, 128, 128]: N sequences take their next tokens; g, beta
     FP32 [T, HV]; dev_err a device int32, zero at first; see include/gdn.h."""
-    _step(lib.gdn_step, "gdn_step", prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev, slot_in, slot_out,
-          stream)
+    _call("gdn_step", prob, (q, k, v, g, beta, cu_seqlens_dev, slot_in, slot_out, states, o, dev_err), stream)
 
 
 def gdn_kda_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None,
                  stream=None):
     """gdn_step with a log decay per key channel: g FP32 [T, HV, 128]; see include/gdn.h."""
-    _step(lib.gdn_kda_step, "gdn_kda_step", prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev, slot_in,
-          slot_out, stream)
+    _call("gdn_kda_step", prob, (q, k, v, g, beta, cu_seqlens_dev, slot_in, slot_out, states, o, dev_err), stream)
 
 
 def gdn_conv1d_step(prob, x, w, b, window, y, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None, stream=None):
     """The convolution + SiLU on a pool of windows [slots, W - 1, C]: x, y [T, C]; w [C, W], b [C] FP32; see
     include/gdn.h."""
-    _check(lib.gdn_conv1d_step(ctypes.byref(prob), _ptr(x), _ptr(w), _ptr(b), _ptr(cu_seqlens_dev), _ptr(slot_in),
-                               _ptr(slot_out), _ptr(window), _ptr(y), _ptr(dev_err), _stream(stream)),
-           "gdn_conv1d_step")
+    _call("gdn_conv1d_step", prob, (x, w, b, cu_seqlens_dev, slot_in, slot_out, window, y, dev_err), stream)
 
 
 def gdn_qk_workspace_bytes(prob) -> int:
@@ -436,9 +445,7 @@ def gdn_qk_workspace_bytes(prob) -> int:
 def gdn_qk_norm_rope_fwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, qo, ko, stream=None):
     """The norm of q [T, HQ, D] and k [T, HK, D] per head with the position rotation: wq, wk FP32 [D] or None, freq FP64
     [rot / 2], positions int32 [T] or None; see include/gdn.h."""
-    _check(lib.gdn_qk_norm_rope_fwd(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(freq),
-                                    _ptr(positions), _ptr(cu_seqlens_dev), _ptr(qo), _ptr(ko), _stream(stream)),
-           "gdn_qk_norm_rope_fwd")
+    _call("gdn_qk_norm_rope_fwd", prob, (q, k, wq, wk, freq, positions, cu_seqlens_dev, qo, ko), stream)
 
 
 def gdn_qk_norm_rope_bwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, dqo, dko, dq, dk, dwq, dwk, workspace,
@@ -447,10 +454,8 @@ def gdn_qk_norm_rope_bwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, dq
     needed); see include/gdn.h."""
     if ws_bytes is None:
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.gdn_qk_norm_rope_bwd(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(freq),
-                                    _ptr(positions), _ptr(cu_seqlens_dev), _ptr(dqo), _ptr(dko), _ptr(dq), _ptr(dk),
-                                    _ptr(dwq), _ptr(dwk), _ptr(workspace), ws_bytes, _stream(stream)),
-           "gdn_qk_norm_rope_bwd")
+    _call("gdn_qk_norm_rope_bwd", prob, (q, k, wq, wk, freq, positions, cu_seqlens_dev, dqo, dko, dq, dk, dwq, dwk,
+                                         workspace), stream, ws_bytes)
 
 
 def gdn_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=4096.0, fast=32.0, slow=1.0):

@@ -3,12 +3,15 @@
 //   z[t, c] = b[c] + sum_i w[c, i] row(t - (W-1) + i)[c],  y = z sigma(z)
 // with row(s) the token s of the sequence, or its window's row before the first token.
 //
-// A thread owns 8 channels and walks a range of tokens with the last W-1 rows in registers.  Long
-// sequences are cut over CTAs; a slot may be read and written by the same call, so whatever reads
-// or writes a sequence's slots is done by one CTA, the one whose range holds the sequence's first
-// token: it also computes the W-1 tokens at the start that need the window (past its range's end if
-// they lie there), and writes the windows of all the sequence's tokens, each thread after it has read the old
-// window of its channels.
+// Bandwidth-bound: a thread owns V neighbouring channels and walks a range of tokens with the last W-1 rows in
+// registers, CS_BATCH rows requested at a time. Few tokens: V = 2 and a range of one token, for the most
+// threads and the shortest chain of loads (64 single tokens of 10,240 channels: TIME_SMALL). Many: V = 4 and ranges
+// of up to 64, which read the taps less often (28,800 tokens: TIME_LARGE).
+//
+// Long sequences are cut over CTAs, and a slot may be read and written by the same call, so whatever
+// reads or writes a sequence's slots is done by one CTA per channel block, the one whose range holds its first
+// token: it also computes the first W-1 tokens, which need the window (past its range's end if they lie
+// there), and writes the windows of all the sequence's tokens from its own copy of the old window and x.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,8 +25,7 @@
 namespace gdn {
 
 constexpr int CS_THREADS = 128;
-constexpr int CS_VEC = 8;         // channels per thread
-constexpr int CS_BATCH = 4;       // rows requested together
+constexpr int CS_BATCH = 8;       // rows requested together
 constexpr int CS_MAXR = 64;       // tokens per range, at most
 
 struct ConvStepArgs {
@@ -56,29 +58,41 @@ __device__ __forceinline__ int sequence_of(const int* cu, int N, int t) {
   return lo;
 }
 
-template <typename E, int W>
+template <typename E, int W, int V>
 __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArgs a) {
   constexpr int H = W > 1 ? W - 1 : 1;
-  const int c0 = (blockIdx.x * CS_THREADS + threadIdx.x) * CS_VEC;
+  const int lane = threadIdx.x & 31;
+  const int ch = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
+  const int c0 = min(ch, a.C - V);   // (threads past the last channel stay for the warps' votes, and store nothing)
+  const bool live = ch < a.C;
   const int lo = blockIdx.y * a.R, hi = min(lo + a.R, a.T);
-  int n = a.cu ? sequence_of(a.cu, a.N, lo) : lo;
-  if (c0 >= a.C) return;   // (whole threads; the warps' search is done)
-  float w[W][CS_VEC], b[CS_VEC];
-#pragma unroll
-  for (int e = 0; e < CS_VEC; ++e) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) w[i][e] = a.w[(int64_t)(c0 + e) * W + i];
-    b[e] = a.b ? a.b[c0 + e] : 0.f;
-  }
   const E* x = static_cast<const E*>(a.x) + c0;
   E* y = static_cast<E*>(a.y) + c0;
   E* win = static_cast<E*>(a.window) + c0;
   const int64_t win_slot = (int64_t)(W - 1) * a.C;
-  Raw8<E> hist[H];   // the W-1 rows before the next token, the newest last
+  float w[V][W], b[V];
+  {
+    RawV<float, 4> taps[V * W / 4 > 0 ? V * W / 4 : 1];
+    const float* wp = a.w + (int64_t)c0 * W;
+    if constexpr (V * W % 4 == 0) {   // (c0 is a multiple of V: 16-byte aligned)
+#pragma unroll
+      for (int i = 0; i < V * W / 4; ++i) {
+        taps[i].load(wp + 4 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[(4 * i + j) / W][(4 * i + j) % W] = __uint_as_float(taps[i].u[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V * W; ++i) w[i / W][i % W] = wp[i];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) b[e] = a.b ? a.b[c0 + e] : 0.f;
+  }
+  int n = a.cu ? sequence_of(a.cu, a.N, lo) : lo;
 
   // sequence n's tokens [t0, t1); one with bad bounds has none
   int t0, t1, from;
-  bool mine, skip;   // this CTA serves the sequence's slots; the sequence is refused
+  bool skip;   // the sequence is refused
   auto enter = [&] {
     t0 = a.cu ? a.cu[n] : n;
     t1 = a.cu ? a.cu[n + 1] : n + 1;
@@ -90,55 +104,42 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
     skip = from < -1 || from >= a.slots;
     if (skip && t0 < t1) *a.err = ST_DEVICE;
   };
+  RawV<E, V> hist[H];   // the W-1 rows before the next token, the newest last
   // tokens [t, end) of the sequence; hist holds the rows before t
   auto walk = [&](int t, const int end) {
     for (; t < end; t += CS_BATCH) {
-      Raw8<E> row[CS_BATCH];
+      RawV<E, V> row[CS_BATCH];
 #pragma unroll
       for (int u = 0; u < CS_BATCH; ++u)
         if (t + u < end) row[u].load(x + (int64_t)(t + u) * a.xs);
 #pragma unroll
       for (int u = 0; u < CS_BATCH; ++u) {
         if (t + u >= end) break;
-        float z[CS_VEC], f[CS_VEC];
+        float z[V], f[V];
 #pragma unroll
-        for (int e = 0; e < CS_VEC; ++e) z[e] = b[e];
+        for (int e = 0; e < V; ++e) z[e] = b[e];
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {
-          hist[i].get(f);
+        for (int i = 0; i < W; ++i) {
+          if (i < W - 1) hist[i].get(f);
+          else row[u].get(f);
 #pragma unroll
-          for (int e = 0; e < CS_VEC; ++e) z[e] = fmaf(w[i][e], f[e], z[e]);
+          for (int e = 0; e < V; ++e) z[e] = fmaf(w[e][i], f[e], z[e]);
         }
-        row[u].get(f);
+        // the fast exponential and division: a few last places, in a value that is rounded to E
 #pragma unroll
-        for (int e = 0; e < CS_VEC; ++e) {
-          z[e] = fmaf(w[W - 1][e], f[e], z[e]);
-          z[e] = z[e] / (1.f + expf(-z[e]));
-        }
-        Raw8<E> out;
+        for (int e = 0; e < V; ++e) z[e] = __fdividef(z[e], 1.f + __expf(-z[e]));
+        RawV<E, V> out;
         out.put(z);
-        out.store(y + (int64_t)(t + u) * a.ys);
-        if (W > 1) {
+        if (live) out.store(y + (int64_t)(t + u) * a.ys);
 #pragma unroll
-          for (int i = 0; i + 1 < W - 1; ++i) hist[i] = hist[i + 1];
-          hist[H - 1] = row[u];
-          if (mine) {
-            const int to = a.slot_out ? a.slot_out[t + u] : t + u == t1 - 1 ? from : -1;
-            if (to < -1 || to >= a.slots) {
-              *a.err = ST_DEVICE;
-            } else if (to >= 0) {
-#pragma unroll
-              for (int i = 0; i < W - 1; ++i) hist[i].store(win + to * win_slot + (int64_t)i * a.C);
-            }
-          }
-        }
+        for (int i = 0; i + 1 < W - 1; ++i) hist[i] = hist[i + 1];
+        if (W > 1) hist[H - 1] = row[u];
       }
     }
   };
 
   enter();
   if (t0 < lo) {   // a sequence that began in an earlier range
-    mine = false;
     const int t = max(lo, min(t0 + W - 1, t1));   // the tokens before are the first token's CTA's
     const int end = min(t1, hi);
     if (t < end && !skip) {
@@ -153,24 +154,32 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
     enter();
     if (t0 >= hi) return;
     if (t0 == t1 || t0 < lo || skip) continue;
-    mine = true;
+    RawV<E, V> old[H];
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
-      if (from >= 0) hist[i].load(win + from * win_slot + (int64_t)i * a.C);
-      else hist[i].zero();
+      if (from >= 0) old[i].load(win + from * win_slot + (int64_t)i * a.C);
+      else old[i].zero();
+      hist[i] = old[i];
     }
-    const int end = min(t1, max(hi, t0 + W - 1));
-    walk(t0, end);
-    if (W > 1 && end < t1) {   // the other tokens are other CTAs', but the windows are this one's
-      for (int s = a.slot_out ? end : t1 - 1; s < t1; ++s) {
-        const int to = a.slot_out ? a.slot_out[s] : from;
+    walk(t0, min(t1, max(hi, t0 + W - 1)));
+    if (W > 1) {
+      // the windows of the sequence's tokens: 32 of them are looked up at a time
+      for (int s0 = a.slot_out ? t0 : t1 - 1; s0 < t1; s0 += 32) {
+        const int to = s0 + lane >= t1 ? -1 : a.slot_out ? a.slot_out[s0 + lane] : lane == 0 ? from : -1;
         if (to < -1 || to >= a.slots) *a.err = ST_DEVICE;
-        if (to < 0 || to >= a.slots) continue;
+        for (unsigned hits = __ballot_sync(~0u, to >= 0 && to < a.slots); hits; hits &= hits - 1) {
+          const int i0 = __ffs(hits) - 1, s = s0 + i0;
+          E* p = win + __shfl_sync(~0u, to, i0) * win_slot;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) {   // (s >= t0 + W - 1: all of them are tokens)
-          Raw8<E> r;
-          r.load(x + (int64_t)(s - (W - 2) + i) * a.xs);
-          r.store(win + to * win_slot + (int64_t)i * a.C);
+          for (int i = 0; i < W - 1; ++i) {
+            const int back = s - t0 - (W - 2) + i;   // the row's place in the sequence; before it: the old window's
+            RawV<E, V> r;
+            if (back >= 0) r.load(x + (int64_t)(t0 + back) * a.xs);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+              if (back + W - 1 == j) r = old[j];
+            if (live) r.store(p + (int64_t)i * a.C);
+          }
         }
       }
     }
@@ -178,14 +187,19 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
   }
 }
 
-template <typename E>
+template <typename E, int V>
 static void launch_conv_step(const ConvStepArgs& a, int W, dim3 grid, cudaStream_t s) {
   switch (W) {
-    case 1: conv_step_kernel<E, 1><<<grid, CS_THREADS, 0, s>>>(a); break;
-    case 2: conv_step_kernel<E, 2><<<grid, CS_THREADS, 0, s>>>(a); break;
-    case 3: conv_step_kernel<E, 3><<<grid, CS_THREADS, 0, s>>>(a); break;
-    default: conv_step_kernel<E, 4><<<grid, CS_THREADS, 0, s>>>(a); break;
+    case 1: conv_step_kernel<E, 1, V><<<grid, CS_THREADS, 0, s>>>(a); break;
+    case 2: conv_step_kernel<E, 2, V><<<grid, CS_THREADS, 0, s>>>(a); break;
+    case 3: conv_step_kernel<E, 3, V><<<grid, CS_THREADS, 0, s>>>(a); break;
+    default: conv_step_kernel<E, 4, V><<<grid, CS_THREADS, 0, s>>>(a); break;
   }
+}
+template <typename E>
+static void launch_conv_step(const ConvStepArgs& a, int W, int vec, dim3 grid, cudaStream_t s) {
+  if (vec == 2) launch_conv_step<E, 2>(a, W, grid, s);
+  else launch_conv_step<E, 4>(a, W, grid, s);
 }
 
 static bool conv_stride(int64_t* s, int C, int esize) {
@@ -228,18 +242,21 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.N = p->N;
   a.C = p->C;
   a.slots = p->slots;
-  // one token per CTA while that leaves the GPU idle, then longer ranges, which read the taps less often
-  const int cols = (p->C + CS_THREADS * CS_VEC - 1) / (CS_THREADS * CS_VEC);
+  // few tokens: two channels a thread and a token a CTA; many: four channels, and ranges that leave every
+  // SM 16 CTAs
+  const bool few = p->T * p->C < (int64_t)sm_count() * 4096;
+  const int vec = few ? 2 : 4;
+  const int cols = (p->C + CS_THREADS * vec - 1) / (CS_THREADS * vec);
   const int64_t ranges = std::max<int64_t>(1, (int64_t)sm_count() * 16 / cols);
-  a.R = (int)std::min<int64_t>(CS_MAXR, (p->T + ranges - 1) / ranges);
+  a.R = few ? 1 : (int)std::min<int64_t>(CS_MAXR, (p->T + ranges - 1) / ranges);
   const int64_t rows = (p->T + a.R - 1) / a.R;
+  if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 4 M tokens, or fewer in very many columns
   const dim3 grid(cols, (unsigned)rows);
-  if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: more than 4 M tokens
   prof_begin(K_CONV_STEP, stream);
   switch (p->dtype) {
-    case GDN_BF16: launch_conv_step<__nv_bfloat16>(a, p->W, grid, stream); break;
-    case GDN_FP16: launch_conv_step<__half>(a, p->W, grid, stream); break;
-    default: launch_conv_step<float>(a, p->W, grid, stream); break;
+    case GDN_BF16: launch_conv_step<__nv_bfloat16>(a, p->W, vec, grid, stream); break;
+    case GDN_FP16: launch_conv_step<__half>(a, p->W, vec, grid, stream); break;
+    default: launch_conv_step<float>(a, p->W, vec, grid, stream); break;
   }
   prof_end(K_CONV_STEP, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -75,4 +75,49 @@ template <> struct Raw8<float> {
   }
 };
 
+// V consecutive values (4 to 16 bytes) as they lie in memory
+template <typename E, int V> struct RawV {
+  static constexpr int WORDS = V * (int)sizeof(E) / 4;
+  uint32_t u[WORDS];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (WORDS == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      u[0] = x.x; u[1] = x.y; u[2] = x.z; u[3] = x.w;
+    } else if constexpr (WORDS == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      u[0] = x.x; u[1] = x.y;
+    } else {
+      u[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
+  __device__ __forceinline__ void store(E* p) const {
+    if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    else *reinterpret_cast<uint32_t*>(p) = u[0];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) u[i] = 0u;
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(E) == 4) {
+        v[i] = __uint_as_float(u[i]);
+      } else {
+        const float2 f = pair_f32(u[i], (const E*)nullptr);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(E) == 4) u[i] = __float_as_uint(v[i]);
+      else u[i] = f32_pair(v[2 * i], v[2 * i + 1], (const E*)nullptr);
+    }
+  }
+};
+
 }  // namespace gdn

@@ -6,10 +6,11 @@
 //   y[i] = r (x[i] (w[i] co[i]) + x[i'] (w[i'] si[i]))   (i' the partner of i),
 // a row costs one sum of squares, its partners and two multiply-adds a value.
 //
-// Fast kernel: bandwidth-bound, every value read and written once.  A row lies in L lanes of 8 values
-// (16-byte accesses for the 16-bit types); a CTA takes tiles of tokens, works out their angles together
-// into shared memory (each once, for all heads), and its groups of L lanes then walk runs of heads of one token, whose
-// coefficients stay in registers, QK_BATCH rows requested at a time.
+// Fast kernel: bandwidth-bound, every value read and written once.  A row lies in L lanes of 8 values; a group of
+// L lanes takes a token and walks its heads with the token's coefficients in registers, while the next rows
+// are on their way into the warp's ring in shared memory.  A warp stays with q or with k, and waits for no
+// other. Few tokens: their heads are split over warps.  PLAIN: a norm, the whole row rotated and no lane without
+// values, which needs no masks.
 // The kernel for other rows (any alignment, odd D, rot not a multiple of 8 in the half layout) gives a
 // warp to each row and stages it in shared memory.
 #include <algorithm>
@@ -21,84 +22,96 @@
 
 namespace gdn {
 
-template <typename E, int L, bool HALF>
+template <typename E, int L, bool HALF, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
-  extern __shared__ __align__(16) uint8_t qk_smem[];
-  const int row_len = angle_row(a.rot), buf = a.tile * row_len;
-  uint64_t* step = reinterpret_cast<uint64_t*>(qk_smem);
-  float* angles = reinterpret_cast<float*>(step + row_len);   // two buffers of cos then sin
-  for (int i = threadIdx.x; i < a.rot / 2; i += QK_THREADS) step[i] = turn_step(a.freq[i]);
-  __syncthreads();
-  constexpr int GROUPS = QK_THREADS / L;
-  const int group = threadIdx.x / L, d0 = (threadIdx.x % L) * 8;
-  const int per_token = a.items[0] + a.items[1], n_items = a.tile * per_token;
-  HalfPartner<L> hp;
-  if (HALF) hp.setup(a.rot);
-  int doc = 0, flip = 0;
-  for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, flip ^= 1) {
-    float* cosv = angles + flip * 2 * buf;
-    float* sinv = cosv + buf;
-    fill_angles(a, step, tile, row_len, cosv, sinv, &doc);
-    __syncthreads();   // (the other buffer's readers are past the last tile's barrier)
-    for (int base = 0; base < n_items; base += GROUPS) {   // (uniform bounds: whole warps shuffle)
-      const int item = base + group, j = item / per_token, e = item - j * per_token;
-      const int64_t t = tile * a.tile + j;
-      const int which = e >= a.items[0];
-      const int h0 = (e - (which ? a.items[0] : 0)) * a.run;
-      const int heads = item < n_items && t < a.T && d0 < a.D ? min(a.run, a.heads[which] - h0) : 0;
-      const E* x = static_cast<const E*>(a.x[which]) + t * a.xt[which] + h0 * a.xh[which] + d0;
-      E* y = static_cast<E*>(a.out[which]) + t * a.yt[which] + h0 * a.yh[which] + d0;
-      float wc[8], ws[8];
-      {
-        float co[8], si[8], w[8], wp[8];
-        const int jj = item < n_items ? j : 0;
-        thread_angles<L, HALF>(a, cosv + jj * row_len, sinv + jj * row_len, row_len, co, si);
-        load_weights(a.w[which], d0, a.D, w);
-        Raw8<float> wr;
-        wr.put(w);
-        if (HALF) {
-          Raw8<float> pr;
-          hp.get(wr, &pr);
-          pr.get(wp);
-        } else {
+  using R = Ring<E, L, 1>;
+  constexpr int VEC = 16 / (int)sizeof(E);   // values of one copy
+  __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
+  E* slots = ring[threadIdx.x >> 5][0];
+  const int l = threadIdx.x % L, mine = (threadIdx.x & 31) / L * R::ROW;
+  int off0, off1;
+  block_offsets<HALF>(a, l, &off0, &off1);
+  const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
+  const bool has = PLAIN || l < a.D / 8;
+  const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
+  const int64_t warps = (int64_t)(which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
+  const int64_t units = which ? a.units[1] : a.units[0];
+  const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
+  const E* xbase = static_cast<const E*>(which ? a.x[1] : a.x[0]) + l * VEC;
+  E* ybase = static_cast<E*>(which ? a.out[1] : a.out[0]) + off0;
+  const int64_t xt = which ? a.xt[1] : a.xt[0], xh = which ? a.xh[1] : a.xh[0];
+  const int64_t yt = which ? a.yt[1] : a.yt[0], yh = which ? a.yh[1] : a.yh[0];
+  Place<L> at, to;   // of the work, and of the rows that are requested
+  at.unit = to.unit = (int64_t)cta * QK_WARPS + (threadIdx.x >> 5);
+  if (at.unit >= units) return;
+  to.enter(a, splits, heads);
+  const E* px = xbase + to.t * xt + to.h * xh;
+  int fill = 0, use = 0;   // slots
+  auto request = [&] {
+    if (to.unit < units) {
+      E* s = slots + fill * R::SLOT + mine + l * VEC;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) wp[i] = w[i ^ 1];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          wc[i] = w[i] * co[i];
-          ws[i] = wp[i] * si[i];
-        }
-      }
-      for (int u0 = 0; u0 < a.run; u0 += QK_BATCH) {
-        Raw8<E> raw[QK_BATCH];
-#pragma unroll
-        for (int u = 0; u < QK_BATCH; ++u) {
-          if (u0 + u < heads) raw[u].load(x + (u0 + u) * a.xh[which]);
-          else raw[u].zero();
-        }
-#pragma unroll
-        for (int u = 0; u < QK_BATCH; ++u) {
-          if (u0 + u >= a.run) break;
-          float v[8], p[8], ss = 0.f;
-          raw[u].get(v);
-          partner<L, HALF>(hp, a, raw[u], p);
-          float r = 1.f;
-          if (a.normed) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-            r = rsqrtf(fmaf(row_sum<L>(ss), a.share, a.eps));
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = r * fmaf(p[i], ws[i], v[i] * wc[i]);
-          if (u0 + u < heads) {
-            raw[u].put(v);
-            raw[u].store(y + (u0 + u) * a.yh[which]);
-          }
+      for (int i = 0; i < R::CHUNKS; ++i)   // lanes past the row's end have none of its chunks
+        if (PLAIN || (l + i * L) * VEC < a.D) copy16(s + i * L * VEC, px + i * L * VEC);
+      px += xh;
+      if (++to.h == to.hend) {
+        to.unit += warps;
+        if (to.unit < units) {
+          to.enter(a, splits, heads);
+          px = xbase + to.t * xt + to.h * xh;
         }
       }
     }
-  }
+    copies_commit();
+    fill = fill + 1 == R::STAGES ? 0 : fill + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < R::STAGES - 1; ++i) request();
+
+  Angles<HALF, sizeof(E) == 2> ang;
+  ang.setup(a, l);
+  float2 w[4];
+  lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
+  do {
+    at.enter(a, splits, heads);
+    float2 wc[4], ws[4];
+    {
+      float2 co[4], si[4];
+      ang.at(a, at.t, l, co, si);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        wc[j] = __fmul2_rn(w[j], co[j]);
+        ws[j] = __fmul2_rn(partner_of<HALF>(w, j), si[j]);
+      }
+    }
+    E* y = ybase + at.t * yt + at.h * yh;
+    const bool keep = at.live && has;
+    for (int h = at.h; h < at.hend; ++h) {
+      copies_wait<R::STAGES - 2>();
+      __syncwarp();   // every lane's share of this slot is there, and the last slot has been read by all
+      request();      // into the last slot
+      float2 v[4], p[4];
+      read_row<E, HALF>(slots + use * R::SLOT + mine + off0, away, v);
+      use = use + 1 == R::STAGES ? 0 : use + 1;
+      if (!PLAIN && !has) only_rotated(v, 0);
+      float r = 1.f;
+      if (PLAIN || a.normed) {
+        float2 s = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) s = __ffma2_rn(v[j], v[j], s);
+        r = rsqrtf(fmaf(row_sum<L>(s.x + s.y), a.share, a.eps));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = partner_of<HALF>(v, j);
+      if (!PLAIN) only_rotated(p, rotated);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = __fmul2_rn(make_float2(r, r), __ffma2_rn(p[j], ws[j], __fmul2_rn(v[j], wc[j])));
+      if (keep) write_row<E, HALF>(y, away, v);
+      y += yh;
+    }
+    at.unit += warps;
+  } while (at.unit < units);
 }
 
 // rows of any kind: a warp per row
@@ -133,7 +146,7 @@ __global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_fwd_row_kernel(const QkA
         const int f = a.half_layout ? (d < half ? d : d - half) : d >> 1;
         const int other = a.half_layout ? (d < half ? d + half : d - half) : d ^ 1;
         float c, s;
-        angle_cos_sin(step[f], p, a.mscale, &c, &s);
+        angle_cos_sin<false>(step[f], p, a.mscale, &c, &s);
         v = v * c + (d < other ? -z[other] : z[other]) * s;
       }
       y[d] = from_f32<E>(r * v);
@@ -144,9 +157,11 @@ __global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_fwd_row_kernel(const QkA
 
 template <typename E, int L>
 static void launch_fwd_rows(const QkArgs& a, int ctas, cudaStream_t s) {
-  const size_t smem = angle_smem(a.rot, a.tile);
-  if (a.half_layout) qk_fwd_kernel<E, L, true><<<ctas, QK_THREADS, smem, s>>>(a);
-  else qk_fwd_kernel<E, L, false><<<ctas, QK_THREADS, smem, s>>>(a);
+  const bool plain = plain_rows(a, L);
+  if (a.half_layout && plain) qk_fwd_kernel<E, L, true, true><<<ctas, QK_THREADS, 0, s>>>(a);
+  else if (a.half_layout) qk_fwd_kernel<E, L, true, false><<<ctas, QK_THREADS, 0, s>>>(a);
+  else if (plain) qk_fwd_kernel<E, L, false, true><<<ctas, QK_THREADS, 0, s>>>(a);
+  else qk_fwd_kernel<E, L, false, false><<<ctas, QK_THREADS, 0, s>>>(a);
 }
 template <typename E>
 static void launch_fwd(const QkArgs& a, bool fast, int ctas, cudaStream_t s) {
@@ -177,7 +192,8 @@ static bool vectors(const void* p, int64_t token, int64_t head, int es) {
 // the kernels' arguments, and whether the fast ones take the rows
 static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k, const float* wq, const float* wk,
                           const double* freq, const int32_t* pos, const int32_t* cu, const void* inq, const void* ink,
-                          void* outq, void* outk, bool back, QkArgs* a, bool* fast) {
+                          void* outq, void* outk, bool back, QkArgs* a, bool* fast,
+                          int* fast_ctas) {
   memset(a, 0, sizeof(*a));
   const int es = elem_bytes(p->dtype);
   const void* x[2] = {q, k};
@@ -223,23 +239,28 @@ static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k,
   a->share = p->norm == GDN_NORM_RMS ? 1.f / (float)p->D : p->norm == GDN_NORM_L2 ? 1.f : 0.f;
   a->eps = p->eps;
   a->mscale = p->mscale;
-  // Runs of up to 8 heads of a token use its coefficients again; shorter ones where the rows would
-  // not give every SM four CTAs' worth of groups.  A tile has tokens for every group of a CTA.
-  const int groups = QK_THREADS / (p->D <= 64 ? 8 : p->D <= 128 ? 16 : 32);
-  const int64_t want = (int64_t)sm_count() * 4 * groups;
-  for (a->run = 8; a->run > 1; a->run /= 2)
-    if (p->T * ((p->HQ + a->run - 1) / a->run + (p->HK + a->run - 1) / a->run) >= want) break;
-  for (int i = 0; i < 2; ++i) a->items[i] = (heads[i] + a->run - 1) / a->run;
-  const int per_token = std::max(1, a->items[0] + a->items[1]);
-  a->tile = std::max(1, std::min(QK_MAX_TILE, groups / per_token));
-  a->tiles = (p->T + a->tile - 1) / a->tile;
+  // A group of lanes for all heads of a token, or, where that leaves an SM fewer than 16 warps, the
+  // heads in shorter runs.  q's and k's shares of the CTAs go by their heads.
+  const int total = p->HQ + p->HK, rows = 32 / (p->D <= 64 ? 8 : p->D <= 128 ? 16 : 32);
+  const int64_t token_groups = (p->T + rows - 1) / rows, want = (int64_t)sm_count() * 16;
+  a->run = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(p->HQ, p->HK), token_groups * total / want));
+  int64_t all = 0;
+  for (int i = 0; i < 2; ++i) {
+    a->splits[i] = (heads[i] + a->run - 1) / a->run;
+    a->units[i] = token_groups * a->splits[i];
+    all += (a->units[i] + QK_WARPS - 1) / QK_WARPS;
+  }
+  const int ctas = (int)std::min<int64_t>(all, (int64_t)sm_count() * QK_CTAS);
+  a->ctas_q = total > 0 ? (int)((int64_t)ctas * p->HQ / total) : 0;
+  if (p->HQ > 0 && p->HK > 0) a->ctas_q = std::max(1, std::min(ctas - 1, a->ctas_q));
+  *fast_ctas = std::max(ctas, p->HQ > 0 && p->HK > 0 ? 2 : 1);
   return GDN_OK;
 }
 
 static int row_ctas(const QkArgs& a) {
   const int64_t rows = a.T * (a.heads[0] + a.heads[1]);
   return (int)std::max<int64_t>(1, std::min<int64_t>((rows + QK_ROW_WARPS - 1) / QK_ROW_WARPS,
-                                                     (int64_t)sm_count() * QK_CTAS * 2));
+                                                     (int64_t)sm_count() * QK_CTAS));
 }
 
 }  // namespace gdn
@@ -264,9 +285,10 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_problem* p, const void* q, const vo
   if (p->T == 0 || p->HQ + p->HK == 0) return GDN_OK;
   QkArgs a;
   bool fast;
-  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, nullptr, nullptr, qo, ko, false, &a, &fast);
+  int fast_ctas;
+  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, nullptr, nullptr, qo, ko, false, &a, &fast, &fast_ctas);
   if (st != GDN_OK) return st;
-  const int ctas = fast ? (int)std::min<int64_t>(a.tiles, (int64_t)sm_count() * QK_CTAS) : row_ctas(a);
+  const int ctas = fast ? fast_ctas : row_ctas(a);
   prof_begin(K_QK_FWD, stream);
   switch (p->dtype) {
     case GDN_BF16: launch_fwd<__nv_bfloat16>(a, fast, ctas, stream); break;
@@ -296,11 +318,11 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_problem* p, const void* q, const vo
   }
   QkArgs a;
   bool fast;
-  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, dqo, dko, dq, dk, true, &a, &fast);
+  int fast_ctas;
+  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, dqo, dko, dq, dk, true, &a, &fast, &fast_ctas);
   if (st != GDN_OK) return st;
   a.part = dwq || dwk ? static_cast<float*>(workspace) : nullptr;
-  const int ctas = fast ? (int)std::min<int64_t>(a.tiles, (int64_t)sm_count() * QK_BWD_CTAS)
-                        : std::min(row_ctas(a), sm_count() * QK_CTAS);
+  const int ctas = fast ? fast_ctas : row_ctas(a);
   prof_begin(K_QK_BWD, stream);
   launch_qk_bwd(a, p->dtype, fast, ctas, dwq, dwk, stream);
   prof_end(K_QK_BWD, stream);

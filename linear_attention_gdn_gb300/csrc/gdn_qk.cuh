@@ -13,14 +13,12 @@
 
 namespace gdn {
 
-constexpr int QK_THREADS = 256;
-constexpr int QK_MAXD = 512;       // any layout
-constexpr int QK_FAST_MAXD = 256;  // rows of 8-value vectors
-constexpr int QK_BATCH = 4;        // rows a thread has requested together
-constexpr int QK_MAX_TILE = 8;     // tokens per tile, at most
-constexpr int QK_CTAS = 8;         // CTAs per SM, at most
-constexpr int QK_BWD_CTAS = 2;     // of the fast backward kernel
-constexpr int QK_ROW_WARPS = 4;    // rows a CTA of the other kernels has at a time
+constexpr int QK_THREADS = 128;     // of the fast kernels' CTAs
+constexpr int QK_WARPS = QK_THREADS / 32;
+constexpr int QK_MAXD = 512;        // any layout
+constexpr int QK_FAST_MAXD = 256;   // rows of 8 values a lane
+constexpr int QK_CTAS = 16;         // CTAs per SM of a grid that walks its work, at most
+constexpr int QK_ROW_WARPS = 4;     // rows a CTA of the other kernels has at a time
 
 struct QkArgs {
   const void* x[2];      // q, k
@@ -38,9 +36,10 @@ struct QkArgs {
   int normed;            // 0: r = 1
   float share, eps;      // r = 1 / sqrt(share x.x + eps)
   float mscale;
-  // the fast kernels' work: tiles of `tile` tokens; per token items[0] + items[1] runs of `run` heads
-  int tile, run, items[2];
-  int64_t tiles;
+  // the fast kernels' work: CTAs 0 .. ctas_q-1 take q, the others k; a unit is `run` heads of as many
+  // neighbouring tokens as a warp has rows
+  int run, splits[2], ctas_q;
+  int64_t units[2];
 };
 
 // turns per position as a fraction of 2^64
@@ -48,10 +47,19 @@ __device__ __forceinline__ uint64_t turn_step(double f) {
   const double t = f * 0.15915494309189533577;   // 1 / (2 pi)
   return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
 }
+// m cos and m sin at position pos. FAST: within 2^-20, by the hardware's functions, for values that are then
+// rounded to 16 bits.
+template <bool FAST>
 __device__ __forceinline__ void angle_cos_sin(uint64_t step, int pos, float m, float* c, float* s) {
   const uint64_t turn = step * (uint64_t)(int64_t)pos;
-  const float half_turns = (float)(int)(uint32_t)(turn >> 32) * (1.f / 2147483648.f);   // [-1, 1]
-  sincospif(half_turns, s, c);
+  const float part = (float)(int)(uint32_t)(turn >> 32);   // of 2^32 a turn: within half a turn
+  if (FAST) {
+    const float angle = part * (3.14159265358979f / 2147483648.f);
+    *c = __cosf(angle);
+    *s = __sinf(angle);
+  } else {
+    sincospif(part * (1.f / 2147483648.f), s, c);
+  }
   *c *= m;
   *s *= m;
 }
@@ -73,117 +81,158 @@ __device__ __forceinline__ int position_of(const QkArgs& a, int64_t t, int* doc)
   return (int)t - a.cu[d];
 }
 
-// cos and sin of a tile's tokens into shared memory, row_len values a token; past rot / 2 the
-// identity.  Every thread has its own document cursor, since tokens only grow.
-__device__ __forceinline__ void fill_angles(const QkArgs& a, const uint64_t* step, int64_t tile, int row_len,
-                                            float* cosv, float* sinv, int* doc) {
-  for (int i = threadIdx.x; i < a.tile * row_len; i += QK_THREADS) {
-    const int j = i / row_len, f = i - j * row_len;
-    const int64_t t = tile * a.tile + j;
-    float c = 1.f, s = 0.f;
-    if (t < a.T && f < a.rot / 2) angle_cos_sin(step[f], position_of(a, t, doc), a.mscale, &c, &s);
-    cosv[i] = c;
-    sinv[i] = s;
+// ---- rows of the fast kernels ----
+// A row lies in L lanes of 8 values, two blocks of 4. In the half layout a lane's blocks are partners, 4 values of the
+// first rotated half and the 4 they are turned with, so that no value crosses lanes; lanes past the rotated part, and all
+// lanes of the pairs layout, have 8 neighbouring values.  Either way pairs 4l .. 4l+3 are lane l's.
+// Values are held as 4 float2: v[j] has the partner v[j ^ 2] (half), or its own other value (pairs).
+template <bool HALF> __device__ __forceinline__ void block_offsets(const QkArgs& a, int l, int* off0, int* off1) {
+  if (HALF && l < a.rot / 8) {
+    *off0 = 4 * l;
+    *off1 = a.rot / 2 + 4 * l;
+  } else {
+    *off0 = 8 * l;   // (rot is a multiple of 8 in the half layout: the lanes before hold rot values)
+    *off1 = 8 * l + 4;
   }
 }
 
-// Partner values of a rotated pair, for a thread with 8 values of a row in L lanes.  In the half layout
-// the partner of a 4-value block is the block half its rotated part away, in another lane: block b of
-// the row goes with b + rot / 8, from the other half with b - rot / 8.
-template <int L> struct HalfPartner {
-  int src[2];   // lanes that hold the partners of this lane's two blocks
-  bool flip;    // a partner is the other block of its lane
-  __device__ __forceinline__ void setup(int rot) {
-    const int lane = threadIdx.x & 31, l = lane % L, away = rot / 8;
-    flip = away & 1;
+template <typename E> __device__ __forceinline__ float2 pair_at(const uint32_t* u, int j) {
+  if constexpr (sizeof(E) == 4) return make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  else return pair_f32(u[j], (const E*)nullptr);
+}
+
+// a lane's 8 values of a row: `p` its first block, `away` elements from there its second
+template <typename E, bool HALF>
+__device__ __forceinline__ void read_row(const E* p, int away, float2 (&v)[4]) {
+  RawV<E, 4> b[2];
+  if constexpr (!HALF && sizeof(E) == 2) {
+    RawV<E, 8> r;
+    r.load(p);
+    b[0].u[0] = r.u[0];
+    b[0].u[1] = r.u[1];
+    b[1].u[0] = r.u[2];
+    b[1].u[1] = r.u[3];
+  } else {
+    b[0].load(p);
+    b[1].load(p + away);
+  }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int b = 2 * l + s;
-      const int p = b < away ? b + away : b < 2 * away ? b - away : b;
-      src[s] = lane - l + p / 2;
+  for (int j = 0; j < 4; ++j) v[j] = pair_at<E>(b[j >> 1].u, j & 1);
+}
+template <typename E, bool HALF>
+__device__ __forceinline__ void write_row(E* p, int away, const float2 (&v)[4]) {
+  RawV<E, 4> b[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float f[4] = {v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y};
+    b[j].put(f);
+  }
+  if constexpr (!HALF && sizeof(E) == 2) {
+    RawV<E, 8> r;
+    r.u[0] = b[0].u[0];
+    r.u[1] = b[0].u[1];
+    r.u[2] = b[1].u[0];
+    r.u[3] = b[1].u[1];
+    r.store(p);
+  } else {
+    b[0].store(p);
+    b[1].store(p + away);
+  }
+}
+
+// Rows on their way to a warp: a ring of STAGES slots of its own shared memory, each the 32 / L rows of one step of
+// the warp (of N tensors). The warp's lanes copy 16 bytes at a time, so that the bytes in flight cost no registers.
+template <typename E, int L, int N> struct Ring {
+  static constexpr int CHUNKS = (int)sizeof(E) / 2;              // 16-byte chunks a lane copies of a row
+  static constexpr int ROW = 8 * L;                              // values a row has room for
+  static constexpr int ROWS = 32 / L;
+  static constexpr int SLOT = N * ROWS * ROW;                    // values
+  static constexpr int STAGES = N * CHUNKS == 1 ? 8 : N * CHUNKS == 2 ? 6 : 4;
+};
+__device__ __forceinline__ void copy16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> __device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+template <bool HALF> __device__ __forceinline__ float2 partner_of(const float2 (&v)[4], int j) {
+  return HALF ? v[j ^ 2] : make_float2(v[j].y, v[j].x);
+}
+// v with zeros where nothing is rotated: an infinite value's neighbour must not take part, not even times a
+// zero sine.  rotated: how many of the lane's 8 values are (0 or 8 in the half layout)
+__device__ __forceinline__ void only_rotated(float2 (&v)[4], int rotated) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (2 * j >= rotated) v[j] = make_float2(0.f, 0.f);
+}
+
+// A lane's four pairs: their turn steps, and cos and sin at a token laid out like the lane's values,
+// y[j] = v[j] co[j] + partner[j] si[j].  Pairs past the rotated part get the identity.
+template <bool HALF, bool FAST> struct Angles {
+  uint64_t step[4];
+  int doc = 0;
+  __device__ __forceinline__ void setup(const QkArgs& a, int l) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) step[i] = 4 * l + i < a.rot / 2 ? turn_step(a.freq[4 * l + i]) : 0;
+  }
+  __device__ __forceinline__ void at(const QkArgs& a, int64_t t, int l, float2 (&co)[4], float2 (&si)[4]) {
+    const int pos = position_of(a, t, &doc);
+    float c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      angle_cos_sin<FAST>(step[i], pos, a.mscale, &c[i], &s[i]);
+      if (4 * l + i >= a.rot / 2) {
+        c[i] = 1.f;
+        s[i] = 0.f;
+      }
     }
-  }
-  __device__ __forceinline__ uint32_t get(uint32_t first, uint32_t second, int s) const {
-    // what a lane sends for block s of the receivers: its own block s, or the other one
-    const uint32_t give = (s == 0) != flip ? first : second;
-    return __shfl_sync(~0u, give, src[s]);
-  }
-  template <typename E> __device__ __forceinline__ void get(const Raw8<E>& x, Raw8<E>* p) const {
-    p->u.x = get(x.u.x, x.u.z, 0);
-    p->u.y = get(x.u.y, x.u.w, 0);
-    p->u.z = get(x.u.x, x.u.z, 1);
-    p->u.w = get(x.u.y, x.u.w, 1);
-  }
-  __device__ __forceinline__ float getf(float first, float second, int s) const {
-    return __uint_as_float(get(__float_as_uint(first), __float_as_uint(second), s));
-  }
-  __device__ __forceinline__ void get(const Raw8<float>& x, Raw8<float>* p) const {
-    p->a = make_float4(getf(x.a.x, x.b.x, 0), getf(x.a.y, x.b.y, 0), getf(x.a.z, x.b.z, 0), getf(x.a.w, x.b.w, 0));
-    p->b = make_float4(getf(x.a.x, x.b.x, 1), getf(x.a.y, x.b.y, 1), getf(x.a.z, x.b.z, 1), getf(x.a.w, x.b.w, 1));
+    if (HALF) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        co[j] = co[j + 2] = make_float2(c[2 * j], c[2 * j + 1]);
+        si[j] = make_float2(-s[2 * j], -s[2 * j + 1]);
+        si[j + 2] = make_float2(s[2 * j], s[2 * j + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        co[j] = make_float2(c[j], c[j]);
+        si[j] = make_float2(-s[j], s[j]);
+      }
+    }
   }
 };
 
-// This thread's cos and signed sin of one token: y[i] = z[i] co[i] + z[partner of i] si[i].  The backward's
-// rotation, by the other angle, is -si.
-template <int L, bool HALF>
-__device__ __forceinline__ void thread_angles(const QkArgs& a, const float* cosv, const float* sinv, int row_len,
-                                              float (&co)[8], float (&si)[8]) {
-  const int d0 = (threadIdx.x % L) * 8;
-  if (HALF) {
-    const int half = a.rot / 2;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int d = d0 + 4 * s;   // half is a multiple of 4: a block of 4 lies in one half
-      if (d < a.rot) {
-        const int f = d < half ? d : d - half;
-        const float4 c = *reinterpret_cast<const float4*>(cosv + f), v = *reinterpret_cast<const float4*>(sinv + f);
-        const float sign = d < half ? -1.f : 1.f;
-        co[4 * s] = c.x; co[4 * s + 1] = c.y; co[4 * s + 2] = c.z; co[4 * s + 3] = c.w;
-        si[4 * s] = sign * v.x; si[4 * s + 1] = sign * v.y; si[4 * s + 2] = sign * v.z; si[4 * s + 3] = sign * v.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          co[4 * s + i] = 1.f;
-          si[4 * s + i] = 0.f;
-        }
-      }
+// A warp's place in its work on one kind of heads: one token for each group of L lanes, `run` heads of them. A group past
+// the last token works on the last one, and keeps nothing.
+template <int L> struct Place {
+  int64_t unit, t;
+  int h, hend;
+  bool live;
+  __device__ __forceinline__ void enter(const QkArgs& a, int splits, int heads) {
+    int64_t tokens = unit;
+    int part = 0;
+    if (splits > 1) {
+      tokens = unit / splits;
+      part = (int)(unit - tokens * splits);
     }
-  } else if (d0 / 2 < row_len) {
-    const float4 c = *reinterpret_cast<const float4*>(cosv + d0 / 2), v = *reinterpret_cast<const float4*>(sinv + d0 / 2);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      co[2 * i] = co[2 * i + 1] = cc[i];
-      si[2 * i] = -ss[i];
-      si[2 * i + 1] = ss[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      co[i] = 1.f;
-      si[i] = 0.f;
-    }
+    t = tokens * (32 / L) + (threadIdx.x & 31) / L;
+    live = t < a.T;
+    t = live ? t : a.T - 1;
+    h = part * a.run;
+    hend = min(h + a.run, heads);
   }
-}
+};
 
-// the partners of a thread's 8 values; zero for values that are not rotated (an infinite neighbour
-// must not meet their zero sine)
-template <int L, bool HALF, typename E>
-__device__ __forceinline__ void partner(const HalfPartner<L>& hp, const QkArgs& a, const Raw8<E>& x, float (&p)[8]) {
-  if (HALF) {
-    Raw8<E> r;
-    hp.get(x, &r);
-    r.get(p);
-  } else {
-    float v[8];
-    x.get(v);
+// The weights of a lane's 8 values (zeros where it has none)
+__device__ __forceinline__ void lane_weights(const float* w, int off0, int off1, bool has, float2 (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
-  }
-  if (a.rot < a.D) {
-    const int rotated = a.rot - (threadIdx.x % L) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = i < rotated ? p[i] : 0.f;
+  for (int j = 0; j < 4; ++j) {
+    const int d = (j < 2 ? off0 : off1) + (j & 1) * 2;
+    v[j] = !has ? make_float2(0.f, 0.f) : w ? make_float2(w[d], w[d + 1]) : make_float2(1.f, 1.f);
   }
 }
 
@@ -193,17 +242,8 @@ template <int L> __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// the 8 weights of this thread (zeros past D)
-__device__ __forceinline__ void load_weights(const float* w, int d0, int D, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = d0 >= D ? 0.f : w ? w[d0 + i] : 1.f;
-}
-
-inline __host__ __device__ int angle_row(int rot) { return (rot / 2 + 7) / 8 * 8; }
-// shared memory of the fast kernels: the turn steps, then two buffers of cos and sin rows
-inline __host__ __device__ size_t angle_smem(int rot, int tile) {
-  return (size_t)angle_row(rot) * 8 + 2 * 2 * (size_t)tile * angle_row(rot) * 4;
-}
+// rows without masks: normed, rotated whole, in L lanes that all have values
+inline bool plain_rows(const QkArgs& a, int L) { return a.normed && a.rot == a.D && a.D == 8 * L; }
 
 // --- gdn_qk_bwd.cu ---
 void launch_qk_bwd(const QkArgs& a, int dtype, bool fast, int ctas, float* dwq, float* dwk, cudaStream_t s);

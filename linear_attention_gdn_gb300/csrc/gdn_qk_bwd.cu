@@ -3,113 +3,144 @@
 // With g' the output's gradient turned back by the token's angle, x^ = x r and c the norm's share:
 //   dx = r (w g' - x^ c sum(w g' x^)),   dw = sum over tokens and heads of g' x^.
 // One pass reads x and the gradient and writes dx: a row's two sums, x.x and (w g').x, are reduced
-// together.  Work and layout are the forward's.  Each thread keeps its channels' share of dwq and dwk in registers
-// over all its rows; they are added over the CTA's groups in order, written as one partial a CTA, and a second
+// together.  Work and layout are the forward's.  Each lane keeps its values' share of dwq and dwk in registers
+// over all its rows; they are added over the CTA's lane groups in order, written as one partial a CTA, and a second
 // kernel adds the partials in order, so results do not depend on scheduling.
 #include "gdn_prof.h"
 #include "gdn_qk.cuh"
 
 namespace gdn {
 
-template <typename E, int L, bool HALF>
-__global__ void __launch_bounds__(QK_THREADS, QK_BWD_CTAS) qk_bwd_kernel(const QkArgs a) {
-  extern __shared__ __align__(16) uint8_t qk_smem[];
-  const int row_len = angle_row(a.rot), buf = a.tile * row_len;
-  uint64_t* step = reinterpret_cast<uint64_t*>(qk_smem);
-  float* angles = reinterpret_cast<float*>(step + row_len);
-  for (int i = threadIdx.x; i < a.rot / 2; i += QK_THREADS) step[i] = turn_step(a.freq[i]);
-  __syncthreads();
-  constexpr int GROUPS = QK_THREADS / L;
-  const int group = threadIdx.x / L, d0 = (threadIdx.x % L) * 8;
-  const int per_token = a.items[0] + a.items[1], n_items = a.tile * per_token;
-  HalfPartner<L> hp;
-  if (HALF) hp.setup(a.rot);
-  float acc[2][8];
+template <typename E, int L, bool HALF, bool PLAIN>
+__global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
+  using R = Ring<E, L, 2>;
+  constexpr int VEC = 16 / (int)sizeof(E);
+  __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
+  E* slots = ring[threadIdx.x >> 5][0];
+  const int l = threadIdx.x % L, mine = (threadIdx.x & 31) / L * R::ROW;
+  int off0, off1;
+  block_offsets<HALF>(a, l, &off0, &off1);
+  const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
+  const bool has = PLAIN || l < a.D / 8;
+  const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
+  const int64_t warps = (int64_t)(which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
+  const int64_t units = which ? a.units[1] : a.units[0];
+  const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
+  const E* xbase = static_cast<const E*>(which ? a.x[1] : a.x[0]) + l * VEC;
+  const E* gbase = static_cast<const E*>(which ? a.in[1] : a.in[0]) + l * VEC;
+  E* dbase = static_cast<E*>(which ? a.out[1] : a.out[0]) + off0;
+  const int64_t xt = which ? a.xt[1] : a.xt[0], xh = which ? a.xh[1] : a.xh[0];
+  const int64_t yt = which ? a.yt[1] : a.yt[0], yh = which ? a.yh[1] : a.yh[0];
+  float2 acc[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
-  int doc = 0, flip = 0;
-  for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, flip ^= 1) {
-    float* cosv = angles + flip * 2 * buf;
-    float* sinv = cosv + buf;
-    fill_angles(a, step, tile, row_len, cosv, sinv, &doc);
-    __syncthreads();
-    for (int base = 0; base < n_items; base += GROUPS) {
-      const int item = base + group, j = item / per_token, e = item - j * per_token;
-      const int64_t t = tile * a.tile + j;
-      const int which = e >= a.items[0];
-      const int h0 = (e - (which ? a.items[0] : 0)) * a.run;
-      const int heads = item < n_items && t < a.T && d0 < a.D ? min(a.run, a.heads[which] - h0) : 0;
-      const int64_t xh = a.xh[which], yh = a.yh[which];
-      const E* x = static_cast<const E*>(a.x[which]) + t * a.xt[which] + h0 * xh + d0;
-      E* dx = static_cast<E*>(a.out[which]) + t * a.xt[which] + h0 * xh + d0;
-      const E* gy = static_cast<const E*>(a.in[which]) + t * a.yt[which] + h0 * yh + d0;
-      float co[8], si[8], w[8], dw[8];
-      const int jj = item < n_items ? j : 0;
-      thread_angles<L, HALF>(a, cosv + jj * row_len, sinv + jj * row_len, row_len, co, si);
-      load_weights(a.w[which], d0, a.D, w);
+  for (int j = 0; j < 4; ++j) acc[j] = make_float2(0.f, 0.f);
+  Place<L> at, to;
+  at.unit = to.unit = (int64_t)cta * QK_WARPS + (threadIdx.x >> 5);
+  if (at.unit < units) {
+    to.enter(a, splits, heads);
+    const E* px = xbase + to.t * xt + to.h * xh;
+    const E* pg = gbase + to.t * yt + to.h * yh;
+    int fill = 0, use = 0;
+    auto request = [&] {
+      if (to.unit < units) {
+        E* s = slots + fill * R::SLOT + mine + l * VEC;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dw[i] = 0.f;
-      for (int u0 = 0; u0 < a.run; u0 += QK_BATCH / 2) {
-        Raw8<E> rx[QK_BATCH / 2], rg[QK_BATCH / 2];
-#pragma unroll
-        for (int u = 0; u < QK_BATCH / 2; ++u) {
-          if (u0 + u < heads) {
-            rx[u].load(x + (u0 + u) * xh);
-            rg[u].load(gy + (u0 + u) * yh);
-          } else {
-            rx[u].zero();
-            rg[u].zero();
+        for (int i = 0; i < R::CHUNKS; ++i)
+          if (PLAIN || (l + i * L) * VEC < a.D) {
+            copy16(s + i * L * VEC, px + i * L * VEC);
+            copy16(s + R::SLOT / 2 + i * L * VEC, pg + i * L * VEC);
           }
-        }
-#pragma unroll
-        for (int u = 0; u < QK_BATCH / 2; ++u) {
-          if (u0 + u >= a.run) break;
-          float v[8], g[8], p[8];
-          rx[u].get(v);
-          rg[u].get(g);
-          partner<L, HALF>(hp, a, rg[u], p);
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            g[i] = fmaf(p[i], -si[i], g[i] * co[i]);
-            ss = fmaf(v[i], v[i], ss);
-            dot = fmaf(w[i] * g[i], v[i], dot);
-          }
-          float r = 1.f, f = 0.f;
-          if (a.normed) {
-            r = rsqrtf(fmaf(row_sum<L>(ss), a.share, a.eps));
-            f = row_sum<L>(dot) * a.share * r * r;
-          }
-          if (u0 + u < heads) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dw[i] = fmaf(g[i], v[i] * r, dw[i]);
-              v[i] = r * (w[i] * g[i] - (a.normed ? v[i] * f : 0.f));
-            }
-            rx[u].put(v);
-            rx[u].store(dx + (u0 + u) * xh);
+        px += xh;
+        pg += yh;
+        if (++to.h == to.hend) {
+          to.unit += warps;
+          if (to.unit < units) {
+            to.enter(a, splits, heads);
+            px = xbase + to.t * xt + to.h * xh;
+            pg = gbase + to.t * yt + to.h * yh;
           }
         }
       }
+      copies_commit();
+      fill = fill + 1 == R::STAGES ? 0 : fill + 1;
+    };
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc[0][i] += which ? 0.f : dw[i];
-        acc[1][i] += which ? dw[i] : 0.f;
+    for (int i = 0; i < R::STAGES - 1; ++i) request();
+
+    Angles<HALF, sizeof(E) == 2> ang;
+    ang.setup(a, l);
+    float2 w[4];
+    lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
+    do {
+      at.enter(a, splits, heads);
+      float2 co[4], si[4];
+      ang.at(a, at.t, l, co, si);
+      E* dx = dbase + at.t * xt + at.h * xh;
+      const bool keep = at.live && has;
+      for (int h = at.h; h < at.hend; ++h) {
+        copies_wait<R::STAGES - 2>();
+        __syncwarp();
+        request();
+        float2 v[4], g[4], p[4];
+        const E* s0 = slots + use * R::SLOT + mine + off0;
+        read_row<E, HALF>(s0, away, v);
+        read_row<E, HALF>(s0 + R::SLOT / 2, away, g);
+        use = use + 1 == R::STAGES ? 0 : use + 1;
+        if (!PLAIN && !has) {
+          only_rotated(v, 0);
+          only_rotated(g, 0);
+        }
+        // turned back: by the opposite sine
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 o = partner_of<HALF>(g, j);
+          p[j] = make_float2(-o.x, -o.y);
+        }
+        if (!PLAIN) only_rotated(p, rotated);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = __ffma2_rn(p[j], si[j], __fmul2_rn(g[j], co[j]));
+        float2 s = __fmul2_rn(v[0], v[0]), d = make_float2(0.f, 0.f), gv[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j) s = __ffma2_rn(v[j], v[j], s);
+          gv[j] = __fmul2_rn(g[j], v[j]);
+          d = __ffma2_rn(gv[j], w[j], d);
+        }
+        float r = 1.f, f = 0.f;
+        if (PLAIN || a.normed) {
+          r = rsqrtf(fmaf(row_sum<L>(s.x + s.y), a.share, a.eps));
+          f = -row_sum<L>(d.x + d.y) * a.share * r * r * r;
+        }
+        const float2 rr = make_float2(r, r), ff = make_float2(f, f);
+        if (at.live) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = __ffma2_rn(gv[j], rr, acc[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = __fmul2_rn(__fmul2_rn(g[j], w[j]), rr);
+          v[j] = PLAIN || a.normed ? __ffma2_rn(v[j], ff, x) : x;
+        }
+        if (keep) write_row<E, HALF>(dx, away, v);
+        dx += xh;
       }
-    }
+      at.unit += warps;
+    } while (at.unit < units);
   }
   if (!a.part) return;
+  constexpr int GROUPS = QK_THREADS / L;
   __shared__ float sums[GROUPS][L * 8];
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[group][d0 + i] = which ? acc[1][i] : acc[0][i];
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += QK_THREADS) {
-      float s = 0.f;
-      for (int g = 0; g < GROUPS; ++g) s += sums[g][d];
-      a.part[((int64_t)blockIdx.x * 2 + which) * a.D + d] = s;
-    }
+  for (int j = 0; j < 4; ++j) {
+    const int d = (j < 2 ? off0 : off1) + (j & 1) * 2;   // (below L * 8 in lanes without values, too)
+    sums[threadIdx.x / L][d] = acc[j].x;
+    sums[threadIdx.x / L][d + 1] = acc[j].y;
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < a.D; d += QK_THREADS) {
+    float s = 0.f;
+    for (int g = 0; g < GROUPS; ++g) s += sums[g][d];
+    a.part[((int64_t)blockIdx.x * 2 + which) * a.D + d] = s;
   }
 }
 
@@ -150,7 +181,7 @@ __global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_bwd_row_kernel(const QkA
         const int f = a.half_layout ? (d < half ? d : d - half) : d >> 1;
         const int other = a.half_layout ? (d < half ? d + half : d - half) : d ^ 1;
         float c, s;
-        angle_cos_sin(step[f], p, a.mscale, &c, &s);
+        angle_cos_sin<false>(step[f], p, a.mscale, &c, &s);
         g[i] = g[i] * c + (d < other ? gin[other] : -gin[other]) * s;
       }
       ss = fmaf(v[i], v[i], ss);
@@ -186,13 +217,17 @@ __global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_bwd_row_kernel(const QkA
   }
 }
 
-// dw[d] = sum over the CTAs' partials: 32 columns of dwq | dwk a CTA, 32 threads a column
-__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas, int D, float* dwq, float* dwk) {
+// dw[d] = sum over the CTAs' partials, 32 columns of dwq | dwk a CTA, 32 threads a column; q's partials are in
+// CTAs 0 .. end_q-1, k's in begin_k .. ctas-1
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int end_q, int begin_k, int ctas, int D,
+                                                     float* dwq, float* dwk) {
   __shared__ float sums[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
-  if (col < 2 * D)
-    for (int b = threadIdx.y; b < ctas; b += 32) s += part[(int64_t)b * 2 * D + col];
+  if (col < 2 * D) {
+    const int end = col < D ? end_q : ctas;
+    for (int b = (col < D ? 0 : begin_k) + threadIdx.y; b < end; b += 32) s += part[(int64_t)b * 2 * D + col];
+  }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && col < 2 * D) {
@@ -206,9 +241,11 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas
 
 template <typename E, int L>
 static void launch_bwd_rows(const QkArgs& a, int ctas, cudaStream_t s) {
-  const size_t smem = angle_smem(a.rot, a.tile);
-  if (a.half_layout) qk_bwd_kernel<E, L, true><<<ctas, QK_THREADS, smem, s>>>(a);
-  else qk_bwd_kernel<E, L, false><<<ctas, QK_THREADS, smem, s>>>(a);
+  const bool plain = plain_rows(a, L);
+  if (a.half_layout && plain) qk_bwd_kernel<E, L, true, true><<<ctas, QK_THREADS, 0, s>>>(a);
+  else if (a.half_layout) qk_bwd_kernel<E, L, true, false><<<ctas, QK_THREADS, 0, s>>>(a);
+  else if (plain) qk_bwd_kernel<E, L, false, true><<<ctas, QK_THREADS, 0, s>>>(a);
+  else qk_bwd_kernel<E, L, false, false><<<ctas, QK_THREADS, 0, s>>>(a);
 }
 template <typename E>
 static void launch_bwd(const QkArgs& a, bool fast, int ctas, cudaStream_t s) {
@@ -224,7 +261,8 @@ void launch_qk_bwd(const QkArgs& a, int dtype, bool fast, int ctas, float* dwq, 
     case GDN_FP16: launch_bwd<__half>(a, fast, ctas, s); break;
     default: launch_bwd<float>(a, fast, ctas, s); break;
   }
-  if (a.part) qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, ctas, a.D, dwq, dwk);
+  if (a.part) qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, fast ? a.ctas_q : ctas, fast ? a.ctas_q : 0,
+                                                                        ctas, a.D, dwq, dwk);
 }
 
 }  // namespace gdn
