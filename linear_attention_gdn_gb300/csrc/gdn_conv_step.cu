@@ -3,10 +3,13 @@
 //   z[t, c] = b[c] + sum_i w[c, i] row(t - (W-1) + i)[c],  y = z sigma(z)
 // with row(s) the token s of the sequence, or its window's row before the first token.
 //
-// Bandwidth-bound: a thread owns V neighbouring channels and walks a range of tokens with the last W-1 rows in
-// registers, CS_BATCH rows requested at a time. Few tokens: V = 2 and a range of one token, for the most
-// threads and the shortest chain of loads (64 single tokens of 10,240 channels: TIME_SMALL). Many: V = 4 and ranges
-// of up to 64, which read the taps less often (28,800 tokens: TIME_LARGE).
+// Bandwidth-bound.  Two kernels:
+//   - one token each (no cu_seqlens): a thread owns two channels and takes the sequences gridDim.y apart, its
+//     taps in registers.  All that does not hang on the slot is requested at once, so that a call is two
+//     loads deep;
+//   - any lengths: a thread owns four channels and walks a range of tokens with the last W-1 rows in registers,
+//     the next rows on their way into shared memory (each thread copies what it reads, so no thread waits
+//     for another).
 //
 // Long sequences are cut over CTAs, and a slot may be read and written by the same call, so whatever
 // reads or writes a sequence's slots is done by one CTA per channel block, the one whose range holds its first
@@ -25,8 +28,11 @@
 namespace gdn {
 
 constexpr int CS_THREADS = 128;
-constexpr int CS_BATCH = 8;       // rows requested together
-constexpr int CS_MAXR = 64;       // tokens per range, at most
+constexpr int CS_VEC = 4;         // channels per thread, and of the kernel for single tokens:
+constexpr int CS_VEC1 = 2;
+constexpr int CS_STAGES = 16;     // rows of a thread on their way
+constexpr int CS_LOOK = 4;        // slot numbers a lane has requested together
+constexpr int CS_MAXR = 256;      // tokens per range, at most
 
 struct ConvStepArgs {
   const void* x;
@@ -41,6 +47,15 @@ struct ConvStepArgs {
   int64_t xs, ys;
   int T, N, C, slots, R;
 };
+
+// z sigma(z), with the hardware's exponential and reciprocal (each within a few last places; the value
+// is then rounded to its type)
+__device__ __forceinline__ float silu(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504088896f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return z * r;
+}
 
 // The last sequence n with cu[n] <= t (0 if there is none), found by a whole warp: 32 probes a step.
 __device__ __forceinline__ int sequence_of(const int* cu, int N, int t) {
@@ -58,9 +73,100 @@ __device__ __forceinline__ int sequence_of(const int* cu, int N, int t) {
   return lo;
 }
 
+// taps and bias of V channels from c0 on, as pairs of channels
+template <int W, int V> struct Taps {
+  float2 w[W][V / 2], b[V / 2];
+  __device__ __forceinline__ void load(const ConvStepArgs& a, int c0) {
+    const float* wp = a.w + (int64_t)c0 * W;   // (c0 is even: 8-byte aligned)
+    float t[V * W];
+#pragma unroll
+    for (int i = 0; i < V * W / 2; ++i) {
+      const float2 f = reinterpret_cast<const float2*>(wp)[i];
+      t[2 * i] = f.x;
+      t[2 * i + 1] = f.y;
+    }
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i][e] = make_float2(t[2 * e * W + i], t[(2 * e + 1) * W + i]);
+      b[e] = a.b ? reinterpret_cast<const float2*>(a.b + c0)[e] : make_float2(0.f, 0.f);
+    }
+  }
+};
+template <typename E, int V> __device__ __forceinline__ void as_pairs(const RawV<E, V>& r, float2 (&h)[V / 2]) {
+  float f[V];
+  r.get(f);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) h[e] = make_float2(f[2 * e], f[2 * e + 1]);
+}
+// y of one row after hist (the W-1 rows before, the newest last), of which it becomes the newest
 template <typename E, int W, int V>
+__device__ __forceinline__ RawV<E, V> conv_row(const Taps<W, V>& k, const RawV<E, V>& row,
+                                               float2 (&hist)[W > 1 ? W - 1 : 1][V / 2]) {
+  float z[V];
+  float2 now[V / 2];
+  as_pairs(row, now);
+#pragma unroll
+  for (int e = 0; e < V / 2; ++e) {
+    float2 s = k.b[e];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) s = __ffma2_rn(k.w[i][e], hist[i][e], s);
+    s = __ffma2_rn(k.w[W - 1][e], now[e], s);
+    z[2 * e] = silu(s.x);
+    z[2 * e + 1] = silu(s.y);
+#pragma unroll
+    for (int i = 0; i + 1 < W - 1; ++i) hist[i][e] = hist[i + 1][e];
+    if (W > 1) hist[W > 1 ? W - 2 : 0][e] = now[e];
+  }
+  RawV<E, V> out;
+  out.put(z);
+  return out;
+}
+
+// one token each: sequence n is token n
+template <typename E, int W>
+__global__ void __launch_bounds__(CS_THREADS) conv_token_kernel(const ConvStepArgs a) {
+  constexpr int V = CS_VEC1, H = W > 1 ? W - 1 : 1;
+  const int c0 = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
+  if (c0 >= a.C) return;
+  Taps<W, V> k;
+  k.load(a, c0);
+  const E* x = static_cast<const E*>(a.x) + c0;
+  E* y = static_cast<E*>(a.y) + c0;
+  E* win = static_cast<E*>(a.window) + c0;
+  const int64_t win_slot = (int64_t)(W - 1) * a.C;
+  for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
+    const int from = a.slot_in ? a.slot_in[n] : n, to = a.slot_out ? a.slot_out[n] : from;
+    RawV<E, V> row, old[H];
+    row.load(x + (int64_t)n * a.xs);
+    if (from < -1 || from >= a.slots) {
+      *a.err = ST_DEVICE;
+      continue;
+    }
+    float2 hist[H][V / 2];
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) {
+      if (from >= 0) old[i].load(win + from * win_slot + (int64_t)i * a.C);
+      else old[i].zero();
+      as_pairs(old[i], hist[i]);
+    }
+    conv_row<E, W, V>(k, row, hist).store(y + (int64_t)n * a.ys);
+    if (W == 1) continue;
+    if (to < -1 || to >= a.slots) {
+      *a.err = ST_DEVICE;
+    } else if (to >= 0) {
+      E* p = win + to * win_slot;
+#pragma unroll
+      for (int i = 0; i + 1 < W - 1; ++i) old[i + 1].store(p + (int64_t)i * a.C);
+      row.store(p + (int64_t)(W - 2) * a.C);
+    }
+  }
+}
+
+template <typename E, int W>
 __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArgs a) {
-  constexpr int H = W > 1 ? W - 1 : 1;
+  constexpr int V = CS_VEC, H = W > 1 ? W - 1 : 1, BYTES = V * (int)sizeof(E);
+  __shared__ __align__(16) uint8_t ring[CS_STAGES][CS_THREADS * BYTES];
   const int lane = threadIdx.x & 31;
   const int ch = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
   const int c0 = min(ch, a.C - V);   // (threads past the last channel stay for the warps' votes, and store nothing)
@@ -70,24 +176,8 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
   E* y = static_cast<E*>(a.y) + c0;
   E* win = static_cast<E*>(a.window) + c0;
   const int64_t win_slot = (int64_t)(W - 1) * a.C;
-  float w[V][W], b[V];
-  {
-    RawV<float, 4> taps[V * W / 4 > 0 ? V * W / 4 : 1];
-    const float* wp = a.w + (int64_t)c0 * W;
-    if constexpr (V * W % 4 == 0) {   // (c0 is a multiple of V: 16-byte aligned)
-#pragma unroll
-      for (int i = 0; i < V * W / 4; ++i) {
-        taps[i].load(wp + 4 * i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[(4 * i + j) / W][(4 * i + j) % W] = __uint_as_float(taps[i].u[j]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V * W; ++i) w[i / W][i % W] = wp[i];
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) b[e] = a.b ? a.b[c0 + e] : 0.f;
-  }
+  Taps<W, V> k;
+  k.load(a, c0);
   int n = a.cu ? sequence_of(a.cu, a.N, lo) : lo;
 
   // sequence n's tokens [t0, t1); one with bad bounds has none
@@ -104,48 +194,65 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
     skip = from < -1 || from >= a.slots;
     if (skip && t0 < t1) *a.err = ST_DEVICE;
   };
-  RawV<E, V> hist[H];   // the W-1 rows before the next token, the newest last
-  // tokens [t, end) of the sequence; hist holds the rows before t
-  auto walk = [&](int t, const int end) {
-    for (; t < end; t += CS_BATCH) {
-      RawV<E, V> row[CS_BATCH];
-#pragma unroll
-      for (int u = 0; u < CS_BATCH; ++u)
-        if (t + u < end) row[u].load(x + (int64_t)(t + u) * a.xs);
-#pragma unroll
-      for (int u = 0; u < CS_BATCH; ++u) {
-        if (t + u >= end) break;
-        float z[V], f[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) z[e] = b[e];
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          if (i < W - 1) hist[i].get(f);
-          else row[u].get(f);
-#pragma unroll
-          for (int e = 0; e < V; ++e) z[e] = fmaf(w[e][i], f[e], z[e]);
-        }
-        // the fast exponential and division: a few last places, in a value that is rounded to E
-#pragma unroll
-        for (int e = 0; e < V; ++e) z[e] = __fdividef(z[e], 1.f + __expf(-z[e]));
-        RawV<E, V> out;
-        out.put(z);
-        if (live) out.store(y + (int64_t)(t + u) * a.ys);
-#pragma unroll
-        for (int i = 0; i + 1 < W - 1; ++i) hist[i] = hist[i + 1];
-        if (W > 1) hist[H - 1] = row[u];
-      }
+  enter();
+  // The rows come in order from the first token on, whoever's they are; the last may be the first W-1
+  // tokens of a sequence that begins at the range's end.
+  int t = t0 < lo ? max(lo, min(t0 + W - 1, t1)) : lo;
+  const int stop = min(hi + W - 1, a.T);
+  const uint32_t landing = (uint32_t)__cvta_generic_to_shared(&ring[0][threadIdx.x * BYTES]);
+  const E* px = x + (int64_t)t * a.xs;
+  E* py = y + (int64_t)t * a.ys;
+  int fed = t, fill = 0, use = 0;
+  auto request = [&] {
+    if (fed < stop) {
+      if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(landing + fill), "l"(px) : "memory");
+      else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(landing + fill), "l"(px) : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++fed;
+    px += a.xs;
+    fill = (fill + CS_THREADS * BYTES) & (CS_STAGES * CS_THREADS * BYTES - 1);
+  };
+#pragma unroll
+  for (int i = 0; i < CS_STAGES - 1; ++i) request();
+  // the row of token t, which is then passed
+  auto take = [&](RawV<E, V>* row) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(CS_STAGES - 2) : "memory");
+    row->load_shared(landing + use);
+    use = (use + CS_THREADS * BYTES) & (CS_STAGES * CS_THREADS * BYTES - 1);
+    request();   // into the slot before
+    ++t;
+    py += a.ys;
+  };
+  float2 hist[H][V / 2];
+  // up to `end` of the sequence; hist holds the rows before
+  auto walk = [&](const int end) {
+    auto one = [&] {
+      E* out = py;
+      RawV<E, V> row;
+      take(&row);
+      const RawV<E, V> r = conv_row<E, W, V>(k, row, hist);
+      if (live) r.store(out);
+    };
+    for (; t + 4 <= end;) {   // (four at a time the rows of hist change names, not registers)
+      one();
+      one();
+      one();
+      one();
+    }
+    while (t < end) one();
   };
 
-  enter();
-  if (t0 < lo) {   // a sequence that began in an earlier range
-    const int t = max(lo, min(t0 + W - 1, t1));   // the tokens before are the first token's CTA's
+  if (t0 < lo) {   // a sequence that began in an earlier range; its tokens before t are the first token's CTA's
     const int end = min(t1, hi);
     if (t < end && !skip) {
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) hist[i].load(x + (int64_t)(t - (W - 1) + i) * a.xs);
-      walk(t, end);
+      for (int i = 0; i < W - 1; ++i) {
+        RawV<E, V> r;
+        r.load(x + (int64_t)(t - (W - 1) + i) * a.xs);
+        as_pairs(r, hist[i]);
+      }
+      walk(end);
     }
     if (t1 >= hi) return;
     ++n;
@@ -154,31 +261,40 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
     enter();
     if (t0 >= hi) return;
     if (t0 == t1 || t0 < lo || skip) continue;
-    RawV<E, V> old[H];
+    RawV<E, V> old[H], passed;
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
       if (from >= 0) old[i].load(win + from * win_slot + (int64_t)i * a.C);
       else old[i].zero();
-      hist[i] = old[i];
+      as_pairs(old[i], hist[i]);
     }
-    walk(t0, min(t1, max(hi, t0 + W - 1)));
+    while (t < t0) take(&passed);   // the tokens of sequences that were refused
+    walk(min(t1, max(hi, t0 + W - 1)));
     if (W > 1) {
-      // the windows of the sequence's tokens: 32 of them are looked up at a time
-      for (int s0 = a.slot_out ? t0 : t1 - 1; s0 < t1; s0 += 32) {
-        const int to = s0 + lane >= t1 ? -1 : a.slot_out ? a.slot_out[s0 + lane] : lane == 0 ? from : -1;
-        if (to < -1 || to >= a.slots) *a.err = ST_DEVICE;
-        for (unsigned hits = __ballot_sync(~0u, to >= 0 && to < a.slots); hits; hits &= hits - 1) {
-          const int i0 = __ffs(hits) - 1, s = s0 + i0;
-          E* p = win + __shfl_sync(~0u, to, i0) * win_slot;
+      // the windows of the sequence's tokens, looked up CS_LOOK * 32 at a time
+      for (int s0 = a.slot_out ? t0 : t1 - 1; s0 < t1; s0 += CS_LOOK * 32) {
+        int to[CS_LOOK];
 #pragma unroll
-          for (int i = 0; i < W - 1; ++i) {
-            const int back = s - t0 - (W - 2) + i;   // the row's place in the sequence; before it: the old window's
-            RawV<E, V> r;
-            if (back >= 0) r.load(x + (int64_t)(t0 + back) * a.xs);
+        for (int q = 0; q < CS_LOOK; ++q) {
+          const int s = s0 + q * 32 + lane;
+          to[q] = s >= t1 ? -1 : a.slot_out ? a.slot_out[s] : q + lane == 0 ? from : -1;
+        }
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-              if (back + W - 1 == j) r = old[j];
-            if (live) r.store(p + (int64_t)i * a.C);
+        for (int q = 0; q < CS_LOOK; ++q) {
+          if (to[q] < -1 || to[q] >= a.slots) *a.err = ST_DEVICE;
+          for (unsigned hits = __ballot_sync(~0u, to[q] >= 0 && to[q] < a.slots); hits; hits &= hits - 1) {
+            const int i0 = __ffs(hits) - 1, first = s0 + q * 32 + i0 - t0 - (W - 2);
+            E* p = win + __shfl_sync(~0u, to[q], i0) * win_slot;
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i) {
+              const int back = first + i;   // the row's place in the sequence; before it: the old window's
+              RawV<E, V> r;
+              if (back >= 0) r.load(x + (int64_t)(t0 + back) * a.xs);
+#pragma unroll
+              for (int j = 0; j < W - 1; ++j)
+                if (back + W - 1 == j) r = old[j];
+              if (live) r.store(p + (int64_t)i * a.C);
+            }
           }
         }
       }
@@ -187,19 +303,17 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
   }
 }
 
-template <typename E, int V>
-static void launch_conv_step(const ConvStepArgs& a, int W, dim3 grid, cudaStream_t s) {
-  switch (W) {
-    case 1: conv_step_kernel<E, 1, V><<<grid, CS_THREADS, 0, s>>>(a); break;
-    case 2: conv_step_kernel<E, 2, V><<<grid, CS_THREADS, 0, s>>>(a); break;
-    case 3: conv_step_kernel<E, 3, V><<<grid, CS_THREADS, 0, s>>>(a); break;
-    default: conv_step_kernel<E, 4, V><<<grid, CS_THREADS, 0, s>>>(a); break;
-  }
+template <typename E, int W> static void launch_conv_step(const ConvStepArgs& a, dim3 grid, cudaStream_t s) {
+  if (a.cu) conv_step_kernel<E, W><<<grid, CS_THREADS, 0, s>>>(a);
+  else conv_token_kernel<E, W><<<grid, CS_THREADS, 0, s>>>(a);
 }
-template <typename E>
-static void launch_conv_step(const ConvStepArgs& a, int W, int vec, dim3 grid, cudaStream_t s) {
-  if (vec == 2) launch_conv_step<E, 2>(a, W, grid, s);
-  else launch_conv_step<E, 4>(a, W, grid, s);
+template <typename E> static void launch_conv_step(const ConvStepArgs& a, int W, dim3 grid, cudaStream_t s) {
+  switch (W) {
+    case 1: launch_conv_step<E, 1>(a, grid, s); break;
+    case 2: launch_conv_step<E, 2>(a, grid, s); break;
+    case 3: launch_conv_step<E, 3>(a, grid, s); break;
+    default: launch_conv_step<E, 4>(a, grid, s); break;
+  }
 }
 
 static bool conv_stride(int64_t* s, int C, int esize) {
@@ -242,21 +356,26 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.N = p->N;
   a.C = p->C;
   a.slots = p->slots;
-  // few tokens: two channels a thread and a token a CTA; many: four channels, and ranges that leave every
-  // SM 16 CTAs
-  const bool few = p->T * p->C < (int64_t)sm_count() * 4096;
-  const int vec = few ? 2 : 4;
-  const int cols = (p->C + CS_THREADS * vec - 1) / (CS_THREADS * vec);
-  const int64_t ranges = std::max<int64_t>(1, (int64_t)sm_count() * 16 / cols);
-  a.R = few ? 1 : (int)std::min<int64_t>(CS_MAXR, (p->T + ranges - 1) / ranges);
-  const int64_t rows = (p->T + a.R - 1) / a.R;
-  if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 4 M tokens, or fewer in very many columns
+  // single tokens: as many sequences side by side as give an SM 16 CTAs; else ranges that give it four rounds
+  // of the 8 CTAs it holds
+  const int per_cta = CS_THREADS * (cu_dev ? CS_VEC : CS_VEC1);
+  const int cols = (p->C + per_cta - 1) / per_cta;
+  int64_t rows;
+  if (cu_dev) {
+    const int64_t ranges = std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols);
+    a.R = (int)std::min<int64_t>(CS_MAXR, (p->T + ranges - 1) / ranges);
+    rows = (p->T + a.R - 1) / a.R;
+  } else {
+    a.R = 1;
+    rows = std::min<int64_t>(p->N, std::max<int64_t>(1, (int64_t)sm_count() * 16 / cols));
+  }
+  if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 16 M tokens, or fewer in very many columns
   const dim3 grid(cols, (unsigned)rows);
   prof_begin(K_CONV_STEP, stream);
   switch (p->dtype) {
-    case GDN_BF16: launch_conv_step<__nv_bfloat16>(a, p->W, vec, grid, stream); break;
-    case GDN_FP16: launch_conv_step<__half>(a, p->W, vec, grid, stream); break;
-    default: launch_conv_step<float>(a, p->W, vec, grid, stream); break;
+    case GDN_BF16: launch_conv_step<__nv_bfloat16>(a, p->W, grid, stream); break;
+    case GDN_FP16: launch_conv_step<__half>(a, p->W, grid, stream); break;
+    default: launch_conv_step<float>(a, p->W, grid, stream); break;
   }
   prof_end(K_CONV_STEP, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -90,6 +90,15 @@ template <typename E, int V> struct RawV {
       u[0] = *reinterpret_cast<const uint32_t*>(p);
     }
   }
+  // from shared memory, by one access of the whole (left to itself the compiler reads 16-bit values one by one)
+  __device__ __forceinline__ void load_shared(uint32_t at) {
+    if constexpr (WORDS == 4)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at) : "memory");
+    else if constexpr (WORDS == 2)
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(at) : "memory");
+    else
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u[0]) : "r"(at) : "memory");
+  }
   __device__ __forceinline__ void store(E* p) const {
     if constexpr (WORDS == 4) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     else if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);

@@ -34,36 +34,41 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
   const bool has = PLAIN || l < a.D / 8;
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
-  const int64_t warps = (int64_t)(which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
-  const int64_t units = which ? a.units[1] : a.units[0];
+  const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
+  const int units = which ? a.units[1] : a.units[0];
   const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
   const E* xbase = static_cast<const E*>(which ? a.x[1] : a.x[0]) + l * VEC;
   E* ybase = static_cast<E*>(which ? a.out[1] : a.out[0]) + off0;
   const int64_t xt = which ? a.xt[1] : a.xt[0], xh = which ? a.xh[1] : a.xh[0];
   const int64_t yt = which ? a.yt[1] : a.yt[0], yh = which ? a.yh[1] : a.yh[0];
   Place<L> at, to;   // of the work, and of the rows that are requested
-  at.unit = to.unit = (int64_t)cta * QK_WARPS + (threadIdx.x >> 5);
+  at.unit = to.unit = cta * QK_WARPS + (threadIdx.x >> 5);
   if (at.unit >= units) return;
   to.enter(a, splits, heads);
   const E* px = xbase + to.t * xt + to.h * xh;
-  int fill = 0, use = 0;   // slots
+  const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine + off0);
+  int fill = 0, use = 0;   // byte offsets of slots
+  bool more = true;
+  const uint32_t landing = (uint32_t)__cvta_generic_to_shared(slots) + (mine + l * VEC) * (int)sizeof(E);
   auto request = [&] {
-    if (to.unit < units) {
-      E* s = slots + fill * R::SLOT + mine + l * VEC;
+    if (more) {
 #pragma unroll
-      for (int i = 0; i < R::CHUNKS; ++i)   // lanes past the row's end have none of its chunks
-        if (PLAIN || (l + i * L) * VEC < a.D) copy16(s + i * L * VEC, px + i * L * VEC);
+      for (int i = 0; i < R::CHUNKS; ++i)
+        if (PLAIN || (l + i * L) * VEC < a.D) {   // lanes past the row's end have none of its chunks
+          copy16(landing + fill + i * L * 16, px + i * L * VEC);
+        }
       px += xh;
-      if (++to.h == to.hend) {
+      if (--to.left == 0) {
         to.unit += warps;
-        if (to.unit < units) {
+        more = to.unit < units;
+        if (more) {
           to.enter(a, splits, heads);
           px = xbase + to.t * xt + to.h * xh;
         }
       }
     }
     copies_commit();
-    fill = fill + 1 == R::STAGES ? 0 : fill + 1;
+    fill = R::next(fill);
   };
 #pragma unroll
   for (int i = 0; i < R::STAGES - 1; ++i) request();
@@ -86,13 +91,13 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
     }
     E* y = ybase + at.t * yt + at.h * yh;
     const bool keep = at.live && has;
-    for (int h = at.h; h < at.hend; ++h) {
+    for (int n = at.left; n > 0; --n) {
       copies_wait<R::STAGES - 2>();
       __syncwarp();   // every lane's share of this slot is there, and the last slot has been read by all
       request();      // into the last slot
       float2 v[4], p[4];
-      read_row<E, HALF>(slots + use * R::SLOT + mine + off0, away, v);
-      use = use + 1 == R::STAGES ? 0 : use + 1;
+      read_row<E, HALF>(read + use, away, v);
+      use = R::next(use);
       if (!PLAIN && !has) only_rotated(v, 0);
       float r = 1.f;
       if (PLAIN || a.normed) {
@@ -247,7 +252,7 @@ static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k,
   int64_t all = 0;
   for (int i = 0; i < 2; ++i) {
     a->splits[i] = (heads[i] + a->run - 1) / a->run;
-    a->units[i] = token_groups * a->splits[i];
+    a->units[i] = (int)(token_groups * a->splits[i]);   // (splits are 1 unless tokens are few)
     all += (a->units[i] + QK_WARPS - 1) / QK_WARPS;
   }
   const int ctas = (int)std::min<int64_t>(all, (int64_t)sm_count() * QK_CTAS);

@@ -38,8 +38,7 @@ struct QkArgs {
   float mscale;
   // the fast kernels' work: CTAs 0 .. ctas_q-1 take q, the others k; a unit is `run` heads of as many
   // neighbouring tokens as a warp has rows
-  int run, splits[2], ctas_q;
-  int64_t units[2];
+  int run, splits[2], units[2], ctas_q;
 };
 
 // turns per position as a fraction of 2^64
@@ -101,20 +100,20 @@ template <typename E> __device__ __forceinline__ float2 pair_at(const uint32_t* 
   else return pair_f32(u[j], (const E*)nullptr);
 }
 
-// a lane's 8 values of a row: `p` its first block, `away` elements from there its second
+// a lane's 8 values of a row in shared memory: `at` its first block, `away` elements from there its second
 template <typename E, bool HALF>
-__device__ __forceinline__ void read_row(const E* p, int away, float2 (&v)[4]) {
+__device__ __forceinline__ void read_row(uint32_t at, int away, float2 (&v)[4]) {
   RawV<E, 4> b[2];
   if constexpr (!HALF && sizeof(E) == 2) {
     RawV<E, 8> r;
-    r.load(p);
+    r.load_shared(at);
     b[0].u[0] = r.u[0];
     b[0].u[1] = r.u[1];
     b[1].u[0] = r.u[2];
     b[1].u[1] = r.u[3];
   } else {
-    b[0].load(p);
-    b[1].load(p + away);
+    b[0].load_shared(at);
+    b[1].load_shared(at + away * (int)sizeof(E));
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = pair_at<E>(b[j >> 1].u, j & 1);
@@ -147,11 +146,12 @@ template <typename E, int L, int N> struct Ring {
   static constexpr int ROW = 8 * L;                              // values a row has room for
   static constexpr int ROWS = 32 / L;
   static constexpr int SLOT = N * ROWS * ROW;                    // values
+  static constexpr int BYTES = SLOT * (int)sizeof(E);
+  static __device__ __forceinline__ int next(int at) { return at + BYTES == STAGES * BYTES ? 0 : at + BYTES; }
   static constexpr int STAGES = N * CHUNKS == 1 ? 8 : N * CHUNKS == 2 ? 6 : 4;
 };
-__device__ __forceinline__ void copy16(void* smem, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING> __device__ __forceinline__ void copies_wait() {
@@ -209,21 +209,20 @@ template <bool HALF, bool FAST> struct Angles {
 // A warp's place in its work on one kind of heads: one token for each group of L lanes, `run` heads of them. A group past
 // the last token works on the last one, and keeps nothing.
 template <int L> struct Place {
-  int64_t unit, t;
-  int h, hend;
+  int unit, h, left;   // left: heads of the run from h on
+  int64_t t;
   bool live;
   __device__ __forceinline__ void enter(const QkArgs& a, int splits, int heads) {
-    int64_t tokens = unit;
-    int part = 0;
+    int tokens = unit, part = 0;
     if (splits > 1) {
       tokens = unit / splits;
-      part = (int)(unit - tokens * splits);
+      part = unit - tokens * splits;
     }
-    t = tokens * (32 / L) + (threadIdx.x & 31) / L;
+    t = (int64_t)tokens * (32 / L) + (threadIdx.x & 31) / L;
     live = t < a.T;
     t = live ? t : a.T - 1;
     h = part * a.run;
-    hend = min(h + a.run, heads);
+    left = min(a.run, heads - h);
   }
 };
 

@@ -23,8 +23,8 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
   const bool has = PLAIN || l < a.D / 8;
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
-  const int64_t warps = (int64_t)(which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
-  const int64_t units = which ? a.units[1] : a.units[0];
+  const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
+  const int units = which ? a.units[1] : a.units[0];
   const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
   const E* xbase = static_cast<const E*>(which ? a.x[1] : a.x[0]) + l * VEC;
   const E* gbase = static_cast<const E*>(which ? a.in[1] : a.in[0]) + l * VEC;
@@ -35,26 +35,29 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = make_float2(0.f, 0.f);
   Place<L> at, to;
-  at.unit = to.unit = (int64_t)cta * QK_WARPS + (threadIdx.x >> 5);
+  at.unit = to.unit = cta * QK_WARPS + (threadIdx.x >> 5);
   if (at.unit < units) {
     to.enter(a, splits, heads);
     const E* px = xbase + to.t * xt + to.h * xh;
     const E* pg = gbase + to.t * yt + to.h * yh;
-    int fill = 0, use = 0;
+    const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine + off0);
+    int fill = 0, use = 0;   // byte offsets of slots
+    bool more = true;
+    const uint32_t landing = (uint32_t)__cvta_generic_to_shared(slots) + (mine + l * VEC) * (int)sizeof(E);
     auto request = [&] {
-      if (to.unit < units) {
-        E* s = slots + fill * R::SLOT + mine + l * VEC;
+      if (more) {
 #pragma unroll
         for (int i = 0; i < R::CHUNKS; ++i)
-          if (PLAIN || (l + i * L) * VEC < a.D) {
-            copy16(s + i * L * VEC, px + i * L * VEC);
-            copy16(s + R::SLOT / 2 + i * L * VEC, pg + i * L * VEC);
+          if (PLAIN || (l + i * L) * VEC < a.D) {   // lanes past the row's end have none of its chunks
+            copy16(landing + fill + i * L * 16, px + i * L * VEC);
+            copy16(landing + R::BYTES / 2 + fill + i * L * 16, pg + i * L * VEC);
           }
         px += xh;
         pg += yh;
-        if (++to.h == to.hend) {
+        if (--to.left == 0) {
           to.unit += warps;
-          if (to.unit < units) {
+          more = to.unit < units;
+          if (more) {
             to.enter(a, splits, heads);
             px = xbase + to.t * xt + to.h * xh;
             pg = gbase + to.t * yt + to.h * yh;
@@ -62,7 +65,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
         }
       }
       copies_commit();
-      fill = fill + 1 == R::STAGES ? 0 : fill + 1;
+      fill = R::next(fill);
     };
 #pragma unroll
     for (int i = 0; i < R::STAGES - 1; ++i) request();
@@ -77,15 +80,15 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
       ang.at(a, at.t, l, co, si);
       E* dx = dbase + at.t * xt + at.h * xh;
       const bool keep = at.live && has;
-      for (int h = at.h; h < at.hend; ++h) {
+      for (int n = at.left; n > 0; --n) {
         copies_wait<R::STAGES - 2>();
         __syncwarp();
         request();
         float2 v[4], g[4], p[4];
-        const E* s0 = slots + use * R::SLOT + mine + off0;
+        const uint32_t s0 = read + use;
         read_row<E, HALF>(s0, away, v);
-        read_row<E, HALF>(s0 + R::SLOT / 2, away, g);
-        use = use + 1 == R::STAGES ? 0 : use + 1;
+        read_row<E, HALF>(s0 + R::BYTES / 2, away, g);
+        use = R::next(use);
         if (!PLAIN && !has) {
           only_rotated(v, 0);
           only_rotated(g, 0);
