@@ -41,10 +41,19 @@ struct QkArgs {
   int run, splits[2], units[2], ctas_q;
 };
 
-// turns per position as a fraction of 2^64
+// f / 2 pi, the turns per position, as a fraction of 2^64 (modulo whole turns): f's 53-bit mantissa times
+// 2^66 / 2 pi, shifted by its exponent, in integers, since FP64 arithmetic is slow here and a single token's call waits for it
 __device__ __forceinline__ uint64_t turn_step(double f) {
-  const double t = f * 0.15915494309189533577;   // 1 / (2 pi)
-  return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
+  constexpr uint64_t PER_TURN = 0xA2F9836E4E441529ull;   // floor(2^66 / 2 pi)
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int e = (int)(bits >> 52) & 0x7ff;
+  if (e == 0) return 0;   // zero, or less than 2^-1022
+  const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  const uint64_t hi = __umul64hi(m, PER_TURN), lo = m * PER_TURN;
+  const int down = 1077 - e;   // f = m 2^(e - 1075), and the product counts 2^-66 turns: down to 2^-64
+  const uint64_t t = down >= 128 ? 0 : down >= 64 ? hi >> (down - 64)
+                     : down > 0 ? (hi << (64 - down)) | (lo >> down) : down > -64 ? lo << -down : 0;
+  return bits >> 63 ? 0 - t : t;
 }
 // m cos and m sin at position pos. FAST: within 2^-20, by the hardware's functions, for values that are then
 // rounded to 16 bits.

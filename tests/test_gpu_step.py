@@ -93,6 +93,31 @@ def test_ragged_lengths_with_every_state_kept(kda):
     check(x, run(x, kda, slot_in, slot_out), slot_in, slot_out)
 
 
+@pytest.mark.parametrize("kda", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("lens", [[12], [13, 14], [33, 0, 7], [64, 100], [1, 0, 300]])
+def test_long_sequences(lens, dtype, kda):
+    """Lengths at which several tokens are taken at a time, with ends at every place of such a block, and states
+    wanted in the middle and nowhere."""
+    T = sum(lens)
+    x = make(lens, 1, 3, 12, dtype, kda, seed=T)
+    slot_in = [2, -1, 0][:len(lens)]
+    slot_out = np.full(T, -1)
+    ends = np.cumsum(lens)
+    slot_out[ends[0] - 1] = 2
+    slot_out[[T // 2, T // 2 + 1, T - 2]] = [3, 4, 5]
+    check(x, run(x, kda, slot_in, slot_out), slot_in, slot_out)
+
+
+@pytest.mark.parametrize("kda", [False, True])
+def test_long_sequences_with_steep_gates(kda):
+    x = make([40], 1, 2, 2, "fp32", kda, seed=13, steep=True)
+    x["g"][7] = -float("inf")
+    slot_out = np.full(40, -1)
+    slot_out[[8, 39]] = [0, 1]
+    check(x, run(x, kda, [1], slot_out), [1], slot_out)
+
+
 def test_default_slots_update_in_place():
     """Without tables sequence n lives in slot n, and is written back after its last token."""
     lens = [2, 0, 5, 1]
