@@ -12,8 +12,6 @@
 // of 8 rows.  The state is read once and stays in registers over all tokens of the sequence.
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_elem.cuh"
@@ -25,7 +23,13 @@ namespace gdn {
 constexpr int ST_WARPS = 2;            // warps per CTA
 constexpr int ST_COLS = 16;            // columns of a warp
 constexpr int ST_PARTS = D / ST_COLS;  // warps per (sequence, head)
-constexpr int ST_LONG = 12;            // tokens a sequence from which on four are taken at a time
+#ifndef STB_TEST
+#define STB_TEST 4
+#endif
+#ifndef STL
+#define STL 12
+#endif
+constexpr int ST_LONG = STL;            // tokens a sequence from which on four are taken at a time
 constexpr float ST_EPS = 1e-6f;        // under the root of the l2 norm
 
 struct StepArgs {
@@ -41,7 +45,7 @@ struct StepArgs {
   void* o;
   int* err;
   int64_t T, qs, ks, vs;
-  int N, H, HV, G, slots, l2norm;
+  int N, H, HV, G, slots, l2norm, sms;
   float scale;
 };
 
@@ -212,69 +216,101 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
 // (k, q without their norms rk, rq).  All products with S0 are independent of the chain over the tokens, which is left
 // with four values a column; and S is scaled once in four tokens.
 //
-// A CTA of STB_WARPS warps has 16 columns a warp of one (sequence, head).  The vectors that all columns share are
-// worked out once a CTA: a phase is STB_WARPS blocks, each prepared by one warp into shared memory, then taken by all
-// warps without a wait. A block ends early where a state has to be written.
-constexpr int STB_WARPS = 4;
-constexpr int STB_TOKENS = 4;                        // tokens of a block
-constexpr int STB_COLS = STB_WARPS * ST_COLS;        // columns of a CTA
-constexpr int STB_PARTS = D / STB_COLS;
+// A warp owns 32 columns of one (sequence, head): lane (r, c) = (lane / 4, lane % 4) has 8 columns of the 16 rows
+// 32 m + 4 r + 0..3, m < 4, in 128 registers, as pairs of rows, so that what it reads of the shared vectors is used
+// eight times and in pairs as it lies.  The vectors that all columns share are worked out once a CTA of WARPS
+// warps: a phase is WARPS blocks, each prepared by one warp into shared memory, then taken by all warps
+// without a wait, while the next phase's rows are copied in. A block ends early where a state has to be written.
+constexpr int STB_TOKENS = 4;   // tokens of a block
+constexpr int STB_COLS = 32;    // columns of a warp
 // sums and scalars of a block
 constexpr int STB_L = 0, STB_M = 6, STB_KK = 16, STB_QQ = 20, STB_BETA = 24, STB_SCALARS = 28;
 
-struct StepBlock {
+constexpr int STB_E_BYTES = STB_TOKENS * STB_COLS * (int)sizeof(float2);
+
+template <int WARPS> struct StepBlock {
+  static constexpr int COLS = WARPS * STB_COLS;
   float kt[STB_TOKENS][D], qt[STB_TOKENS][D];   // E(0,t) k_t, E(0,t) q_t
   float kh[STB_TOKENS][D];                      // E(t,4) k_t
   float decay[D];                               // E(0,4)
-  float v[STB_TOKENS][STB_COLS];
+  float v[STB_TOKENS][COLS];
   float scalars[STB_SCALARS];                   // the pair sums, then rk, rq scale, beta
 };
 
-// One warp prepares the block of `len` tokens from t on; tokens past len change nothing.
-template <typename E, bool KDA>
-__device__ __forceinline__ void prepare_block(const StepArgs& a, int h, int part, int t, int len, StepBlock* blk) {
+// The rows of a phase's tokens as they lie in memory (one FP32 g a token, or one a channel).
+template <typename E, bool KDA, int WARPS> struct alignas(16) StepRaw {
+  static constexpr int TOKENS = WARPS * STB_TOKENS;
+  E k[TOKENS][D], q[TOKENS][D];
+  E v[TOKENS][WARPS * STB_COLS];
+  float g[TOKENS][KDA ? D : 1];
+  float beta[TOKENS];
+};
+__device__ __forceinline__ void copy_async16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_async4(void* smem, const void* global) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+}
+// A warp's share of the copies: the tokens first + 4 warp + 0..3, as far as there are any
+template <typename E, bool KDA, int WARPS>
+__device__ __forceinline__ void request_rows(const StepArgs& a, int h, int part, int first, int t1, int warp,
+                                             StepRaw<E, KDA, WARPS>* raw) {
+  constexpr int VEC = 16 / (int)sizeof(E), ROW = D / VEC, VROW = WARPS * STB_COLS / VEC;
   const int lane = threadIdx.x & 31, hq = h / a.G;
-  float k[4][4], q[4][4], dec[4][4], v[4][STB_COLS / 32], beta = 0.f;
-  RawV<E, 4> rk[4], rq[4];
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int64_t ts = t + s;
-    if (s < len) {
-      rk[s].load(static_cast<const E*>(a.k) + ts * a.ks + hq * D + lane * 4);
-      rq[s].load(static_cast<const E*>(a.q) + ts * a.qs + hq * D + lane * 4);
-      const E* vp = static_cast<const E*>(a.v) + ts * a.vs + h * D + part * STB_COLS + lane;
-#pragma unroll
-      for (int i = 0; i < STB_COLS / 32; ++i) v[s][i] = to_f32(vp[32 * i]);
-      if (KDA) {
-        const float4 g = *reinterpret_cast<const float4*>(a.g + (ts * a.HV + h) * D + lane * 4);
-        dec[s][0] = g.x; dec[s][1] = g.y; dec[s][2] = g.z; dec[s][3] = g.w;
-      } else {
-        dec[s][0] = a.g[ts * a.HV + h];
-      }
-    } else {
-      rk[s].zero();
-      rq[s].zero();
-#pragma unroll
-      for (int i = 0; i < STB_COLS / 32; ++i) v[s][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dec[s][i] = 0.f;
+  for (int i0 = 0; i0 < STB_TOKENS * ROW; i0 += 32) {
+    const int i = i0 + lane, j = warp * STB_TOKENS + i / ROW, x = i % ROW * VEC;
+    const int64_t t = first + j;
+    if (t < t1) {
+      copy_async16(&raw->k[j][x], static_cast<const E*>(a.k) + t * a.ks + hq * D + x);
+      copy_async16(&raw->q[j][x], static_cast<const E*>(a.q) + t * a.qs + hq * D + x);
     }
   }
-  if (lane >= STB_BETA && lane - STB_BETA < len) beta = a.beta[(int64_t)(t + lane - STB_BETA) * a.HV + h];
+#pragma unroll
+  for (int i0 = 0; i0 < STB_TOKENS * VROW; i0 += 32) {
+    const int i = i0 + lane, j = warp * STB_TOKENS + i / VROW, x = i % VROW * VEC;
+    const int64_t t = first + j;
+    if (i < STB_TOKENS * VROW && t < t1)
+      copy_async16(&raw->v[j][x], static_cast<const E*>(a.v) + t * a.vs + h * D + part * (WARPS * STB_COLS) + x);
+  }
+  if (KDA) {
+#pragma unroll
+    for (int i = 0; i < STB_TOKENS; ++i) {
+      const int j = warp * STB_TOKENS + i;
+      const int64_t t = first + j;
+      if (t < t1) copy_async16(&raw->g[j][KDA ? lane * 4 : 0], a.g + (t * a.HV + h) * D + lane * 4);
+    }
+  }
+  const int j = warp * STB_TOKENS + lane % STB_TOKENS;
+  const int64_t t = first + j;
+  if (lane < STB_TOKENS && t < t1) copy_async4(&raw->beta[j], a.beta + t * a.HV + h);
+  if (!KDA && lane >= 8 && lane < 8 + STB_TOKENS && t < t1) copy_async4(&raw->g[j][0], a.g + t * a.HV + h);
+}
+
+// One warp prepares the block of `len` tokens from the phase's token j on; tokens past len change nothing.
+template <typename E, bool KDA, int WARPS>
+__device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E, KDA, WARPS>& raw, int j, int len,
+                                              StepBlock<WARPS>* blk) {
+  constexpr int COLS = StepBlock<WARPS>::COLS;
+  const int lane = threadIdx.x & 31;
+  float k[4][4], q[4][4], dec[4][4];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    rk[s].get(k[s]);
-    rq[s].get(q[s]);
-    if (KDA) {
+    RawV<E, 4> x;
+    x.zero();
+    if (s < len) x.load_shared(smem_u32(&raw.k[j + s][lane * 4]));
+    x.get(k[s]);
+    x.zero();
+    if (s < len) x.load_shared(smem_u32(&raw.q[j + s][lane * 4]));
+    x.get(q[s]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dec[s][i] = expf(dec[s][i]);
-    } else {
-      dec[s][0] = expf(dec[s][0]);
-      dec[s][1] = dec[s][2] = dec[s][3] = dec[s][0];
-    }
+    for (int i = 0; i < COLS / 32; ++i) blk->v[s][lane + 32 * i] = s < len ? to_f32(raw.v[j + s][lane + 32 * i]) : 0.f;
+    // (the fast exponential: off by a few last places of a value at most one, times |g| e^g of the argument's rounding)
 #pragma unroll
-    for (int i = 0; i < STB_COLS / 32; ++i) blk->v[s][lane + 32 * i] = v[s][i];
+    for (int i = 0; i < 4; ++i)
+      dec[s][i] = s >= len ? 1.f : KDA || i == 0 ? __expf(raw.g[j + s][KDA ? lane * 4 + i : 0]) : dec[s][0];
   }
+  const float beta = lane >= STB_BETA && lane - STB_BETA < len ? raw.beta[j + lane - STB_BETA] : 0.f;
   float sums[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) sums[i] = 0.f;
@@ -322,12 +358,38 @@ __device__ __forceinline__ void prepare_block(const StepArgs& a, int h, int part
   if (lane < STB_SCALARS) blk->scalars[lane] = x;
 }
 
-template <typename E, bool KDA>
-__global__ void __launch_bounds__(STB_WARPS * 32, 4) step_block_kernel(const StepArgs a) {
+// Few sequences of unlike lengths are all on the GPU at once, and an SM's time is the sum of its CTAs': so the CTAs go by
+// falling length, and every second row of them over the SMs in the other direction (586 tokens in lengths
+// 0 .. 160 at HV = 48: BALANCED us, in the sequences' own order UNBALANCED us).
+constexpr int STB_SORTED = 32;   // sequences that one warp ranks
+__device__ __forceinline__ int balanced_place(const StepArgs& a, int place, int places) {
+  if (a.N > STB_SORTED) return place;
+  const int row = place / a.sms, first = row * a.sms;
+  return row & 1 ? first + min(a.sms, places - first) - 1 - (place - first) : place;
+}
+__device__ __forceinline__ int sequence_of_rank(const StepArgs& a, int rank) {
+  if (a.N > STB_SORTED || !a.cu) return rank;
+  const int lane = threadIdx.x & 31, len = lane < a.N ? a.cu[lane + 1] - a.cu[lane] : INT32_MIN;
+  int before = 0;   // sequences that are longer, or as long and earlier
+  for (int i = 0; i < a.N; ++i) {
+    const int other = __shfl_sync(~0u, len, i);
+    before += other > len || (other == len && i < lane);
+  }
+  return __ffs(__ballot_sync(~0u, lane < a.N && before == rank)) - 1;
+}
+
+template <typename E, bool KDA, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const StepArgs a) {
+  using Block = StepBlock<WARPS>;
+  using Raw = StepRaw<E, KDA, WARPS>;
+  constexpr int PARTS = D / Block::COLS;
   extern __shared__ __align__(16) uint8_t step_smem[];
-  StepBlock* blocks = reinterpret_cast<StepBlock*>(step_smem);
+  Block* blocks = reinterpret_cast<Block*>(step_smem);
+  Raw* raw = reinterpret_cast<Raw*>(step_smem + WARPS * sizeof(Block));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-  const int part = blockIdx.x % STB_PARTS, h = blockIdx.x / STB_PARTS % a.HV, n = blockIdx.x / STB_PARTS / a.HV;
+  const int place = balanced_place(a, blockIdx.x, gridDim.x);
+  const int part = place % PARTS, h = place / PARTS % a.HV;
+  const int n = sequence_of_rank(a, place / PARTS / a.HV);
   int t0, t1;
   if (!sequence_bounds(a.cu, n, a.T, &t0, &t1)) {
     if (threadIdx.x == 0) *a.err = ST_DEVICE;
@@ -339,188 +401,188 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 4) step_block_kernel(const Ste
     if (threadIdx.x == 0) *a.err = ST_DEVICE;
     return;
   }
-  // This lane has 4 columns of the rows 32 m + 4 r + 0..3, m < 4, as pairs of rows: S[2 m + i][col] holds the rows
-  // 32 m + 4 r + 2 i and the next
+  request_rows<E, KDA, WARPS>(a, h, part, t0, t1, warp, raw);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  // where the state after token first + lane goes: -1 nowhere
+  auto wanted = [&](int first) {
+    const int look = first + lane;
+    return look >= t1 ? -1 : a.slot_out ? a.slot_out[look] : look == t1 - 1 ? from : -1;
+  };
+  int wants = wanted(t0);
+  // S[2 m + i][x]: the rows 32 m + 4 r + 2 i and the next, of this lane's column x ^ (r & 6).  With the columns in that
+  // order a lane always gives the upper half of its sums away and keeps the lower.
   const int64_t slot_elems = (int64_t)a.HV * STATE_F32;
-  const int col0 = part * STB_COLS + warp * ST_COLS + c * 4;
-  const int64_t at = (int64_t)h * STATE_F32 + r * 4 * D + col0;
-  float2 S[8][4];
+  const int64_t at = (int64_t)h * STATE_F32 + r * 4 * D + part * Block::COLS + warp * STB_COLS + c * 8;
+  float2 S[8][8];
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    if (from >= 0) {
-      const float* p = a.states + from * slot_elems + at + ((m >> 1) * 32 + (m & 1) * 2) * D;
-      x = *reinterpret_cast<const float4*>(p);
-      y = *reinterpret_cast<const float4*>(p + D);
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int x = 0; x < 8; x += 2) {   // two columns at a time
+      float2 top = make_float2(0.f, 0.f), low = top;
+      if (from >= 0) {
+        const float* p = a.states + from * slot_elems + at + ((m >> 1) * 32 + (m & 1) * 2) * D + (x ^ (r & 6));
+        top = *reinterpret_cast<const float2*>(p);
+        low = *reinterpret_cast<const float2*>(p + D);
+      }
+      S[m][x] = make_float2(top.x, low.x);
+      S[m][x + 1] = make_float2(top.y, low.y);
     }
-    S[m][0] = make_float2(x.x, y.x);
-    S[m][1] = make_float2(x.y, y.y);
-    S[m][2] = make_float2(x.z, y.z);
-    S[m][3] = make_float2(x.w, y.w);
-  }
-  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-  const int own = c * 4 + (b3 ? 2 : 0) + (b2 ? 1 : 0);   // this lane's column of the sums, within the warp's
-  E* op = static_cast<E*>(a.o) + (int64_t)h * D + part * STB_COLS + warp * ST_COLS + own;
+  const int own = c * 8 + r;   // this lane's column of the sums, within the warp's
+  E* op = static_cast<E*>(a.o) + (int64_t)h * D + part * Block::COLS + warp * STB_COLS + own;
+  float2(*se)[STB_COLS] = reinterpret_cast<float2(*)[STB_COLS]>(
+      step_smem + WARPS * sizeof(Block) + sizeof(Raw) + warp * STB_E_BYTES);   // every e twice: pairs as they are used
 
   int t = t0;
   while (t < t1) {
     // the phase's blocks: up to 4 tokens each, a state that is wanted only at a block's end
-    const int look = t + lane;
-    const int wants = look >= t1 ? -1 : a.slot_out ? a.slot_out[look] : look == t1 - 1 ? from : -1;
     const unsigned cuts = __ballot_sync(~0u, wants != -1);
-    auto length = [&](int pos) {
-      const int len = min(STB_TOKENS, t1 - t - pos), cut = __ffs(pos < 32 ? cuts >> pos : 0u);
+    auto length = [&](int pos) {   // (pos < 32: a phase has at most 4 * 4 tokens)
+      const int len = min(STB_TOKENS, t1 - t - pos), cut = __ffs(cuts >> pos);
       return cut ? min(len, cut) : len;
     };
-    int pos = 0;
-    for (int b = 0; b < warp; ++b) pos += length(pos);
-    __syncthreads();   // the last phase's blocks have been read
+    int mine = 0, all = 0;   // where this warp's block begins, and how many tokens the phase has
+    for (int b = 0; b < WARPS; ++b) {
+      if (b == warp) mine = all;
+      all += length(all);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();   // the rows are there, and the last phase's blocks have been read
     {
-      const int len = length(pos);
-      if (len > 0) prepare_block<E, KDA>(a, h, part, t + pos, len, blocks + warp);
+      const int len = length(mine);
+      if (warp == 0 || mine < all) prepare_block<E, KDA, WARPS>(a, *raw, mine, len, blocks + warp);
     }
     __syncthreads();
-    pos = 0;
-    for (int b = 0; b < STB_WARPS; ++b) {
+    request_rows<E, KDA, WARPS>(a, h, part, t + all, t1, warp, raw);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int next_wants = wanted(t + all);
+    int pos = 0;
+#pragma unroll 1
+    for (int b = 0; b < WARPS; ++b) {
       const int len = length(pos);
       if (len <= 0) break;
-      const StepBlock& blk = blocks[b];
-      // S0^T with the vectors of two tokens at a time: sum[token][u, o][column]
-      float sum[4][2][4];
+      const Block& blk = blocks[b];
+      // S0^T with a token's two vectors, summed over the 8 row lanes: y[token][u, o] of column `own`
+      float y[4][2];
 #pragma unroll
-      for (int two = 0; two < 2; ++two) {
-        float2 acc[2][2][4];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i >> 3][i >> 2 & 1][i & 3] = make_float2(0.f, 0.f);
+      for (int s = 0; s < 4; ++s) {
+        float2 acc[2][8];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int kind = 0; kind < 2; ++kind) {
+            const float4 x = *reinterpret_cast<const float4*>((kind ? blk.qt[s] : blk.kt[s]) + 32 * m + 4 * r);
 #pragma unroll
-            for (int kind = 0; kind < 2; ++kind) {
-              const float* src = kind ? blk.qt[2 * two + i] : blk.kt[2 * two + i];
-              const float4 x = *reinterpret_cast<const float4*>(src + 32 * m + 4 * r);
-#pragma unroll
-              for (int col = 0; col < 4; ++col) {
-                acc[i][kind][col] = __ffma2_rn(S[2 * m][col], make_float2(x.x, x.y), acc[i][kind][col]);
-                acc[i][kind][col] = __ffma2_rn(S[2 * m + 1][col], make_float2(x.z, x.w), acc[i][kind][col]);
-              }
+            for (int i = 0; i < 8; ++i) {
+              acc[kind][i] = m ? __ffma2_rn(S[2 * m][i], make_float2(x.x, x.y), acc[kind][i])
+                               : __fmul2_rn(S[0][i], make_float2(x.x, x.y));
+              acc[kind][i] = __ffma2_rn(S[2 * m + 1][i], make_float2(x.z, x.w), acc[kind][i]);
             }
+          }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = acc[i >> 3][i >> 2 & 1][i & 3];
-          sum[2 * two + (i >> 3)][i >> 2 & 1][i & 3] = x.x + x.y;
+        for (int kind = 0; kind < 2; ++kind) {
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = acc[kind][i].x + acc[kind][i].y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] += __shfl_xor_sync(~0u, w[4 + i], 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[i] += __shfl_xor_sync(~0u, w[2 + i], 8);
+          const float give = lane & 4 ? w[0] : w[1];
+          y[s][kind] = (lane & 4 ? w[1] : w[0]) + __shfl_xor_sync(~0u, give, 4);
         }
       }
-      // over the 8 row lanes: a lane ends with column `own`, of u (bit 4 clear) or o (set), all four tokens
-      float y[4];
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        float w[4], z[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = (b4 ? sum[s][1][i] : sum[s][0][i]) + __shfl_xor_sync(~0u, b4 ? sum[s][0][i] : sum[s][1][i], 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          z[i] = (b3 ? w[2 + i] : w[i]) + __shfl_xor_sync(~0u, b3 ? w[i] : w[2 + i], 8);
-        y[s] = (b2 ? z[1] : z[0]) + __shfl_xor_sync(~0u, b2 ? z[0] : z[1], 4);
-      }
-      float sc[STB_SCALARS];
+      // the chain over the tokens
+      float sc[STB_SCALARS], e[4];
 #pragma unroll
       for (int i = 0; i < STB_SCALARS / 4; ++i) {
         const float4 x = *reinterpret_cast<const float4*>(blk.scalars + 4 * i);
         sc[4 * i] = x.x; sc[4 * i + 1] = x.y; sc[4 * i + 2] = x.z; sc[4 * i + 3] = x.w;
       }
-      float e[4];
+      __syncwarp();   // the last block's e have been read
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        float u = y[s];
+        float u = y[s][0], o = y[s][1];
 #pragma unroll
-        for (int i = 0; i < s; ++i) u = fmaf(sc[STB_L + s * (s - 1) / 2 + i], e[i], u);
+        for (int i = 0; i < s; ++i) {
+          u = fmaf(sc[STB_L + s * (s - 1) / 2 + i], e[i], u);
+          o = fmaf(sc[STB_M + s * (s + 1) / 2 + i], e[i], o);
+        }
         const float rk = sc[STB_KK + s];
-        e[s] = rk * sc[STB_BETA + s] * fmaf(-rk, u, blk.v[s][warp * ST_COLS + own]);
+        e[s] = rk * sc[STB_BETA + s] * fmaf(-rk, u, blk.v[s][warp * STB_COLS + own]);
+        o = fmaf(sc[STB_M + s * (s + 1) / 2 + s], e[s], o);
+        se[s][own] = make_float2(e[s], e[s]);
+        if (s < len) op[(int64_t)(t + pos + s) * a.HV * D] = from_f32<E>(sc[STB_QQ + s] * o);
       }
-      float2 f[4][4];   // e of this lane's columns, twice each
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const float mine = __shfl_sync(~0u, e[s], lane & 15);   // the u lane's, in the o lane too
-#pragma unroll
-        for (int col = 0; col < 4; ++col) {
-          const float x = __shfl_sync(~0u, mine, c + ((col >> 1) << 3) + ((col & 1) << 2));
-          f[s][col] = make_float2(x, x);
-        }
-        e[s] = mine;
-      }
-      if (b4) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          float o = y[s];
-#pragma unroll
-          for (int i = 0; i <= s; ++i) o = fmaf(sc[STB_M + s * (s + 1) / 2 + i], e[i], o);
-          if (s < len) op[(int64_t)(t + pos + s) * a.HV * D] = from_f32<E>(sc[STB_QQ + s] * o);
-        }
-      }
+      __syncwarp();
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const float4 x = *reinterpret_cast<const float4*>(blk.decay + 32 * m + 4 * r);
 #pragma unroll
-        for (int col = 0; col < 4; ++col) {
-          S[2 * m][col] = __fmul2_rn(S[2 * m][col], make_float2(x.x, x.y));
-          S[2 * m + 1][col] = __fmul2_rn(S[2 * m + 1][col], make_float2(x.z, x.w));
+        for (int i = 0; i < 8; ++i) {
+          S[2 * m][i] = __fmul2_rn(S[2 * m][i], make_float2(x.x, x.y));
+          S[2 * m + 1][i] = __fmul2_rn(S[2 * m + 1][i], make_float2(x.z, x.w));
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        float2 f[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(&se[s][c * 8 + (i ^ (r & 6))]);
+          f[i] = make_float2(x.x, x.y);
+          f[i + 1] = make_float2(x.z, x.w);
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int m = 0; m < 4; ++m) {
           const float4 k = *reinterpret_cast<const float4*>(blk.kh[s] + 32 * m + 4 * r);
 #pragma unroll
-          for (int col = 0; col < 4; ++col) {
-            S[2 * m][col] = __ffma2_rn(make_float2(k.x, k.y), f[s][col], S[2 * m][col]);
-            S[2 * m + 1][col] = __ffma2_rn(make_float2(k.z, k.w), f[s][col], S[2 * m + 1][col]);
+          for (int i = 0; i < 8; ++i) {
+            S[2 * m][i] = __ffma2_rn(make_float2(k.x, k.y), f[i], S[2 * m][i]);
+            S[2 * m + 1][i] = __ffma2_rn(make_float2(k.z, k.w), f[i], S[2 * m + 1][i]);
           }
         }
       }
       pos += len;
-      if (cuts >> (pos - 1) & 1) {   // (pos <= 4 STB_WARPS <= 32)
+      if (cuts >> (pos - 1) & 1) {
         const int to = __shfl_sync(~0u, wants, pos - 1);
         if (to < 0 || to >= a.slots) {
           if (lane == 0) *a.err = ST_DEVICE;
         } else {
-          float* p = a.states + to * slot_elems + at;
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            float* row = p + ((m >> 1) * 32 + (m & 1) * 2) * D;
-            *reinterpret_cast<float4*>(row) = make_float4(S[m][0].x, S[m][1].x, S[m][2].x, S[m][3].x);
-            *reinterpret_cast<float4*>(row + D) = make_float4(S[m][0].y, S[m][1].y, S[m][2].y, S[m][3].y);
-          }
+          for (int m = 0; m < 8; ++m)
+#pragma unroll
+            for (int x = 0; x < 8; x += 2) {
+              float* p = a.states + to * slot_elems + at + ((m >> 1) * 32 + (m & 1) * 2) * D + (x ^ (r & 6));
+              *reinterpret_cast<float2*>(p) = make_float2(S[m][x].x, S[m][x + 1].x);
+              *reinterpret_cast<float2*>(p + D) = make_float2(S[m][x].y, S[m][x + 1].y);
+            }
         }
       }
     }
-    t += pos;
+    t += all;
+    wants = next_wants;
   }
 }
 
-constexpr int STB_SMEM = STB_WARPS * (int)sizeof(StepBlock);
-
+template <typename E, bool KDA, int WARPS> constexpr int step_smem_bytes() {
+  return WARPS * ((int)sizeof(StepBlock<WARPS>) + STB_E_BYTES) + (int)sizeof(StepRaw<E, KDA, WARPS>);
+}
+template <typename E, bool KDA, int WARPS>
+static bool launch_step_blocks(const StepArgs& a, unsigned ctas, cudaStream_t s) {
+  constexpr int bytes = step_smem_bytes<E, KDA, WARPS>();
+  if (bytes > 48 * 1024 && cudaFuncSetAttribute(step_block_kernel<E, KDA, WARPS>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  step_block_kernel<E, KDA, WARPS><<<ctas, WARPS * 32, bytes, s>>>(a);
+  return true;
+}
 template <typename E, bool KDA>
-static void launch_step(const StepArgs& a, bool long_rows, unsigned ctas, cudaStream_t s) {
-  if (long_rows) step_block_kernel<E, KDA><<<ctas, STB_WARPS * 32, STB_SMEM, s>>>(a);
-  else step_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
-}
-
-template <typename E, bool KDA> static bool allow_smem() {
-  return cudaFuncSetAttribute(step_block_kernel<E, KDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, STB_SMEM) ==
-         cudaSuccess;
-}
-// once a device
-static bool step_setup() {
-  static std::mutex mu;
-  static bool done[128] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return false;
-  std::lock_guard<std::mutex> lk(mu);
-  if (!done[dev])
-    done[dev] = allow_smem<__nv_bfloat16, false>() && allow_smem<__half, false>() && allow_smem<float, false>() &&
-                allow_smem<__nv_bfloat16, true>() && allow_smem<__half, true>() && allow_smem<float, true>();
-  return done[dev];
+static bool launch_step(const StepArgs& a, int block_warps, unsigned ctas, cudaStream_t s) {
+  if (block_warps == 4) return launch_step_blocks<E, KDA, 4>(a, ctas, s);
+  if (block_warps == 2) return launch_step_blocks<E, KDA, 2>(a, ctas, s);
+  if (block_warps == 1) return launch_step_blocks<E, KDA, 1>(a, ctas, s);
+  step_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
+  return true;
 }
 
 static bool step_stride(int64_t* s, int heads, int esize) {
@@ -549,9 +611,12 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(o) ||
       (p->slots > 0 && !aligned16(states)))
     return GDN_ERR_INVALID_ARG;
-  // by the mean length, all that the host knows
+  // Four tokens at a time or one, by the mean length, which is all that the host knows; and then a CTA for all columns
+  // of a head, or, where those leave SMs without one, for each 32 of them.
   const bool long_rows = p->T >= (int64_t)p->N * ST_LONG;
-  const int64_t ctas = (int64_t)p->N * p->HV * (long_rows ? STB_PARTS : ST_PARTS / ST_WARPS);
+  const int64_t heads = (int64_t)p->N * p->HV;
+  const int block_warps = !long_rows ? 0 : STB_TEST;
+  const int64_t ctas = heads * (block_warps ? D / STB_COLS / block_warps : ST_PARTS / ST_WARPS);
   if (ctas > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   a.q = q;
   a.k = k;
@@ -570,18 +635,19 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   a.HV = p->HV;
   a.G = p->HV / p->H;
   a.slots = p->slots;
+  a.sms = sm_count();
   a.l2norm = p->l2norm;
   a.scale = p->scale;
-  if (!step_setup()) return GDN_ERR_CUDA;
   const int id = KDA ? K_KDA_STEP : K_STEP;
   prof_begin(id, stream);
+  bool ok;
   switch (p->dtype) {
-    case GDN_BF16: launch_step<__nv_bfloat16, KDA>(a, long_rows, (unsigned)ctas, stream); break;
-    case GDN_FP16: launch_step<__half, KDA>(a, long_rows, (unsigned)ctas, stream); break;
-    default: launch_step<float, KDA>(a, long_rows, (unsigned)ctas, stream); break;
+    case GDN_BF16: ok = launch_step<__nv_bfloat16, KDA>(a, block_warps, (unsigned)ctas, stream); break;
+    case GDN_FP16: ok = launch_step<__half, KDA>(a, block_warps, (unsigned)ctas, stream); break;
+    default: ok = launch_step<float, KDA>(a, block_warps, (unsigned)ctas, stream); break;
   }
   prof_end(id, stream);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return ok && cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace gdn
