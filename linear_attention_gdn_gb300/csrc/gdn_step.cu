@@ -7,9 +7,13 @@
 // The norms enter as scalars: k^ = rk k, q^ = rq q.
 //
 // The columns of S are independent given k^ and q^, so a warp owns 16 columns of one head's state,
-// with no other warp to wait for: lane (r, c), r = lane / 4, c = lane % 4, holds the columns 4c .. 4c+3
-// of the rows 8r .. 8r+7 and 64+8r .. 64+8r+7 (64 registers).  A load of the warp covers 64 contiguous bytes
-// of 8 rows.  The state is read once and stays in registers over all tokens of the sequence.
+// with no other warp to wait for: lane (r, c) = (lane / 4, lane % 4) holds the columns 4c .. 4c+3 of the rows
+// 8r .. 8r+7 and 64+8r .. 64+8r+7 in 64 registers.  A load of the warp covers 64 contiguous bytes of 8 rows.  The
+// state is read once and stays in registers over all tokens of the sequence.
+//
+// One token a sequence is bound by the states' bytes: 512 sequences of 48 heads move 3.24 GB in 462 us, 7.0 TB/s;
+// one sequence (6.3 MB) takes 2.7 us, most of it the launch and two dependent loads.  Longer sequences are bound by FP32
+// arithmetic, 4 multiply-adds a state value a token (step_kernel) or 3 1/4 (step_block_kernel).
 #include <cuda_runtime.h>
 
 #include "gdn.h"
@@ -23,13 +27,6 @@ namespace gdn {
 constexpr int ST_WARPS = 2;            // warps per CTA
 constexpr int ST_COLS = 16;            // columns of a warp
 constexpr int ST_PARTS = D / ST_COLS;  // warps per (sequence, head)
-#ifndef STB_TEST
-#define STB_TEST 4
-#endif
-#ifndef STL
-#define STL 12
-#endif
-constexpr int ST_LONG = STL;            // tokens a sequence from which on four are taken at a time
 constexpr float ST_EPS = 1e-6f;        // under the root of the l2 norm
 
 struct StepArgs {
@@ -61,8 +58,22 @@ __device__ __forceinline__ bool sequence_bounds(const int* cu, int n, int64_t T,
   return *t0 >= 0 && *t1 >= *t0 && *t1 <= T;
 }
 
+// What follows the sums of one token, the same in both kernels of single tokens: e = rk d of a column from its u, and
+// its output from S'^T q^ and e.
+struct StepOut {
+  float e, rq;
+};
+__device__ __forceinline__ StepOut step_column(const StepArgs& a, float kk, float qq, float u, float beta, float v) {
+  const float rk = a.l2norm ? rsqrtf(kk + ST_EPS) : 1.f, rq = a.l2norm ? rsqrtf(qq + ST_EPS) : 1.f;
+  return {__fmul_rn(__fmul_rn(beta, rk), __fmaf_rn(-rk, u, v)), __fmul_rn(a.scale, rq)};
+}
+__device__ __forceinline__ float step_output(const StepOut& x, float kq, float sum, float e) {
+  return __fmul_rn(x.rq, __fmaf_rn(kq, e, sum));
+}
+
+// about one token a sequence
 template <typename E, bool KDA>
-__global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(ST_WARPS * 32) step_token_kernel(const StepArgs a) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
   const int part = (int)(item % ST_PARTS);
@@ -124,14 +135,14 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
       const float* gp = a.g + ((int64_t)t * a.HV + h) * D + r * 8;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float e = expf(gp[(j & 7) + (j >> 3) * 64]);
+        const float e = __expf(gp[(j & 7) + (j >> 3) * 64]);
         S[j].x *= e;
         S[j].y *= e;
         S[j].z *= e;
         S[j].w *= e;
       }
     } else {
-      const float e = expf(a.g[(int64_t)t * a.HV + h]);
+      const float e = __expf(a.g[(int64_t)t * a.HV + h]);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         S[j].x *= e;
@@ -140,59 +151,51 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
         S[j].w *= e;
       }
     }
-    float s[8], kk = 0.f, qq = 0.f, kq = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+    // even and odd rows apart, and then as step_kernel does it: the same bits
+    float s[2][8], kk[2], qq[2], kq[2];
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      s[0] += S[j].x * k[j];
-      s[1] += S[j].y * k[j];
-      s[2] += S[j].z * k[j];
-      s[3] += S[j].w * k[j];
-      s[4] += S[j].x * q[j];
-      s[5] += S[j].y * q[j];
-      s[6] += S[j].z * q[j];
-      s[7] += S[j].w * q[j];
-      kk += k[j] * k[j];
-      qq += q[j] * q[j];
-      kq += k[j] * q[j];
+      const int i = j & 1;
+      const float col[4] = {S[j].x, S[j].y, S[j].z, S[j].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        s[i][x] = j < 2 ? __fmul_rn(col[x], k[j]) : __fmaf_rn(col[x], k[j], s[i][x]);
+        s[i][4 + x] = j < 2 ? __fmul_rn(col[x], q[j]) : __fmaf_rn(col[x], q[j], s[i][4 + x]);
+      }
+      kk[i] = j < 2 ? __fmul_rn(k[j], k[j]) : __fmaf_rn(k[j], k[j], kk[i]);
+      qq[i] = j < 2 ? __fmul_rn(q[j], q[j]) : __fmaf_rn(q[j], q[j], qq[i]);
+      kq[i] = j < 2 ? __fmul_rn(k[j], q[j]) : __fmaf_rn(k[j], q[j], kq[i]);
     }
     // sums over the 8 row lanes; the 8 column sums are spread over them on the way
+    float n0 = __fadd_rn(kk[0], kk[1]), n1 = __fadd_rn(qq[0], qq[1]), n2 = __fadd_rn(kq[0], kq[1]);
 #pragma unroll
     for (int x = 4; x <= 16; x <<= 1) {
-      kk += __shfl_xor_sync(~0u, kk, x);
-      qq += __shfl_xor_sync(~0u, qq, x);
-      kq += __shfl_xor_sync(~0u, kq, x);
+      n0 += __shfl_xor_sync(~0u, n0, x);
+      n1 += __shfl_xor_sync(~0u, n1, x);
+      n2 += __shfl_xor_sync(~0u, n2, x);
     }
     const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-    float w[4], y[2], sum;
+    float w[4], y[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float keep = b4 ? s[4 + i] : s[i], give = b4 ? s[i] : s[4 + i];
-      w[i] = keep + __shfl_xor_sync(~0u, give, 16);
+      const float u = __fadd_rn(s[0][i], s[1][i]), o = __fadd_rn(s[0][4 + i], s[1][4 + i]);
+      w[i] = (b4 ? o : u) + __shfl_xor_sync(~0u, b4 ? u : o, 16);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float keep = b3 ? w[2 + i] : w[i], give = b3 ? w[i] : w[2 + i];
-      y[i] = keep + __shfl_xor_sync(~0u, give, 8);
-    }
-    {
-      const float keep = b2 ? y[1] : y[0], give = b2 ? y[0] : y[1];
-      sum = keep + __shfl_xor_sync(~0u, give, 4);
-    }
-    const float rk = a.l2norm ? rsqrtf(kk + ST_EPS) : 1.f, rq = a.l2norm ? rsqrtf(qq + ST_EPS) : 1.f;
-    const float d = beta * (v - rk * sum);   // of column `own`, in the lanes with bit 4 clear
+    for (int i = 0; i < 2; ++i) y[i] = (b3 ? w[2 + i] : w[i]) + __shfl_xor_sync(~0u, b3 ? w[i] : w[2 + i], 8);
+    const float sum = (b2 ? y[1] : y[0]) + __shfl_xor_sync(~0u, b2 ? y[0] : y[1], 4);
+    const StepOut r1 = step_column(a, n0, n1, sum, beta, v);
     float f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = rk * __shfl_sync(~0u, d, c + ((i >> 1) << 3) + ((i & 1) << 2));
-    const float dq = __shfl_xor_sync(~0u, d, 16);
-    if (b4) op[(int64_t)t * a.HV * D] = from_f32<E>(a.scale * rq * (sum + kq * rk * dq));
+    for (int i = 0; i < 4; ++i) f[i] = __shfl_sync(~0u, r1.e, c + ((i >> 1) << 3) + ((i & 1) << 2));
+    const float e1 = __shfl_xor_sync(~0u, r1.e, 16);
+    if (b4) op[(int64_t)t * a.HV * D] = from_f32<E>(step_output(r1, n2, sum, e1));
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      S[j].x += k[j] * f[0];
-      S[j].y += k[j] * f[1];
-      S[j].z += k[j] * f[2];
-      S[j].w += k[j] * f[3];
+      S[j].x = __fmaf_rn(k[j], f[0], S[j].x);
+      S[j].y = __fmaf_rn(k[j], f[1], S[j].y);
+      S[j].z = __fmaf_rn(k[j], f[2], S[j].z);
+      S[j].w = __fmaf_rn(k[j], f[3], S[j].w);
     }
     const int to = a.slot_out ? a.slot_out[t] : t == t1 - 1 ? from : -1;
     if (to >= a.slots || to < -1) {
@@ -201,6 +204,163 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
       float* p = a.states + to * slot_elems + at;
 #pragma unroll
       for (int j = 0; j < 16; ++j) *reinterpret_cast<float4*>(p + ((j & 7) + (j >> 3) * 64) * D) = S[j];
+    }
+  }
+}
+
+// what a lane needs of one token
+template <typename E, bool KDA> struct StepToken {
+  Raw8<E> k[2], q[2];   // of its rows
+  float4 g[KDA ? 4 : 1];
+  float beta;
+  E v;                  // of its column of the sums
+  int to;
+};
+
+// a few tokens: the next one's rows are requested a token ahead, and rows lie in pairs for the paired FP32 instructions
+template <typename E, bool KDA>
+__global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
+  const int part = (int)(item % ST_PARTS);
+  const int h = (int)(item / ST_PARTS % a.HV);
+  const int64_t n = item / ST_PARTS / a.HV;
+  if (n >= a.N) return;
+  int t0, t1;
+  if (!sequence_bounds(a.cu, (int)n, a.T, &t0, &t1)) {
+    if (lane == 0) *a.err = ST_DEVICE;
+    return;
+  }
+  if (t0 == t1) return;
+  const int from = a.slot_in ? a.slot_in[n] : (int)n;
+  if (from < -1 || from >= a.slots) {
+    if (lane == 0) *a.err = ST_DEVICE;
+    return;
+  }
+  // element offset of this lane's first value within a slot
+  const int64_t slot_elems = (int64_t)a.HV * STATE_F32;
+  const int64_t at = (int64_t)h * STATE_F32 + r * 8 * D + part * ST_COLS + c * 4;
+  float2 S[8][4];   // [pair of rows][column]
+  if (from >= 0) {
+    const float* p = a.states + from * slot_elems + at;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float* row = p + ((j & 3) * 2 + (j >> 2) * 64) * D;
+      const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + D);
+      S[j][0] = make_float2(x.x, y.x);
+      S[j][1] = make_float2(x.y, y.y);
+      S[j][2] = make_float2(x.z, y.z);
+      S[j][3] = make_float2(x.w, y.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) S[j >> 2][j & 3] = make_float2(0.f, 0.f);
+  }
+  // after the sums, lanes with bit 4 clear hold u and those with it set S'^T q^, of this column
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+  const int own = part * ST_COLS + c * 4 + (b3 ? 2 : 0) + (b2 ? 1 : 0);
+  const int hq = h / a.G;
+  auto request = [&](int64_t t, StepToken<E, KDA>* x) {
+    const E* kp = static_cast<const E*>(a.k) + t * a.ks + hq * D + r * 8;
+    const E* qp = static_cast<const E*>(a.q) + t * a.qs + hq * D + r * 8;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      x->k[m].load(kp + 64 * m);
+      x->q[m].load(qp + 64 * m);
+    }
+    if constexpr (KDA) {
+      const float4* g = reinterpret_cast<const float4*>(a.g + (t * a.HV + h) * D + r * 8);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) x->g[m] = g[(m & 1) + (m >> 1) * 16];
+    } else {
+      x->g[0].x = a.g[t * a.HV + h];
+    }
+    x->beta = a.beta[t * a.HV + h];
+    x->v = static_cast<const E*>(a.v)[t * a.vs + h * D + own];
+    x->to = a.slot_out ? a.slot_out[t] : t == t1 - 1 ? from : -1;
+  };
+  StepToken<E, KDA> x;
+  request(t0, &x);
+  E* op = static_cast<E*>(a.o) + ((int64_t)t0 * a.HV + h) * D + own;
+  for (int t = t0; t < t1; ++t, op += (int64_t)a.HV * D) {
+    // decay: the fast exponential is off by a few last places of a value at most one, and by |g| e^g of the argument's
+    // rounding, which is less than that
+    if constexpr (KDA) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 g = x.g[j >> 1];
+        const float2 e = j & 1 ? make_float2(__expf(g.z), __expf(g.w)) : make_float2(__expf(g.x), __expf(g.y));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[j][i] = __fmul2_rn(S[j][i], e);
+      }
+    } else {
+      const float e = __expf(x.g[0].x);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) S[j >> 2][j & 3] = __fmul2_rn(S[j >> 2][j & 3], make_float2(e, e));
+    }
+    float2 k[8], s[2][4];
+    float2 kk = make_float2(0.f, 0.f), qq = kk, kq = kk;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float kf[8], qf[8];
+      x.k[m].get(kf);
+      x.q[m].get(qf);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int p = 4 * m + j;
+        k[p] = make_float2(kf[2 * j], kf[2 * j + 1]);
+        const float2 q = make_float2(qf[2 * j], qf[2 * j + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[0][i] = p ? __ffma2_rn(S[p][i], k[p], s[0][i]) : __fmul2_rn(S[p][i], k[p]);
+          s[1][i] = p ? __ffma2_rn(S[p][i], q, s[1][i]) : __fmul2_rn(S[p][i], q);
+        }
+        kk = __ffma2_rn(k[p], k[p], kk);
+        qq = __ffma2_rn(q, q, qq);
+        kq = __ffma2_rn(k[p], q, kq);
+      }
+    }
+    const float beta = x.beta, v = to_f32(x.v);
+    const int to = x.to;
+    if (t + 1 < t1) request(t + 1, &x);
+    // sums over the 8 row lanes; the 8 column sums are spread over them on the way
+    float n0 = kk.x + kk.y, n1 = qq.x + qq.y, n2 = kq.x + kq.y;
+#pragma unroll
+    for (int d = 4; d <= 16; d <<= 1) {
+      n0 += __shfl_xor_sync(~0u, n0, d);
+      n1 += __shfl_xor_sync(~0u, n1, d);
+      n2 += __shfl_xor_sync(~0u, n2, d);
+    }
+    float w[4], y[2], sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = s[0][i].x + s[0][i].y, o = s[1][i].x + s[1][i].y;
+      w[i] = (b4 ? o : u) + __shfl_xor_sync(~0u, b4 ? u : o, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y[i] = (b3 ? w[2 + i] : w[i]) + __shfl_xor_sync(~0u, b3 ? w[i] : w[2 + i], 8);
+    sum = (b2 ? y[1] : y[0]) + __shfl_xor_sync(~0u, b2 ? y[0] : y[1], 4);
+    const StepOut r1 = step_column(a, n0, n1, sum, beta, v);
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = __shfl_sync(~0u, r1.e, c + ((i >> 1) << 3) + ((i & 1) << 2));
+      f[i] = make_float2(e, e);
+    }
+    const float e1 = __shfl_xor_sync(~0u, r1.e, 16);
+    if (b4) *op = from_f32<E>(step_output(r1, n2, sum, e1));
+#pragma unroll
+    for (int j = 0; j < 32; ++j) S[j >> 2][j & 3] = __ffma2_rn(k[j >> 2], f[j & 3], S[j >> 2][j & 3]);
+    if (to >= a.slots || to < -1) {
+      if (lane == 0) *a.err = ST_DEVICE;
+    } else if (to >= 0) {
+      float* p = a.states + to * slot_elems + at;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float* row = p + ((j & 3) * 2 + (j >> 2) * 64) * D;
+        *reinterpret_cast<float4*>(row) = make_float4(S[j][0].x, S[j][1].x, S[j][2].x, S[j][3].x);
+        *reinterpret_cast<float4*>(row + D) = make_float4(S[j][0].y, S[j][1].y, S[j][2].y, S[j][3].y);
+      }
     }
   }
 }
@@ -218,30 +378,31 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
 //
 // A warp owns 32 columns of one (sequence, head): lane (r, c) = (lane / 4, lane % 4) has 8 columns of the 16 rows
 // 32 m + 4 r + 0..3, m < 4, in 128 registers, as pairs of rows, so that what it reads of the shared vectors is used
-// eight times and in pairs as it lies.  The vectors that all columns share are worked out once a CTA of WARPS
-// warps: a phase is WARPS blocks, each prepared by one warp into shared memory, then taken by all warps
+// eight times and in pairs as it lies.  The vectors that all columns share are worked out once a CTA of STB_WARPS
+// warps: a phase is STB_WARPS blocks, each prepared by one warp into shared memory, then taken by all warps
 // without a wait, while the next phase's rows are copied in. A block ends early where a state has to be written.
+constexpr int STB_MIN_TOKENS = 10;      // a sequence, on average
+constexpr int64_t STB_MIN_WORK = 12288; // tokens times heads
+constexpr int STB_WARPS = 4;
 constexpr int STB_TOKENS = 4;   // tokens of a block
-constexpr int STB_COLS = 32;    // columns of a warp
+constexpr int STB_COLS = 32;    // columns of a warp: STB_WARPS of them are a head
 // sums and scalars of a block
 constexpr int STB_L = 0, STB_M = 6, STB_KK = 16, STB_QQ = 20, STB_BETA = 24, STB_SCALARS = 28;
 
 constexpr int STB_E_BYTES = STB_TOKENS * STB_COLS * (int)sizeof(float2);
 
-template <int WARPS> struct StepBlock {
-  static constexpr int COLS = WARPS * STB_COLS;
+struct StepBlock {
   float kt[STB_TOKENS][D], qt[STB_TOKENS][D];   // E(0,t) k_t, E(0,t) q_t
   float kh[STB_TOKENS][D];                      // E(t,4) k_t
   float decay[D];                               // E(0,4)
-  float v[STB_TOKENS][COLS];
+  float v[STB_TOKENS][D];
   float scalars[STB_SCALARS];                   // the pair sums, then rk, rq scale, beta
 };
 
 // The rows of a phase's tokens as they lie in memory (one FP32 g a token, or one a channel).
-template <typename E, bool KDA, int WARPS> struct alignas(16) StepRaw {
-  static constexpr int TOKENS = WARPS * STB_TOKENS;
-  E k[TOKENS][D], q[TOKENS][D];
-  E v[TOKENS][WARPS * STB_COLS];
+template <typename E, bool KDA> struct alignas(16) StepRaw {
+  static constexpr int TOKENS = STB_WARPS * STB_TOKENS;
+  E k[TOKENS][D], q[TOKENS][D], v[TOKENS][D];
   float g[TOKENS][KDA ? D : 1];
   float beta[TOKENS];
 };
@@ -252,10 +413,10 @@ __device__ __forceinline__ void copy_async4(void* smem, const void* global) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
 }
 // A warp's share of the copies: the tokens first + 4 warp + 0..3, as far as there are any
-template <typename E, bool KDA, int WARPS>
-__device__ __forceinline__ void request_rows(const StepArgs& a, int h, int part, int first, int t1, int warp,
-                                             StepRaw<E, KDA, WARPS>* raw) {
-  constexpr int VEC = 16 / (int)sizeof(E), ROW = D / VEC, VROW = WARPS * STB_COLS / VEC;
+template <typename E, bool KDA>
+__device__ __forceinline__ void request_rows(const StepArgs& a, int h, int first, int t1, int warp,
+                                             StepRaw<E, KDA>* raw) {
+  constexpr int VEC = 16 / (int)sizeof(E), ROW = D / VEC;
   const int lane = threadIdx.x & 31, hq = h / a.G;
 #pragma unroll
   for (int i0 = 0; i0 < STB_TOKENS * ROW; i0 += 32) {
@@ -264,14 +425,8 @@ __device__ __forceinline__ void request_rows(const StepArgs& a, int h, int part,
     if (t < t1) {
       copy_async16(&raw->k[j][x], static_cast<const E*>(a.k) + t * a.ks + hq * D + x);
       copy_async16(&raw->q[j][x], static_cast<const E*>(a.q) + t * a.qs + hq * D + x);
+      copy_async16(&raw->v[j][x], static_cast<const E*>(a.v) + t * a.vs + h * D + x);
     }
-  }
-#pragma unroll
-  for (int i0 = 0; i0 < STB_TOKENS * VROW; i0 += 32) {
-    const int i = i0 + lane, j = warp * STB_TOKENS + i / VROW, x = i % VROW * VEC;
-    const int64_t t = first + j;
-    if (i < STB_TOKENS * VROW && t < t1)
-      copy_async16(&raw->v[j][x], static_cast<const E*>(a.v) + t * a.vs + h * D + part * (WARPS * STB_COLS) + x);
   }
   if (KDA) {
 #pragma unroll
@@ -288,10 +443,9 @@ __device__ __forceinline__ void request_rows(const StepArgs& a, int h, int part,
 }
 
 // One warp prepares the block of `len` tokens from the phase's token j on; tokens past len change nothing.
-template <typename E, bool KDA, int WARPS>
-__device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E, KDA, WARPS>& raw, int j, int len,
-                                              StepBlock<WARPS>* blk) {
-  constexpr int COLS = StepBlock<WARPS>::COLS;
+template <typename E, bool KDA>
+__device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E, KDA>& raw, int j, int len,
+                                              StepBlock* blk) {
   const int lane = threadIdx.x & 31;
   float k[4][4], q[4][4], dec[4][4];
 #pragma unroll
@@ -304,7 +458,7 @@ __device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E
     if (s < len) x.load_shared(smem_u32(&raw.q[j + s][lane * 4]));
     x.get(q[s]);
 #pragma unroll
-    for (int i = 0; i < COLS / 32; ++i) blk->v[s][lane + 32 * i] = s < len ? to_f32(raw.v[j + s][lane + 32 * i]) : 0.f;
+    for (int i = 0; i < D / 32; ++i) blk->v[s][lane + 32 * i] = s < len ? to_f32(raw.v[j + s][lane + 32 * i]) : 0.f;
     // (the fast exponential: off by a few last places of a value at most one, times |g| e^g of the argument's rounding)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -360,7 +514,7 @@ __device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E
 
 // Few sequences of unlike lengths are all on the GPU at once, and an SM's time is the sum of its CTAs': so the CTAs go by
 // falling length, and every second row of them over the SMs in the other direction (586 tokens in lengths
-// 0 .. 160 at HV = 48: BALANCED us, in the sequences' own order UNBALANCED us).
+// 0 .. 160 at HV = 48: 105 us, in the sequences' own order 127 us).
 constexpr int STB_SORTED = 32;   // sequences that one warp ranks
 __device__ __forceinline__ int balanced_place(const StepArgs& a, int place, int places) {
   if (a.N > STB_SORTED) return place;
@@ -378,18 +532,15 @@ __device__ __forceinline__ int sequence_of_rank(const StepArgs& a, int rank) {
   return __ffs(__ballot_sync(~0u, lane < a.N && before == rank)) - 1;
 }
 
-template <typename E, bool KDA, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const StepArgs a) {
-  using Block = StepBlock<WARPS>;
-  using Raw = StepRaw<E, KDA, WARPS>;
-  constexpr int PARTS = D / Block::COLS;
+template <typename E, bool KDA>
+__global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const StepArgs a) {
+  using Raw = StepRaw<E, KDA>;
   extern __shared__ __align__(16) uint8_t step_smem[];
-  Block* blocks = reinterpret_cast<Block*>(step_smem);
-  Raw* raw = reinterpret_cast<Raw*>(step_smem + WARPS * sizeof(Block));
+  StepBlock* blocks = reinterpret_cast<StepBlock*>(step_smem);
+  Raw* raw = reinterpret_cast<Raw*>(step_smem + STB_WARPS * sizeof(StepBlock));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
   const int place = balanced_place(a, blockIdx.x, gridDim.x);
-  const int part = place % PARTS, h = place / PARTS % a.HV;
-  const int n = sequence_of_rank(a, place / PARTS / a.HV);
+  const int h = place % a.HV, n = sequence_of_rank(a, place / a.HV);
   int t0, t1;
   if (!sequence_bounds(a.cu, n, a.T, &t0, &t1)) {
     if (threadIdx.x == 0) *a.err = ST_DEVICE;
@@ -401,7 +552,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const
     if (threadIdx.x == 0) *a.err = ST_DEVICE;
     return;
   }
-  request_rows<E, KDA, WARPS>(a, h, part, t0, t1, warp, raw);
+  request_rows<E, KDA>(a, h, t0, t1, warp, raw);
   asm volatile("cp.async.commit_group;" ::: "memory");
   // where the state after token first + lane goes: -1 nowhere
   auto wanted = [&](int first) {
@@ -412,7 +563,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const
   // S[2 m + i][x]: the rows 32 m + 4 r + 2 i and the next, of this lane's column x ^ (r & 6).  With the columns in that
   // order a lane always gives the upper half of its sums away and keeps the lower.
   const int64_t slot_elems = (int64_t)a.HV * STATE_F32;
-  const int64_t at = (int64_t)h * STATE_F32 + r * 4 * D + part * Block::COLS + warp * STB_COLS + c * 8;
+  const int64_t at = (int64_t)h * STATE_F32 + r * 4 * D + warp * STB_COLS + c * 8;
   float2 S[8][8];
 #pragma unroll
   for (int m = 0; m < 8; ++m)
@@ -428,9 +579,9 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const
       S[m][x + 1] = make_float2(top.y, low.y);
     }
   const int own = c * 8 + r;   // this lane's column of the sums, within the warp's
-  E* op = static_cast<E*>(a.o) + (int64_t)h * D + part * Block::COLS + warp * STB_COLS + own;
+  E* op = static_cast<E*>(a.o) + (int64_t)h * D + warp * STB_COLS + own;
   float2(*se)[STB_COLS] = reinterpret_cast<float2(*)[STB_COLS]>(
-      step_smem + WARPS * sizeof(Block) + sizeof(Raw) + warp * STB_E_BYTES);   // every e twice: pairs as they are used
+      step_smem + STB_WARPS * sizeof(StepBlock) + sizeof(Raw) + warp * STB_E_BYTES);   // every e twice: pairs as they are used
 
   int t = t0;
   while (t < t1) {
@@ -441,7 +592,7 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const
       return cut ? min(len, cut) : len;
     };
     int mine = 0, all = 0;   // where this warp's block begins, and how many tokens the phase has
-    for (int b = 0; b < WARPS; ++b) {
+    for (int b = 0; b < STB_WARPS; ++b) {
       if (b == warp) mine = all;
       all += length(all);
     }
@@ -449,18 +600,18 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const
     __syncthreads();   // the rows are there, and the last phase's blocks have been read
     {
       const int len = length(mine);
-      if (warp == 0 || mine < all) prepare_block<E, KDA, WARPS>(a, *raw, mine, len, blocks + warp);
+      if (warp == 0 || mine < all) prepare_block<E, KDA>(a, *raw, mine, len, blocks + warp);
     }
     __syncthreads();
-    request_rows<E, KDA, WARPS>(a, h, part, t + all, t1, warp, raw);
+    request_rows<E, KDA>(a, h, t + all, t1, warp, raw);
     asm volatile("cp.async.commit_group;" ::: "memory");
     const int next_wants = wanted(t + all);
     int pos = 0;
 #pragma unroll 1
-    for (int b = 0; b < WARPS; ++b) {
+    for (int b = 0; b < STB_WARPS; ++b) {
       const int len = length(pos);
       if (len <= 0) break;
-      const Block& blk = blocks[b];
+      const StepBlock& blk = blocks[b];
       // S0^T with a token's two vectors, summed over the 8 row lanes: y[token][u, o] of column `own`
       float y[4][2];
 #pragma unroll
@@ -564,24 +715,18 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) step_block_kernel(const
   }
 }
 
-template <typename E, bool KDA, int WARPS> constexpr int step_smem_bytes() {
-  return WARPS * ((int)sizeof(StepBlock<WARPS>) + STB_E_BYTES) + (int)sizeof(StepRaw<E, KDA, WARPS>);
-}
-template <typename E, bool KDA, int WARPS>
-static bool launch_step_blocks(const StepArgs& a, unsigned ctas, cudaStream_t s) {
-  constexpr int bytes = step_smem_bytes<E, KDA, WARPS>();
-  if (bytes > 48 * 1024 && cudaFuncSetAttribute(step_block_kernel<E, KDA, WARPS>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return false;
-  step_block_kernel<E, KDA, WARPS><<<ctas, WARPS * 32, bytes, s>>>(a);
-  return true;
-}
-template <typename E, bool KDA>
-static bool launch_step(const StepArgs& a, int block_warps, unsigned ctas, cudaStream_t s) {
-  if (block_warps == 4) return launch_step_blocks<E, KDA, 4>(a, ctas, s);
-  if (block_warps == 2) return launch_step_blocks<E, KDA, 2>(a, ctas, s);
-  if (block_warps == 1) return launch_step_blocks<E, KDA, 1>(a, ctas, s);
-  step_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
+template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool blocks, unsigned ctas, cudaStream_t s) {
+  if (blocks) {
+    constexpr int bytes = STB_WARPS * ((int)sizeof(StepBlock) + STB_E_BYTES) + (int)sizeof(StepRaw<E, KDA>);
+    if (cudaFuncSetAttribute(step_block_kernel<E, KDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+        cudaSuccess)
+      return false;
+    step_block_kernel<E, KDA><<<ctas, STB_WARPS * 32, bytes, s>>>(a);
+  } else if (a.T > 2 * (int64_t)a.N) {
+    step_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
+  } else {
+    step_token_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
+  }
   return true;
 }
 
@@ -611,12 +756,13 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(o) ||
       (p->slots > 0 && !aligned16(states)))
     return GDN_ERR_INVALID_ARG;
-  // Four tokens at a time or one, by the mean length, which is all that the host knows; and then a CTA for all columns
-  // of a head, or, where those leave SMs without one, for each 32 of them.
-  const bool long_rows = p->T >= (int64_t)p->N * ST_LONG;
-  const int64_t heads = (int64_t)p->N * p->HV;
-  const int block_warps = !long_rows ? 0 : STB_TEST;
-  const int64_t ctas = heads * (block_warps ? D / STB_COLS / block_warps : ST_PARTS / ST_WARPS);
+  // By the mean length, which is all that the host knows of the lengths: up to two tokens the kernel of the fewest
+  // registers (64 sequences of 48 heads with one token 61 us against 70, with two 73 against 81), then the one with the next
+  // token's rows on their way; and, for ten tokens and more and enough of them in all to fill the SMs, four tokens at a
+  // time (64 sequences of 16 tokens: 179 us against 222, 32 of 128: 533 against 796; but 16 of 12: 50 against 44, one of
+  // 64: 35 against 30).
+  const bool blocks = p->T >= (int64_t)p->N * STB_MIN_TOKENS && p->T * p->HV >= STB_MIN_WORK;
+  const int64_t ctas = (int64_t)p->N * p->HV * (blocks ? 1 : ST_PARTS / ST_WARPS);
   if (ctas > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   a.q = q;
   a.k = k;
@@ -642,9 +788,9 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   prof_begin(id, stream);
   bool ok;
   switch (p->dtype) {
-    case GDN_BF16: ok = launch_step<__nv_bfloat16, KDA>(a, block_warps, (unsigned)ctas, stream); break;
-    case GDN_FP16: ok = launch_step<__half, KDA>(a, block_warps, (unsigned)ctas, stream); break;
-    default: ok = launch_step<float, KDA>(a, block_warps, (unsigned)ctas, stream); break;
+    case GDN_BF16: ok = launch_step<__nv_bfloat16, KDA>(a, blocks, (unsigned)ctas, stream); break;
+    case GDN_FP16: ok = launch_step<__half, KDA>(a, blocks, (unsigned)ctas, stream); break;
+    default: ok = launch_step<float, KDA>(a, blocks, (unsigned)ctas, stream); break;
   }
   prof_end(id, stream);
   return ok && cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

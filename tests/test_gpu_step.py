@@ -118,6 +118,48 @@ def test_long_sequences_with_steep_gates(kda):
     check(x, run(x, kda, [1], slot_out), [1], slot_out)
 
 
+@pytest.mark.parametrize("kda", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("lens", [[257], [200, 61], [33, 0, 230], [1, 90, 170], [64, 64, 64, 65, 5]])
+def test_enough_tokens_to_be_taken_in_blocks(lens, dtype, kda):
+    """Sums of tokens and heads at which four tokens are taken at a time: ends at every place of a block and of a
+    phase of blocks, unlike lengths, states wanted in the middle of a block, in a row, and nowhere."""
+    T = sum(lens)
+    x = make(lens, 16, 48, 14, dtype, kda, seed=T + len(lens))
+    slot_in = [2, -1, 0, 7, 9][:len(lens)]
+    slot_out = np.full(T, -1)
+    ends = np.cumsum(lens)
+    slot_out[ends[0] - 1], slot_out[-1] = 2, 6
+    slot_out[[T // 2, T // 2 + 1, T - 2]] = [3, 4, 5]
+    check(x, run(x, kda, slot_in, slot_out), slot_in, slot_out)
+
+
+def test_blocks_with_steep_gates_in_place():
+    x = make([140, 130], 2, 48, 2, "fp32", True, seed=14, steep=True)
+    x["g"][7] = x["g"][141] = -float("inf")
+    x["g"][20, :, ::2] = 0.0
+    slot_out = np.full(270, -1)
+    slot_out[[139, 269]] = [0, 1]
+    check(x, run(x, True, None, None), [0, 1], slot_out)
+
+
+def test_blocks_report_bad_tables():
+    x = make([150, 150], 1, 48, 3, "bf16", False, seed=15)
+    good = run(x, False, [0, 1], None)
+    slot_out = np.full(300, -1)
+    slot_out[[77, 149, 299]] = [9, 0, 1]
+    o, pool, status = run(x, False, [0, 1], slot_out)
+    # (a state that is wanted ends a block, so the first sequence's sums are taken in another order)
+    assert status == 7 and torch.equal(o[150:], good[0][150:]) and torch.equal(pool[1], good[1][1])
+    slot_out[77] = -1
+    check(x, (o, pool, 0), [0, 1], slot_out)
+    for slot_in, cu in (([3, 1], [0, 150, 300]), ([0, 1], [-1, 150, 300])):
+        o, pool, status = run(dict(x, cu=np.array(cu, np.int32)), False, slot_in, None)
+        assert status == 7 and torch.equal(o[150:], good[0][150:]) and torch.equal(pool[1], good[1][1])
+    _, pool, status = run(dict(x, cu=np.array([0, 150, 301], np.int32)), False, [0, 1], None)
+    assert status == 7 and torch.equal(pool[0], good[1][0]) and torch.equal(pool[1].cpu(), x["states"][1])
+
+
 def test_default_slots_update_in_place():
     """Without tables sequence n lives in slot n, and is written back after its last token."""
     lens = [2, 0, 5, 1]
