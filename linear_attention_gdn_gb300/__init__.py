@@ -402,19 +402,31 @@ def gdn_conv1d_bwd(prob, x, w, b, cu_seqlens_dev, cu_seqlens_host, dy, dx, dw, d
 def _call(where, prob, pointers, stream, *size):
     """One call of an entry point whose arguments are a problem, pointers, at most a size, and the stream.  A single token's
     call is as short as its launch, so tensors' addresses go to ctypes as plain integers (None is NULL)."""
-    st = getattr(lib, where)(prob, *[x.data_ptr() if hasattr(x, "data_ptr") else _ptr(x) for x in pointers], *size,
-                             _raw_stream() if stream is None else _stream(stream))
+    try:
+        addresses = [None if x is None else x.data_ptr() for x in pointers]
+    except AttributeError:   # an array or an address among them
+        addresses = [_ptr(x) for x in pointers]
+    st = getattr(_Lazy._h or _loaded(), where)(prob, *addresses, *size,
+                                               _raw_stream() if stream is None else _stream(stream))
     if st != 0:
         raise GDNError(st, where)
 
 
+def _loaded():
+    _Lazy._h = _load()
+    return _Lazy._h
+
+
 def _raw_stream():
     """Address of torch's current stream on the current device."""
+    global _raw_stream
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without the Stream object, where torch has it
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    else:   # without making the Stream object, where torch has it
+        _raw_stream = lambda: raw(device())  # noqa: E731
+    return torch.cuda.current_stream().cuda_stream   # (the first call: this also initialises CUDA)
 
 
 def gdn_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None,

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -44,11 +45,15 @@ namespace gdn {
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int sm_count() {
-  int dev = 0, n = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) n = 152;
-  }
-  return n > 0 ? n : 152;
+  constexpr int MOST = 128;
+  static std::atomic<int> known[MOST];   // of each device, once asked
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  const bool kept = dev >= 0 && dev < MOST;
+  if (kept && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+  if (kept) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 static gdn_status validate_problem(const gdn_problem* p, const int32_t* cu) {

@@ -160,20 +160,23 @@ __global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_fwd_row_kernel(const QkA
   }
 }
 
-template <typename E, int L>
-static void launch_fwd_rows(const QkArgs& a, int ctas, cudaStream_t s) {
-  const bool plain = plain_rows(a, L);
-  if (a.half_layout && plain) qk_fwd_kernel<E, L, true, true><<<ctas, QK_THREADS, 0, s>>>(a);
-  else if (a.half_layout) qk_fwd_kernel<E, L, true, false><<<ctas, QK_THREADS, 0, s>>>(a);
-  else if (plain) qk_fwd_kernel<E, L, false, true><<<ctas, QK_THREADS, 0, s>>>(a);
-  else qk_fwd_kernel<E, L, false, false><<<ctas, QK_THREADS, 0, s>>>(a);
+template <typename E, int L, bool HALF, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_fwd_kernel<E, L, HALF, PLAIN>);
+  const int ctas = divide_work(a, L, resident);
+  qk_fwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
 }
-template <typename E>
-static void launch_fwd(const QkArgs& a, bool fast, int ctas, cudaStream_t s) {
-  if (!fast) qk_fwd_row_kernel<E><<<ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
-  else if (a.D <= 64) launch_fwd_rows<E, 8>(a, ctas, s);
-  else if (a.D <= 128) launch_fwd_rows<E, 16>(a, ctas, s);
-  else launch_fwd_rows<E, 32>(a, ctas, s);
+template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
+  const bool plain = plain_rows(a, L);
+  if (a.half_layout && plain) launch_fwd_kernel<E, L, true, true>(a, s);
+  else if (a.half_layout) launch_fwd_kernel<E, L, true, false>(a, s);
+  else if (plain) launch_fwd_kernel<E, L, false, true>(a, s);
+  else launch_fwd_kernel<E, L, false, false>(a, s);
+}
+template <typename E> static void launch_fwd(QkArgs& a, bool fast, int row_ctas, cudaStream_t s) {
+  if (!fast) qk_fwd_row_kernel<E><<<row_ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
+  else if (a.D <= 64) launch_fwd_rows<E, 8>(a, s);
+  else if (a.D <= 128) launch_fwd_rows<E, 16>(a, s);
+  else launch_fwd_rows<E, 32>(a, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -197,8 +200,7 @@ static bool vectors(const void* p, int64_t token, int64_t head, int es) {
 // the kernels' arguments, and whether the fast ones take the rows
 static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k, const float* wq, const float* wk,
                           const double* freq, const int32_t* pos, const int32_t* cu, const void* inq, const void* ink,
-                          void* outq, void* outk, bool back, QkArgs* a, bool* fast,
-                          int* fast_ctas) {
+                          void* outq, void* outk, bool back, QkArgs* a, bool* fast) {
   memset(a, 0, sizeof(*a));
   const int es = elem_bytes(p->dtype);
   const void* x[2] = {q, k};
@@ -244,28 +246,13 @@ static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k,
   a->share = p->norm == GDN_NORM_RMS ? 1.f / (float)p->D : p->norm == GDN_NORM_L2 ? 1.f : 0.f;
   a->eps = p->eps;
   a->mscale = p->mscale;
-  // A group of lanes for all heads of a token, or, where that leaves an SM fewer than 16 warps, the
-  // heads in shorter runs.  q's and k's shares of the CTAs go by their heads.
-  const int total = p->HQ + p->HK, rows = 32 / (p->D <= 64 ? 8 : p->D <= 128 ? 16 : 32);
-  const int64_t token_groups = (p->T + rows - 1) / rows, want = (int64_t)sm_count() * 16;
-  a->run = (int)std::max<int64_t>(1, std::min<int64_t>(std::max(p->HQ, p->HK), token_groups * total / want));
-  int64_t all = 0;
-  for (int i = 0; i < 2; ++i) {
-    a->splits[i] = (heads[i] + a->run - 1) / a->run;
-    a->units[i] = (int)(token_groups * a->splits[i]);   // (splits are 1 unless tokens are few)
-    all += (a->units[i] + QK_WARPS - 1) / QK_WARPS;
-  }
-  const int ctas = (int)std::min<int64_t>(all, (int64_t)sm_count() * QK_CTAS);
-  a->ctas_q = total > 0 ? (int)((int64_t)ctas * p->HQ / total) : 0;
-  if (p->HQ > 0 && p->HK > 0) a->ctas_q = std::max(1, std::min(ctas - 1, a->ctas_q));
-  *fast_ctas = std::max(ctas, p->HQ > 0 && p->HK > 0 ? 2 : 1);
   return GDN_OK;
 }
 
 static int row_ctas(const QkArgs& a) {
   const int64_t rows = a.T * (a.heads[0] + a.heads[1]);
   return (int)std::max<int64_t>(1, std::min<int64_t>((rows + QK_ROW_WARPS - 1) / QK_ROW_WARPS,
-                                                     (int64_t)sm_count() * QK_CTAS));
+                                                     (int64_t)sm_count() * 16));
 }
 
 }  // namespace gdn
@@ -290,15 +277,13 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_problem* p, const void* q, const vo
   if (p->T == 0 || p->HQ + p->HK == 0) return GDN_OK;
   QkArgs a;
   bool fast;
-  int fast_ctas;
-  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, nullptr, nullptr, qo, ko, false, &a, &fast, &fast_ctas);
+  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, nullptr, nullptr, qo, ko, false, &a, &fast);
   if (st != GDN_OK) return st;
-  const int ctas = fast ? fast_ctas : row_ctas(a);
   prof_begin(K_QK_FWD, stream);
   switch (p->dtype) {
-    case GDN_BF16: launch_fwd<__nv_bfloat16>(a, fast, ctas, stream); break;
-    case GDN_FP16: launch_fwd<__half>(a, fast, ctas, stream); break;
-    default: launch_fwd<float>(a, fast, ctas, stream); break;
+    case GDN_BF16: launch_fwd<__nv_bfloat16>(a, fast, row_ctas(a), stream); break;
+    case GDN_FP16: launch_fwd<__half>(a, fast, row_ctas(a), stream); break;
+    default: launch_fwd<float>(a, fast, row_ctas(a), stream); break;
   }
   prof_end(K_QK_FWD, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -323,13 +308,11 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_problem* p, const void* q, const vo
   }
   QkArgs a;
   bool fast;
-  int fast_ctas;
-  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, dqo, dko, dq, dk, true, &a, &fast, &fast_ctas);
+  st = qk_args(p, q, k, wq, wk, freq, positions, cu_dev, dqo, dko, dq, dk, true, &a, &fast);
   if (st != GDN_OK) return st;
   a.part = dwq || dwk ? static_cast<float*>(workspace) : nullptr;
-  const int ctas = fast ? fast_ctas : row_ctas(a);
   prof_begin(K_QK_BWD, stream);
-  launch_qk_bwd(a, p->dtype, fast, ctas, dwq, dwk, stream);
+  launch_qk_bwd(a, p->dtype, fast, row_ctas(a), dwq, dwk, stream);
   prof_end(K_QK_BWD, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

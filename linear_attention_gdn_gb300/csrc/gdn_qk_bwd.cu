@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int end_
   float s = 0.f;
   if (col < 2 * D) {
     const int end = col < D ? end_q : ctas;
+#pragma unroll 8
     for (int b = (col < D ? 0 : begin_k) + threadIdx.y; b < end; b += 32) s += part[(int64_t)b * 2 * D + col];
   }
   sums[threadIdx.y][threadIdx.x] = s;
@@ -242,30 +243,35 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int end_
   }
 }
 
-template <typename E, int L>
-static void launch_bwd_rows(const QkArgs& a, int ctas, cudaStream_t s) {
-  const bool plain = plain_rows(a, L);
-  if (a.half_layout && plain) qk_bwd_kernel<E, L, true, true><<<ctas, QK_THREADS, 0, s>>>(a);
-  else if (a.half_layout) qk_bwd_kernel<E, L, true, false><<<ctas, QK_THREADS, 0, s>>>(a);
-  else if (plain) qk_bwd_kernel<E, L, false, true><<<ctas, QK_THREADS, 0, s>>>(a);
-  else qk_bwd_kernel<E, L, false, false><<<ctas, QK_THREADS, 0, s>>>(a);
+template <typename E, int L, bool HALF, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_bwd_kernel<E, L, HALF, PLAIN>);
+  const int ctas = divide_work(a, L, resident);
+  qk_bwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
+  return ctas;
 }
-template <typename E>
-static void launch_bwd(const QkArgs& a, bool fast, int ctas, cudaStream_t s) {
-  if (!fast) qk_bwd_row_kernel<E><<<ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
-  else if (a.D <= 64) launch_bwd_rows<E, 8>(a, ctas, s);
-  else if (a.D <= 128) launch_bwd_rows<E, 16>(a, ctas, s);
-  else launch_bwd_rows<E, 32>(a, ctas, s);
+template <typename E, int L> static int launch_bwd_rows(QkArgs& a, cudaStream_t s) {
+  const bool plain = plain_rows(a, L);
+  if (a.half_layout && plain) return launch_bwd_kernel<E, L, true, true>(a, s);
+  if (a.half_layout) return launch_bwd_kernel<E, L, true, false>(a, s);
+  if (plain) return launch_bwd_kernel<E, L, false, true>(a, s);
+  return launch_bwd_kernel<E, L, false, false>(a, s);
+}
+// returns the CTAs, each of which has left partial sums
+template <typename E> static int launch_bwd(QkArgs& a, bool fast, int row_ctas, cudaStream_t s) {
+  if (fast && a.D <= 64) return launch_bwd_rows<E, 8>(a, s);
+  if (fast && a.D <= 128) return launch_bwd_rows<E, 16>(a, s);
+  if (fast) return launch_bwd_rows<E, 32>(a, s);
+  qk_bwd_row_kernel<E><<<row_ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
+  return row_ctas;
 }
 
-void launch_qk_bwd(const QkArgs& a, int dtype, bool fast, int ctas, float* dwq, float* dwk, cudaStream_t s) {
-  switch (dtype) {
-    case GDN_BF16: launch_bwd<__nv_bfloat16>(a, fast, ctas, s); break;
-    case GDN_FP16: launch_bwd<__half>(a, fast, ctas, s); break;
-    default: launch_bwd<float>(a, fast, ctas, s); break;
-  }
-  if (a.part) qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, fast ? a.ctas_q : ctas, fast ? a.ctas_q : 0,
-                                                                        ctas, a.D, dwq, dwk);
+void launch_qk_bwd(QkArgs& a, int dtype, bool fast, int row_ctas, float* dwq, float* dwk, cudaStream_t s) {
+  const int ctas = dtype == GDN_BF16 ? launch_bwd<__nv_bfloat16>(a, fast, row_ctas, s)
+                   : dtype == GDN_FP16 ? launch_bwd<__half>(a, fast, row_ctas, s)
+                                       : launch_bwd<float>(a, fast, row_ctas, s);
+  if (a.part)
+    qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, fast ? a.ctas_q : ctas, fast ? a.ctas_q : 0,
+                                                              ctas, a.D, dwq, dwk);
 }
 
 }  // namespace gdn
