@@ -356,7 +356,7 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.N = p->N;
   a.C = p->C;
   a.slots = p->slots;
-  // single tokens: as many sequences side by side as give an SM 16 CTAs; else ranges that give it four rounds
+  // single tokens: as many sequences side by side as give an SM 32 CTAs; else ranges that give it four rounds
   // of the 8 CTAs it holds
   const int per_cta = CS_THREADS * (cu_dev ? CS_VEC : CS_VEC1);
   const int cols = (p->C + per_cta - 1) / per_cta;
@@ -367,7 +367,7 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
     rows = (p->T + a.R - 1) / a.R;
   } else {
     a.R = 1;
-    rows = std::min<int64_t>(p->N, std::max<int64_t>(1, (int64_t)sm_count() * 16 / cols));
+    rows = std::min<int64_t>(p->N, std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols));
   }
   if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 16 M tokens, or fewer in very many columns
   const dim3 grid(cols, (unsigned)rows);

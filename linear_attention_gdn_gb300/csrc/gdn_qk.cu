@@ -9,10 +9,10 @@
 // Fast kernel: bandwidth-bound, every value read and written once.  A row lies in L lanes of 8 values; a group of
 // L lanes takes a token and walks its heads with the token's coefficients in registers, while the next rows
 // are on their way into the warp's ring in shared memory.  A warp stays with q or with k, and waits for no
-// other. Few tokens: their heads are split over warps.  PLAIN: a norm, the whole row rotated and no lane without
-// values, which needs no masks.
-// The kernel for other rows (any alignment, odd D, rot not a multiple of 8 in the half layout) gives a
-// warp to each row and stages it in shared memory.
+// other. Few tokens: their heads are split over warps.  PLAIN: a norm and the whole row rotated, which
+// needs no masks.
+// The kernel for other rows (any alignment, odd D, rot not a multiple of 8 in the half layout) spreads a row over a
+// warp, value by value, and takes partners from shared memory.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   int off0, off1;
   block_offsets<HALF>(a, l, &off0, &off1);
   const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
-  const bool has = PLAIN || l < a.D / 8;
+  const bool has = l < a.D / 8;
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
   const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
   const int units = which ? a.units[1] : a.units[0];
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
     if (more) {
 #pragma unroll
       for (int i = 0; i < R::CHUNKS; ++i)
-        if (PLAIN || (l + i * L) * VEC < a.D) {   // lanes past the row's end have none of its chunks
+        if ((l + i * L) * VEC < a.D) {   // lanes past the row's end have none of its chunks
           copy16(landing + fill + i * L * 16, px + i * L * VEC);
         }
       px += xh;
@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
     copies_commit();
     fill = R::next(fill);
   };
+  clear_ring<E, L, 1>(slots, a.D);
 #pragma unroll
   for (int i = 0; i < R::STAGES - 1; ++i) request();
 
@@ -98,7 +99,6 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
       float2 v[4], p[4];
       read_row<E, HALF>(read + use, away, v);
       use = R::next(use);
-      if (!PLAIN && !has) only_rotated(v, 0);
       float r = 1.f;
       if (PLAIN || a.normed) {
         float2 s = __fmul2_rn(v[0], v[0]);
@@ -119,44 +119,47 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   } while (at.unit < units);
 }
 
-// rows of any kind: a warp per row
-template <typename E>
-__global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_fwd_row_kernel(const QkArgs a) {
-  __shared__ float rows[QK_ROW_WARPS][QK_MAXD];
-  const int lane = threadIdx.x & 31;
+// rows of any kind: lane i has the values i, i + 32, ... (PER of them) of each row of its warp's token
+template <typename E, int PER>
+__global__ void __launch_bounds__(QK_THREADS) qk_fwd_row_kernel(const QkArgs a) {
+  __shared__ float rows[QK_WARPS][PER * 32];
   float* z = rows[threadIdx.x >> 5];
-  const int total = a.heads[0] + a.heads[1], half = a.rot / 2;
-  __shared__ uint64_t step[QK_MAXD / 2];
-  for (int i = threadIdx.x; i < half; i += QK_ROW_WARPS * 32) step[i] = turn_step(a.freq[i]);
-  __syncthreads();
-  int doc = 0;
-  const int64_t warps = (int64_t)gridDim.x * QK_ROW_WARPS;
-  for (int64_t row = (int64_t)blockIdx.x * QK_ROW_WARPS + (threadIdx.x >> 5); row < a.T * total; row += warps) {
-    const int64_t t = row / total;
-    const int e = (int)(row - t * total), which = e >= a.heads[0], h = e - (which ? a.heads[0] : 0);
-    const E* x = static_cast<const E*>(a.x[which]) + t * a.xt[which] + h * a.xh[which];
-    E* y = static_cast<E*>(a.out[which]) + t * a.yt[which] + h * a.yh[which];
-    float ss = 0.f;
-    for (int d = lane; d < a.D; d += 32) {
-      const float v = to_f32(x[d]);
-      ss = fmaf(v, v, ss);
-      z[d] = v * (a.w[which] ? a.w[which][d] : 1.f);
-    }
-    const float r = a.normed ? rsqrtf(fmaf(row_sum<32>(ss), a.share, a.eps)) : 1.f;
-    const int p = position_of(a, t, &doc);
-    __syncwarp();
-    for (int d = lane; d < a.D; d += 32) {
-      float v = z[d];
-      if (d < a.rot) {
-        const int f = a.half_layout ? (d < half ? d : d - half) : d >> 1;
-        const int other = a.half_layout ? (d < half ? d + half : d - half) : d ^ 1;
-        float c, s;
-        angle_cos_sin<false>(step[f], p, a.mscale, &c, &s);
-        v = v * c + (d < other ? -z[other] : z[other]) * s;
+  const int lane = threadIdx.x & 31;
+  const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
+  const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
+  const int units = which ? a.units[1] : a.units[0];
+  const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
+  const int64_t xh = which ? a.xh[1] : a.xh[0], yh = which ? a.yh[1] : a.yh[0];
+  Place<32> at;
+  at.unit = cta * QK_WARPS + (threadIdx.x >> 5);
+  RowAngles<PER> ang;
+  ang.setup(a);
+  float w[PER];
+  row_weights<PER>(which ? a.w[1] : a.w[0], a.D, w);
+  for (; at.unit < units; at.unit += warps) {
+    at.enter(a, splits, heads);
+    ang.at(a, at.t);
+    const E* x = static_cast<const E*>(which ? a.x[1] : a.x[0]) + at.t * (which ? a.xt[1] : a.xt[0]) + at.h * xh;
+    E* y = static_cast<E*>(which ? a.out[1] : a.out[0]) + at.t * (which ? a.yt[1] : a.yt[0]) + at.h * yh;
+    for (int n = at.left; n > 0; --n, x += xh, y += yh) {
+      float v[PER], ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        v[i] = lane + 32 * i < a.D ? to_f32(x[lane + 32 * i]) : 0.f;
+        ss = fmaf(v[i], v[i], ss);
       }
-      y[d] = from_f32<E>(r * v);
+      __syncwarp();   // the last row has been read
+#pragma unroll
+      for (int i = 0; i < PER; ++i) z[lane + 32 * i] = v[i] *= w[i];
+      const float r = a.normed ? rsqrtf(fmaf(row_sum<32>(ss), a.share, a.eps)) : 1.f;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (lane + 32 * i >= a.D) break;
+        if (lane + 32 * i < a.rot) v[i] = fmaf(z[ang.partner[i]], ang.s[i], v[i] * ang.c[i]);
+        y[lane + 32 * i] = from_f32<E>(r * v[i]);
+      }
     }
-    __syncwarp();
   }
 }
 
@@ -166,14 +169,20 @@ template <typename E, int L, bool HALF, bool PLAIN> static void launch_fwd_kerne
   qk_fwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
 }
 template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
-  const bool plain = plain_rows(a, L);
+  const bool plain = plain_rows(a);
   if (a.half_layout && plain) launch_fwd_kernel<E, L, true, true>(a, s);
   else if (a.half_layout) launch_fwd_kernel<E, L, true, false>(a, s);
   else if (plain) launch_fwd_kernel<E, L, false, true>(a, s);
   else launch_fwd_kernel<E, L, false, false>(a, s);
 }
-template <typename E> static void launch_fwd(QkArgs& a, bool fast, int row_ctas, cudaStream_t s) {
-  if (!fast) qk_fwd_row_kernel<E><<<row_ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
+template <typename E, int PER> static void launch_fwd_any(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_fwd_row_kernel<E, PER>);
+  const int ctas = divide_work(a, 32, resident);
+  qk_fwd_row_kernel<E, PER><<<ctas, QK_THREADS, 0, s>>>(a);
+}
+template <typename E> static void launch_fwd(QkArgs& a, bool fast, cudaStream_t s) {
+  if (!fast && a.D <= 128) launch_fwd_any<E, 4>(a, s);
+  else if (!fast) launch_fwd_any<E, QK_MAXD / 32>(a, s);
   else if (a.D <= 64) launch_fwd_rows<E, 8>(a, s);
   else if (a.D <= 128) launch_fwd_rows<E, 16>(a, s);
   else launch_fwd_rows<E, 32>(a, s);
@@ -249,12 +258,6 @@ static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k,
   return GDN_OK;
 }
 
-static int row_ctas(const QkArgs& a) {
-  const int64_t rows = a.T * (a.heads[0] + a.heads[1]);
-  return (int)std::max<int64_t>(1, std::min<int64_t>((rows + QK_ROW_WARPS - 1) / QK_ROW_WARPS,
-                                                     (int64_t)sm_count() * 16));
-}
-
 }  // namespace gdn
 
 using namespace gdn;
@@ -281,9 +284,9 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_problem* p, const void* q, const vo
   if (st != GDN_OK) return st;
   prof_begin(K_QK_FWD, stream);
   switch (p->dtype) {
-    case GDN_BF16: launch_fwd<__nv_bfloat16>(a, fast, row_ctas(a), stream); break;
-    case GDN_FP16: launch_fwd<__half>(a, fast, row_ctas(a), stream); break;
-    default: launch_fwd<float>(a, fast, row_ctas(a), stream); break;
+    case GDN_BF16: launch_fwd<__nv_bfloat16>(a, fast, stream); break;
+    case GDN_FP16: launch_fwd<__half>(a, fast, stream); break;
+    default: launch_fwd<float>(a, fast, stream); break;
   }
   prof_end(K_QK_FWD, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
@@ -312,7 +315,7 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_problem* p, const void* q, const vo
   if (st != GDN_OK) return st;
   a.part = dwq || dwk ? static_cast<float*>(workspace) : nullptr;
   prof_begin(K_QK_BWD, stream);
-  launch_qk_bwd(a, p->dtype, fast, row_ctas(a), dwq, dwk, stream);
+  launch_qk_bwd(a, p->dtype, fast, dwq, dwk, stream);
   prof_end(K_QK_BWD, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

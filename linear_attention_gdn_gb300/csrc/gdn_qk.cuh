@@ -13,13 +13,12 @@
 
 namespace gdn {
 
-constexpr int QK_THREADS = 128;     // of the fast kernels' CTAs
+constexpr int QK_THREADS = 128;
 constexpr int QK_WARPS = QK_THREADS / 32;
 constexpr int QK_MAXD = 512;        // any layout
 constexpr int QK_FAST_MAXD = 256;   // rows of 8 values a lane
 constexpr int QK_CTAS = 64;         // CTAs per SM of a grid that walks its work, at most
 constexpr int QK_UNITS = 4;         // units a warp has, if there are enough
-constexpr int QK_ROW_WARPS = 4;     // rows a CTA of the other kernels has at a time
 
 struct QkArgs {
   const void* x[2];      // q, k
@@ -37,7 +36,7 @@ struct QkArgs {
   int normed;            // 0: r = 1
   float share, eps;      // r = 1 / sqrt(share x.x + eps)
   float mscale;
-  // the fast kernels' work (divide_work): CTAs 0 .. ctas_q-1 take q, the others k; a unit is `run` heads of as many
+  // the work (divide_work): CTAs 0 .. ctas_q-1 take q, the others k; a unit is `run` heads of as many
   // neighbouring tokens as a warp has rows
   int run, splits[2], units[2], ctas_q;
 };
@@ -160,6 +159,16 @@ template <typename E, int L, int N> struct Ring {
   static __device__ __forceinline__ int next(int at) { return at + BYTES == STAGES * BYTES ? 0 : at + BYTES; }
   static constexpr int STAGES = N * CHUNKS == 1 ? 8 : N * CHUNKS == 2 ? 6 : 4;
 };
+// Values of a row past D are never copied, and are zero from the start.
+template <typename E, int L, int N> __device__ __forceinline__ void clear_ring(E* slots, int D) {
+  using R = Ring<E, L, N>;
+  if (D == R::ROW) return;
+  for (int i = threadIdx.x & 31; i < R::STAGES * R::SLOT / R::ROW * (R::ROW - D); i += 32) {
+    const int row = i / (R::ROW - D);
+    slots[row * R::ROW + D + i - row * (R::ROW - D)] = from_f32<E>(0.f);
+  }
+  __syncwarp();
+}
 __device__ __forceinline__ void copy16(uint32_t smem, const void* global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
 }
@@ -251,10 +260,44 @@ template <int L> __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// rows without masks: normed, rotated whole, in L lanes that all have values
-inline bool plain_rows(const QkArgs& a, int L) { return a.normed && a.rot == a.D && a.D == 8 * L; }
+// ---- rows of any kind, value by value: lane i has the values i, i + 32, ... ----
+template <int PER> struct RowAngles {
+  float c[PER], s[PER];   // value = value c + partner s
+  int partner[PER];
+  int doc = 0;
+  uint64_t step[PER];
+  __device__ __forceinline__ void setup(const QkArgs& a) {
+    const int half = a.rot / 2;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int d = (threadIdx.x & 31) + 32 * i;
+      partner[i] = a.half_layout ? (d < half ? d + half : d - half) : d ^ 1;
+      step[i] = d < a.rot ? turn_step(a.freq[a.half_layout ? (d < half ? d : d - half) : d >> 1]) : 0;
+    }
+  }
+  __device__ __forceinline__ void at(const QkArgs& a, int64_t t) {
+    const int pos = position_of(a, t, &doc);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int d = (threadIdx.x & 31) + 32 * i;
+      if (d >= a.rot) break;
+      angle_cos_sin<false>(step[i], pos, a.mscale, &c[i], &s[i]);
+      if (d < partner[i]) s[i] = -s[i];
+    }
+  }
+};
+template <int PER> __device__ __forceinline__ void row_weights(const float* w, int D, float (&v)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int d = (threadIdx.x & 31) + 32 * i;
+    v[i] = d >= D ? 0.f : w ? w[d] : 1.f;
+  }
+}
 
-// Divides the fast kernels' work: runs of heads as long as the warps that the GPU holds at once (`resident` CTAs an SM)
+// rows without masks: normed and rotated whole
+inline bool plain_rows(const QkArgs& a) { return a.normed && a.rot == a.D; }
+
+// Divides the work: runs of heads as long as the warps that the GPU holds at once (`resident` CTAs an SM)
 // get QK_UNITS units each; then a whole number of such rounds of CTAs, so that SMs that are ahead take more of
 // them (262,144 tokens of 16 + 16 heads, forward: one round 741 us, three 662, ten 633; but one where a round is all
 // there is work for: 5,001 tokens backward, one round 33 us, three 39); and q's and k's shares by their heads. Returns the
@@ -292,6 +335,6 @@ template <typename K> inline int resident_ctas(K kernel) {
 }
 
 // --- gdn_qk_bwd.cu ---
-void launch_qk_bwd(QkArgs& a, int dtype, bool fast, int row_ctas, float* dwq, float* dwk, cudaStream_t s);
+void launch_qk_bwd(QkArgs& a, int dtype, bool fast, float* dwq, float* dwk, cudaStream_t s);
 
 }  // namespace gdn

@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   int off0, off1;
   block_offsets<HALF>(a, l, &off0, &off1);
   const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
-  const bool has = PLAIN || l < a.D / 8;
+  const bool has = l < a.D / 8;
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
   const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
   const int units = which ? a.units[1] : a.units[0];
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
       if (more) {
 #pragma unroll
         for (int i = 0; i < R::CHUNKS; ++i)
-          if (PLAIN || (l + i * L) * VEC < a.D) {   // lanes past the row's end have none of its chunks
+          if ((l + i * L) * VEC < a.D) {   // lanes past the row's end have none of its chunks
             copy16(landing + fill + i * L * 16, px + i * L * VEC);
             copy16(landing + R::BYTES / 2 + fill + i * L * 16, pg + i * L * VEC);
           }
@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
       copies_commit();
       fill = R::next(fill);
     };
+    clear_ring<E, L, 2>(slots, a.D);
 #pragma unroll
     for (int i = 0; i < R::STAGES - 1; ++i) request();
 
@@ -89,10 +90,6 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
         read_row<E, HALF>(s0, away, v);
         read_row<E, HALF>(s0 + R::BYTES / 2, away, g);
         use = R::next(use);
-        if (!PLAIN && !has) {
-          only_rotated(v, 0);
-          only_rotated(g, 0);
-        }
         // turned back: by the opposite sine
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -147,90 +144,84 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(QK_ROW_WARPS * 32) qk_bwd_row_kernel(const QkArgs a) {
-  __shared__ float rows[QK_ROW_WARPS][QK_MAXD];
-  __shared__ float sums[QK_ROW_WARPS][QK_MAXD];
-  constexpr int PER = QK_MAXD / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* gin = rows[warp];
-  const int total = a.heads[0] + a.heads[1], half = a.rot / 2;
-  __shared__ uint64_t step[QK_MAXD / 2];
-  for (int i = threadIdx.x; i < half; i += QK_ROW_WARPS * 32) step[i] = turn_step(a.freq[i]);
-  __syncthreads();
-  float acc[2][PER];
+// rows of any kind, as in the forward
+template <typename E, int PER>
+__global__ void __launch_bounds__(QK_THREADS) qk_bwd_row_kernel(const QkArgs a) {
+  __shared__ float rows[QK_WARPS][PER * 32];
+  const int lane = threadIdx.x & 31;
+  float* z = rows[threadIdx.x >> 5];
+  const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
+  const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
+  const int units = which ? a.units[1] : a.units[0];
+  const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
+  const int64_t xh = which ? a.xh[1] : a.xh[0], yh = which ? a.yh[1] : a.yh[0];
+  Place<32> at;
+  at.unit = cta * QK_WARPS + (threadIdx.x >> 5);
+  RowAngles<PER> ang;
+  ang.setup(a);
+  float w[PER], acc[PER];
+  row_weights<PER>(which ? a.w[1] : a.w[0], a.D, w);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) acc[0][i] = acc[1][i] = 0.f;
-  int doc = 0;
-  const int64_t warps = (int64_t)gridDim.x * QK_ROW_WARPS;
-  for (int64_t row = (int64_t)blockIdx.x * QK_ROW_WARPS + warp; row < a.T * total; row += warps) {
-    const int64_t t = row / total;
-    const int e = (int)(row - t * total), which = e >= a.heads[0], h = e - (which ? a.heads[0] : 0);
-    const E* x = static_cast<const E*>(a.x[which]) + t * a.xt[which] + h * a.xh[which];
-    E* dx = static_cast<E*>(a.out[which]) + t * a.xt[which] + h * a.xh[which];
-    const E* gy = static_cast<const E*>(a.in[which]) + t * a.yt[which] + h * a.yh[which];
-    for (int d = lane; d < a.D; d += 32) gin[d] = to_f32(gy[d]);
-    const int p = position_of(a, t, &doc);
-    __syncwarp();
-    float v[PER], g[PER], ss = 0.f, dot = 0.f;
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  for (; at.unit < units; at.unit += warps) {
+    at.enter(a, splits, heads);
+    ang.at(a, at.t);
+    const int64_t first = at.t * (which ? a.xt[1] : a.xt[0]) + at.h * xh;
+    const E* x = static_cast<const E*>(which ? a.x[1] : a.x[0]) + first;
+    E* dx = static_cast<E*>(which ? a.out[1] : a.out[0]) + first;
+    const E* gy = static_cast<const E*>(which ? a.in[1] : a.in[0]) + at.t * (which ? a.yt[1] : a.yt[0]) + at.h * yh;
+    for (int n = at.left; n > 0; --n, x += xh, dx += xh, gy += yh) {
+      float v[PER], g[PER], ss = 0.f, dot = 0.f;
+      __syncwarp();   // the last row has been read
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int d = lane + 32 * i;
-      v[i] = g[i] = 0.f;
-      if (d >= a.D) continue;
-      v[i] = to_f32(x[d]);
-      g[i] = gin[d];
-      if (d < a.rot) {
-        const int f = a.half_layout ? (d < half ? d : d - half) : d >> 1;
-        const int other = a.half_layout ? (d < half ? d + half : d - half) : d ^ 1;
-        float c, s;
-        angle_cos_sin<false>(step[f], p, a.mscale, &c, &s);
-        g[i] = g[i] * c + (d < other ? gin[other] : -gin[other]) * s;
+      for (int i = 0; i < PER; ++i) {
+        v[i] = lane + 32 * i < a.D ? to_f32(x[lane + 32 * i]) : 0.f;
+        z[lane + 32 * i] = g[i] = lane + 32 * i < a.D ? to_f32(gy[lane + 32 * i]) : 0.f;
       }
-      ss = fmaf(v[i], v[i], ss);
-      dot = fmaf(g[i] * (a.w[which] ? a.w[which][d] : 1.f), v[i], dot);
-    }
-    float r = 1.f, f = 0.f;
-    if (a.normed) {
-      r = rsqrtf(fmaf(row_sum<32>(ss), a.share, a.eps));
-      f = row_sum<32>(dot) * a.share * r * r;
-    }
+      __syncwarp();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int d = lane + 32 * i;
-      if (d >= a.D) continue;
-      if (which) acc[1][i] = fmaf(g[i], v[i] * r, acc[1][i]);
-      else acc[0][i] = fmaf(g[i], v[i] * r, acc[0][i]);
-      const float wg = g[i] * (a.w[which] ? a.w[which][d] : 1.f);
-      dx[d] = from_f32<E>(r * (wg - (a.normed ? v[i] * f : 0.f)));
+      for (int i = 0; i < PER; ++i) {
+        // turned back: by the opposite sine
+        if (lane + 32 * i < a.rot) g[i] = fmaf(-z[ang.partner[i]], ang.s[i], g[i] * ang.c[i]);
+        ss = fmaf(v[i], v[i], ss);
+        dot = fmaf(g[i] * w[i], v[i], dot);
+      }
+      float r = 1.f, f = 0.f;
+      if (a.normed) {
+        r = rsqrtf(fmaf(row_sum<32>(ss), a.share, a.eps));
+        f = row_sum<32>(dot) * a.share * r * r;
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (lane + 32 * i >= a.D) break;
+        acc[i] = fmaf(g[i], v[i] * r, acc[i]);
+        dx[lane + 32 * i] = from_f32<E>(r * (g[i] * w[i] - (a.normed ? v[i] * f : 0.f)));
+      }
     }
-    __syncwarp();
   }
   if (!a.part) return;
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sums[warp][lane + 32 * i] = which ? acc[1][i] : acc[0][i];
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += QK_ROW_WARPS * 32) {
-      float s = 0.f;
-      for (int g = 0; g < QK_ROW_WARPS; ++g) s += sums[g][d];
-      a.part[((int64_t)blockIdx.x * 2 + which) * a.D + d] = s;
-    }
+  for (int i = 0; i < PER; ++i) z[lane + 32 * i] = acc[i];
+  __syncthreads();
+  for (int d = threadIdx.x; d < a.D; d += QK_THREADS) {
+    float s = 0.f;
+    for (int g = 0; g < QK_WARPS; ++g) s += rows[g][d];
+    a.part[((int64_t)blockIdx.x * 2 + which) * a.D + d] = s;
   }
 }
 
 // dw[d] = sum over the CTAs' partials, 32 columns of dwq | dwk a CTA, 32 threads a column; q's partials are in
-// CTAs 0 .. end_q-1, k's in begin_k .. ctas-1
-__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int end_q, int begin_k, int ctas, int D,
+// CTAs 0 .. ctas_q-1, k's in the others
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas_q, int ctas, int D,
                                                      float* dwq, float* dwk) {
   __shared__ float sums[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (col < 2 * D) {
-    const int end = col < D ? end_q : ctas;
+    const int end = col < D ? ctas_q : ctas;
 #pragma unroll 8
-    for (int b = (col < D ? 0 : begin_k) + threadIdx.y; b < end; b += 32) s += part[(int64_t)b * 2 * D + col];
+    for (int b = (col < D ? 0 : ctas_q) + threadIdx.y; b < end; b += 32) s += part[(int64_t)b * 2 * D + col];
   }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -250,28 +241,32 @@ template <typename E, int L, bool HALF, bool PLAIN> static int launch_bwd_kernel
   return ctas;
 }
 template <typename E, int L> static int launch_bwd_rows(QkArgs& a, cudaStream_t s) {
-  const bool plain = plain_rows(a, L);
+  const bool plain = plain_rows(a);
   if (a.half_layout && plain) return launch_bwd_kernel<E, L, true, true>(a, s);
   if (a.half_layout) return launch_bwd_kernel<E, L, true, false>(a, s);
   if (plain) return launch_bwd_kernel<E, L, false, true>(a, s);
   return launch_bwd_kernel<E, L, false, false>(a, s);
 }
+template <typename E, int PER> static int launch_bwd_any(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_bwd_row_kernel<E, PER>);
+  const int ctas = divide_work(a, 32, resident);
+  qk_bwd_row_kernel<E, PER><<<ctas, QK_THREADS, 0, s>>>(a);
+  return ctas;
+}
 // returns the CTAs, each of which has left partial sums
-template <typename E> static int launch_bwd(QkArgs& a, bool fast, int row_ctas, cudaStream_t s) {
-  if (fast && a.D <= 64) return launch_bwd_rows<E, 8>(a, s);
-  if (fast && a.D <= 128) return launch_bwd_rows<E, 16>(a, s);
-  if (fast) return launch_bwd_rows<E, 32>(a, s);
-  qk_bwd_row_kernel<E><<<row_ctas, QK_ROW_WARPS * 32, 0, s>>>(a);
-  return row_ctas;
+template <typename E> static int launch_bwd(QkArgs& a, bool fast, cudaStream_t s) {
+  if (!fast) return a.D <= 128 ? launch_bwd_any<E, 4>(a, s) : launch_bwd_any<E, QK_MAXD / 32>(a, s);
+  if (a.D <= 64) return launch_bwd_rows<E, 8>(a, s);
+  if (a.D <= 128) return launch_bwd_rows<E, 16>(a, s);
+  return launch_bwd_rows<E, 32>(a, s);
 }
 
-void launch_qk_bwd(QkArgs& a, int dtype, bool fast, int row_ctas, float* dwq, float* dwk, cudaStream_t s) {
-  const int ctas = dtype == GDN_BF16 ? launch_bwd<__nv_bfloat16>(a, fast, row_ctas, s)
-                   : dtype == GDN_FP16 ? launch_bwd<__half>(a, fast, row_ctas, s)
-                                       : launch_bwd<float>(a, fast, row_ctas, s);
+void launch_qk_bwd(QkArgs& a, int dtype, bool fast, float* dwq, float* dwk, cudaStream_t s) {
+  const int ctas = dtype == GDN_BF16 ? launch_bwd<__nv_bfloat16>(a, fast, s)
+                   : dtype == GDN_FP16 ? launch_bwd<__half>(a, fast, s)
+                                       : launch_bwd<float>(a, fast, s);
   if (a.part)
-    qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, fast ? a.ctas_q : ctas, fast ? a.ctas_q : 0,
-                                                              ctas, a.D, dwq, dwk);
+    qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, a.ctas_q, ctas, a.D, dwq, dwk);
 }
 
 }  // namespace gdn
