@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_row_kernel(const QkArgs a) 
 
 template <typename E, int L, bool HALF, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_fwd_kernel<E, L, HALF, PLAIN>);
-  const int ctas = divide_work(a, L, resident);
+  const int ctas = divide_work(a, L, resident, 1);
   qk_fwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
 }
 template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
@@ -177,7 +177,7 @@ template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t
 }
 template <typename E, int PER> static void launch_fwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_fwd_row_kernel<E, PER>);
-  const int ctas = divide_work(a, 32, resident);
+  const int ctas = divide_work(a, 32, resident, 1);
   qk_fwd_row_kernel<E, PER><<<ctas, QK_THREADS, 0, s>>>(a);
 }
 template <typename E> static void launch_fwd(QkArgs& a, bool fast, cudaStream_t s) {

@@ -18,7 +18,6 @@ constexpr int QK_WARPS = QK_THREADS / 32;
 constexpr int QK_MAXD = 512;        // any layout
 constexpr int QK_FAST_MAXD = 256;   // rows of 8 values a lane
 constexpr int QK_CTAS = 64;         // CTAs per SM of a grid that walks its work, at most
-constexpr int QK_UNITS = 4;         // units a warp has, if there are enough
 
 struct QkArgs {
   const void* x[2];      // q, k
@@ -297,16 +296,16 @@ template <int PER> __device__ __forceinline__ void row_weights(const float* w, i
 // rows without masks: normed and rotated whole
 inline bool plain_rows(const QkArgs& a) { return a.normed && a.rot == a.D; }
 
-// Divides the work: runs of heads as long as the warps that the GPU holds at once (`resident` CTAs an SM)
-// get QK_UNITS units each; then a whole number of such rounds of CTAs, so that SMs that are ahead take more of
-// them (262,144 tokens of 16 + 16 heads, forward: one round 741 us, three 662, ten 633; but one where a round is all
-// there is work for: 5,001 tokens backward, one round 33 us, three 39); and q's and k's shares by their heads. Returns the
-// CTAs.
-inline int divide_work(QkArgs& a, int L, int resident) {
+// Divides the work: runs of heads as long as the warps that the GPU holds at once (`resident` CTAs an SM) get `least`
+// units each; then a whole number of such rounds of CTAs, so that SMs that are ahead take more of them (262,144
+// tokens of 16 + 16 heads, forward: one round 741 us, three 662, ten 633); and q's and k's shares by their heads. least
+// is 1 for the forward and, since every CTA leaves partial sums to add, 2 for the backward (32,768 tokens, forward: 82 us
+// with 1, 97 with 4; backward 139 with 1, 130 with 2, 133 with 4).  Returns the CTAs.
+inline int divide_work(QkArgs& a, int L, int resident, int least) {
   const int total = a.heads[0] + a.heads[1], rows = 32 / L;
   const int64_t round = (int64_t)sm_count() * (resident < 1 ? 1 : resident);
   const int64_t groups = (a.T + rows - 1) / rows, most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
-  int64_t run = groups * total / (round * QK_WARPS * QK_UNITS);
+  int64_t run = groups * total / (round * QK_WARPS * least);
   run = run < 1 ? 1 : run > most ? most : run;
   a.run = (int)run;
   int64_t units = 0, ctas = 0;
@@ -316,7 +315,7 @@ inline int divide_work(QkArgs& a, int L, int resident) {
     units += a.units[i];
     ctas += (a.units[i] + QK_WARPS - 1) / QK_WARPS;
   }
-  int64_t rounds = units / (round * QK_WARPS * QK_UNITS);
+  int64_t rounds = units / (round * QK_WARPS * least);
   rounds = rounds < 1 ? 1 : rounds > 10 ? 10 : rounds;
   const int64_t limit = round * rounds < (int64_t)sm_count() * QK_CTAS ? round * rounds : (int64_t)sm_count() * QK_CTAS;
   if (ctas > limit) ctas = limit;

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas
 
 template <typename E, int L, bool HALF, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_bwd_kernel<E, L, HALF, PLAIN>);
-  const int ctas = divide_work(a, L, resident);
+  const int ctas = divide_work(a, L, resident, 2);
   qk_bwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
   return ctas;
 }
@@ -249,7 +249,7 @@ template <typename E, int L> static int launch_bwd_rows(QkArgs& a, cudaStream_t 
 }
 template <typename E, int PER> static int launch_bwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_bwd_row_kernel<E, PER>);
-  const int ctas = divide_work(a, 32, resident);
+  const int ctas = divide_work(a, 32, resident, 2);
   qk_bwd_row_kernel<E, PER><<<ctas, QK_THREADS, 0, s>>>(a);
   return ctas;
 }
