@@ -24,7 +24,7 @@
 
 namespace gdn {
 
-constexpr int ST_WARPS = 2;            // warps per CTA
+constexpr int ST_WARPS = 1;            // warps per CTA
 constexpr int ST_COLS = 16;            // columns of a warp
 constexpr int ST_PARTS = D / ST_COLS;  // warps per (sequence, head)
 constexpr float ST_EPS = 1e-6f;        // under the root of the l2 norm
@@ -218,8 +218,10 @@ template <typename E, bool KDA> struct StepToken {
 };
 
 // a few tokens: the next one's rows are requested a token ahead, and rows lie in pairs for the paired FP32 instructions
+// (registers for 12 and 14 warps an SM: 64 sequences of 8 tokens 137 us with one decay a channel and 115 with one a
+// head; left to the compiler 177 and 125)
 template <typename E, bool KDA>
-__global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(ST_WARPS * 32, KDA ? 12 : 14) step_kernel(const StepArgs a) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
   const int part = (int)(item % ST_PARTS);
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_kernel(const StepArgs a) {
 // eight times and in pairs as it lies.  The vectors that all columns share are worked out once a CTA of STB_WARPS
 // warps: a phase is STB_WARPS blocks, each prepared by one warp into shared memory, then taken by all warps
 // without a wait, while the next phase's rows are copied in. A block ends early where a state has to be written.
-constexpr int STB_MIN_TOKENS = 10;      // a sequence, on average
+constexpr int STB_MIN_TOKENS = 12;      // a sequence, on average
 constexpr int64_t STB_MIN_WORK = 12288; // tokens times heads
 constexpr int STB_WARPS = 4;
 constexpr int STB_TOKENS = 4;   // tokens of a block
@@ -722,7 +724,7 @@ template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool 
         cudaSuccess)
       return false;
     step_block_kernel<E, KDA><<<ctas, STB_WARPS * 32, bytes, s>>>(a);
-  } else if (a.T > 2 * (int64_t)a.N) {
+  } else if (a.T > a.N) {
     step_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
   } else {
     step_token_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
@@ -756,11 +758,10 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(o) ||
       (p->slots > 0 && !aligned16(states)))
     return GDN_ERR_INVALID_ARG;
-  // By the mean length, which is all that the host knows of the lengths: up to two tokens the kernel of the fewest
-  // registers (64 sequences of 48 heads with one token 61 us against 70, with two 73 against 81), then the one with the next
-  // token's rows on their way; and, for ten tokens and more and enough of them in all to fill the SMs, four tokens at a
-  // time (64 sequences of 16 tokens: 179 us against 222, 32 of 128: 533 against 796; but 16 of 12: 50 against 44, one of
-  // 64: 35 against 30).
+  // By the mean length, which is all that the host knows of the lengths: one token, step_token_kernel (64 sequences of
+  // 48 heads 60 us; step_kernel, with more registers, 70); a few, step_kernel (64 of 8: 115 us; step_block_kernel 157);
+  // from 12 on, if tokens times heads fill the SMs, step_block_kernel (64 of 16: 182 us against 204, 32 of 128: 533
+  // against 796, one of 256: 117 against 141; but 16 of 16: 58 against 57, one of 64: 35 against 30).
   const bool blocks = p->T >= (int64_t)p->N * STB_MIN_TOKENS && p->T * p->HV >= STB_MIN_WORK;
   const int64_t ctas = (int64_t)p->N * p->HV * (blocks ? 1 : ST_PARTS / ST_WARPS);
   if (ctas > INT32_MAX) return GDN_ERR_UNSUPPORTED;
