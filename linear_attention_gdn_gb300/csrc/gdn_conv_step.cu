@@ -32,6 +32,8 @@ constexpr int CS_VEC = 4;         // channels per thread, and of the kernel for 
 constexpr int CS_VEC1 = 2;
 constexpr int CS_STAGES = 16;     // rows of a thread on their way
 constexpr int CS_LOOK = 4;        // slot numbers a lane has requested together
+constexpr int CS_ROUND = 7;       // CTAs an SM holds
+constexpr int CS_LONG = 64;       // tokens of a long range
 constexpr int CS_MAXR = 256;      // tokens per range, at most
 
 struct ConvStepArgs {
@@ -356,14 +358,15 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.N = p->N;
   a.C = p->C;
   a.slots = p->slots;
-  // single tokens: as many sequences side by side as give an SM 32 CTAs; else ranges that give it four rounds
-  // of the 8 CTAs it holds
+  // single tokens: as many sequences side by side as give an SM 32 CTAs
   const int per_cta = CS_THREADS * (cu_dev ? CS_VEC : CS_VEC1);
   const int cols = (p->C + per_cta - 1) / per_cta;
   int64_t rows;
   if (cu_dev) {
-    const int64_t ranges = std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols);
-    a.R = (int)std::min<int64_t>(CS_MAXR, (p->T + ranges - 1) / ranges);
+    // one round of CTAs, whose start is most of their time while ranges are short, or several of longer ones (29
+    // sequences of up to 106 tokens: one round of 24 tokens 14 us, four of 6 23 us)
+    const int64_t round = std::max<int64_t>(1, (int64_t)sm_count() * CS_ROUND / cols), one = (p->T + round - 1) / round;
+    a.R = (int)(one <= CS_LONG ? one : std::min<int64_t>(CS_MAXR, std::max<int64_t>(CS_LONG, (one + 3) / 4)));
     rows = (p->T + a.R - 1) / a.R;
   } else {
     a.R = 1;

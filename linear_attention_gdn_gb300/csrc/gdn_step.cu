@@ -221,7 +221,7 @@ template <typename E, bool KDA> struct StepToken {
 // (registers for 12 and 14 warps an SM: 64 sequences of 8 tokens 137 us with one decay a channel and 115 with one a
 // head; left to the compiler 177 and 125)
 template <typename E, bool KDA>
-__global__ void __launch_bounds__(ST_WARPS * 32, KDA ? 12 : 14) step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14) step_kernel(const StepArgs a) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
   const int part = (int)(item % ST_PARTS);
