@@ -17,6 +17,7 @@ constexpr int QK_THREADS = 128;
 constexpr int QK_WARPS = QK_THREADS / 32;
 constexpr int QK_MAXD = 512;        // any layout
 constexpr int QK_FAST_MAXD = 256;   // rows of 8 values a lane
+constexpr int QK_STEPS = 16;
 constexpr int QK_CTAS = 64;         // CTAs per SM of a grid that walks its work, at most
 
 struct QkArgs {
@@ -298,7 +299,8 @@ inline bool plain_rows(const QkArgs& a) { return a.normed && a.rot == a.D; }
 
 // Divides the work: runs of heads as long as the warps that the GPU holds at once (`resident` CTAs an SM) get `least`
 // units each; then a whole number of such rounds of CTAs, so that SMs that are ahead take more of them (262,144
-// tokens of 16 + 16 heads, forward: one round 741 us, three 662, ten 633); and q's and k's shares by their heads. least
+// tokens of 16 + 16 heads, forward: one round 741 us, three 662, ten 633), as long as a warp has least * QK_STEPS rows a
+// group for its start (74,155 tokens of 1 + 1 heads of 64, forward: 14 us against 25); and q's and k's shares by their heads. least
 // is 1 for the forward and, since every CTA leaves partial sums to add, 2 for the backward (32,768 tokens, forward: 82 us
 // with 1, 97 with 4; backward 139 with 1, 130 with 2, 133 with 4).  Returns the CTAs.
 inline int divide_work(QkArgs& a, int L, int resident, int least) {
@@ -308,14 +310,13 @@ inline int divide_work(QkArgs& a, int L, int resident, int least) {
   int64_t run = groups * total / (round * QK_WARPS * least);
   run = run < 1 ? 1 : run > most ? most : run;
   a.run = (int)run;
-  int64_t units = 0, ctas = 0;
+  int64_t ctas = 0;
   for (int i = 0; i < 2; ++i) {
     a.splits[i] = (a.heads[i] + a.run - 1) / a.run;
     a.units[i] = (int)(groups * a.splits[i]);   // (below 2^31: splits are 1 unless tokens are few)
-    units += a.units[i];
     ctas += (a.units[i] + QK_WARPS - 1) / QK_WARPS;
   }
-  int64_t rounds = units / (round * QK_WARPS * least);
+  int64_t rounds = groups * total / (round * QK_WARPS * QK_STEPS * least);
   rounds = rounds < 1 ? 1 : rounds > 10 ? 10 : rounds;
   const int64_t limit = round * rounds < (int64_t)sm_count() * QK_CTAS ? round * rounds : (int64_t)sm_count() * QK_CTAS;
   if (ctas > limit) ctas = limit;
