@@ -10,6 +10,7 @@ this package fails if the compiled library is missing (build it with
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -399,22 +400,37 @@ def gdn_conv1d_bwd(prob, x, w, b, cu_seqlens_dev, cu_seqlens_host, dy, dx, dw, d
            "gdn_conv1d_bwd")
 
 
-def _call(where, prob, pointers, stream, *size):
-    """One call of an entry point whose arguments are a problem, pointers, at most a size, and the stream.  A single token's
-    call is as short as its launch, so tensors' addresses go to ctypes as plain integers (None is NULL)."""
-    try:
-        addresses = [None if x is None else x.data_ptr() for x in pointers]
-    except AttributeError:   # an array or an address among them
-        addresses = [_ptr(x) for x in pointers]
-    st = getattr(_Lazy._h or _loaded(), where)(prob, *addresses, *size,
-                                               _raw_stream() if stream is None else _stream(stream))
+_entries = {}   # name -> address of the entry point
+_native = None   # csrc/gdn_call.c
+
+
+def _entry(where):
+    """The address of an entry point; loads the library and the marshalling module at the first."""
+    global _native
+    if _native is None:
+        if not os.path.exists(_build.CALL):
+            raise ImportError(f"_gdn_call.so not built ({_build.CALL}); run linear_attention_gdn_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_gdn_call", _build.CALL)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _native = module.call
+    _entries[where] = ctypes.cast(getattr(lib, where), ctypes.c_void_p).value
+    return _entries[where]
+
+
+def _call(where, kind, prob, size, stream, *pointers):
+    """One call of an entry point whose arguments are a problem, pointers, at most a size, and the stream.  A single
+    token's call is as short as its launch, so these go past ctypes (csrc/gdn_call.c)."""
+    if type(prob) is not kind:
+        raise TypeError(f"{where} takes a {kind.__name__}, not {type(prob).__name__}")
+    entry = _entries.get(where) or _entry(where)
+    if stream is None:
+        stream = _raw_stream()
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    st = _native(entry, ctypes.addressof(prob), size, stream, *pointers)
     if st != 0:
         raise GDNError(st, where)
-
-
-def _loaded():
-    _Lazy._h = _load()
-    return _Lazy._h
 
 
 def _raw_stream():
@@ -433,19 +449,22 @@ def gdn_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, sl
              stream=None):
     """The recurrent form on a pool of states, FP32 [slots, HV, 128, 128]: N sequences take their next tokens; g, beta
     FP32 [T, HV]; dev_err a device int32, zero at first; see include/gdn.h."""
-    _call("gdn_step", prob, (q, k, v, g, beta, cu_seqlens_dev, slot_in, slot_out, states, o, dev_err), stream)
+    _call("gdn_step", gdn_step_problem, prob, None, stream, q, k, v, g, beta, cu_seqlens_dev, slot_in, slot_out,
+          states, o, dev_err)
 
 
 def gdn_kda_step(prob, q, k, v, g, beta, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None,
                  stream=None):
     """gdn_step with a log decay per key channel: g FP32 [T, HV, 128]; see include/gdn.h."""
-    _call("gdn_kda_step", prob, (q, k, v, g, beta, cu_seqlens_dev, slot_in, slot_out, states, o, dev_err), stream)
+    _call("gdn_kda_step", gdn_step_problem, prob, None, stream, q, k, v, g, beta, cu_seqlens_dev, slot_in, slot_out,
+          states, o, dev_err)
 
 
 def gdn_conv1d_step(prob, x, w, b, window, y, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None, stream=None):
     """The convolution + SiLU on a pool of windows [slots, W - 1, C]: x, y [T, C]; w [C, W], b [C] FP32; see
     include/gdn.h."""
-    _call("gdn_conv1d_step", prob, (x, w, b, cu_seqlens_dev, slot_in, slot_out, window, y, dev_err), stream)
+    _call("gdn_conv1d_step", gdn_conv_step_problem, prob, None, stream, x, w, b, cu_seqlens_dev, slot_in, slot_out,
+          window, y, dev_err)
 
 
 def gdn_qk_workspace_bytes(prob) -> int:
@@ -457,7 +476,8 @@ def gdn_qk_workspace_bytes(prob) -> int:
 def gdn_qk_norm_rope_fwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, qo, ko, stream=None):
     """The norm of q [T, HQ, D] and k [T, HK, D] per head with the position rotation: wq, wk FP32 [D] or None, freq FP64
     [rot / 2], positions int32 [T] or None; see include/gdn.h."""
-    _call("gdn_qk_norm_rope_fwd", prob, (q, k, wq, wk, freq, positions, cu_seqlens_dev, qo, ko), stream)
+    _call("gdn_qk_norm_rope_fwd", gdn_qk_problem, prob, None, stream, q, k, wq, wk, freq, positions, cu_seqlens_dev, qo,
+          ko)
 
 
 def gdn_qk_norm_rope_bwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, dqo, dko, dq, dk, dwq, dwk, workspace,
@@ -466,8 +486,8 @@ def gdn_qk_norm_rope_bwd(prob, q, k, wq, wk, freq, positions, cu_seqlens_dev, dq
     needed); see include/gdn.h."""
     if ws_bytes is None:
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call("gdn_qk_norm_rope_bwd", prob, (q, k, wq, wk, freq, positions, cu_seqlens_dev, dqo, dko, dq, dk, dwq, dwk,
-                                         workspace), stream, ws_bytes)
+    _call("gdn_qk_norm_rope_bwd", gdn_qk_problem, prob, ws_bytes, stream, q, k, wq, wk, freq, positions, cu_seqlens_dev,
+          dqo, dko, dq, dk, dwq, dwk, workspace)
 
 
 def gdn_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original=4096.0, fast=32.0, slow=1.0):

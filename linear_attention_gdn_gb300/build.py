@@ -3,7 +3,8 @@
 Each .cu under csrc/ compiles to an object in parallel with
     nvcc -gencode arch=compute_103a,code=sm_103a -O3 -lineinfo
 and the objects link into one shared library exporting the C ABI of
-include/gdn.h.  No torch, no cmake.
+include/gdn.h.  csrc/gdn_call.c, the binding's argument marshalling, is a Python
+extension of its own (_gdn_call.so).  No torch, no cmake.
 """
 from __future__ import annotations
 
@@ -12,12 +13,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
+CALL = os.path.join(BUILD, "_gdn_call.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -44,15 +47,24 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([NVCC, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
 
+    call_src = os.path.join(CSRC, "gdn_call.c")
+    if force or _stale(CALL, [call_src]):
+        jobs_call = [[os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                      call_src, "-o", CALL + f".{os.getpid()}.tmp"]]
+    else:
+        jobs_call = []
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0 or verbose:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed: " + " ".join(cmd))
+            raise RuntimeError("failed: " + " ".join(cmd))
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        list(ex.map(run, jobs))
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + 1, os.cpu_count() or 1))) as ex:
+        list(ex.map(run, jobs + jobs_call))
+    if jobs_call:
+        os.replace(CALL + f".{os.getpid()}.tmp", CALL)
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         run([NVCC, *ARCH, "-shared", "-o", tmp, *objs])

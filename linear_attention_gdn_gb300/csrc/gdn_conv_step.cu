@@ -33,6 +33,7 @@ constexpr int CS_VEC1 = 2;
 constexpr int CS_STAGES = 16;     // rows of a thread on their way
 constexpr int CS_LOOK = 4;        // slot numbers a lane has requested together
 constexpr int CS_ROUND = 7;       // CTAs an SM holds
+constexpr int CS_ROUND1 = 12;     // and of the kernel for single tokens
 constexpr int CS_LONG = 64;       // tokens of a long range
 constexpr int CS_MAXR = 256;      // tokens per range, at most
 
@@ -47,7 +48,8 @@ struct ConvStepArgs {
   void* y;
   int* err;
   int64_t xs, ys;
-  int T, N, C, slots, R;
+  int T, N, C, slots;
+  int R;   // tokens of a range; with single tokens the sequences that a thread has at a time
 };
 
 // z sigma(z), with the hardware's exponential and reciprocal (each within a few last places; the value
@@ -79,13 +81,24 @@ __device__ __forceinline__ int sequence_of(const int* cu, int N, int t) {
 template <int W, int V> struct Taps {
   float2 w[W][V / 2], b[V / 2];
   __device__ __forceinline__ void load(const ConvStepArgs& a, int c0) {
-    const float* wp = a.w + (int64_t)c0 * W;   // (c0 is even: 8-byte aligned)
+    const float* wp = a.w + (int64_t)c0 * W;   // (c0 is a multiple of V)
     float t[V * W];
+    if constexpr (V * W % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < V * W / 2; ++i) {
-      const float2 f = reinterpret_cast<const float2*>(wp)[i];
-      t[2 * i] = f.x;
-      t[2 * i + 1] = f.y;
+      for (int i = 0; i < V * W / 4; ++i) {
+        const float4 f = reinterpret_cast<const float4*>(wp)[i];
+        t[4 * i] = f.x;
+        t[4 * i + 1] = f.y;
+        t[4 * i + 2] = f.z;
+        t[4 * i + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V * W / 2; ++i) {
+        const float2 f = reinterpret_cast<const float2*>(wp)[i];
+        t[2 * i] = f.x;
+        t[2 * i + 1] = f.y;
+      }
     }
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
@@ -125,42 +138,62 @@ __device__ __forceinline__ RawV<E, V> conv_row(const Taps<W, V>& k, const RawV<E
   return out;
 }
 
-// one token each: sequence n is token n
-template <typename E, int W>
+// one token each: sequence n is token n; U sequences at a time
+template <typename E, int W, int U>
 __global__ void __launch_bounds__(CS_THREADS) conv_token_kernel(const ConvStepArgs a) {
   constexpr int V = CS_VEC1, H = W > 1 ? W - 1 : 1;
   const int c0 = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
   if (c0 >= a.C) return;
-  Taps<W, V> k;
-  k.load(a, c0);
   const E* x = static_cast<const E*>(a.x) + c0;
   E* y = static_cast<E*>(a.y) + c0;
   E* win = static_cast<E*>(a.window) + c0;
   const int64_t win_slot = (int64_t)(W - 1) * a.C;
-  for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-    const int from = a.slot_in ? a.slot_in[n] : n, to = a.slot_out ? a.slot_out[n] : from;
-    RawV<E, V> row, old[H];
-    row.load(x + (int64_t)n * a.xs);
-    if (from < -1 || from >= a.slots) {
-      *a.err = ST_DEVICE;
-      continue;
-    }
-    float2 hist[H][V / 2];
+  Taps<W, V> k;
+  bool first = true;
+  for (int n0 = blockIdx.y * U; n0 < a.N; n0 += gridDim.y * U) {
+    int from[U], to[U];
+    RawV<E, V> row[U], old[U][H];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i) {
-      if (from >= 0) old[i].load(win + from * win_slot + (int64_t)i * a.C);
-      else old[i].zero();
-      as_pairs(old[i], hist[i]);
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + u;
+      from[u] = to[u] = -2;   // past the last sequence: nothing to do
+      if (n >= a.N) continue;
+      from[u] = a.slot_in ? a.slot_in[n] : n;
+      to[u] = a.slot_out ? a.slot_out[n] : from[u];
+      row[u].load(x + (int64_t)n * a.xs);
     }
-    conv_row<E, W, V>(k, row, hist).store(y + (int64_t)n * a.ys);
-    if (W == 1) continue;
-    if (to < -1 || to >= a.slots) {
-      *a.err = ST_DEVICE;
-    } else if (to >= 0) {
-      E* p = win + to * win_slot;
+    if (first) k.load(a, c0);
+    first = false;
 #pragma unroll
-      for (int i = 0; i + 1 < W - 1; ++i) old[i + 1].store(p + (int64_t)i * a.C);
-      row.store(p + (int64_t)(W - 2) * a.C);
+    for (int u = 0; u < U; ++u) {
+      const bool some = from[u] >= 0 && from[u] < a.slots;
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) {
+        if (some) old[u][i].load(win + from[u] * win_slot + (int64_t)i * a.C);
+        else old[u][i].zero();
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + u;
+      if (n >= a.N) break;
+      if (from[u] < -1 || from[u] >= a.slots) {
+        *a.err = ST_DEVICE;
+        continue;
+      }
+      float2 hist[H][V / 2];
+#pragma unroll
+      for (int i = 0; i < W - 1; ++i) as_pairs(old[u][i], hist[i]);
+      conv_row<E, W, V>(k, row[u], hist).store(y + (int64_t)n * a.ys);
+      if (W == 1) continue;
+      if (to[u] < -1 || to[u] >= a.slots) {
+        *a.err = ST_DEVICE;
+      } else if (to[u] >= 0) {
+        E* p = win + to[u] * win_slot;
+#pragma unroll
+        for (int i = 0; i + 1 < W - 1; ++i) old[u][i + 1].store(p + (int64_t)i * a.C);
+        row[u].store(p + (int64_t)(W - 2) * a.C);
+      }
     }
   }
 }
@@ -307,7 +340,8 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
 
 template <typename E, int W> static void launch_conv_step(const ConvStepArgs& a, dim3 grid, cudaStream_t s) {
   if (a.cu) conv_step_kernel<E, W><<<grid, CS_THREADS, 0, s>>>(a);
-  else conv_token_kernel<E, W><<<grid, CS_THREADS, 0, s>>>(a);
+  else if (a.R == 1) conv_token_kernel<E, W, 1><<<grid, CS_THREADS, 0, s>>>(a);
+  else conv_token_kernel<E, W, 2><<<grid, CS_THREADS, 0, s>>>(a);
 }
 template <typename E> static void launch_conv_step(const ConvStepArgs& a, int W, dim3 grid, cudaStream_t s) {
   switch (W) {
@@ -358,7 +392,6 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.N = p->N;
   a.C = p->C;
   a.slots = p->slots;
-  // single tokens: as many sequences side by side as give an SM 32 CTAs
   const int per_cta = CS_THREADS * (cu_dev ? CS_VEC : CS_VEC1);
   const int cols = (p->C + per_cta - 1) / per_cta;
   int64_t rows;
@@ -369,8 +402,10 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
     a.R = (int)(one <= CS_LONG ? one : std::min<int64_t>(CS_MAXR, std::max<int64_t>(CS_LONG, (one + 3) / 4)));
     rows = (p->T + a.R - 1) / a.R;
   } else {
-    a.R = 1;
-    rows = std::min<int64_t>(p->N, std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols));
+    // one sequence a CTA column while the GPU holds them all, then two (64 of 10,240 channels: 4.1 us with one, TWO
+    // with two), side by side as far as they give an SM 32 CTAs
+    a.R = (int64_t)p->N * cols <= (int64_t)sm_count() * CS_ROUND1 ? 1 : 2;
+    rows = std::min<int64_t>((p->N + a.R - 1) / a.R, std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols));
   }
   if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 16 M tokens, or fewer in very many columns
   const dim3 grid(cols, (unsigned)rows);

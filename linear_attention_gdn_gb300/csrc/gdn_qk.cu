@@ -74,16 +74,17 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
 #pragma unroll
   for (int i = 0; i < R::STAGES - 1; ++i) request();
 
+  at.enter(a, splits, heads);
+  int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead: its load is not waited for)
   Angles<HALF, sizeof(E) == 2> ang;
   ang.setup(a, l);
   float2 w[4];
   lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
-  do {
-    at.enter(a, splits, heads);
+  for (;;) {
     float2 wc[4], ws[4];
     {
       float2 co[4], si[4];
-      ang.at(a, at.t, l, co, si);
+      ang.at(a, pos, l, co, si);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         wc[j] = __fmul2_rn(w[j], co[j]);
@@ -92,7 +93,13 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
     }
     E* y = ybase + at.t * yt + at.h * yh;
     const bool keep = at.live && has;
-    for (int n = at.left; n > 0; --n) {
+    const int rows = at.left;
+    at.unit += warps;
+    if (at.unit < units) {
+      at.enter(a, splits, heads);
+      pos = position_of(a, at.t, &doc);
+    }
+    for (int n = rows; n > 0; --n) {
       copies_wait<R::STAGES - 2>();
       __syncwarp();   // every lane's share of this slot is there, and the last slot has been read by all
       request();      // into the last slot
@@ -115,8 +122,8 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
       if (keep) write_row<E, HALF>(y, away, v);
       y += yh;
     }
-    at.unit += warps;
-  } while (at.unit < units);
+    if (at.unit >= units) return;
+  }
 }
 
 // rows of any kind: lane i has the values i, i + 32, ... (PER of them) of each row of its warp's token

@@ -71,17 +71,24 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
 #pragma unroll
     for (int i = 0; i < R::STAGES - 1; ++i) request();
 
+    at.enter(a, splits, heads);
+    int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead)
     Angles<HALF, sizeof(E) == 2> ang;
     ang.setup(a, l);
     float2 w[4];
     lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
     do {
-      at.enter(a, splits, heads);
       float2 co[4], si[4];
-      ang.at(a, at.t, l, co, si);
+      ang.at(a, pos, l, co, si);
       E* dx = dbase + at.t * xt + at.h * xh;
-      const bool keep = at.live && has;
-      for (int n = at.left; n > 0; --n) {
+      const bool live = at.live, keep = live && has;
+      const int rows = at.left;
+      at.unit += warps;
+      if (at.unit < units) {
+        at.enter(a, splits, heads);
+        pos = position_of(a, at.t, &doc);
+      }
+      for (int n = rows; n > 0; --n) {
         copies_wait<R::STAGES - 2>();
         __syncwarp();
         request();
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
           f = -row_sum<L>(d.x + d.y) * a.share * r * r * r;
         }
         const float2 rr = make_float2(r, r), ff = make_float2(f, f);
-        if (at.live) {
+        if (live) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = __ffma2_rn(gv[j], rr, acc[j]);
         }
@@ -124,7 +131,6 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
         if (keep) write_row<E, HALF>(dx, away, v);
         dx += xh;
       }
-      at.unit += warps;
     } while (at.unit < units);
   }
   if (!a.part) return;
