@@ -23,11 +23,13 @@
 #include "gdn_common.cuh"
 #include "gdn_elem.cuh"
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 #include "gdn_prof.h"
 
 namespace gdn {
 
 constexpr int CS_THREADS = 128;
+constexpr int CS_THREADS1 = 128;  // of a CTA of the kernel for single tokens
 constexpr int CS_VEC = 4;         // channels per thread, and of the kernel for single tokens:
 constexpr int CS_VEC1 = 2;
 constexpr int CS_STAGES = 16;     // rows of a thread on their way
@@ -140,9 +142,10 @@ __device__ __forceinline__ RawV<E, V> conv_row(const Taps<W, V>& k, const RawV<E
 
 // one token each: sequence n is token n; U sequences at a time
 template <typename E, int W, int U>
-__global__ void __launch_bounds__(CS_THREADS) conv_token_kernel(const ConvStepArgs a) {
+__global__ void __launch_bounds__(CS_THREADS1) conv_token_kernel(const ConvStepArgs a) {
+  chain_kernel();
   constexpr int V = CS_VEC1, H = W > 1 ? W - 1 : 1;
-  const int c0 = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
+  const int c0 = (blockIdx.x * CS_THREADS1 + threadIdx.x) * V;
   if (c0 >= a.C) return;
   const E* x = static_cast<const E*>(a.x) + c0;
   E* y = static_cast<E*>(a.y) + c0;
@@ -200,6 +203,7 @@ __global__ void __launch_bounds__(CS_THREADS) conv_token_kernel(const ConvStepAr
 
 template <typename E, int W>
 __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArgs a) {
+  chain_kernel();
   constexpr int V = CS_VEC, H = W > 1 ? W - 1 : 1, BYTES = V * (int)sizeof(E);
   __shared__ __align__(16) uint8_t ring[CS_STAGES][CS_THREADS * BYTES];
   const int lane = threadIdx.x & 31;
@@ -339,9 +343,9 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
 }
 
 template <typename E, int W> static void launch_conv_step(const ConvStepArgs& a, dim3 grid, cudaStream_t s) {
-  if (a.cu) conv_step_kernel<E, W><<<grid, CS_THREADS, 0, s>>>(a);
-  else if (a.R == 1) conv_token_kernel<E, W, 1><<<grid, CS_THREADS, 0, s>>>(a);
-  else conv_token_kernel<E, W, 2><<<grid, CS_THREADS, 0, s>>>(a);
+  if (a.cu) launch_chained(conv_step_kernel<E, W>, grid, CS_THREADS, 0, s, a);
+  else if (a.R == 1) launch_chained(conv_token_kernel<E, W, 1>, grid, CS_THREADS1, 0, s, a);
+  else launch_chained(conv_token_kernel<E, W, 2>, grid, CS_THREADS1, 0, s, a);
 }
 template <typename E> static void launch_conv_step(const ConvStepArgs& a, int W, dim3 grid, cudaStream_t s) {
   switch (W) {
@@ -392,7 +396,7 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.N = p->N;
   a.C = p->C;
   a.slots = p->slots;
-  const int per_cta = CS_THREADS * (cu_dev ? CS_VEC : CS_VEC1);
+  const int per_cta = cu_dev ? CS_THREADS * CS_VEC : CS_THREADS1 * CS_VEC1;
   const int cols = (p->C + per_cta - 1) / per_cta;
   int64_t rows;
   if (cu_dev) {
@@ -402,9 +406,9 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
     a.R = (int)(one <= CS_LONG ? one : std::min<int64_t>(CS_MAXR, std::max<int64_t>(CS_LONG, (one + 3) / 4)));
     rows = (p->T + a.R - 1) / a.R;
   } else {
-    // one sequence a CTA column while the GPU holds them all, then two (64 of 10,240 channels: 4.1 us with one, TWO
+    // one sequence a CTA column while the GPU holds them all, then two (64 of 10,240 channels: 4.1 us with one, 3.2
     // with two), side by side as far as they give an SM 32 CTAs
-    a.R = (int64_t)p->N * cols <= (int64_t)sm_count() * CS_ROUND1 ? 1 : 2;
+    a.R = (int64_t)p->N * cols <= (int64_t)sm_count() * CS_ROUND1 * 128 / CS_THREADS1 ? 1 : 2;
     rows = std::min<int64_t>((p->N + a.R - 1) / a.R, std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols));
   }
   if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 16 M tokens, or fewer in very many columns

@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "gdn_launch.cuh"
 #include "gdn_prof.h"
 #include "gdn_qk.cuh"
 
@@ -24,6 +25,7 @@ namespace gdn {
 
 template <typename E, int L, bool HALF, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
+  chain_kernel();
   using R = Ring<E, L, 1>;
   constexpr int VEC = 16 / (int)sizeof(E);   // values of one copy
   __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
@@ -45,6 +47,12 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   at.unit = to.unit = cta * QK_WARPS + (threadIdx.x >> 5);
   if (at.unit >= units) return;
   to.enter(a, splits, heads);
+  at = to;
+  int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead: its load is not waited for)
+  Angles<HALF, sizeof(E) == 2> ang;
+  ang.request(a, l);
+  float2 w[4];
+  lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
   const E* px = xbase + to.t * xt + to.h * xh;
   const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine + off0);
   int fill = 0, use = 0;   // byte offsets of slots
@@ -74,12 +82,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
 #pragma unroll
   for (int i = 0; i < R::STAGES - 1; ++i) request();
 
-  at.enter(a, splits, heads);
-  int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead: its load is not waited for)
-  Angles<HALF, sizeof(E) == 2> ang;
-  ang.setup(a, l);
-  float2 w[4];
-  lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
+  ang.setup();
   for (;;) {
     float2 wc[4], ws[4];
     {
@@ -129,6 +132,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
 // rows of any kind: lane i has the values i, i + 32, ... (PER of them) of each row of its warp's token
 template <typename E, int PER>
 __global__ void __launch_bounds__(QK_THREADS) qk_fwd_row_kernel(const QkArgs a) {
+  chain_kernel();
   __shared__ float rows[QK_WARPS][PER * 32];
   float* z = rows[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_row_kernel(const QkArgs a) 
 template <typename E, int L, bool HALF, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_fwd_kernel<E, L, HALF, PLAIN>);
   const int ctas = divide_work(a, L, resident, 1);
-  qk_fwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
+  launch_chained(qk_fwd_kernel<E, L, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
 }
 template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
   const bool plain = plain_rows(a);
@@ -185,7 +189,7 @@ template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t
 template <typename E, int PER> static void launch_fwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_fwd_row_kernel<E, PER>);
   const int ctas = divide_work(a, 32, resident, 1);
-  qk_fwd_row_kernel<E, PER><<<ctas, QK_THREADS, 0, s>>>(a);
+  launch_chained(qk_fwd_row_kernel<E, PER>, ctas, QK_THREADS, 0, s, a);
 }
 template <typename E> static void launch_fwd(QkArgs& a, bool fast, cudaStream_t s) {
   if (!fast && a.D <= 128) launch_fwd_any<E, 4>(a, s);

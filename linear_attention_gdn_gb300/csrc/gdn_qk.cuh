@@ -192,9 +192,15 @@ __device__ __forceinline__ void only_rotated(float2 (&v)[4], int rotated) {
 // y[j] = v[j] co[j] + partner[j] si[j].  Pairs past the rotated part get the identity.
 template <bool HALF, bool FAST> struct Angles {
   uint64_t step[4];
-  __device__ __forceinline__ void setup(const QkArgs& a, int l) {
+  double f[4];
+  // the frequencies are requested first, and converted when the rows' copies are on their way
+  __device__ __forceinline__ void request(const QkArgs& a, int l) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) step[i] = 4 * l + i < a.rot / 2 ? turn_step(a.freq[4 * l + i]) : 0;
+    for (int i = 0; i < 4; ++i) f[i] = 4 * l + i < a.rot / 2 ? a.freq[4 * l + i] : 0.0;
+  }
+  __device__ __forceinline__ void setup() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) step[i] = turn_step(f[i]);
   }
   __device__ __forceinline__ void at(const QkArgs& a, int pos, int l, float2 (&co)[4], float2 (&si)[4]) {
     float c[4], s[4];

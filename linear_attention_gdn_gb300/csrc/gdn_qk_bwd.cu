@@ -6,6 +6,7 @@
 // together.  Work and layout are the forward's.  Each lane keeps its values' share of dwq and dwk in registers
 // over all its rows; they are added over the CTA's lane groups in order, written as one partial a CTA, and a second
 // kernel adds the partials in order, so results do not depend on scheduling.
+#include "gdn_launch.cuh"
 #include "gdn_prof.h"
 #include "gdn_qk.cuh"
 
@@ -13,6 +14,7 @@ namespace gdn {
 
 template <typename E, int L, bool HALF, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
+  chain_kernel();
   using R = Ring<E, L, 2>;
   constexpr int VEC = 16 / (int)sizeof(E);
   __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
@@ -38,6 +40,12 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   at.unit = to.unit = cta * QK_WARPS + (threadIdx.x >> 5);
   if (at.unit < units) {
     to.enter(a, splits, heads);
+    at = to;
+    int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead)
+    Angles<HALF, sizeof(E) == 2> ang;
+    ang.request(a, l);
+    float2 w[4];
+    lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
     const E* px = xbase + to.t * xt + to.h * xh;
     const E* pg = gbase + to.t * yt + to.h * yh;
     const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine + off0);
@@ -71,12 +79,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
 #pragma unroll
     for (int i = 0; i < R::STAGES - 1; ++i) request();
 
-    at.enter(a, splits, heads);
-    int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead)
-    Angles<HALF, sizeof(E) == 2> ang;
-    ang.setup(a, l);
-    float2 w[4];
-    lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
+    ang.setup();
     do {
       float2 co[4], si[4];
       ang.at(a, pos, l, co, si);
@@ -153,6 +156,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
 // rows of any kind, as in the forward
 template <typename E, int PER>
 __global__ void __launch_bounds__(QK_THREADS) qk_bwd_row_kernel(const QkArgs a) {
+  chain_kernel();
   __shared__ float rows[QK_WARPS][PER * 32];
   const int lane = threadIdx.x & 31;
   float* z = rows[threadIdx.x >> 5];
@@ -221,6 +225,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_row_kernel(const QkArgs a) 
 // CTAs 0 .. ctas_q-1, k's in the others
 __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas_q, int ctas, int D,
                                                      float* dwq, float* dwk) {
+  chain_kernel();
   __shared__ float sums[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas
 template <typename E, int L, bool HALF, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_bwd_kernel<E, L, HALF, PLAIN>);
   const int ctas = divide_work(a, L, resident, 2);
-  qk_bwd_kernel<E, L, HALF, PLAIN><<<ctas, QK_THREADS, 0, s>>>(a);
+  launch_chained(qk_bwd_kernel<E, L, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
   return ctas;
 }
 template <typename E, int L> static int launch_bwd_rows(QkArgs& a, cudaStream_t s) {
@@ -256,7 +261,7 @@ template <typename E, int L> static int launch_bwd_rows(QkArgs& a, cudaStream_t 
 template <typename E, int PER> static int launch_bwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_bwd_row_kernel<E, PER>);
   const int ctas = divide_work(a, 32, resident, 2);
-  qk_bwd_row_kernel<E, PER><<<ctas, QK_THREADS, 0, s>>>(a);
+  launch_chained(qk_bwd_row_kernel<E, PER>, ctas, QK_THREADS, 0, s, a);
   return ctas;
 }
 // returns the CTAs, each of which has left partial sums
@@ -272,7 +277,7 @@ void launch_qk_bwd(QkArgs& a, int dtype, bool fast, float* dwq, float* dwk, cuda
                    : dtype == GDN_FP16 ? launch_bwd<__half>(a, fast, s)
                                        : launch_bwd<float>(a, fast, s);
   if (a.part)
-    qk_dw_kernel<<<(2 * a.D + 31) / 32, dim3(32, 32), 0, s>>>(a.part, a.ctas_q, ctas, a.D, dwq, dwk);
+    launch_chained(qk_dw_kernel, (2 * a.D + 31) / 32, dim3(32, 32), 0, s, a.part, a.ctas_q, ctas, a.D, dwq, dwk);
 }
 
 }  // namespace gdn

@@ -20,6 +20,7 @@
 #include "gdn_common.cuh"
 #include "gdn_elem.cuh"
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 #include "gdn_prof.h"
 
 namespace gdn {
@@ -74,6 +75,7 @@ __device__ __forceinline__ float step_output(const StepOut& x, float kq, float s
 // about one token a sequence
 template <typename E, bool KDA>
 __global__ void __launch_bounds__(ST_WARPS * 32) step_token_kernel(const StepArgs a) {
+  chain_kernel();
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
   const int part = (int)(item % ST_PARTS);
@@ -222,6 +224,7 @@ template <typename E, bool KDA> struct StepToken {
 // head; left to the compiler 177 and 125)
 template <typename E, bool KDA>
 __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14) step_kernel(const StepArgs a) {
+  chain_kernel();
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
   const int part = (int)(item % ST_PARTS);
@@ -536,6 +539,7 @@ __device__ __forceinline__ int sequence_of_rank(const StepArgs& a, int rank) {
 
 template <typename E, bool KDA>
 __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const StepArgs a) {
+  previous_kernel_done();   // (its own dependents would take the places of balanced_place: 127 us for 105)
   using Raw = StepRaw<E, KDA>;
   extern __shared__ __align__(16) uint8_t step_smem[];
   StepBlock* blocks = reinterpret_cast<StepBlock*>(step_smem);
@@ -723,11 +727,11 @@ template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool 
     if (cudaFuncSetAttribute(step_block_kernel<E, KDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
       return false;
-    step_block_kernel<E, KDA><<<ctas, STB_WARPS * 32, bytes, s>>>(a);
+    launch_chained(step_block_kernel<E, KDA>, ctas, STB_WARPS * 32, bytes, s, a);
   } else if (a.T > a.N) {
-    step_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
+    launch_chained(step_kernel<E, KDA>, ctas, ST_WARPS * 32, 0, s, a);
   } else {
-    step_token_kernel<E, KDA><<<ctas, ST_WARPS * 32, 0, s>>>(a);
+    launch_chained(step_token_kernel<E, KDA>, ctas, ST_WARPS * 32, 0, s, a);
   }
   return true;
 }
