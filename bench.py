@@ -149,13 +149,15 @@ def peaks():
 
 def source_hash():
     """Hash of the GDN kernels' sources (the conv1d front, profiled apart, and
-    the tensor-core probe, which is not on the path, are left out) with comments
-    and whitespace removed, so that a change to a comment keeps the committed
-    ncu figures valid."""
+    what is not on the path, the tensor-core probe and the generation and q/k
+    operators, are left out) with comments and whitespace removed, so that a
+    change to a comment keeps the committed ncu figures valid."""
+    off_path = ("gdn_conv1d.cu", "gdn_probe.cu", "gdn_step.cu", "gdn_conv_step.cu", "gdn_qk.cu", "gdn_qk_bwd.cu",
+                "gdn_qk.cuh", "gdn_elem.cuh", "gdn_launch.cuh", "gdn_call.c")
     h = hashlib.sha256()
     cs = os.path.join(ROOT, "linear_attention_gdn_gb300", "csrc")
     for f in sorted(os.listdir(cs)):
-        if f in ("gdn_conv1d.cu", "gdn_probe.cu"):
+        if f in off_path:
             continue
         t = open(os.path.join(cs, f), encoding="utf-8").read()
         t = re.sub(r"/\*.*?\*/", " ", t, flags=re.S)
