@@ -28,6 +28,7 @@ namespace gdn {
 constexpr int ST_WARPS = 1;            // warps per CTA
 constexpr int ST_COLS = 16;            // columns of a warp
 constexpr int ST_PARTS = D / ST_COLS;  // warps per (sequence, head)
+constexpr int ST_FEW = 4;              // few heads: one to so many SMs
 constexpr float ST_EPS = 1e-6f;        // under the root of the l2 norm
 
 struct StepArgs {
@@ -210,47 +211,57 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_token_kernel(const StepArg
   }
 }
 
+// The layout of a warp with ROWL row lanes: lane (r, c) = (lane / COLL, lane % COLL) holds the columns 4c .. 4c+3 of ROWS
+// rows, in GROUPS runs of 8 neighbouring ones: 8 r + 64 m + 0 .. 7.  8 row lanes (16 rows a lane, 16 columns a warp) need the
+// fewest instructions in all, 16 (8 rows, 8 columns) fewer in a warp, whose chain from token to token is all there is to
+// wait for where warps are few.
+template <int ROWL> struct StepLayout {
+  static constexpr int COLL = 32 / ROWL, COLS = 4 * COLL, PARTS = D / COLS, ROWS = D / ROWL, GROUPS = ROWS / 8;
+  static constexpr int PAIRS = ROWS / 2;
+  // the first row, within a lane's, of the pair p
+  static __device__ __forceinline__ int row(int p) { return p % 4 * 2 + p / 4 * 64; }
+};
+
 // what a lane needs of one token
-template <typename E, bool KDA> struct StepToken {
-  Raw8<E> k[2], q[2];   // of its rows
-  float4 g[KDA ? 4 : 1];
+template <typename E, bool KDA, int ROWL> struct StepToken {
+  using L = StepLayout<ROWL>;
+  Raw8<E> k[L::GROUPS], q[L::GROUPS];   // of its rows
+  float4 g[KDA ? L::ROWS / 4 : 1];
   float beta;
   E v;                  // of its column of the sums
   int to;
 };
 
 // a few tokens: the next one's rows are requested a token ahead, and rows lie in pairs for the paired FP32 instructions
-// (registers for 12 and 14 warps an SM: 64 sequences of 8 tokens 137 us with one decay a channel and 115 with one a
-// head; left to the compiler 177 and 125)
-template <typename E, bool KDA>
-__global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14) step_kernel(const StepArgs a) {
+// BUSY: registers for 12 and 16 warps an SM (64 sequences of 8 tokens 137 us with one decay a channel and 115 with one a
+// head; left to the compiler 177 and 125), where there are so many warps.
+template <typename E, bool KDA, int ROWL, bool BUSY>
+__global__ void __launch_bounds__(32, !BUSY ? 1 : KDA || sizeof(E) == 4 ? 12 : 16) step_kernel(const StepArgs a) {
   chain_kernel();
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int64_t item = (int64_t)blockIdx.x * ST_WARPS + (threadIdx.x >> 5);
-  const int part = (int)(item % ST_PARTS);
-  const int h = (int)(item / ST_PARTS % a.HV);
-  const int64_t n = item / ST_PARTS / a.HV;
-  if (n >= a.N) return;
+  using L = StepLayout<ROWL>;
+  using Token = StepToken<E, KDA, ROWL>;
+  const int lane = threadIdx.x & 31, r = lane / L::COLL, c = lane % L::COLL;
+  const int part = blockIdx.x % L::PARTS, h = blockIdx.x / L::PARTS % a.HV, n = blockIdx.x / L::PARTS / a.HV;
   int t0, t1;
-  if (!sequence_bounds(a.cu, (int)n, a.T, &t0, &t1)) {
+  if (!sequence_bounds(a.cu, n, a.T, &t0, &t1)) {
     if (lane == 0) *a.err = ST_DEVICE;
     return;
   }
   if (t0 == t1) return;
-  const int from = a.slot_in ? a.slot_in[n] : (int)n;
+  const int from = a.slot_in ? a.slot_in[n] : n;
   if (from < -1 || from >= a.slots) {
     if (lane == 0) *a.err = ST_DEVICE;
     return;
   }
   // element offset of this lane's first value within a slot
   const int64_t slot_elems = (int64_t)a.HV * STATE_F32;
-  const int64_t at = (int64_t)h * STATE_F32 + r * 8 * D + part * ST_COLS + c * 4;
-  float2 S[8][4];   // [pair of rows][column]
+  const int64_t at = (int64_t)h * STATE_F32 + r * 8 * D + part * L::COLS + c * 4;
+  float2 S[L::PAIRS][4];   // [pair of rows][column]
   if (from >= 0) {
     const float* p = a.states + from * slot_elems + at;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float* row = p + ((j & 3) * 2 + (j >> 2) * 64) * D;
+    for (int j = 0; j < L::PAIRS; ++j) {
+      const float* row = p + L::row(j) * D;
       const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + D);
       S[j][0] = make_float2(x.x, y.x);
       S[j][1] = make_float2(x.y, y.y);
@@ -259,24 +270,25 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) S[j >> 2][j & 3] = make_float2(0.f, 0.f);
+    for (int j = 0; j < 4 * L::PAIRS; ++j) S[j >> 2][j & 3] = make_float2(0.f, 0.f);
   }
   // after the sums, lanes with bit 4 clear hold u and those with it set S'^T q^, of this column
   const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-  const int own = part * ST_COLS + c * 4 + (b3 ? 2 : 0) + (b2 ? 1 : 0);
+  const int own = part * L::COLS + c * 4 + (b3 ? 2 : 0) + (b2 ? 1 : 0);
+  const bool writer = b4 && (lane & 3) < L::COLL;   // (further row lanes have copies of the sums)
   const int hq = h / a.G;
-  auto request = [&](int64_t t, StepToken<E, KDA>* x) {
+  auto request = [&](int64_t t, Token* x) {
     const E* kp = static_cast<const E*>(a.k) + t * a.ks + hq * D + r * 8;
     const E* qp = static_cast<const E*>(a.q) + t * a.qs + hq * D + r * 8;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < L::GROUPS; ++m) {
       x->k[m].load(kp + 64 * m);
       x->q[m].load(qp + 64 * m);
     }
     if constexpr (KDA) {
       const float4* g = reinterpret_cast<const float4*>(a.g + (t * a.HV + h) * D + r * 8);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) x->g[m] = g[(m & 1) + (m >> 1) * 16];
+      for (int m = 0; m < L::ROWS / 4; ++m) x->g[m] = g[(m & 1) + (m >> 1) * 16];
     } else {
       x->g[0].x = a.g[t * a.HV + h];
     }
@@ -284,7 +296,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
     x->v = static_cast<const E*>(a.v)[t * a.vs + h * D + own];
     x->to = a.slot_out ? a.slot_out[t] : t == t1 - 1 ? from : -1;
   };
-  StepToken<E, KDA> x;
+  Token x;
   request(t0, &x);
   E* op = static_cast<E*>(a.o) + ((int64_t)t0 * a.HV + h) * D + own;
   for (int t = t0; t < t1; ++t, op += (int64_t)a.HV * D) {
@@ -292,7 +304,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
     // rounding, which is less than that
     if constexpr (KDA) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < L::PAIRS; ++j) {
         const float4 g = x.g[j >> 1];
         const float2 e = j & 1 ? make_float2(__expf(g.z), __expf(g.w)) : make_float2(__expf(g.x), __expf(g.y));
 #pragma unroll
@@ -301,12 +313,12 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
     } else {
       const float e = __expf(x.g[0].x);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) S[j >> 2][j & 3] = __fmul2_rn(S[j >> 2][j & 3], make_float2(e, e));
+      for (int j = 0; j < 4 * L::PAIRS; ++j) S[j >> 2][j & 3] = __fmul2_rn(S[j >> 2][j & 3], make_float2(e, e));
     }
-    float2 k[8], s[2][4];
+    float2 k[L::PAIRS], s[2][4];
     float2 kk = make_float2(0.f, 0.f), qq = kk, kq = kk;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < L::GROUPS; ++m) {
       float kf[8], qf[8];
       x.k[m].get(kf);
       x.q[m].get(qf);
@@ -331,7 +343,7 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
     // sums over the 8 row lanes; the 8 column sums are spread over them on the way
     float n0 = kk.x + kk.y, n1 = qq.x + qq.y, n2 = kq.x + kq.y;
 #pragma unroll
-    for (int d = 4; d <= 16; d <<= 1) {
+    for (int d = L::COLL; d <= 16; d <<= 1) {
       n0 += __shfl_xor_sync(~0u, n0, d);
       n1 += __shfl_xor_sync(~0u, n1, d);
       n2 += __shfl_xor_sync(~0u, n2, d);
@@ -345,6 +357,8 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
 #pragma unroll
     for (int i = 0; i < 2; ++i) y[i] = (b3 ? w[2 + i] : w[i]) + __shfl_xor_sync(~0u, b3 ? w[i] : w[2 + i], 8);
     sum = (b2 ? y[1] : y[0]) + __shfl_xor_sync(~0u, b2 ? y[0] : y[1], 4);
+#pragma unroll
+    for (int d = L::COLL; d < 4; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
     const StepOut r1 = step_column(a, n0, n1, sum, beta, v);
     float2 f[4];
 #pragma unroll
@@ -353,16 +367,16 @@ __global__ void __launch_bounds__(ST_WARPS * 32, KDA || sizeof(E) == 4 ? 12 : 14
       f[i] = make_float2(e, e);
     }
     const float e1 = __shfl_xor_sync(~0u, r1.e, 16);
-    if (b4) *op = from_f32<E>(step_output(r1, n2, sum, e1));
+    if (writer) *op = from_f32<E>(step_output(r1, n2, sum, e1));
 #pragma unroll
-    for (int j = 0; j < 32; ++j) S[j >> 2][j & 3] = __ffma2_rn(k[j >> 2], f[j & 3], S[j >> 2][j & 3]);
+    for (int j = 0; j < 4 * L::PAIRS; ++j) S[j >> 2][j & 3] = __ffma2_rn(k[j >> 2], f[j & 3], S[j >> 2][j & 3]);
     if (to >= a.slots || to < -1) {
       if (lane == 0) *a.err = ST_DEVICE;
     } else if (to >= 0) {
       float* p = a.states + to * slot_elems + at;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float* row = p + ((j & 3) * 2 + (j >> 2) * 64) * D;
+      for (int j = 0; j < L::PAIRS; ++j) {
+        float* row = p + L::row(j) * D;
         *reinterpret_cast<float4*>(row) = make_float4(S[j][0].x, S[j][1].x, S[j][2].x, S[j][3].x);
         *reinterpret_cast<float4*>(row + D) = make_float4(S[j][0].y, S[j][1].y, S[j][2].y, S[j][3].y);
       }
@@ -721,17 +735,21 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
   }
 }
 
-template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool blocks, unsigned ctas, cudaStream_t s) {
+template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool blocks, unsigned heads, cudaStream_t s) {
   if (blocks) {
     constexpr int bytes = STB_WARPS * ((int)sizeof(StepBlock) + STB_E_BYTES) + (int)sizeof(StepRaw<E, KDA>);
     if (cudaFuncSetAttribute(step_block_kernel<E, KDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
         cudaSuccess)
       return false;
-    launch_chained(step_block_kernel<E, KDA>, ctas, STB_WARPS * 32, bytes, s, a);
-  } else if (a.T > a.N) {
-    launch_chained(step_kernel<E, KDA>, ctas, ST_WARPS * 32, 0, s, a);
+    launch_chained(step_block_kernel<E, KDA>, heads, STB_WARPS * 32, bytes, s, a);
+  } else if (heads <= a.sms / ST_FEW) {   // single tokens, too: their bits are the same as a sequence's
+    launch_chained(step_kernel<E, KDA, 16, false>, heads * StepLayout<16>::PARTS, 32, 0, s, a);
+  } else if (a.T <= a.N) {
+    launch_chained(step_token_kernel<E, KDA>, heads * ST_PARTS / ST_WARPS, ST_WARPS * 32, 0, s, a);
+  } else if (heads <= a.sms) {
+    launch_chained(step_kernel<E, KDA, 8, false>, heads * StepLayout<8>::PARTS, 32, 0, s, a);
   } else {
-    launch_chained(step_token_kernel<E, KDA>, ctas, ST_WARPS * 32, 0, s, a);
+    launch_chained(step_kernel<E, KDA, 8, true>, heads * StepLayout<8>::PARTS, 32, 0, s, a);
   }
   return true;
 }
@@ -762,13 +780,16 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(o) ||
       (p->slots > 0 && !aligned16(states)))
     return GDN_ERR_INVALID_ARG;
-  // By the mean length, which is all that the host knows of the lengths: one token, step_token_kernel (64 sequences of
-  // 48 heads 60 us; step_kernel, with more registers, 70); a few, step_kernel (64 of 8: 115 us; step_block_kernel 157);
-  // from 12 on, if tokens times heads fill the SMs, step_block_kernel (64 of 16: 182 us against 204, 32 of 128: 533
-  // against 796, one of 256: 117 against 141; but 16 of 16: 58 against 57, one of 64: 35 against 30).
-  const bool blocks = p->T >= (int64_t)p->N * STB_MIN_TOKENS && p->T * p->HV >= STB_MIN_WORK;
-  const int64_t ctas = (int64_t)p->N * p->HV * (blocks ? 1 : ST_PARTS / ST_WARPS);
-  if (ctas > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  // By the sequences' heads and their mean length, which is all that the host knows of the lengths.  Few heads, for which
+  // the chain from token to token is all: step_kernel with 8 columns a warp (one sequence of 64 tokens and 4 heads 20 us,
+  // with 16 columns 32).  Else one token: step_token_kernel (64 sequences of 48 heads 60 us; step_kernel, with more
+  // registers, 70); a few, step_kernel (64 of 8: 115 us; step_block_kernel 157); from 12 on, if tokens times heads fill the
+  // SMs, step_block_kernel (64 of 16: 182 us against 204, 32 of 128: 533 against 796; but 16 of 16: 58 against 57, one of
+  // 64: 35 against 30).
+  const int64_t heads = (int64_t)p->N * p->HV;
+  const bool blocks = heads > sm_count() / ST_FEW && p->T >= (int64_t)p->N * STB_MIN_TOKENS &&
+                      p->T * p->HV >= STB_MIN_WORK;
+  if (heads * StepLayout<16>::PARTS > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -793,9 +814,9 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   prof_begin(id, stream);
   bool ok;
   switch (p->dtype) {
-    case GDN_BF16: ok = launch_step<__nv_bfloat16, KDA>(a, blocks, (unsigned)ctas, stream); break;
-    case GDN_FP16: ok = launch_step<__half, KDA>(a, blocks, (unsigned)ctas, stream); break;
-    default: ok = launch_step<float, KDA>(a, blocks, (unsigned)ctas, stream); break;
+    case GDN_BF16: ok = launch_step<__nv_bfloat16, KDA>(a, blocks, (unsigned)heads, stream); break;
+    case GDN_FP16: ok = launch_step<__half, KDA>(a, blocks, (unsigned)heads, stream); break;
+    default: ok = launch_step<float, KDA>(a, blocks, (unsigned)heads, stream); break;
   }
   prof_end(id, stream);
   return ok && cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

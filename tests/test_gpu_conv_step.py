@@ -136,3 +136,22 @@ def test_single_tokens_are_the_sequence():
         assert status == 0 and torch.equal(yj, want[[j, 6 + j]])
         one["window"] = w2.cpu()
     assert torch.equal(one["window"], win.cpu())
+
+
+@pytest.mark.parametrize("N", [131, 701])
+@pytest.mark.parametrize("W", [1, 3, 4])
+def test_more_single_tokens_than_the_gpu_holds(N, W):
+    """Single tokens of so many channels that a thread takes two sequences at a time, an odd number of them, and then goes
+    on to further ones; slots of no order, some of none."""
+    rng = np.random.default_rng(N + W)
+    x = make([1] * N, 4096, W, N + 5, "bf16", seed=N)
+    slot_in = rng.permutation(N + 5)[:N]
+    slot_out = slot_in.copy()
+    slot_in[::7] = -1
+    slot_out[3::11] = -1
+    check(x, run(x, list(slot_in), list(slot_out), cu=None), slot_in, slot_out)
+    bad = slot_in.copy()
+    bad[N - 1] = N + 5
+    y, win, status = run(x, list(bad), list(slot_out), cu=None)
+    good = run(x, list(slot_in), list(slot_out), cu=None)
+    assert status == 7 and torch.equal(y[:N - 1], good[0][:N - 1])

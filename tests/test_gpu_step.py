@@ -315,3 +315,19 @@ def test_graph_replay_takes_new_lengths():
         graph.replay()
         want = run(y, False, None, None)
         assert torch.equal(o, want[0]) and torch.equal(d["states"], want[1])
+
+
+@pytest.mark.parametrize("kda", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("N,H,HV", [(1, 1, 1), (3, 2, 4), (2, 19, 19), (1, 13, 39), (20, 1, 2), (160, 1, 1)])
+def test_head_counts_around_the_kernels_choice(N, H, HV, dtype, kda):
+    """Few heads, a middle number and many, each with single tokens and with a few: the kernels differ in how they spread a
+    state over warps."""
+    for lens in ([1] * N, [1 + (3 * n + 1) % 5 for n in range(N)]):
+        T = sum(lens)
+        x = make(lens, H, HV, N + 2, dtype, kda, seed=N * HV + T)
+        slot_in = [(n + 1) % (N + 2) if n % 3 else -1 for n in range(N)]
+        slot_out = np.full(T, -1)
+        for n, end in enumerate(np.cumsum(lens)):
+            slot_out[end - 1] = (n + 1) % (N + 2)
+        check(x, run(x, kda, slot_in, slot_out, packed=True), slot_in, slot_out)
