@@ -300,6 +300,11 @@ gdn_status gdn_kda_bwd(const gdn_problem *prob, const void *q, const void *k, co
  *              is not written to.  The call never clears the word.
  * The states are read once and written once per slot_out, whatever the number of tokens; sums and
  * states are FP32.  Long prompts belong to gdn_fwd_states.
+ * T up to 2^30 (else GDN_ERR_UNSUPPORTED, as for the two operators below).
+ *
+ * The kernels of gdn_step, gdn_kda_step, gdn_conv1d_step and gdn_qk_norm_rope_* are launched with programmatic stream
+ * serialization: they may be placed while the kernel before them in the stream ends, and wait for it before they touch
+ * memory; to the caller the stream is in order as always.
  */
 typedef struct {
     int64_t T;        /* tokens in all; 0 does nothing */
@@ -370,8 +375,9 @@ gdn_status gdn_conv1d_step(const gdn_conv_step_problem *prob, const void *x, con
  * Forward: qo, ko; each may be its input (same strides).  Backward: dq, dk (each may be dqo, dko), and the
  * weights' gradients dwq, dwk [D] FP32 (each NULL: not wanted; not NULL with its w NULL is allowed), summed
  * over all tokens and heads in a fixed order.  x must be what the forward read.
- * Any even rot <= D, any D <= 512, any alignment of at least the element's; sums in FP32.
- * Rows whose values, strides and pointers are in whole 16 bytes take the fast kernels.
+ * Any even rot <= D, any D <= 512, any alignment of at least the element's; sums in FP32.  The fast kernels take
+ * strides and pointers in whole 16 bytes, D a multiple of 8 up to 256 and, in the half layout, rot a multiple of 8; the
+ * others are several times slower.
  * gdn_qk_workspace_bytes: the backward's scratch (16-byte aligned), for the partial sums of dwq and dwk.
  */
 #define GDN_ROPE_HALF 0

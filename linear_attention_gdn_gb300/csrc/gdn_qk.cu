@@ -279,7 +279,10 @@ gdn_status gdn_qk_workspace_bytes(const gdn_qk_problem* p, size_t* bytes) {
   const gdn_status st = qk_check(p);
   if (st != GDN_OK) return st;
   if (!bytes) return GDN_ERR_INVALID_ARG;
-  *bytes = (size_t)sm_count() * QK_CTAS * 2 * p->D * sizeof(float);
+  // two rows of partial sums a CTA, of which there are at most so many an SM (divide_work), and a warp has at least a row
+  const int64_t rows = (p->T * p->HQ + QK_WARPS - 1) / QK_WARPS + (p->T * p->HK + QK_WARPS - 1) / QK_WARPS;
+  const int64_t ctas = std::max<int64_t>(2, std::min<int64_t>(rows, (int64_t)sm_count() * QK_CTAS));
+  *bytes = (size_t)ctas * 2 * p->D * sizeof(float);
   return GDN_OK;
 }
 

@@ -221,27 +221,30 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_row_kernel(const QkArgs a) 
   }
 }
 
-// dw[d] = sum over the CTAs' partials, 32 columns of dwq | dwk a CTA, 32 threads a column; q's partials are in
-// CTAs 0 .. ctas_q-1, k's in the others
-__global__ void __launch_bounds__(1024) qk_dw_kernel(const float* part, int ctas_q, int ctas, int D,
-                                                     float* dwq, float* dwk) {
+// dw[d] = sum over the CTAs' partials, DW_COLS columns of dwq | dwk a CTA and DW_ROWS threads a column, so that a thread's
+// own sum is a few loads deep (3,648 CTAs' partials out of DRAM: 32 columns and 32 threads 10.3 us, so 8.6); q's
+// partials are in CTAs 0 .. ctas_q-1, k's in the others
+constexpr int DW_COLS = 8, DW_ROWS = 128;
+__global__ void __launch_bounds__(DW_COLS * DW_ROWS) qk_dw_kernel(const float* part, int ctas_q, int ctas, int D,
+                                                                  float* dwq, float* dwk) {
   chain_kernel();
-  __shared__ float sums[32][33];
-  const int col = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float sums[DW_ROWS][DW_COLS + 1];
+  const int col = blockIdx.x * DW_COLS + threadIdx.x, ty = threadIdx.y;
   float s = 0.f;
   if (col < 2 * D) {
     const int end = col < D ? ctas_q : ctas;
 #pragma unroll 8
-    for (int b = (col < D ? 0 : ctas_q) + threadIdx.y; b < end; b += 32) s += part[(int64_t)b * 2 * D + col];
+    for (int b = (col < D ? 0 : ctas_q) + ty; b < end; b += DW_ROWS) s += part[(int64_t)b * 2 * D + col];
   }
-  sums[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y == 0 && col < 2 * D) {
-    float v = 0.f;
+  sums[ty][threadIdx.x] = s;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += sums[i][threadIdx.x];
+  for (int half = DW_ROWS / 2; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (ty < half) sums[ty][threadIdx.x] += sums[ty + half][threadIdx.x];
+  }
+  if (ty == 0 && col < 2 * D) {
     float* dw = col < D ? dwq : dwk;
-    if (dw) dw[col < D ? col : col - D] = v;
+    if (dw) dw[col < D ? col : col - D] = sums[0][threadIdx.x];
   }
 }
 
@@ -277,7 +280,7 @@ void launch_qk_bwd(QkArgs& a, int dtype, bool fast, float* dwq, float* dwk, cuda
                    : dtype == GDN_FP16 ? launch_bwd<__half>(a, fast, s)
                                        : launch_bwd<float>(a, fast, s);
   if (a.part)
-    launch_chained(qk_dw_kernel, (2 * a.D + 31) / 32, dim3(32, 32), 0, s, a.part, a.ctas_q, ctas, a.D, dwq, dwk);
+    launch_chained(qk_dw_kernel, (2 * a.D + DW_COLS - 1) / DW_COLS, dim3(DW_COLS, DW_ROWS), 0, s, a.part, a.ctas_q, ctas, a.D, dwq, dwk);
 }
 
 }  // namespace gdn
