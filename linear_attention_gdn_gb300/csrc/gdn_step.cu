@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
           o = fmaf(sc[STB_M + s * (s + 1) / 2 + i], e[i], o);
         }
         const float rk = sc[STB_KK + s];
-        e[s] = rk * sc[STB_BETA + s] * fmaf(-rk, u, blk.v[s][warp * STB_COLS + own]);
+        // (none from tokens past len: of infinite values their zeros would make NaN)
+        e[s] = s < len ? rk * sc[STB_BETA + s] * fmaf(-rk, u, blk.v[s][warp * STB_COLS + own]) : 0.f;
         o = fmaf(sc[STB_M + s * (s + 1) / 2 + s], e[s], o);
         se[s][own] = make_float2(e[s], e[s]);
         if (s < len) op[(int64_t)(t + pos + s) * a.HV * D] = from_f32<E>(sc[STB_QQ + s] * o);

@@ -143,6 +143,27 @@ def test_blocks_with_steep_gates_in_place():
     check(x, run(x, True, None, None), [0, 1], slot_out)
 
 
+@pytest.mark.parametrize("kda", [False, True])
+@pytest.mark.parametrize("lens", [[257], [200, 62], [130, 133]])
+def test_blocks_end_with_their_last_token(lens, kda):
+    """An infinite value at the last token of a block that is not full makes its state's column infinite, with k's
+    signs: what the block lacks takes no part.  All else has the bits of a finite value's run."""
+    T = sum(lens)
+    x = make(lens, 16, 48, len(lens), "bf16", kda, seed=T)
+    x["k"][T - 1][x["k"][T - 1] == 0] = 1.0
+    good = run(x, kda, None, None)
+    x["v"][T - 1, 5, 17] = float("inf")
+    o, pool, status = run(x, kda, None, None)
+    assert status == 0 and good[2] == 0
+    column = pool[-1, 5, :, 17].cpu()
+    assert torch.equal(column, torch.sign(x["k"][T - 1, 5 // 3].float()) * float("inf"))
+    pool[-1, 5, :, 17] = good[1][-1, 5, :, 17]
+    assert torch.equal(pool, good[1])
+    assert not torch.isfinite(o[T - 1, 5, 17])
+    o[T - 1, 5, 17] = good[0][T - 1, 5, 17]
+    assert torch.equal(o, good[0])
+
+
 def test_blocks_report_bad_tables():
     x = make([150, 150], 1, 48, 3, "bf16", False, seed=15)
     good = run(x, False, [0, 1], None)
