@@ -400,8 +400,9 @@ __global__ void __launch_bounds__(32, !BUSY ? 1 : KDA || sizeof(E) == 4 ? 12 : 1
 // eight times and in pairs as it lies.  The vectors that all columns share are worked out once a CTA of STB_WARPS
 // warps: a phase is STB_WARPS blocks, each prepared by one warp into shared memory, then taken by all warps
 // without a wait, while the next phase's rows are copied in. A block ends early where a state has to be written.
-constexpr int STB_MIN_TOKENS = 12;      // a sequence, on average
-constexpr int64_t STB_MIN_WORK = 12288; // tokens times heads
+constexpr int STB_MIN_TOKENS = 24;      // a sequence, on average
+constexpr int STB_MIN_FULL = 12;        // and where tokens times heads are as many as
+constexpr int64_t STB_FULL = 12288;
 constexpr int STB_WARPS = 4;
 constexpr int STB_TOKENS = 4;   // tokens of a block
 constexpr int STB_COLS = 32;    // columns of a warp: STB_WARPS of them are a head
@@ -784,12 +785,14 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   // By the sequences' heads and their mean length, which is all that the host knows of the lengths.  Few heads, for which
   // the chain from token to token is all: step_kernel with 8 columns a warp (one sequence of 64 tokens and 4 heads 20 us,
   // with 16 columns 32).  Else one token: step_token_kernel (64 sequences of 48 heads 60 us; step_kernel, with more
-  // registers, 70); a few, step_kernel (64 of 8: 115 us; step_block_kernel 157); from 12 on, if tokens times heads fill the
-  // SMs, step_block_kernel (64 of 16: 182 us against 204, 32 of 128: 533 against 796; but 16 of 16: 58 against 57, one of
-  // 64: 35 against 30).
+  // registers, 70); a few, step_kernel (64 of 8: 115 us; step_block_kernel 157); from 24 on, step_block_kernel, a CTA a
+  // head, unless they leave half of the SMs without one (3 of 48 heads, 16 tokens: 15 us against 14, 32: 22 against 24,
+  // 64: 36 against 44; one of 64: 34 against 28); from 12 on where warps are so many that only the work counts (64 of 16:
+  // 182 us against 204, 32 of 128: 533 against 796; but 16 of 16: 58 against 57).
   const int64_t heads = (int64_t)p->N * p->HV;
-  const bool blocks = heads > sm_count() / ST_FEW && p->T >= (int64_t)p->N * STB_MIN_TOKENS &&
-                      p->T * p->HV >= STB_MIN_WORK;
+  const bool blocks = heads > sm_count() / 2 &&
+                      (p->T >= (int64_t)p->N * STB_MIN_TOKENS ||
+                       (p->T >= (int64_t)p->N * STB_MIN_FULL && p->T * p->HV >= STB_FULL));
   if (heads * StepLayout<16>::PARTS > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   a.q = q;
   a.k = k;

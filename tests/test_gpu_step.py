@@ -352,3 +352,19 @@ def test_head_counts_around_the_kernels_choice(N, H, HV, dtype, kda):
         for n, end in enumerate(np.cumsum(lens)):
             slot_out[end - 1] = (n + 1) % (N + 2)
         check(x, run(x, kda, slot_in, slot_out, packed=True), slot_in, slot_out)
+
+
+@pytest.mark.parametrize("kda", [False, True])
+@pytest.mark.parametrize("H,HV,lens", [(16, 48, [24, 24]), (16, 48, [24, 23]), (13, 39, [30, 21]), (19, 38, [30, 21]),
+                                       (2, 4, [24] * 20), (8, 16, [0, 60, 1, 80, 4, 0]), (1, 1, [25] * 80)])
+def test_lengths_around_the_choice_of_blocks(H, HV, lens, kda):
+    """Lengths from which a CTA a head takes four tokens at a time, and heads for which it does: a state wanted within."""
+    T, N = sum(lens), len(lens)
+    x = make(lens, H, HV, N + 3, "bf16", kda, seed=T + HV)
+    slot_out = np.full(T, -1)
+    ends = np.cumsum(lens)
+    for n in range(N):
+        if lens[n]:
+            slot_out[ends[n] - 1] = n
+    slot_out[10:13] = [N, N + 1, N + 2]
+    check(x, run(x, kda, list(range(N)), slot_out), list(range(N)), slot_out)
