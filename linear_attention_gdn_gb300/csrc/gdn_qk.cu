@@ -6,7 +6,7 @@
 //   y[i] = r (x[i] (w[i] co[i]) + x[i'] (w[i'] si[i]))   (i' the partner of i),
 // a row costs one sum of squares, its partners and two multiply-adds a value.
 //
-// Fast kernel: bandwidth-bound, every value read and written once.  A row lies in L lanes of 8 values; a group of
+// Fast kernel: bandwidth-bound, every value read and written once.  A row lies in L lanes of 8 or 24 values; a group of
 // L lanes takes a token and walks its heads with the token's coefficients in registers, while the next rows
 // are on their way into the warp's ring in shared memory.  A warp stays with q or with k, and waits for no
 // other. Few tokens: their heads are split over warps.  PLAIN: a norm and the whole row rotated, which
@@ -23,24 +23,22 @@
 
 namespace gdn {
 
-template <typename E, int L, bool HALF, bool PLAIN>
+template <typename E, int L, int M, bool HALF, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   chain_kernel();
-  using R = Ring<E, L, 1>;
+  using R = Ring<E, L, 1, M>;
   constexpr int VEC = 16 / (int)sizeof(E);   // values of one copy
   __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
   E* slots = ring[threadIdx.x >> 5][0];
   const int l = threadIdx.x % L, mine = (threadIdx.x & 31) / L * R::ROW;
-  int off0, off1;
-  block_offsets<HALF>(a, l, &off0, &off1);
-  const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
-  const bool has = l < a.D / 8;
+  Pieces<L, M, HALF> piece;
+  piece.setup(a, l);
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
   const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
   const int units = which ? a.units[1] : a.units[0];
   const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
   const E* xbase = static_cast<const E*>(which ? a.x[1] : a.x[0]) + l * VEC;
-  E* ybase = static_cast<E*>(which ? a.out[1] : a.out[0]) + off0;
+  E* ybase = static_cast<E*>(which ? a.out[1] : a.out[0]);
   const int64_t xt = which ? a.xt[1] : a.xt[0], xh = which ? a.xh[1] : a.xh[0];
   const int64_t yt = which ? a.yt[1] : a.yt[0], yh = which ? a.yh[1] : a.yh[0];
   Place<L> at, to;   // of the work, and of the rows that are requested
@@ -49,12 +47,14 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   to.enter(a, splits, heads);
   at = to;
   int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead: its load is not waited for)
-  Angles<HALF, sizeof(E) == 2> ang;
+  Angles<L, M, HALF, sizeof(E) == 2> ang;
   ang.request(a, l);
-  float2 w[4];
-  lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
+  float2 w[M][4];
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+    piece_weights(which ? a.w[1] : a.w[0], piece.off[m], piece.away[m], piece.has[m], w[m]);
   const E* px = xbase + to.t * xt + to.h * xh;
-  const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine + off0);
+  const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine);
   int fill = 0, use = 0;   // byte offsets of slots
   bool more = true;
   const uint32_t landing = (uint32_t)__cvta_generic_to_shared(slots) + (mine + l * VEC) * (int)sizeof(E);
@@ -78,24 +78,25 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
     copies_commit();
     fill = R::next(fill);
   };
-  clear_ring<E, L, 1>(slots, a.D);
+  clear_ring<E, L, 1, M>(slots, a.D);
 #pragma unroll
   for (int i = 0; i < R::STAGES - 1; ++i) request();
 
   ang.setup();
   for (;;) {
-    float2 wc[4], ws[4];
-    {
+    float2 wc[M][4], ws[M][4];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
       float2 co[4], si[4];
-      ang.at(a, pos, l, co, si);
+      ang.at(a, pos, l, m, co, si);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        wc[j] = __fmul2_rn(w[j], co[j]);
-        ws[j] = __fmul2_rn(partner_of<HALF>(w, j), si[j]);
+        wc[m][j] = __fmul2_rn(w[m][j], co[j]);
+        ws[m][j] = __fmul2_rn(partner_of<HALF>(w[m], j), si[j]);
       }
     }
     E* y = ybase + at.t * yt + at.h * yh;
-    const bool keep = at.live && has;
+    const bool keep = at.live;
     const int rows = at.left;
     at.unit += warps;
     if (at.unit < units) {
@@ -106,23 +107,29 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
       copies_wait<R::STAGES - 2>();
       __syncwarp();   // every lane's share of this slot is there, and the last slot has been read by all
       request();      // into the last slot
-      float2 v[4], p[4];
-      read_row<E, HALF>(read + use, away, v);
+      float2 v[M][4];
+#pragma unroll
+      for (int m = 0; m < M; ++m) read_row<E, HALF>(read + use + piece.off[m] * (int)sizeof(E), piece.away[m], v[m]);
       use = R::next(use);
       float r = 1.f;
       if (PLAIN || a.normed) {
-        float2 s = __fmul2_rn(v[0], v[0]);
+        float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 1; j < 4; ++j) s = __ffma2_rn(v[j], v[j], s);
+        for (int j = 0; j < 4 * M; ++j)
+          s = j ? __ffma2_rn(v[j / 4][j % 4], v[j / 4][j % 4], s) : __fmul2_rn(v[0][0], v[0][0]);
         r = rsqrtf(fmaf(row_sum<L>(s.x + s.y), a.share, a.eps));
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = partner_of<HALF>(v, j);
-      if (!PLAIN) only_rotated(p, rotated);
+      for (int m = 0; m < M; ++m) {
+        float2 p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = __fmul2_rn(make_float2(r, r), __ffma2_rn(p[j], ws[j], __fmul2_rn(v[j], wc[j])));
-      if (keep) write_row<E, HALF>(y, away, v);
+        for (int j = 0; j < 4; ++j) p[j] = partner_of<HALF>(v[m], j);
+        if (!PLAIN) only_rotated(p, piece.rotated[m]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[m][j] = __fmul2_rn(make_float2(r, r), __ffma2_rn(p[j], ws[m][j], __fmul2_rn(v[m][j], wc[m][j])));
+        if (keep && piece.has[m]) write_row<E, HALF>(y + piece.off[m], piece.away[m], v[m]);
+      }
       y += yh;
     }
     if (at.unit >= units) return;
@@ -174,29 +181,33 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_row_kernel(const QkArgs a) 
   }
 }
 
-template <typename E, int L, bool HALF, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
-  static const int resident = resident_ctas(qk_fwd_kernel<E, L, HALF, PLAIN>);
+template <typename E, int L, int M, bool HALF, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_fwd_kernel<E, L, M, HALF, PLAIN>);
   const int ctas = divide_work(a, L, resident, 1);
-  launch_chained(qk_fwd_kernel<E, L, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
+  launch_chained(qk_fwd_kernel<E, L, M, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
 }
-template <typename E, int L> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
+template <typename E, int L, int M> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
   const bool plain = plain_rows(a);
-  if (a.half_layout && plain) launch_fwd_kernel<E, L, true, true>(a, s);
-  else if (a.half_layout) launch_fwd_kernel<E, L, true, false>(a, s);
-  else if (plain) launch_fwd_kernel<E, L, false, true>(a, s);
-  else launch_fwd_kernel<E, L, false, false>(a, s);
+  if (a.half_layout && plain) launch_fwd_kernel<E, L, M, true, true>(a, s);
+  else if (a.half_layout) launch_fwd_kernel<E, L, M, true, false>(a, s);
+  else if (plain) launch_fwd_kernel<E, L, M, false, true>(a, s);
+  else launch_fwd_kernel<E, L, M, false, false>(a, s);
 }
 template <typename E, int PER> static void launch_fwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_fwd_row_kernel<E, PER>);
   const int ctas = divide_work(a, 32, resident, 1);
   launch_chained(qk_fwd_row_kernel<E, PER>, ctas, QK_THREADS, 0, s, a);
 }
+// L and M by the row's length, and three_pieces
 template <typename E> static void launch_fwd(QkArgs& a, bool fast, cudaStream_t s) {
-  if (!fast && a.D <= 128) launch_fwd_any<E, 4>(a, s);
-  else if (!fast) launch_fwd_any<E, QK_MAXD / 32>(a, s);
-  else if (a.D <= 64) launch_fwd_rows<E, 8>(a, s);
-  else if (a.D <= 128) launch_fwd_rows<E, 16>(a, s);
-  else launch_fwd_rows<E, 32>(a, s);
+  if (!fast) return a.D <= 128 ? launch_fwd_any<E, 4>(a, s) : launch_fwd_any<E, QK_MAXD / 32>(a, s);
+  if constexpr (sizeof(E) == 2) {
+    if (three_pieces(a) && a.D > 64 && a.D <= 96) return launch_fwd_rows<E, 4, 3>(a, s);
+    if (three_pieces(a) && a.D > 128 && a.D <= 192) return launch_fwd_rows<E, 8, 3>(a, s);
+  }
+  if (a.D <= 64) return launch_fwd_rows<E, 8, 1>(a, s);
+  if (a.D <= 128) return launch_fwd_rows<E, 16, 1>(a, s);
+  launch_fwd_rows<E, 32, 1>(a, s);
 }
 
 // ---------------------------------------------------------------------------

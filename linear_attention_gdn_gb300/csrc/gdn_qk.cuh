@@ -16,7 +16,7 @@ namespace gdn {
 constexpr int QK_THREADS = 128;
 constexpr int QK_WARPS = QK_THREADS / 32;
 constexpr int QK_MAXD = 512;        // any layout
-constexpr int QK_FAST_MAXD = 256;   // rows of 8 values a lane
+constexpr int QK_FAST_MAXD = 256;   // rows of pieces of 8 values
 constexpr int QK_STEPS = 16;
 constexpr int QK_CTAS = 64;         // CTAs per SM of a grid that walks its work, at most
 
@@ -90,26 +90,34 @@ __device__ __forceinline__ int position_of(const QkArgs& a, int64_t t, int* doc)
 }
 
 // ---- rows of the fast kernels ----
-// A row lies in L lanes of 8 values, two blocks of 4. In the half layout a lane's blocks are partners, 4 values of the
-// first rotated half and the 4 they are turned with, so that no value crosses lanes; lanes past the rotated part, and all
-// lanes of the pairs layout, have 8 neighbouring values.  Either way pairs 4l .. 4l+3 are lane l's.
+// A row lies in pieces of 8 values, two blocks of 4: L lanes have M pieces each, the pieces l, l + L, .. of lane l.  In the
+// half layout a piece's blocks are partners, 4 values of the first rotated half and the 4 they are turned with, so that
+// no value crosses lanes; pieces past the rotated part, and all of the pairs layout, have 8 neighbouring values.  Either
+// way pairs 4i .. 4i+3 are piece i's.
 // Values are held as 4 float2: v[j] has the partner v[j ^ 2] (half), or its own other value (pairs).
-template <bool HALF> __device__ __forceinline__ void block_offsets(const QkArgs& a, int l, int* off0, int* off1) {
-  if (HALF && l < a.rot / 8) {
-    *off0 = 4 * l;
-    *off1 = a.rot / 2 + 4 * l;
-  } else {
-    *off0 = 8 * l;   // (rot is a multiple of 8 in the half layout: the lanes before hold rot values)
-    *off1 = 8 * l + 4;
+template <int L, int M, bool HALF> struct Pieces {
+  int off[M], away[M];   // of the first block, and from there to the second
+  int rotated[M];        // how many of the 8 values are (0 or 8 in the half layout)
+  bool has[M];           // the row is so long
+  __device__ __forceinline__ void setup(const QkArgs& a, int l) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int i = l + m * L;
+      const bool apart = HALF && i < a.rot / 8;
+      off[m] = apart ? 4 * i : 8 * i;   // (rot is a multiple of 8 in the half layout: the pieces before hold rot values)
+      away[m] = apart ? a.rot / 2 : 4;
+      rotated[m] = HALF ? (apart ? 8 : 0) : a.rot - 8 * i;
+      has[m] = i < a.D / 8;
+    }
   }
-}
+};
 
 template <typename E> __device__ __forceinline__ float2 pair_at(const uint32_t* u, int j) {
   if constexpr (sizeof(E) == 4) return make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
   else return pair_f32(u[j], (const E*)nullptr);
 }
 
-// a lane's 8 values of a row in shared memory: `at` its first block, `away` elements from there its second
+// a piece of a row in shared memory: `at` its first block, `away` elements from there its second
 template <typename E, bool HALF>
 __device__ __forceinline__ void read_row(uint32_t at, int away, float2 (&v)[4]) {
   RawV<E, 4> b[2];
@@ -150,18 +158,18 @@ __device__ __forceinline__ void write_row(E* p, int away, const float2 (&v)[4]) 
 
 // Rows on their way to a warp: a ring of STAGES slots of its own shared memory, each the 32 / L rows of one step of
 // the warp (of N tensors). The warp's lanes copy 16 bytes at a time, so that the bytes in flight cost no registers.
-template <typename E, int L, int N> struct Ring {
-  static constexpr int CHUNKS = (int)sizeof(E) / 2;              // 16-byte chunks a lane copies of a row
-  static constexpr int ROW = 8 * L;                              // values a row has room for
+template <typename E, int L, int N, int M> struct Ring {
+  static constexpr int CHUNKS = M * (int)sizeof(E) / 2;          // 16-byte chunks a lane copies of a row
+  static constexpr int ROW = 8 * L * M;                              // values a row has room for
   static constexpr int ROWS = 32 / L;
   static constexpr int SLOT = N * ROWS * ROW;                    // values
   static constexpr int BYTES = SLOT * (int)sizeof(E);
   static __device__ __forceinline__ int next(int at) { return at + BYTES == STAGES * BYTES ? 0 : at + BYTES; }
-  static constexpr int STAGES = N * CHUNKS == 1 ? 8 : N * CHUNKS == 2 ? 6 : 4;
+  static constexpr int STAGES = N * CHUNKS == 1 ? 8 : N * CHUNKS == 2 ? 6 : N * CHUNKS < 6 ? 4 : 3;
 };
 // Values of a row past D are never copied, and are zero from the start.
-template <typename E, int L, int N> __device__ __forceinline__ void clear_ring(E* slots, int D) {
-  using R = Ring<E, L, N>;
+template <typename E, int L, int N, int M> __device__ __forceinline__ void clear_ring(E* slots, int D) {
+  using R = Ring<E, L, N, M>;
   if (D == R::ROW) return;
   for (int i = threadIdx.x & 31; i < R::STAGES * R::SLOT / R::ROW * (R::ROW - D); i += 32) {
     const int row = i / (R::ROW - D);
@@ -181,33 +189,37 @@ template <bool HALF> __device__ __forceinline__ float2 partner_of(const float2 (
   return HALF ? v[j ^ 2] : make_float2(v[j].y, v[j].x);
 }
 // v with zeros where nothing is rotated: an infinite value's neighbour must not take part, not even times a
-// zero sine.  rotated: how many of the lane's 8 values are (0 or 8 in the half layout)
+// zero sine.  rotated: as in Pieces
 __device__ __forceinline__ void only_rotated(float2 (&v)[4], int rotated) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (2 * j >= rotated) v[j] = make_float2(0.f, 0.f);
 }
 
-// A lane's four pairs: their turn steps, and cos and sin at a token laid out like the lane's values,
+// A lane's pairs, four a piece: their turn steps, and cos and sin at a token laid out like the lane's values,
 // y[j] = v[j] co[j] + partner[j] si[j].  Pairs past the rotated part get the identity.
-template <bool HALF, bool FAST> struct Angles {
-  uint64_t step[4];
-  double f[4];
+template <int L, int M, bool HALF, bool FAST> struct Angles {
+  uint64_t step[M][4];
+  double f[M][4];
   // the frequencies are requested first, and converted when the rows' copies are on their way
   __device__ __forceinline__ void request(const QkArgs& a, int l) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = 4 * l + i < a.rot / 2 ? a.freq[4 * l + i] : 0.0;
+    for (int i = 0; i < 4 * M; ++i) {
+      const int p = 4 * (l + i / 4 * L) + i % 4;
+      f[i / 4][i % 4] = p < a.rot / 2 ? a.freq[p] : 0.0;
+    }
   }
   __device__ __forceinline__ void setup() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) step[i] = turn_step(f[i]);
+    for (int i = 0; i < 4 * M; ++i) step[i / 4][i % 4] = turn_step(f[i / 4][i % 4]);
   }
-  __device__ __forceinline__ void at(const QkArgs& a, int pos, int l, float2 (&co)[4], float2 (&si)[4]) {
+  // of piece m
+  __device__ __forceinline__ void at(const QkArgs& a, int pos, int l, int m, float2 (&co)[4], float2 (&si)[4]) {
     float c[4], s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      angle_cos_sin<FAST>(step[i], pos, a.mscale, &c[i], &s[i]);
-      if (4 * l + i >= a.rot / 2) {
+      angle_cos_sin<FAST>(step[m][i], pos, a.mscale, &c[i], &s[i]);
+      if (4 * (l + m * L) + i >= a.rot / 2) {
         c[i] = 1.f;
         s[i] = 0.f;
       }
@@ -249,11 +261,11 @@ template <int L> struct Place {
   }
 };
 
-// The weights of a lane's 8 values (zeros where it has none)
-__device__ __forceinline__ void lane_weights(const float* w, int off0, int off1, bool has, float2 (&v)[4]) {
+// The weights of a piece (zeros where there is none)
+__device__ __forceinline__ void piece_weights(const float* w, int off, int away, bool has, float2 (&v)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int d = (j < 2 ? off0 : off1) + (j & 1) * 2;
+    const int d = off + (j < 2 ? 0 : away) + (j & 1) * 2;
     v[j] = !has ? make_float2(0.f, 0.f) : w ? make_float2(w[d], w[d + 1]) : make_float2(1.f, 1.f);
   }
 }
@@ -300,6 +312,12 @@ template <int PER> __device__ __forceinline__ void row_weights(const float* w, i
 
 // rows without masks: normed and rotated whole
 inline bool plain_rows(const QkArgs& a) { return a.normed && a.rot == a.D; }
+
+// 16-bit rows of 9 .. 12 and of 17 .. 24 pieces, which would leave up to half of 16 or 32 lanes without any, lie in 4 and 8 lanes
+// of three: their kernels would be bound by instructions (100,000 tokens of 16 + 4 heads of 96: forward 120 us, with one
+// piece a lane 149, backward 191 and 230; FP32 rows reach the copy rate as they are).  Not so a few rows, for which a
+// lane's own work is all (one token 3.05 and 2.64 us; 64: 3.17 and 3.16; 300: 3.79 and 4.90).
+inline bool three_pieces(const QkArgs& a) { return a.T * (a.heads[0] + a.heads[1]) >= 8 * sm_count(); }
 
 // Divides the work: runs of heads as long as the warps that the GPU holds at once (`resident` CTAs an SM) get `least`
 // units each; then a whole number of such rounds of CTAs, so that SMs that are ahead take more of them (262,144

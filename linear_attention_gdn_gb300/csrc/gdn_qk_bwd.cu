@@ -12,43 +12,43 @@
 
 namespace gdn {
 
-template <typename E, int L, bool HALF, bool PLAIN>
+template <typename E, int L, int M, bool HALF, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   chain_kernel();
-  using R = Ring<E, L, 2>;
+  using R = Ring<E, L, 2, M>;
   constexpr int VEC = 16 / (int)sizeof(E);
   __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
   E* slots = ring[threadIdx.x >> 5][0];
   const int l = threadIdx.x % L, mine = (threadIdx.x & 31) / L * R::ROW;
-  int off0, off1;
-  block_offsets<HALF>(a, l, &off0, &off1);
-  const int away = off1 - off0, rotated = HALF ? (l < a.rot / 8 ? 8 : 0) : a.rot - 8 * l;
-  const bool has = l < a.D / 8;
+  Pieces<L, M, HALF> piece;
+  piece.setup(a, l);
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
   const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
   const int units = which ? a.units[1] : a.units[0];
   const int splits = which ? a.splits[1] : a.splits[0], heads = which ? a.heads[1] : a.heads[0];
   const E* xbase = static_cast<const E*>(which ? a.x[1] : a.x[0]) + l * VEC;
   const E* gbase = static_cast<const E*>(which ? a.in[1] : a.in[0]) + l * VEC;
-  E* dbase = static_cast<E*>(which ? a.out[1] : a.out[0]) + off0;
+  E* dbase = static_cast<E*>(which ? a.out[1] : a.out[0]);
   const int64_t xt = which ? a.xt[1] : a.xt[0], xh = which ? a.xh[1] : a.xh[0];
   const int64_t yt = which ? a.yt[1] : a.yt[0], yh = which ? a.yh[1] : a.yh[0];
-  float2 acc[4];
+  float2 acc[M][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = make_float2(0.f, 0.f);
+  for (int j = 0; j < 4 * M; ++j) acc[j / 4][j % 4] = make_float2(0.f, 0.f);
   Place<L> at, to;
   at.unit = to.unit = cta * QK_WARPS + (threadIdx.x >> 5);
   if (at.unit < units) {
     to.enter(a, splits, heads);
     at = to;
     int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead)
-    Angles<HALF, sizeof(E) == 2> ang;
+    Angles<L, M, HALF, sizeof(E) == 2> ang;
     ang.request(a, l);
-    float2 w[4];
-    lane_weights(which ? a.w[1] : a.w[0], off0, off1, has, w);
+    float2 w[M][4];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      piece_weights(which ? a.w[1] : a.w[0], piece.off[m], piece.away[m], piece.has[m], w[m]);
     const E* px = xbase + to.t * xt + to.h * xh;
     const E* pg = gbase + to.t * yt + to.h * yh;
-    const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine + off0);
+    const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine);
     int fill = 0, use = 0;   // byte offsets of slots
     bool more = true;
     const uint32_t landing = (uint32_t)__cvta_generic_to_shared(slots) + (mine + l * VEC) * (int)sizeof(E);
@@ -75,16 +75,17 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
       copies_commit();
       fill = R::next(fill);
     };
-    clear_ring<E, L, 2>(slots, a.D);
+    clear_ring<E, L, 2, M>(slots, a.D);
 #pragma unroll
     for (int i = 0; i < R::STAGES - 1; ++i) request();
 
     ang.setup();
     do {
-      float2 co[4], si[4];
-      ang.at(a, pos, l, co, si);
+      float2 co[M][4], si[M][4];
+#pragma unroll
+      for (int m = 0; m < M; ++m) ang.at(a, pos, l, m, co[m], si[m]);
       E* dx = dbase + at.t * xt + at.h * xh;
-      const bool live = at.live, keep = live && has;
+      const bool live = at.live;
       const int rows = at.left;
       at.unit += warps;
       if (at.unit < units) {
@@ -95,26 +96,32 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
         copies_wait<R::STAGES - 2>();
         __syncwarp();
         request();
-        float2 v[4], g[4], p[4];
-        const uint32_t s0 = read + use;
-        read_row<E, HALF>(s0, away, v);
-        read_row<E, HALF>(s0 + R::BYTES / 2, away, g);
-        use = R::next(use);
-        // turned back: by the opposite sine
+        float2 v[M][4], g[M][4], gv[M][4];
+        float2 s = make_float2(0.f, 0.f), d = s;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 o = partner_of<HALF>(g, j);
-          p[j] = make_float2(-o.x, -o.y);
+        for (int m = 0; m < M; ++m) {
+          const uint32_t from = read + use + piece.off[m] * (int)sizeof(E);
+          read_row<E, HALF>(from, piece.away[m], v[m]);
+          read_row<E, HALF>(from + R::BYTES / 2, piece.away[m], g[m]);
         }
-        if (!PLAIN) only_rotated(p, rotated);
+        use = R::next(use);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = __ffma2_rn(p[j], si[j], __fmul2_rn(g[j], co[j]));
-        float2 s = __fmul2_rn(v[0], v[0]), d = make_float2(0.f, 0.f), gv[4];
+        for (int m = 0; m < M; ++m) {
+          // turned back: by the opposite sine
+          float2 p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j) s = __ffma2_rn(v[j], v[j], s);
-          gv[j] = __fmul2_rn(g[j], v[j]);
-          d = __ffma2_rn(gv[j], w[j], d);
+          for (int j = 0; j < 4; ++j) {
+            const float2 o = partner_of<HALF>(g[m], j);
+            p[j] = make_float2(-o.x, -o.y);
+          }
+          if (!PLAIN) only_rotated(p, piece.rotated[m]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            g[m][j] = __ffma2_rn(p[j], si[m][j], __fmul2_rn(g[m][j], co[m][j]));
+            s = m + j ? __ffma2_rn(v[m][j], v[m][j], s) : __fmul2_rn(v[m][j], v[m][j]);
+            gv[m][j] = __fmul2_rn(g[m][j], v[m][j]);
+            d = __ffma2_rn(gv[m][j], w[m][j], d);
+          }
         }
         float r = 1.f, f = 0.f;
         if (PLAIN || a.normed) {
@@ -124,27 +131,32 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
         const float2 rr = make_float2(r, r), ff = make_float2(f, f);
         if (live) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = __ffma2_rn(gv[j], rr, acc[j]);
+          for (int j = 0; j < 4 * M; ++j) acc[j / 4][j % 4] = __ffma2_rn(gv[j / 4][j % 4], rr, acc[j / 4][j % 4]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = __fmul2_rn(__fmul2_rn(g[j], w[j]), rr);
-          v[j] = PLAIN || a.normed ? __ffma2_rn(v[j], ff, x) : x;
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = __fmul2_rn(__fmul2_rn(g[m][j], w[m][j]), rr);
+            v[m][j] = PLAIN || a.normed ? __ffma2_rn(v[m][j], ff, x) : x;
+          }
+          if (live && piece.has[m]) write_row<E, HALF>(dx + piece.off[m], piece.away[m], v[m]);
         }
-        if (keep) write_row<E, HALF>(dx, away, v);
         dx += xh;
       }
     } while (at.unit < units);
   }
   if (!a.part) return;
   constexpr int GROUPS = QK_THREADS / L;
-  __shared__ float sums[GROUPS][L * 8];
+  __shared__ float sums[GROUPS][L * M * 8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int d = (j < 2 ? off0 : off1) + (j & 1) * 2;   // (below L * 8 in lanes without values, too)
-    sums[threadIdx.x / L][d] = acc[j].x;
-    sums[threadIdx.x / L][d + 1] = acc[j].y;
-  }
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // (places below L * M * 8 in lanes without values, too)
+      const int d = piece.off[m] + (j < 2 ? 0 : piece.away[m]) + (j & 1) * 2;
+      sums[threadIdx.x / L][d] = acc[m][j].x;
+      sums[threadIdx.x / L][d + 1] = acc[m][j].y;
+    }
   __syncthreads();
   for (int d = threadIdx.x; d < a.D; d += QK_THREADS) {
     float s = 0.f;
@@ -248,18 +260,18 @@ __global__ void __launch_bounds__(DW_COLS * DW_ROWS) qk_dw_kernel(const float* p
   }
 }
 
-template <typename E, int L, bool HALF, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
-  static const int resident = resident_ctas(qk_bwd_kernel<E, L, HALF, PLAIN>);
+template <typename E, int L, int M, bool HALF, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_bwd_kernel<E, L, M, HALF, PLAIN>);
   const int ctas = divide_work(a, L, resident, 2);
-  launch_chained(qk_bwd_kernel<E, L, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
+  launch_chained(qk_bwd_kernel<E, L, M, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
   return ctas;
 }
-template <typename E, int L> static int launch_bwd_rows(QkArgs& a, cudaStream_t s) {
+template <typename E, int L, int M> static int launch_bwd_rows(QkArgs& a, cudaStream_t s) {
   const bool plain = plain_rows(a);
-  if (a.half_layout && plain) return launch_bwd_kernel<E, L, true, true>(a, s);
-  if (a.half_layout) return launch_bwd_kernel<E, L, true, false>(a, s);
-  if (plain) return launch_bwd_kernel<E, L, false, true>(a, s);
-  return launch_bwd_kernel<E, L, false, false>(a, s);
+  if (a.half_layout && plain) return launch_bwd_kernel<E, L, M, true, true>(a, s);
+  if (a.half_layout) return launch_bwd_kernel<E, L, M, true, false>(a, s);
+  if (plain) return launch_bwd_kernel<E, L, M, false, true>(a, s);
+  return launch_bwd_kernel<E, L, M, false, false>(a, s);
 }
 template <typename E, int PER> static int launch_bwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_bwd_row_kernel<E, PER>);
@@ -267,12 +279,16 @@ template <typename E, int PER> static int launch_bwd_any(QkArgs& a, cudaStream_t
   launch_chained(qk_bwd_row_kernel<E, PER>, ctas, QK_THREADS, 0, s, a);
   return ctas;
 }
-// returns the CTAs, each of which has left partial sums
+// returns the CTAs, each of which has left partial sums (L and M by the row's length, and three_pieces)
 template <typename E> static int launch_bwd(QkArgs& a, bool fast, cudaStream_t s) {
   if (!fast) return a.D <= 128 ? launch_bwd_any<E, 4>(a, s) : launch_bwd_any<E, QK_MAXD / 32>(a, s);
-  if (a.D <= 64) return launch_bwd_rows<E, 8>(a, s);
-  if (a.D <= 128) return launch_bwd_rows<E, 16>(a, s);
-  return launch_bwd_rows<E, 32>(a, s);
+  if constexpr (sizeof(E) == 2) {
+    if (three_pieces(a) && a.D > 64 && a.D <= 96) return launch_bwd_rows<E, 4, 3>(a, s);
+    if (three_pieces(a) && a.D > 128 && a.D <= 192) return launch_bwd_rows<E, 8, 3>(a, s);
+  }
+  if (a.D <= 64) return launch_bwd_rows<E, 8, 1>(a, s);
+  if (a.D <= 128) return launch_bwd_rows<E, 16, 1>(a, s);
+  return launch_bwd_rows<E, 32, 1>(a, s);
 }
 
 void launch_qk_bwd(QkArgs& a, int dtype, bool fast, float* dwq, float* dwk, cudaStream_t s) {

@@ -197,3 +197,45 @@ def test_offsets_past_32_bits():
     gdn.gdn_qk_norm_rope_fwd(prob, q, k, part["wq"].cuda(), part["wk"].cuda(), f, pos, None, q, k)
     want = run(part, freqs(128), 128)
     assert torch.equal(q[-64:], want[0]) and torch.equal(k[-64:], want[1])
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("dtype,D,rot,norm", [("bf16", 72, 72, "rms"), ("bf16", 80, 80, "l2"), ("fp16", 88, 24, "rms"),
+                                              ("bf16", 96, 96, "rms"), ("fp16", 96, 8, "none"), ("bf16", 96, 0, "rms"),
+                                              ("bf16", 136, 136, "rms"), ("fp16", 160, 40, "l2"),
+                                              ("bf16", 192, 192, "rms"), ("bf16", 184, 96, "none")])
+def test_rows_of_three_pieces_a_lane(dtype, D, rot, norm, layout):
+    """Head sizes between powers of two, in enough rows: padded ones, also in place."""
+    x = make(211, 5, 2, D, dtype, seed=D + rot)
+    kw = dict(rot=rot, layout=layout, norm=norm, pad=8, pos=[7 * i - 3 for i in range(211)], m=1.1)
+    want = run(x, freqs(rot), **kw)
+    check(x, want, freqs(rot), **kw)
+    got = run(x, freqs(rot), in_place=True, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [1, 8, 100, 200])
+@pytest.mark.parametrize("D", [96, 192])
+def test_rows_around_the_choice_of_pieces(T, D):
+    x = make(T, 9, 3, D, "fp16", seed=T)
+    check(x, run(x, freqs(48), 48), freqs(48), 48)
+
+
+@pytest.mark.parametrize("D,rot,layout", [(80, 80, "half"), (96, 48, "pairs"), (192, 96, "half")])
+def test_many_rows_of_three_pieces_a_lane(D, rot, layout):
+    x = make(6007, 7, 1, D, "bf16", seed=D)
+    kw = dict(rot=rot, layout=layout, cu=[0, 1000, 1000, 6007])
+    check(x, run(x, freqs(rot), **kw), freqs(rot), **kw)
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("D", [96, 192])
+def test_infinities_stay_in_their_values_of_three_pieces(layout, D):
+    rot = D // 2
+    x = make(1500, 1, 1, D, "bf16", seed=8)
+    x["q"][0, 0, D - 9], x["q"][0, 0, D - 1], x["q"][1, 0, 3] = float("inf"), float("nan"), float("inf")
+    y = run(x, freqs(rot), rot, layout=layout, norm="none")[0]
+    bad = torch.zeros(1500, 1, D, dtype=torch.bool)
+    bad[0, 0, D - 9] = bad[0, 0, D - 1] = bad[1, 0, 3] = True
+    bad[1, 0, 3 + rot // 2 if layout == "half" else 2] = True
+    assert torch.equal(torch.isfinite(y.cpu()), ~bad)
