@@ -3,17 +3,18 @@
 //   z[t, c] = b[c] + sum_i w[c, i] row(t - (W-1) + i)[c],  y = z sigma(z)
 // with row(s) the token s of the sequence, or its window's row before the first token.
 //
-// Bandwidth-bound.  Two kernels:
+// Bandwidth-bound.  Three ways:
 //   - one token each (no cu_seqlens): a thread owns two channels and takes the sequences gridDim.y apart, its
 //     taps in registers.  All that does not hang on the slot is requested at once, so that a call is two
 //     loads deep;
+//   - short sequences among any: a thread owns four channels of one sequence, and asks for four tokens at a time;
 //   - any lengths: a thread owns four channels and walks a range of tokens with the last W-1 rows in registers,
 //     the next rows on their way into shared memory (each thread copies what it reads, so no thread waits
 //     for another).
 //
 // Long sequences are cut over CTAs, and a slot may be read and written by the same call, so whatever
 // reads or writes a sequence's slots is done by one CTA per channel block, the one whose range holds its first
-// token: it also computes the first W-1 tokens, which need the window (past its range's end if they lie
+// token (a short one's own CTA): it also computes the first W-1 tokens, which need the window (past its range's end if they lie
 // there), and writes the windows of all the sequence's tokens from its own copy of the old window and x.
 #include <cuda_runtime.h>
 
@@ -33,6 +34,9 @@ constexpr int CS_THREADS1 = 128;  // of a CTA of the kernel for single tokens
 constexpr int CS_VEC = 4;         // channels per thread, and of the kernel for single tokens:
 constexpr int CS_VEC1 = 2;
 constexpr int CS_STAGES = 16;     // rows of a thread on their way
+constexpr int CS_FEW = 4;         // tokens of a short sequence that a thread has in registers
+constexpr int CS_SHORT = 16;      // tokens up to which a sequence of many is a thread's own
+constexpr int CS_MEAN = 8;        // where the mean is no more than so many
 constexpr int CS_LOOK = 4;        // slot numbers a lane has requested together
 constexpr int CS_ROUND = 7;       // CTAs an SM holds
 constexpr int CS_ROUND1 = 12;     // and of the kernel for single tokens
@@ -201,16 +205,80 @@ __global__ void __launch_bounds__(CS_THREADS1) conv_token_kernel(const ConvStepA
   }
 }
 
-template <typename E, int W>
-__global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArgs a) {
+// A short sequence: a thread takes CS_FEW tokens at a time, their rows and slots requested together.
+template <typename E, int W> __device__ __forceinline__ void short_sequence(const ConvStepArgs& a, int n, int c0) {
+  constexpr int V = CS_VEC, H = W - 1;
+  const E* x = static_cast<const E*>(a.x) + c0;
+  E* y = static_cast<E*>(a.y) + c0;
+  E* win = static_cast<E*>(a.window) + c0;
+  const int64_t win_slot = (int64_t)H * a.C;
+  const int t0 = a.cu[n], t1 = a.cu[n + 1], from = a.slot_in ? a.slot_in[n] : n;
+  Taps<W, V> k;
+  k.load(a, c0);
+  if (t0 < 0 || t1 < t0 || t1 > a.T) {
+    *a.err = ST_DEVICE;
+    return;
+  }
+  if (t0 == t1 || t1 - t0 > CS_SHORT) return;
+  if (from < -1 || from >= a.slots) {
+    *a.err = ST_DEVICE;
+    return;
+  }
+  RawV<E, V> row[H + CS_FEW];   // the rows before the first token, and the tokens'
+  float2 hist[W > 1 ? H : 1][V / 2];
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    if (from >= 0) row[i].load(win + from * win_slot + (int64_t)i * a.C);
+    else row[i].zero();
+  }
+  for (int t = t0; t < t1; t += CS_FEW) {
+    int to[CS_FEW];
+#pragma unroll
+    for (int i = 0; i < CS_FEW; ++i) {
+      to[i] = -1;
+      if (t + i >= t1) continue;
+      row[H + i].load(x + (int64_t)(t + i) * a.xs);
+      to[i] = a.slot_out ? a.slot_out[t + i] : t + i == t1 - 1 ? from : -1;
+    }
+    if (t == t0) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) as_pairs(row[i], hist[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CS_FEW; ++i) {
+      if (t + i >= t1) break;
+      conv_row<E, W, V>(k, row[H + i], hist).store(y + (int64_t)(t + i) * a.ys);
+      if (W == 1 || to[i] == -1) continue;
+      if (to[i] < -1 || to[i] >= a.slots) {
+        *a.err = ST_DEVICE;
+        continue;
+      }
+#pragma unroll
+      for (int j = 0; j < H; ++j) row[i + 1 + j].store(win + to[i] * win_slot + (int64_t)j * a.C);
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) row[i] = row[CS_FEW + i];
+  }
+}
+
+// MIXED: many sequences with few tokens on average.  The first a.N rows of CTAs take a sequence each if it is
+// short, the others ranges of tokens, of which they leave those out. (The ranges first: 64 sequences of 8 tokens 8.9 us
+// for 8.2, but 63 of one token and one of 400 7.7 for 9.5.)
+template <typename E, int W, bool MIXED>
+__global__ void __launch_bounds__(CS_THREADS, !MIXED ? 0 : sizeof(E) == 2 ? 6 : 4) conv_step_kernel(const ConvStepArgs a) {
   chain_kernel();
   constexpr int V = CS_VEC, H = W > 1 ? W - 1 : 1, BYTES = V * (int)sizeof(E);
+  if (MIXED && blockIdx.y < a.N) {
+    const int c = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
+    if (c < a.C) short_sequence<E, W>(a, blockIdx.y, c);
+    return;
+  }
   __shared__ __align__(16) uint8_t ring[CS_STAGES][CS_THREADS * BYTES];
   const int lane = threadIdx.x & 31;
   const int ch = (blockIdx.x * CS_THREADS + threadIdx.x) * V;
   const int c0 = min(ch, a.C - V);   // (threads past the last channel stay for the warps' votes, and store nothing)
   const bool live = ch < a.C;
-  const int lo = blockIdx.y * a.R, hi = min(lo + a.R, a.T);
+  const int lo = (blockIdx.y - (MIXED ? a.N : 0)) * a.R, hi = min(lo + a.R, a.T);
   const E* x = static_cast<const E*>(a.x) + c0;
   E* y = static_cast<E*>(a.y) + c0;
   E* win = static_cast<E*>(a.window) + c0;
@@ -218,6 +286,18 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
   Taps<W, V> k;
   k.load(a, c0);
   int n = a.cu ? sequence_of(a.cu, a.N, lo) : lo;
+  // the next sequence from m on that begins before hi and is not short
+  auto next_long = [&](int m) {
+    for (; m < a.N; m += 32) {
+      const bool in = m + lane < a.N;
+      const int s = in ? a.cu[m + lane] : 0, e = in ? a.cu[m + lane + 1] : 0;
+      const unsigned past = __ballot_sync(~0u, !in || s >= hi);
+      const unsigned found = __ballot_sync(~0u, in && s < hi && e > s + CS_SHORT) & (past ? (past & -past) - 1 : ~0u);
+      if (found) return m + __ffs(found) - 1;
+      if (past) break;
+    }
+    return a.N;
+  };
 
   // sequence n's tokens [t0, t1); one with bad bounds has none
   int t0, t1, from;
@@ -236,7 +316,13 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
   enter();
   // The rows come in order from the first token on, whoever's they are; the last may be the first W-1
   // tokens of a sequence that begins at the range's end.
-  int t = t0 < lo ? max(lo, min(t0 + W - 1, t1)) : lo;
+  if (MIXED && t1 - t0 <= CS_SHORT) {   // (its CTA has reported what is wrong with it)
+    if (t0 < lo && t1 >= hi) return;
+    n = next_long(n);
+    if (n == a.N) return;
+    enter();
+  }
+  int t = t0 < lo ? max(lo, min(t0 + W - 1, t1)) : MIXED ? max(t0, lo) : lo;
   const int stop = min(hi + W - 1, a.T);
   const uint32_t landing = (uint32_t)__cvta_generic_to_shared(&ring[0][threadIdx.x * BYTES]);
   const E* px = x + (int64_t)t * a.xs;
@@ -296,7 +382,8 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
     if (t1 >= hi) return;
     ++n;
   }
-  for (; n < a.N; ++n) {   // the sequences that begin in this range
+  if (MIXED) n = next_long(n);
+  for (; n < a.N; n = MIXED ? next_long(n + 1) : n + 1) {   // the sequences that begin in this range
     enter();
     if (t0 >= hi) return;
     if (t0 == t1 || t0 < lo || skip) continue;
@@ -342,17 +429,18 @@ __global__ void __launch_bounds__(CS_THREADS) conv_step_kernel(const ConvStepArg
   }
 }
 
-template <typename E, int W> static void launch_conv_step(const ConvStepArgs& a, dim3 grid, cudaStream_t s) {
-  if (a.cu) launch_chained(conv_step_kernel<E, W>, grid, CS_THREADS, 0, s, a);
+template <typename E, int W> static void launch_conv_step(const ConvStepArgs& a, bool mixed, dim3 grid, cudaStream_t s) {
+  if (a.cu && mixed) launch_chained(conv_step_kernel<E, W, true>, grid, CS_THREADS, 0, s, a);
+  else if (a.cu) launch_chained(conv_step_kernel<E, W, false>, grid, CS_THREADS, 0, s, a);
   else if (a.R == 1) launch_chained(conv_token_kernel<E, W, 1>, grid, CS_THREADS1, 0, s, a);
   else launch_chained(conv_token_kernel<E, W, 2>, grid, CS_THREADS1, 0, s, a);
 }
-template <typename E> static void launch_conv_step(const ConvStepArgs& a, int W, dim3 grid, cudaStream_t s) {
+template <typename E> static void launch_conv_step(const ConvStepArgs& a, int W, bool mixed, dim3 grid, cudaStream_t s) {
   switch (W) {
-    case 1: launch_conv_step<E, 1>(a, grid, s); break;
-    case 2: launch_conv_step<E, 2>(a, grid, s); break;
-    case 3: launch_conv_step<E, 3>(a, grid, s); break;
-    default: launch_conv_step<E, 4>(a, grid, s); break;
+    case 1: launch_conv_step<E, 1>(a, mixed, grid, s); break;
+    case 2: launch_conv_step<E, 2>(a, mixed, grid, s); break;
+    case 3: launch_conv_step<E, 3>(a, mixed, grid, s); break;
+    default: launch_conv_step<E, 4>(a, mixed, grid, s); break;
   }
 }
 
@@ -398,13 +486,18 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   a.slots = p->slots;
   const int per_cta = cu_dev ? CS_THREADS * CS_VEC : CS_THREADS1 * CS_VEC1;
   const int cols = (p->C + per_cta - 1) / per_cta;
+  // Few tokens a sequence on average: short sequences apart from the ranges (10,240 channels, 64 of 1-4 tokens: 5.8 us against
+  // 8.6; 63 of one and one of 400: 9.5 against 19.0; 64 of 8: 8.2 against 10.1; but 256 of 8: 26.2 against 26.3, 256 of
+  // 16: 46 against 45, 64 of 20: 17 against 14).  32,768 of them and the ranges of their tokens fit grid.y.
+  const bool mixed = cu_dev && p->N <= 32768 && p->T <= (int64_t)p->N * CS_MEAN;
   int64_t rows;
   if (cu_dev) {
     // one round of CTAs, whose start is most of their time while ranges are short, or several of longer ones (29
     // sequences of up to 106 tokens: one round of 24 tokens 14 us, four of 6 23 us)
     const int64_t round = std::max<int64_t>(1, (int64_t)sm_count() * CS_ROUND / cols), one = (p->T + round - 1) / round;
     a.R = (int)(one <= CS_LONG ? one : std::min<int64_t>(CS_MAXR, std::max<int64_t>(CS_LONG, (one + 3) / 4)));
-    rows = (p->T + a.R - 1) / a.R;
+    if (mixed) a.R = std::max(a.R, CS_SHORT);
+    rows = (p->T + a.R - 1) / a.R + (mixed ? p->N : 0);
   } else {
     // one sequence a CTA column while the GPU holds them all, then two (64 of 10,240 channels: 4.1 us with one, 3.2
     // with two), side by side as far as they give an SM 32 CTAs
@@ -415,9 +508,9 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   const dim3 grid(cols, (unsigned)rows);
   prof_begin(K_CONV_STEP, stream);
   switch (p->dtype) {
-    case GDN_BF16: launch_conv_step<__nv_bfloat16>(a, p->W, grid, stream); break;
-    case GDN_FP16: launch_conv_step<__half>(a, p->W, grid, stream); break;
-    default: launch_conv_step<float>(a, p->W, grid, stream); break;
+    case GDN_BF16: launch_conv_step<__nv_bfloat16>(a, p->W, mixed, grid, stream); break;
+    case GDN_FP16: launch_conv_step<__half>(a, p->W, mixed, grid, stream); break;
+    default: launch_conv_step<float>(a, p->W, mixed, grid, stream); break;
   }
   prof_end(K_CONV_STEP, stream);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

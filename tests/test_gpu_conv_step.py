@@ -155,3 +155,64 @@ def test_more_single_tokens_than_the_gpu_holds(N, W):
     y, win, status = run(x, list(bad), list(slot_out), cu=None)
     good = run(x, list(slot_in), list(slot_out), cu=None)
     assert status == 7 and torch.equal(y[:N - 1], good[0][:N - 1])
+
+
+@pytest.mark.parametrize("dtype,W,C", [("bf16", 4, 1032), ("fp16", 3, 520), ("fp32", 2, 64), ("fp32", 4, 520), ("bf16", 1, 8)])
+def test_short_sequences_among_long_ones(dtype, W, C):
+    """Few tokens on average: sequences around the length up to which they are taken apart from the long ones' ranges, long ones
+    in a row, at the start, across several ranges and at the end; in place, from nowhere and to nowhere."""
+    rng = np.random.default_rng(C + W)
+    for lens in ([17, 16, 15, 0] + [1] * 60 + [300, 31, 0, 33] + [2, 4, 3, 1] * 10, [1] * 100 + [400], [18] + [0] * 3,
+                 [1, 0, 40, 41, 0, 1] + [1] * 34):
+        N = len(lens)
+        x = make(lens, C, W, N + 4, dtype, seed=N)
+        order = rng.permutation(N + 4)[:N]
+        out = last_slots(lens, order)
+        check(x, run(x, list(order), out, pad=8), order, out)
+        slot_in = order.copy()
+        slot_in[::5] = -1
+        out[::3] = -1
+        check(x, run(x, list(slot_in), list(out)), slot_in, out)
+
+
+def test_every_window_of_short_and_long_sequences_kept():
+    lens = [4, 1, 0, 16, 17, 2, 50, 3] + [2] * 12 + [0] * 8
+    T = sum(lens)
+    x = make(lens, 136, 4, T + 5, "bf16", seed=21)
+    slot_in = [n % 5 if n % 4 else -1 for n in range(len(lens))]
+    slot_out = [5 + (7 * t + 3) % T for t in range(T)]   # (T = 117: every slot once)
+    check(x, run(x, slot_in, slot_out), slot_in, slot_out)
+
+
+def test_bad_tables_among_short_and_long_sequences():
+    """What is wrong is reported and skipped, the other sequences are served; nothing outside the tables is touched."""
+    lens = [1] * 10 + [40] + [2] * 10
+    T, N = sum(lens), len(lens)
+    x = make(lens, 24, 4, N + 1, "bf16", seed=22)
+    out = last_slots(lens, range(N))
+    good = run(x, list(range(N)), out)
+    rows = np.repeat(np.arange(N), lens)
+    for n, slot in ((10, N + 1), (10, -4), (3, N + 9), (15, -2)):
+        slot_in = list(range(N))
+        slot_in[n] = slot
+        y, win, status = run(x, slot_in, out)
+        keep = torch.from_numpy(rows != n)
+        assert status == 7 and torch.equal(y.cpu()[keep], good[0].cpu()[keep])
+        assert torch.equal(win[n].cpu(), x["window"][n])
+    for n in (10, 3):
+        bad = out.copy()
+        bad[np.cumsum(lens)[n] - 1] = N + 1
+        y, win, status = run(x, list(range(N)), list(bad))
+        assert status == 7 and torch.equal(y, good[0]) and torch.equal(win[n].cpu(), x["window"][n])
+    for i, v in ((N, T + 3), (0, -2), (11, 5), (10, 60), (11, T + 40)):
+        cu = x["cu"].copy()
+        cu[i] = v
+        _, win, status = run(dict(x, cu=cu), list(range(N)), out)
+        assert status == 7 and torch.equal(win[N].cpu(), x["window"][N])
+
+
+def test_more_sequences_than_rows_of_the_grid():
+    rng = np.random.default_rng(5)
+    lens = list(rng.integers(0, 3, 33000))
+    x = make(lens, 8, 4, 33000, "bf16", seed=23)
+    check(x, run(x, None, None), list(range(33000)), last_slots(lens, range(33000)))
