@@ -376,7 +376,7 @@ gdn_status gdn_conv1d_step(const gdn_conv_step_problem *prob, const void *x, con
  * weights' gradients dwq, dwk [D] FP32 (each NULL: not wanted; not NULL with its w NULL is allowed), summed
  * over all tokens and heads in a fixed order.  x must be what the forward read.
  * Any even rot <= D, any D <= 512, any alignment of at least the element's; sums in FP32.  The fast kernels take
- * strides and pointers in whole 16 bytes, D a multiple of 8 up to 256 and, in the half layout, rot a multiple of 8; the
+ * strides and pointers in whole 16 bytes, D a multiple of 8 up to 256 and, in the half layout, rot a multiple of 4; the
  * others are several times slower.
  * gdn_qk_workspace_bytes: the backward's scratch (16-byte aligned), for the partial sums of dwq and dwk.
  */

@@ -11,7 +11,7 @@
 // are on their way into the warp's ring in shared memory.  A warp stays with q or with k, and waits for no
 // other. Few tokens: their heads are split over warps.  PLAIN: a norm and the whole row rotated, which
 // needs no masks.
-// The kernel for other rows (any alignment, odd D, rot not a multiple of 8 in the half layout) spreads a row over a
+// The kernel for other rows (any alignment, odd D, rot not a multiple of 4 in the half layout) spreads a row over a
 // warp, value by value, and takes partners from shared memory.
 #include <algorithm>
 #include <cmath>
@@ -23,7 +23,7 @@
 
 namespace gdn {
 
-template <typename E, int L, int M, bool HALF, bool PLAIN>
+template <typename E, int L, int M, int LAYOUT, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   chain_kernel();
   using R = Ring<E, L, 1, M>;
@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
   E* slots = ring[threadIdx.x >> 5][0];
   const int l = threadIdx.x % L, mine = (threadIdx.x & 31) / L * R::ROW;
-  Pieces<L, M, HALF> piece;
+  Pieces<L, M, LAYOUT> piece;
   piece.setup(a, l);
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
   const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
@@ -47,12 +47,12 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
   to.enter(a, splits, heads);
   at = to;
   int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead: its load is not waited for)
-  Angles<L, M, HALF, sizeof(E) == 2> ang;
+  Angles<L, M, LAYOUT, sizeof(E) == 2> ang;
   ang.request(a, l);
   float2 w[M][4];
 #pragma unroll
   for (int m = 0; m < M; ++m)
-    piece_weights(which ? a.w[1] : a.w[0], piece.off[m], piece.away[m], piece.has[m], w[m]);
+    piece_weights(which ? a.w[1] : a.w[0], piece, m, w[m]);
   const E* px = xbase + to.t * xt + to.h * xh;
   const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine);
   int fill = 0, use = 0;   // byte offsets of slots
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         wc[m][j] = __fmul2_rn(w[m][j], co[j]);
-        ws[m][j] = __fmul2_rn(partner_of<HALF>(w[m], j), si[j]);
+        ws[m][j] = __fmul2_rn(partner_of<LAYOUT>(w[m], j), si[j]);
       }
     }
     E* y = ybase + at.t * yt + at.h * yh;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
       request();      // into the last slot
       float2 v[M][4];
 #pragma unroll
-      for (int m = 0; m < M; ++m) read_row<E, HALF>(read + use + piece.off[m] * (int)sizeof(E), piece.away[m], v[m]);
+      for (int m = 0; m < M; ++m) read_piece<E, 0>(read + use, piece, m, v[m]);
       use = R::next(use);
       float r = 1.f;
       if (PLAIN || a.normed) {
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_kernel(const QkArgs a) {
       for (int m = 0; m < M; ++m) {
         float2 p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = partner_of<HALF>(v[m], j);
-        if (!PLAIN) only_rotated(p, piece.rotated[m]);
+        for (int j = 0; j < 4; ++j) p[j] = partner_of<LAYOUT>(v[m], j);
+        if (!PLAIN) piece.only_rotated(m, p);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           v[m][j] = __fmul2_rn(make_float2(r, r), __ffma2_rn(p[j], ws[m][j], __fmul2_rn(v[m][j], wc[m][j])));
-        if (keep && piece.has[m]) write_row<E, HALF>(y + piece.off[m], piece.away[m], v[m]);
+        if (keep && piece.has[m]) write_piece<E>(y, piece, m, v[m]);
       }
       y += yh;
     }
@@ -181,17 +181,18 @@ __global__ void __launch_bounds__(QK_THREADS) qk_fwd_row_kernel(const QkArgs a) 
   }
 }
 
-template <typename E, int L, int M, bool HALF, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
-  static const int resident = resident_ctas(qk_fwd_kernel<E, L, M, HALF, PLAIN>);
+template <typename E, int L, int M, int LAYOUT, bool PLAIN> static void launch_fwd_kernel(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_fwd_kernel<E, L, M, LAYOUT, PLAIN>);
   const int ctas = divide_work(a, L, resident, 1);
-  launch_chained(qk_fwd_kernel<E, L, M, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
+  launch_chained(qk_fwd_kernel<E, L, M, LAYOUT, PLAIN>, ctas, QK_THREADS, 0, s, a);
 }
 template <typename E, int L, int M> static void launch_fwd_rows(QkArgs& a, cudaStream_t s) {
   const bool plain = plain_rows(a);
-  if (a.half_layout && plain) launch_fwd_kernel<E, L, M, true, true>(a, s);
-  else if (a.half_layout) launch_fwd_kernel<E, L, M, true, false>(a, s);
-  else if (plain) launch_fwd_kernel<E, L, M, false, true>(a, s);
-  else launch_fwd_kernel<E, L, M, false, false>(a, s);
+  if (a.half_layout && a.rot % 8 != 0) launch_fwd_kernel<E, L, M, HALF_BY_4, false>(a, s);
+  else if (a.half_layout && plain) launch_fwd_kernel<E, L, M, HALF, true>(a, s);
+  else if (a.half_layout) launch_fwd_kernel<E, L, M, HALF, false>(a, s);
+  else if (plain) launch_fwd_kernel<E, L, M, PAIRS, true>(a, s);
+  else launch_fwd_kernel<E, L, M, PAIRS, false>(a, s);
 }
 template <typename E, int PER> static void launch_fwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_fwd_row_kernel<E, PER>);
@@ -240,7 +241,7 @@ static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k,
   const int heads[2] = {p->HQ, p->HK};
   const int64_t st[2][4] = {{p->q_token, p->q_head, p->qo_token, p->qo_head},
                             {p->k_token, p->k_head, p->ko_token, p->ko_head}};
-  *fast = p->D % 8 == 0 && p->D <= QK_FAST_MAXD && (p->layout == GDN_ROPE_PAIRS || p->rot % 8 == 0);
+  *fast = p->D % 8 == 0 && p->D <= QK_FAST_MAXD && (p->layout == GDN_ROPE_PAIRS || p->rot % 4 == 0);
   for (int i = 0; i < 2; ++i) {
     a->heads[i] = heads[i];
     if (heads[i] == 0) continue;

@@ -92,23 +92,42 @@ __device__ __forceinline__ int position_of(const QkArgs& a, int64_t t, int* doc)
 // ---- rows of the fast kernels ----
 // A row lies in pieces of 8 values, two blocks of 4: L lanes have M pieces each, the pieces l, l + L, .. of lane l.  In the
 // half layout a piece's blocks are partners, 4 values of the first rotated half and the 4 they are turned with, so that
-// no value crosses lanes; pieces past the rotated part, and all of the pairs layout, have 8 neighbouring values.  Either
-// way pairs 4i .. 4i+3 are piece i's.
+// no value crosses lanes; pieces past the rotated part, and all of the pairs layout, have 8 neighbouring values.  Where the
+// rotated part is 4 and a multiple of 8, that goes for each half of a piece by itself (HALF_BY_4: 100,000 tokens of 16 + 4
+// heads of 80, 20 rotated, forward 186 us and backward 283; the kernel for any rows 346 and 588).  Either way pairs 4i .. 4i+3
+// are piece i's.
 // Values are held as 4 float2: v[j] has the partner v[j ^ 2] (half), or its own other value (pairs).
-template <int L, int M, bool HALF> struct Pieces {
-  int off[M], away[M];   // of the first block, and from there to the second
-  int rotated[M];        // how many of the 8 values are (0 or 8 in the half layout)
-  bool has[M];           // the row is so long
+enum { PAIRS = 0, HALF = 1, HALF_BY_4 = 2 };
+template <int L, int M, int LAYOUT> struct Pieces {
+  static constexpr int B = LAYOUT == HALF_BY_4 ? 2 : 1;   // parts of a piece
+  int off[M][B], away[M][B];   // of a part's first block, and from there to the second
+  int rotated[M];              // how many of the piece's values are
+  bool has[M];                 // the row is so long
   __device__ __forceinline__ void setup(const QkArgs& a, int l) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       const int i = l + m * L;
-      const bool apart = HALF && i < a.rot / 8;
-      off[m] = apart ? 4 * i : 8 * i;   // (rot is a multiple of 8 in the half layout: the pieces before hold rot values)
-      away[m] = apart ? a.rot / 2 : 4;
-      rotated[m] = HALF ? (apart ? 8 : 0) : a.rot - 8 * i;
+      rotated[m] = LAYOUT == PAIRS ? a.rot - 8 * i : 0;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int e = B * i + b;
+        const bool apart = LAYOUT != PAIRS && e < a.rot * B / 8;   // (whole parts: those before hold rot values)
+        off[m][b] = (apart ? 4 : 8) / B * e;
+        away[m][b] = apart ? a.rot / 2 : 4 / B;
+        if (apart) rotated[m] += 8 / B;
+      }
       has[m] = i < a.D / 8;
     }
+  }
+  // of v[j]
+  __device__ __forceinline__ int place(int m, int j) const {
+    return B == 2 ? off[m][j & (B - 1)] + (j < 2 ? 0 : away[m][j & (B - 1)]) : off[m][0] + (j < 2 ? 0 : away[m][0]) + (j & 1) * 2;
+  }
+  // v with zeros where nothing is rotated: an infinite value's neighbour must not take part, not even times a zero sine
+  __device__ __forceinline__ void only_rotated(int m, float2 (&v)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((LAYOUT == HALF_BY_4 ? 4 * (j & 1) : 2 * j) >= rotated[m]) v[j] = make_float2(0.f, 0.f);
   }
 };
 
@@ -117,11 +136,21 @@ template <typename E> __device__ __forceinline__ float2 pair_at(const uint32_t* 
   else return pair_f32(u[j], (const E*)nullptr);
 }
 
-// a piece of a row in shared memory: `at` its first block, `away` elements from there its second
-template <typename E, bool HALF>
-__device__ __forceinline__ void read_row(uint32_t at, int away, float2 (&v)[4]) {
+// piece m of the row at `row` + PAST bytes in shared memory
+template <typename E, int PAST, int L, int M, int LAYOUT>
+__device__ __forceinline__ void read_piece(uint32_t row, const Pieces<L, M, LAYOUT>& p, int m, float2 (&v)[4]) {
+  if constexpr (LAYOUT == HALF_BY_4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      RawV<E, 2> r;
+      r.load_shared(row + p.place(m, j) * (int)sizeof(E) + PAST);
+      v[j] = pair_at<E>(r.u, 0);
+    }
+    return;
+  }
+  const uint32_t at = row + p.off[m][0] * (int)sizeof(E) + PAST;   // (PAST here: the backward 946 us, at the loads 954)
   RawV<E, 4> b[2];
-  if constexpr (!HALF && sizeof(E) == 2) {
+  if constexpr (LAYOUT == PAIRS && sizeof(E) == 2) {
     RawV<E, 8> r;
     r.load_shared(at);
     b[0].u[0] = r.u[0];
@@ -130,29 +159,40 @@ __device__ __forceinline__ void read_row(uint32_t at, int away, float2 (&v)[4]) 
     b[1].u[1] = r.u[3];
   } else {
     b[0].load_shared(at);
-    b[1].load_shared(at + away * (int)sizeof(E));
+    b[1].load_shared(at + p.away[m][0] * (int)sizeof(E));
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = pair_at<E>(b[j >> 1].u, j & 1);
 }
-template <typename E, bool HALF>
-__device__ __forceinline__ void write_row(E* p, int away, const float2 (&v)[4]) {
+template <typename E, int L, int M, int LAYOUT>
+__device__ __forceinline__ void write_piece(E* row, const Pieces<L, M, LAYOUT>& p, int m, const float2 (&v)[4]) {
+  if constexpr (LAYOUT == HALF_BY_4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      RawV<E, 2> r;
+      const float f[2] = {v[j].x, v[j].y};
+      r.put(f);
+      r.store(row + p.place(m, j));
+    }
+    return;
+  }
+  E* at = row + p.off[m][0];
   RawV<E, 4> b[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const float f[4] = {v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y};
     b[j].put(f);
   }
-  if constexpr (!HALF && sizeof(E) == 2) {
+  if constexpr (LAYOUT == PAIRS && sizeof(E) == 2) {
     RawV<E, 8> r;
     r.u[0] = b[0].u[0];
     r.u[1] = b[0].u[1];
     r.u[2] = b[1].u[0];
     r.u[3] = b[1].u[1];
-    r.store(p);
+    r.store(at);
   } else {
-    b[0].store(p);
-    b[1].store(p + away);
+    b[0].store(at);
+    b[1].store(at + p.away[m][0]);
   }
 }
 
@@ -185,20 +225,13 @@ template <int PENDING> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-template <bool HALF> __device__ __forceinline__ float2 partner_of(const float2 (&v)[4], int j) {
-  return HALF ? v[j ^ 2] : make_float2(v[j].y, v[j].x);
-}
-// v with zeros where nothing is rotated: an infinite value's neighbour must not take part, not even times a
-// zero sine.  rotated: as in Pieces
-__device__ __forceinline__ void only_rotated(float2 (&v)[4], int rotated) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (2 * j >= rotated) v[j] = make_float2(0.f, 0.f);
+template <int LAYOUT> __device__ __forceinline__ float2 partner_of(const float2 (&v)[4], int j) {
+  return LAYOUT != PAIRS ? v[j ^ 2] : make_float2(v[j].y, v[j].x);
 }
 
 // A lane's pairs, four a piece: their turn steps, and cos and sin at a token laid out like the lane's values,
 // y[j] = v[j] co[j] + partner[j] si[j].  Pairs past the rotated part get the identity.
-template <int L, int M, bool HALF, bool FAST> struct Angles {
+template <int L, int M, int LAYOUT, bool FAST> struct Angles {
   uint64_t step[M][4];
   double f[M][4];
   // the frequencies are requested first, and converted when the rows' copies are on their way
@@ -224,7 +257,7 @@ template <int L, int M, bool HALF, bool FAST> struct Angles {
         s[i] = 0.f;
       }
     }
-    if (HALF) {
+    if (LAYOUT != PAIRS) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         co[j] = co[j + 2] = make_float2(c[2 * j], c[2 * j + 1]);
@@ -261,12 +294,13 @@ template <int L> struct Place {
   }
 };
 
-// The weights of a piece (zeros where there is none)
-__device__ __forceinline__ void piece_weights(const float* w, int off, int away, bool has, float2 (&v)[4]) {
+// The weights of piece m (zeros where there is none)
+template <int L, int M, int LAYOUT>
+__device__ __forceinline__ void piece_weights(const float* w, const Pieces<L, M, LAYOUT>& p, int m, float2 (&v)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int d = off + (j < 2 ? 0 : away) + (j & 1) * 2;
-    v[j] = !has ? make_float2(0.f, 0.f) : w ? make_float2(w[d], w[d + 1]) : make_float2(1.f, 1.f);
+    const int d = p.place(m, j);
+    v[j] = !p.has[m] ? make_float2(0.f, 0.f) : w ? make_float2(w[d], w[d + 1]) : make_float2(1.f, 1.f);
   }
 }
 

@@ -12,7 +12,7 @@
 
 namespace gdn {
 
-template <typename E, int L, int M, bool HALF, bool PLAIN>
+template <typename E, int L, int M, int LAYOUT, bool PLAIN>
 __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   chain_kernel();
   using R = Ring<E, L, 2, M>;
@@ -20,7 +20,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   __shared__ __align__(16) E ring[QK_WARPS][R::STAGES][R::SLOT];
   E* slots = ring[threadIdx.x >> 5][0];
   const int l = threadIdx.x % L, mine = (threadIdx.x & 31) / L * R::ROW;
-  Pieces<L, M, HALF> piece;
+  Pieces<L, M, LAYOUT> piece;
   piece.setup(a, l);
   const int which = blockIdx.x >= a.ctas_q, cta = blockIdx.x - (which ? a.ctas_q : 0);
   const int warps = (which ? gridDim.x - a.ctas_q : a.ctas_q) * QK_WARPS;
@@ -40,12 +40,12 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
     to.enter(a, splits, heads);
     at = to;
     int doc = 0, pos = position_of(a, at.t, &doc);   // (a unit ahead)
-    Angles<L, M, HALF, sizeof(E) == 2> ang;
+    Angles<L, M, LAYOUT, sizeof(E) == 2> ang;
     ang.request(a, l);
     float2 w[M][4];
 #pragma unroll
     for (int m = 0; m < M; ++m)
-      piece_weights(which ? a.w[1] : a.w[0], piece.off[m], piece.away[m], piece.has[m], w[m]);
+      piece_weights(which ? a.w[1] : a.w[0], piece, m, w[m]);
     const E* px = xbase + to.t * xt + to.h * xh;
     const E* pg = gbase + to.t * yt + to.h * yh;
     const uint32_t read = (uint32_t)__cvta_generic_to_shared(slots + mine);
@@ -100,9 +100,8 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
         float2 s = make_float2(0.f, 0.f), d = s;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          const uint32_t from = read + use + piece.off[m] * (int)sizeof(E);
-          read_row<E, HALF>(from, piece.away[m], v[m]);
-          read_row<E, HALF>(from + R::BYTES / 2, piece.away[m], g[m]);
+          read_piece<E, 0>(read + use, piece, m, v[m]);
+          read_piece<E, R::BYTES / 2>(read + use, piece, m, g[m]);
         }
         use = R::next(use);
 #pragma unroll
@@ -111,10 +110,10 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
           float2 p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 o = partner_of<HALF>(g[m], j);
+            const float2 o = partner_of<LAYOUT>(g[m], j);
             p[j] = make_float2(-o.x, -o.y);
           }
-          if (!PLAIN) only_rotated(p, piece.rotated[m]);
+          if (!PLAIN) piece.only_rotated(m, p);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             g[m][j] = __ffma2_rn(p[j], si[m][j], __fmul2_rn(g[m][j], co[m][j]));
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
             const float2 x = __fmul2_rn(__fmul2_rn(g[m][j], w[m][j]), rr);
             v[m][j] = PLAIN || a.normed ? __ffma2_rn(v[m][j], ff, x) : x;
           }
-          if (live && piece.has[m]) write_row<E, HALF>(dx + piece.off[m], piece.away[m], v[m]);
+          if (live && piece.has[m]) write_piece<E>(dx, piece, m, v[m]);
         }
         dx += xh;
       }
@@ -153,7 +152,7 @@ __global__ void __launch_bounds__(QK_THREADS) qk_bwd_kernel(const QkArgs a) {
   for (int m = 0; m < M; ++m)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {   // (places below L * M * 8 in lanes without values, too)
-      const int d = piece.off[m] + (j < 2 ? 0 : piece.away[m]) + (j & 1) * 2;
+      const int d = piece.place(m, j);
       sums[threadIdx.x / L][d] = acc[m][j].x;
       sums[threadIdx.x / L][d + 1] = acc[m][j].y;
     }
@@ -260,18 +259,19 @@ __global__ void __launch_bounds__(DW_COLS * DW_ROWS) qk_dw_kernel(const float* p
   }
 }
 
-template <typename E, int L, int M, bool HALF, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
-  static const int resident = resident_ctas(qk_bwd_kernel<E, L, M, HALF, PLAIN>);
+template <typename E, int L, int M, int LAYOUT, bool PLAIN> static int launch_bwd_kernel(QkArgs& a, cudaStream_t s) {
+  static const int resident = resident_ctas(qk_bwd_kernel<E, L, M, LAYOUT, PLAIN>);
   const int ctas = divide_work(a, L, resident, 2);
-  launch_chained(qk_bwd_kernel<E, L, M, HALF, PLAIN>, ctas, QK_THREADS, 0, s, a);
+  launch_chained(qk_bwd_kernel<E, L, M, LAYOUT, PLAIN>, ctas, QK_THREADS, 0, s, a);
   return ctas;
 }
 template <typename E, int L, int M> static int launch_bwd_rows(QkArgs& a, cudaStream_t s) {
   const bool plain = plain_rows(a);
-  if (a.half_layout && plain) return launch_bwd_kernel<E, L, M, true, true>(a, s);
-  if (a.half_layout) return launch_bwd_kernel<E, L, M, true, false>(a, s);
-  if (plain) return launch_bwd_kernel<E, L, M, false, true>(a, s);
-  return launch_bwd_kernel<E, L, M, false, false>(a, s);
+  if (a.half_layout && a.rot % 8 != 0) return launch_bwd_kernel<E, L, M, HALF_BY_4, false>(a, s);
+  if (a.half_layout && plain) return launch_bwd_kernel<E, L, M, HALF, true>(a, s);
+  if (a.half_layout) return launch_bwd_kernel<E, L, M, HALF, false>(a, s);
+  if (plain) return launch_bwd_kernel<E, L, M, PAIRS, true>(a, s);
+  return launch_bwd_kernel<E, L, M, PAIRS, false>(a, s);
 }
 template <typename E, int PER> static int launch_bwd_any(QkArgs& a, cudaStream_t s) {
   static const int resident = resident_ctas(qk_bwd_row_kernel<E, PER>);

@@ -239,3 +239,29 @@ def test_infinities_stay_in_their_values_of_three_pieces(layout, D):
     bad[0, 0, D - 9] = bad[0, 0, D - 1] = bad[1, 0, 3] = True
     bad[1, 0, 3 + rot // 2 if layout == "half" else 2] = True
     assert torch.equal(torch.isfinite(y.cpu()), ~bad)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("D,rot", [(80, 20), (96, 12), (128, 4), (64, 60), (256, 100), (192, 180), (8, 4), (136, 68)])
+def test_halves_of_rotated_parts_that_are_4_and_a_multiple_of_8(D, rot, dtype):
+    """A rotated half that is an even number of values, no multiple of 4: few rows, and enough for all kernels; padded."""
+    for T in (5, 301):
+        x = make(T, 4, 1, D, dtype, seed=D + rot)
+        kw = dict(rot=rot, pad=8, norm="l2" if T == 5 else "rms", cu=[0, 3, T])
+        want = run(x, freqs(rot), **kw)
+        check(x, want, freqs(rot), **kw)
+        got = run(x, freqs(rot), in_place=True, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [3, 1300])
+def test_infinities_stay_in_their_values_of_such_halves(T):
+    D, rot = 80, 20
+    x = make(T, 1, 1, D, "bf16", seed=9)
+    for d in (20, 22, 79):   # the first values that are not rotated, and the last
+        x["q"][0, 0, d] = float("inf")
+    x["q"][1, 0, 9], x["q"][2, 0, 11] = float("nan"), float("inf")
+    y = run(x, freqs(rot), rot, norm="none")[0]
+    bad = torch.zeros(T, 1, D, dtype=torch.bool)
+    bad[0, 0, [20, 22, 79]] = bad[1, 0, [9, 19]] = bad[2, 0, [1, 11]] = True
+    assert torch.equal(torch.isfinite(y.cpu()), ~bad)
