@@ -395,21 +395,30 @@ __global__ void __launch_bounds__(32, !BUSY ? 1 : KDA || sizeof(E) == 4 ? 12 : 1
 // (k, q without their norms rk, rq).  All products with S0 are independent of the chain over the tokens, which is left
 // with four values a column; and S is scaled once in four tokens.
 //
-// A warp owns 32 columns of one (sequence, head): lane (r, c) = (lane / 4, lane % 4) has 8 columns of the 16 rows
-// 32 m + 4 r + 0..3, m < 4, in 128 registers, as pairs of rows, so that what it reads of the shared vectors is used
-// eight times and in pairs as it lies.  The vectors that all columns share are worked out once a CTA of STB_WARPS
-// warps: a phase is STB_WARPS blocks, each prepared by one warp into shared memory, then taken by all warps
-// without a wait, while the next phase's rows are copied in. A block ends early where a state has to be written.
+// A warp owns CPL columns of each of 32 / ROWL lanes c = lane % (32 / ROWL), and lane r = lane / (32 / ROWL) of them the rows
+// 4 ROWL m + 4 r + 0..3 for all m, as pairs of rows, so that what it reads of the shared vectors is used CPL times and in
+// pairs as it lies.  The vectors that all columns share are worked out once a CTA: a phase is STB_WARPS blocks, each
+// prepared by one warp into shared memory, then taken by all warps without a wait, while the next phase's rows are copied
+// in.  A block ends early where a state has to be written.
+//
+// Many heads: 32 columns a warp (8 row lanes of 8 columns, 128 registers of state), a head a CTA, whose warps prepare
+// and then take.  Few heads, for which the chain from block to block is all: 8 columns a warp (16 row lanes of 4), a quarter of a
+// head a CTA, and the next phase is prepared by STB_WARPS further warps meanwhile (BESIDE; one sequence of 160 tokens
+// and 4 heads 39 us, token by token 48).
 constexpr int STB_MIN_TOKENS = 24;      // a sequence, on average
+constexpr int STB_MIN_FEW = 32;         // where heads are few
 constexpr int STB_MIN_FULL = 12;        // and where tokens times heads are as many as
 constexpr int64_t STB_FULL = 12288;
 constexpr int STB_WARPS = 4;
 constexpr int STB_TOKENS = 4;   // tokens of a block
-constexpr int STB_COLS = 32;    // columns of a warp: STB_WARPS of them are a head
 // sums and scalars of a block
 constexpr int STB_L = 0, STB_M = 6, STB_KK = 16, STB_QQ = 20, STB_BETA = 24, STB_SCALARS = 28;
 
-constexpr int STB_E_BYTES = STB_TOKENS * STB_COLS * (int)sizeof(float2);
+template <int ROWL, int CPL> struct BlockLayout {
+  static constexpr int COLL = 32 / ROWL, COLS = CPL * COLL, PARTS = D / (STB_WARPS * COLS);   // PARTS: CTAs of a head
+  static constexpr int APART = 4 * ROWL, RUNS = D / APART;
+  static constexpr int E_BYTES = STB_TOKENS * COLS * (int)sizeof(float2);
+};
 
 struct StepBlock {
   float kt[STB_TOKENS][D], qt[STB_TOKENS][D];   // E(0,t) k_t, E(0,t) q_t
@@ -552,16 +561,23 @@ __device__ __forceinline__ int sequence_of_rank(const StepArgs& a, int rank) {
   return __ffs(__ballot_sync(~0u, lane < a.N && before == rank)) - 1;
 }
 
-template <typename E, bool KDA>
-__global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const StepArgs a) {
+template <int ID, int THREADS> __device__ __forceinline__ void barrier() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
+template <typename E, bool KDA, int ROWL, int CPL, bool BESIDE>
+__global__ void __launch_bounds__(STB_WARPS * (BESIDE ? 64 : 32), 2) step_block_kernel(const StepArgs a) {
   previous_kernel_done();   // (its own dependents would take the places of balanced_place: 127 us for 105)
   using Raw = StepRaw<E, KDA>;
   extern __shared__ __align__(16) uint8_t step_smem[];
-  StepBlock* blocks = reinterpret_cast<StepBlock*>(step_smem);
-  Raw* raw = reinterpret_cast<Raw*>(step_smem + STB_WARPS * sizeof(StepBlock));
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+  using L = BlockLayout<ROWL, CPL>;
+  constexpr int BUFFERS = BESIDE ? 2 : 1;
+  StepBlock(*blocks)[STB_WARPS] = reinterpret_cast<StepBlock(*)[STB_WARPS]>(step_smem);
+  Raw* raw = reinterpret_cast<Raw*>(step_smem + BUFFERS * STB_WARPS * sizeof(StepBlock));
+  __shared__ int targets[BUFFERS][32];   // BESIDE: `wants` of a phase
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane / L::COLL, c = lane % L::COLL;
   const int place = balanced_place(a, blockIdx.x, gridDim.x);
-  const int h = place % a.HV, n = sequence_of_rank(a, place / a.HV);
+  const int part = place % L::PARTS, h = place / L::PARTS % a.HV, n = sequence_of_rank(a, place / L::PARTS / a.HV);
   int t0, t1;
   if (!sequence_bounds(a.cu, n, a.T, &t0, &t1)) {
     if (threadIdx.x == 0) *a.err = ST_DEVICE;
@@ -573,78 +589,108 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
     if (threadIdx.x == 0) *a.err = ST_DEVICE;
     return;
   }
-  request_rows<E, KDA>(a, h, t0, t1, warp, raw);
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  // where the state after token first + lane goes: -1 nowhere
+  int t = t0, buffer = 0;
+  unsigned cuts = 0;
+  // a phase's blocks: up to 4 tokens each, a state that is wanted only at a block's end
+  auto length = [&](int pos) {   // (pos < 32: a phase has at most 4 * 4 tokens)
+    const int len = min(STB_TOKENS, t1 - t - pos), cut = __ffs(cuts >> pos);
+    return cut ? min(len, cut) : len;
+  };
   auto wanted = [&](int first) {
     const int look = first + lane;
     return look >= t1 ? -1 : a.slot_out ? a.slot_out[look] : look == t1 - 1 ? from : -1;
   };
-  int wants = wanted(t0);
-  // S[2 m + i][x]: the rows 32 m + 4 r + 2 i and the next, of this lane's column x ^ (r & 6).  With the columns in that
+  const int w = BESIDE ? warp - STB_WARPS : warp;   // of the warps that prepare
+  int wants = -1, next_wants = -1;   // where the states after a phase's tokens go: -1 nowhere
+  auto begin = [&] {
+    request_rows<E, KDA>(a, h, t0, t1, w, raw);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next_wants = wanted(t0);
+  };
+  // the next phase's blocks; its number of tokens
+  auto prepare = [&](StepBlock* phase) {
+    wants = next_wants;
+    cuts = __ballot_sync(~0u, wants != -1);
+    int mine = 0, all = 0;   // where this warp's block begins
+    for (int b = 0; b < STB_WARPS; ++b) {
+      if (b == w) mine = all;
+      all += length(all);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    barrier<1, STB_WARPS * 32>();   // the rows are there (and where the same warps take them, the last phase's blocks have been read)
+    if (BESIDE && w == 0) targets[BESIDE ? buffer : 0][lane] = wants;
+    if (w == 0 || mine < all) prepare_block<E, KDA>(a, *raw, mine, length(mine), phase + w);
+    barrier<1, STB_WARPS * 32>();   // the blocks are there, and the rows have been read
+    request_rows<E, KDA>(a, h, t + all, t1, w, raw);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next_wants = wanted(t + all);
+    return all;
+  };
+  if (BESIDE && warp >= STB_WARPS) {
+    begin();
+    while (t < t1) {
+      const int all = prepare(blocks[buffer]);
+      barrier<0, STB_WARPS * 64>();   // the phase may be taken, and the other buffer written
+      t += all;
+      buffer ^= 1;
+    }
+    return;
+  }
+  if (!BESIDE) begin();
+  // S[2 m + i][x]: the rows 4 ROWL m + 4 r + 2 i and the next, of this lane's column x ^ turn.  With the columns in that
   // order a lane always gives the upper half of its sums away and keeps the lower.
+  const int own_x = CPL == 8 ? lane >> 2 : lane >> 3, turn = own_x & (CPL - 2);
+  const int column = (part * STB_WARPS + warp) * L::COLS;   // the warp's first
   const int64_t slot_elems = (int64_t)a.HV * STATE_F32;
-  const int64_t at = (int64_t)h * STATE_F32 + r * 4 * D + warp * STB_COLS + c * 8;
-  float2 S[8][8];
+  const int64_t at = (int64_t)h * STATE_F32 + r * 4 * D + column + c * CPL;
+  float2 S[2 * L::RUNS][CPL];
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int m = 0; m < 2 * L::RUNS; ++m)
 #pragma unroll
-    for (int x = 0; x < 8; x += 2) {   // two columns at a time
+    for (int x = 0; x < CPL; x += 2) {   // two columns at a time
       float2 top = make_float2(0.f, 0.f), low = top;
       if (from >= 0) {
-        const float* p = a.states + from * slot_elems + at + ((m >> 1) * 32 + (m & 1) * 2) * D + (x ^ (r & 6));
+        const float* p = a.states + from * slot_elems + at + ((m >> 1) * L::APART + (m & 1) * 2) * D + (x ^ turn);
         top = *reinterpret_cast<const float2*>(p);
         low = *reinterpret_cast<const float2*>(p + D);
       }
       S[m][x] = make_float2(top.x, low.x);
       S[m][x + 1] = make_float2(top.y, low.y);
     }
-  const int own = c * 8 + r;   // this lane's column of the sums, within the warp's
-  E* op = static_cast<E*>(a.o) + (int64_t)h * D + warp * STB_COLS + own;
-  float2(*se)[STB_COLS] = reinterpret_cast<float2(*)[STB_COLS]>(
-      step_smem + STB_WARPS * sizeof(StepBlock) + sizeof(Raw) + warp * STB_E_BYTES);   // every e twice: pairs as they are used
+  const int own = c * CPL + own_x;   // this lane's column of the sums, within the warp's
+  const bool writer = lane % (L::COLL * 32 / L::COLS) < L::COLL;   // (further lanes have copies of the sums)
+  E* op = static_cast<E*>(a.o) + (int64_t)h * D + column + own;
+  float2(*se)[L::COLS] = reinterpret_cast<float2(*)[L::COLS]>(   // every e twice: pairs as they are used
+      step_smem + BUFFERS * STB_WARPS * sizeof(StepBlock) + sizeof(Raw) + warp * L::E_BYTES);
 
-  int t = t0;
   while (t < t1) {
-    // the phase's blocks: up to 4 tokens each, a state that is wanted only at a block's end
-    const unsigned cuts = __ballot_sync(~0u, wants != -1);
-    auto length = [&](int pos) {   // (pos < 32: a phase has at most 4 * 4 tokens)
-      const int len = min(STB_TOKENS, t1 - t - pos), cut = __ffs(cuts >> pos);
-      return cut ? min(len, cut) : len;
-    };
-    int mine = 0, all = 0;   // where this warp's block begins, and how many tokens the phase has
-    for (int b = 0; b < STB_WARPS; ++b) {
-      if (b == warp) mine = all;
-      all += length(all);
+    int all = 0;   // (the blocks' lengths added up once more: 107 us for 105)
+    if (BESIDE) {
+      barrier<0, STB_WARPS * 64>();
+      wants = targets[BESIDE ? buffer : 0][lane];
+      cuts = __ballot_sync(~0u, wants != -1);
+    } else {
+      all = prepare(blocks[0]);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();   // the rows are there, and the last phase's blocks have been read
-    {
-      const int len = length(mine);
-      if (warp == 0 || mine < all) prepare_block<E, KDA>(a, *raw, mine, len, blocks + warp);
-    }
-    __syncthreads();
-    request_rows<E, KDA>(a, h, t + all, t1, warp, raw);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    const int next_wants = wanted(t + all);
+    const StepBlock* phase = blocks[BESIDE ? buffer : 0];
     int pos = 0;
 #pragma unroll 1
     for (int b = 0; b < STB_WARPS; ++b) {
       const int len = length(pos);
       if (len <= 0) break;
-      const StepBlock& blk = blocks[b];
-      // S0^T with a token's two vectors, summed over the 8 row lanes: y[token][u, o] of column `own`
+      const StepBlock& blk = phase[b];
+      // S0^T with a token's two vectors, summed over the row lanes: y[token][u, o] of column `own`
       float y[4][2];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        float2 acc[2][8];
+        float2 acc[2][CPL];
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < L::RUNS; ++m)
 #pragma unroll
           for (int kind = 0; kind < 2; ++kind) {
-            const float4 x = *reinterpret_cast<const float4*>((kind ? blk.qt[s] : blk.kt[s]) + 32 * m + 4 * r);
+            const float4 x = *reinterpret_cast<const float4*>((kind ? blk.qt[s] : blk.kt[s]) + L::APART * m + 4 * r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < CPL; ++i) {
               acc[kind][i] = m ? __ffma2_rn(S[2 * m][i], make_float2(x.x, x.y), acc[kind][i])
                                : __fmul2_rn(S[0][i], make_float2(x.x, x.y));
               acc[kind][i] = __ffma2_rn(S[2 * m + 1][i], make_float2(x.z, x.w), acc[kind][i]);
@@ -652,15 +698,19 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
           }
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
-          float w[8];
+          float w[CPL];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = acc[kind][i].x + acc[kind][i].y;
+          for (int i = 0; i < CPL; ++i) w[i] = acc[kind][i].x + acc[kind][i].y;
+          int d = 16;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] += __shfl_xor_sync(~0u, w[4 + i], 16);
+          for (int half = CPL / 2; half > 1; half >>= 1, d >>= 1)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) w[i] += __shfl_xor_sync(~0u, w[2 + i], 8);
-          const float give = lane & 4 ? w[0] : w[1];
-          y[s][kind] = (lane & 4 ? w[1] : w[0]) + __shfl_xor_sync(~0u, give, 4);
+            for (int i = 0; i < half; ++i) w[i] += __shfl_xor_sync(~0u, w[half + i], d);
+          const bool upper = lane & d;
+          float sum = (upper ? w[1] : w[0]) + __shfl_xor_sync(~0u, upper ? w[0] : w[1], d);
+#pragma unroll
+          for (d >>= 1; d >= L::COLL; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+          y[s][kind] = sum;
         }
       }
       // the chain over the tokens
@@ -681,17 +731,17 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
         }
         const float rk = sc[STB_KK + s];
         // (none from tokens past len: of infinite values their zeros would make NaN)
-        e[s] = s < len ? rk * sc[STB_BETA + s] * fmaf(-rk, u, blk.v[s][warp * STB_COLS + own]) : 0.f;
+        e[s] = s < len ? rk * sc[STB_BETA + s] * fmaf(-rk, u, blk.v[s][column + own]) : 0.f;
         o = fmaf(sc[STB_M + s * (s + 1) / 2 + s], e[s], o);
         se[s][own] = make_float2(e[s], e[s]);
-        if (s < len) op[(int64_t)(t + pos + s) * a.HV * D] = from_f32<E>(sc[STB_QQ + s] * o);
+        if (s < len && writer) op[(int64_t)(t + pos + s) * a.HV * D] = from_f32<E>(sc[STB_QQ + s] * o);
       }
       __syncwarp();
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const float4 x = *reinterpret_cast<const float4*>(blk.decay + 32 * m + 4 * r);
+      for (int m = 0; m < L::RUNS; ++m) {
+        const float4 x = *reinterpret_cast<const float4*>(blk.decay + L::APART * m + 4 * r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < CPL; ++i) {
           S[2 * m][i] = __fmul2_rn(S[2 * m][i], make_float2(x.x, x.y));
           S[2 * m + 1][i] = __fmul2_rn(S[2 * m + 1][i], make_float2(x.z, x.w));
         }
@@ -700,16 +750,16 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
       for (int s = 0; s < 4; ++s) {
         float2 f[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float4 x = *reinterpret_cast<const float4*>(&se[s][c * 8 + (i ^ (r & 6))]);
+        for (int i = 0; i < CPL; i += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(&se[s][c * CPL + (i ^ turn)]);
           f[i] = make_float2(x.x, x.y);
           f[i + 1] = make_float2(x.z, x.w);
         }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float4 k = *reinterpret_cast<const float4*>(blk.kh[s] + 32 * m + 4 * r);
+        for (int m = 0; m < L::RUNS; ++m) {
+          const float4 k = *reinterpret_cast<const float4*>(blk.kh[s] + L::APART * m + 4 * r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < CPL; ++i) {
             S[2 * m][i] = __ffma2_rn(make_float2(k.x, k.y), f[i], S[2 * m][i]);
             S[2 * m + 1][i] = __ffma2_rn(make_float2(k.z, k.w), f[i], S[2 * m + 1][i]);
           }
@@ -722,28 +772,35 @@ __global__ void __launch_bounds__(STB_WARPS * 32, 2) step_block_kernel(const Ste
           if (lane == 0) *a.err = ST_DEVICE;
         } else {
 #pragma unroll
-          for (int m = 0; m < 8; ++m)
+          for (int m = 0; m < 2 * L::RUNS; ++m)
 #pragma unroll
-            for (int x = 0; x < 8; x += 2) {
-              float* p = a.states + to * slot_elems + at + ((m >> 1) * 32 + (m & 1) * 2) * D + (x ^ (r & 6));
+            for (int x = 0; x < CPL; x += 2) {
+              float* p = a.states + to * slot_elems + at + ((m >> 1) * L::APART + (m & 1) * 2) * D + (x ^ turn);
               *reinterpret_cast<float2*>(p) = make_float2(S[m][x].x, S[m][x + 1].x);
               *reinterpret_cast<float2*>(p + D) = make_float2(S[m][x].y, S[m][x + 1].y);
             }
         }
       }
     }
-    t += all;
-    wants = next_wants;
+    t += BESIDE ? pos : all;
+    buffer ^= 1;
   }
+}
+
+template <typename E, bool KDA, int ROWL, int CPL, bool BESIDE>
+static bool launch_blocks(const StepArgs& a, unsigned heads, cudaStream_t s) {
+  using L = BlockLayout<ROWL, CPL>;
+  constexpr int bytes = STB_WARPS * ((BESIDE ? 2 : 1) * (int)sizeof(StepBlock) + L::E_BYTES) + (int)sizeof(StepRaw<E, KDA>);
+  const auto kernel = step_block_kernel<E, KDA, ROWL, CPL, BESIDE>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  launch_chained(kernel, heads * L::PARTS, STB_WARPS * (BESIDE ? 64 : 32), bytes, s, a);
+  return true;
 }
 
 template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool blocks, unsigned heads, cudaStream_t s) {
   if (blocks) {
-    constexpr int bytes = STB_WARPS * ((int)sizeof(StepBlock) + STB_E_BYTES) + (int)sizeof(StepRaw<E, KDA>);
-    if (cudaFuncSetAttribute(step_block_kernel<E, KDA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-        cudaSuccess)
-      return false;
-    launch_chained(step_block_kernel<E, KDA>, heads, STB_WARPS * 32, bytes, s, a);
+    if (heads > a.sms / 2) return launch_blocks<E, KDA, 8, 8, false>(a, heads, s);
+    return launch_blocks<E, KDA, 16, 4, true>(a, heads, s);
   } else if (heads <= a.sms / ST_FEW) {   // single tokens, too: their bits are the same as a sequence's
     launch_chained(step_kernel<E, KDA, 16, false>, heads * StepLayout<16>::PARTS, 32, 0, s, a);
   } else if (a.T <= a.N) {
@@ -786,13 +843,14 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   // the chain from token to token is all: step_kernel with 8 columns a warp (one sequence of 64 tokens and 4 heads 20 us,
   // with 16 columns 32).  Else one token: step_token_kernel (64 sequences of 48 heads 60 us; step_kernel, with more
   // registers, 70); a few, step_kernel (64 of 8: 115 us; step_block_kernel 157); from 24 on, step_block_kernel, a CTA a
-  // head, unless they leave half of the SMs without one (3 of 48 heads, 16 tokens: 15 us against 14, 32: 22 against 24,
-  // 64: 36 against 44; one of 64: 34 against 28); from 12 on where warps are so many that only the work counts (64 of 16:
-  // 182 us against 204, 32 of 128: 533 against 796; but 16 of 16: 58 against 57).
+  // head, if that fills half of the SMs (3 of 48 heads, 16 tokens: 15 us against 14, 32: 22 against 24,
+  // 64: 36 against 44); with fewer a quarter of a head a CTA, from 32 on (4 heads, 24 tokens: 9.5 us against 9.0, 32: 11.3
+  // against 11.3, 64: 18 against 20, 160: 39 against 48; 48 heads, 64: 26 against 28); and from 12 on where warps are so many
+  // that only the work counts (64 of 16: 182 us against 204, 32 of 128: 533 against 796; but 16 of 16: 58 against 57).
   const int64_t heads = (int64_t)p->N * p->HV;
-  const bool blocks = heads > sm_count() / 2 &&
-                      (p->T >= (int64_t)p->N * STB_MIN_TOKENS ||
-                       (p->T >= (int64_t)p->N * STB_MIN_FULL && p->T * p->HV >= STB_FULL));
+  const bool blocks = heads <= sm_count() / 2 ? p->T >= (int64_t)p->N * STB_MIN_FEW
+                                              : p->T >= (int64_t)p->N * STB_MIN_TOKENS ||
+                                                    (p->T >= (int64_t)p->N * STB_MIN_FULL && p->T * p->HV >= STB_FULL);
   if (heads * StepLayout<16>::PARTS > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   a.q = q;
   a.k = k;

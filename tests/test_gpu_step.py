@@ -368,3 +368,42 @@ def test_lengths_around_the_choice_of_blocks(H, HV, lens, kda):
             slot_out[ends[n] - 1] = n
     slot_out[10:13] = [N, N + 1, N + 2]
     check(x, run(x, kda, list(range(N)), slot_out), list(range(N)), slot_out)
+
+
+@pytest.mark.parametrize("kda", [False, True])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("H,HV,lens", [(1, 1, [32]), (2, 4, [33, 40]), (1, 3, [31, 0, 90, 2]), (1, 1, [200]),
+                                       (1, 2, [35] * 18), (16, 64, [67])])
+def test_few_heads_in_blocks(H, HV, lens, dtype, kda):
+    """Few heads and long sequences, whose blocks are prepared by other warps: states wanted in a row, in the middle and at
+    the end, from a slot and from none."""
+    T, N = sum(lens), len(lens)
+    x = make(lens, H, HV, 2 * N + 9, dtype, kda, seed=T + HV)
+    slot_in = [n if n % 3 != 1 else -1 for n in range(N)]
+    slot_out = np.full(T, -1)
+    ends = np.cumsum(lens)
+    for n in range(N):
+        if lens[n]:
+            slot_out[ends[n] - 1] = N + n
+    first = list(range(3, 8)) + [17, 30]
+    slot_out[first] = [2 * N + i for i in range(len(first))]
+    check(x, run(x, kda, slot_in, slot_out, packed=N == 2), slot_in, slot_out)
+
+
+def test_few_heads_in_blocks_keep_every_state_and_report_bad_tables():
+    x = make([60, 50], 1, 3, 112, "fp32", True, seed=31, steep=True)
+    x["g"][7] = x["g"][61] = -float("inf")
+    every = [2 + t for t in range(110)]
+    check(x, run(x, True, [0, 1], every), [0, 1], every)
+    good = run(x, True, [0, 1], None)
+    bad = np.full(110, -1)
+    bad[[20, 59, 109]] = [112, 0, 1]
+    o, pool, status = run(x, True, [0, 1], bad)
+    bad[20] = -1
+    assert status == 7 and torch.equal(o[60:], good[0][60:])
+    check(x, (o, pool, 0), [0, 1], bad)
+    for slot_in, cu in (([112, 1], [0, 60, 110]), ([0, 1], [-1, 60, 110])):
+        o, pool, status = run(dict(x, cu=np.array(cu, np.int32)), True, slot_in, None)
+        assert status == 7 and torch.equal(o[60:], good[0][60:]) and torch.equal(pool[1], good[1][1])
+    _, pool, status = run(dict(x, cu=np.array([0, 60, 111], np.int32)), True, [0, 1], None)
+    assert status == 7 and torch.equal(pool[0], good[1][0]) and torch.equal(pool[1].cpu(), x["states"][1])
