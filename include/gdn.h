@@ -338,7 +338,8 @@ gdn_status gdn_kda_step(const gdn_step_problem *prob, const void *q, const void 
  *              be NULL); the rows of a prompt's end, or zero rows where there are fewer;
  *   dtype      of x, y and window; strides and pointers in whole 16 bytes.
  * cu_seqlens_dev, slot_in (-1: zero rows), slot_out and dev_err are gdn_step's; a sequence with a
- * bad slot_in is skipped.  1 <= W <= 4, C a multiple of 8.
+ * bad slot_in or bad bounds is skipped (where cu_seqlens goes back, sequences after that may be, too).
+ * 1 <= W <= 4, C a multiple of 8.
  */
 typedef struct {
     int64_t T;

@@ -305,10 +305,7 @@ __global__ void __launch_bounds__(CS_THREADS, !MIXED ? 0 : sizeof(E) == 2 ? 6 : 
   auto enter = [&] {
     t0 = a.cu ? a.cu[n] : n;
     t1 = a.cu ? a.cu[n + 1] : n + 1;
-    if (t0 < 0 || t1 < t0 || t1 > a.T) {
-      *a.err = ST_DEVICE;
-      t1 = t0;
-    }
+    if (t0 < 0 || t1 < t0 || t1 > a.T) t1 = t0;   // (reported apart)
     from = a.slot_in ? a.slot_in[n] : n;
     skip = from < -1 || from >= a.slots;
     if (skip && t0 < t1) *a.err = ST_DEVICE;
@@ -340,6 +337,13 @@ __global__ void __launch_bounds__(CS_THREADS, !MIXED ? 0 : sizeof(E) == 2 ? 6 : 
   };
 #pragma unroll
   for (int i = 0; i < CS_STAGES - 1; ++i) request();
+  // A range meets only the sequences that its tokens lie in, and bad bounds have none: all are looked over here.
+  if (!MIXED && blockIdx.x == 0) {
+    for (unsigned m = blockIdx.y * CS_THREADS + threadIdx.x; m < (unsigned)a.N; m += gridDim.y * CS_THREADS) {
+      const int b = a.cu[m], e = a.cu[m + 1];
+      if (b < 0 || e < b || e > a.T) *a.err = ST_DEVICE;
+    }
+  }
   // the row of token t, which is then passed
   auto take = [&](RawV<E, V>* row) {
     asm volatile("cp.async.wait_group %0;" ::"n"(CS_STAGES - 2) : "memory");

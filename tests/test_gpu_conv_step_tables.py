@@ -1,0 +1,75 @@
+"""The convolution step (gdn_conv1d_step) with bounds that are none: the error word is set wherever in the batch they
+lie, what is wrong is skipped, and the sequences beside are served."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_conv_step import last_slots, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+def starts(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("C", [16, 10240])   # ranges of one token and of many
+@pytest.mark.parametrize("lens,change,bad", [
+    ([400, 0], {2: 500}, 1),             # a sequence behind the last token
+    ([400, 0, 0], {2: 500, 3: 500}, 1),  # (and an empty one behind that)
+    ([0, 400], {0: -5}, 0),              # a negative start in front of a sequence at 0
+    ([200, 192, 0, 8], {3: 390}, 2),     # bounds that go back, between sequences
+    ([392, 0, 8], {2: 380}, 1),
+])
+def test_bad_bounds_of_long_sequences_are_reported(lens, change, bad, C):
+    """Few sequences of many tokens, whose ranges are not walked through the bad one."""
+    N, T = len(lens), sum(lens)
+    x = make(lens, C, 4, N + 1, "bf16", seed=C + N)
+    good = run(x, None, None)
+    assert good[2] == 0
+    cu = x["cu"].copy()
+    for i, v in change.items():
+        cu[i] = v
+    y, win, status = run(dict(x, cu=cu), None, None)
+    assert status == 7
+    assert torch.equal(win[bad].cpu(), x["window"][bad]) and torch.equal(win[N].cpu(), x["window"][N])
+    first = min([T] + [int(v) for v in cu if 0 <= v <= T and v not in x["cu"]])   # (a start moved back overlaps what is before)
+    assert torch.equal(y[:first], good[0][:first])
+    for n in range(N):
+        if n != bad and lens[n] and cu[n] == x["cu"][n] and cu[n + 1] == x["cu"][n + 1]:
+            assert torch.equal(win[n], good[1][n])
+
+
+@pytest.mark.parametrize("at,value", [(33000, 10 ** 6), (20001, 10 ** 6), (0, -3), (7, -1), (32999, 5)])
+def test_bad_bounds_among_very_many_sequences_are_reported(at, value):
+    rng = np.random.default_rng(6)
+    lens = list(rng.integers(0, 3, 33000))
+    x = make(lens, 8, 4, 33001, "bf16", seed=24)
+    cu = x["cu"].copy()
+    cu[at] = value
+    _, win, status = run(dict(x, cu=cu), None, None)
+    assert status == 7 and torch.equal(win[33000].cpu(), x["window"][33000])
+
+
+def test_graph_replay_with_more_tokens_than_it_was_captured_for():
+    """Replayed with lengths whose sum is past the captured T, at a sequence's start: reported, the others served."""
+    import linear_attention_gdn_gb300 as gdn
+    lens = [300, 60, 40]
+    x = make(lens, 512, 4, 3, "bf16", seed=25)
+    want = run(x, None, None)
+    T, C = x["x"].shape
+    win, y = x["window"].cuda(), torch.full((T, C), float("nan"), dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.from_numpy(x["cu"]).cuda()
+    d, w, b = x["x"].cuda(), x["w"].cuda(), x["b"].cuda()
+    prob = gdn.conv_step_problem(T, 3, C, 3)
+    gdn.gdn_conv1d_step(prob, d, w, b, win.clone(), y, err, cu_seqlens_dev=cu)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_conv1d_step(prob, d, w, b, win, y, err, cu_seqlens_dev=cu)
+    assert gdn.gdn_device_status(err) == 0
+    cu.copy_(torch.from_numpy(starts([300, 100, 70])))
+    graph.replay()
+    assert gdn.gdn_device_status(err) == 7
+    assert torch.equal(y[:360], want[0][:360]) and torch.equal(win[0], want[1][0])
+    assert torch.equal(win[2].cpu(), x["window"][2])
