@@ -192,10 +192,9 @@ __global__ void __launch_bounds__(CS_THREADS1) conv_token_kernel(const ConvStepA
 #pragma unroll
       for (int i = 0; i < W - 1; ++i) as_pairs(old[u][i], hist[i]);
       conv_row<E, W, V>(k, row[u], hist).store(y + (int64_t)n * a.ys);
-      if (W == 1) continue;
       if (to[u] < -1 || to[u] >= a.slots) {
         *a.err = ST_DEVICE;
-      } else if (to[u] >= 0) {
+      } else if (W > 1 && to[u] >= 0) {
         E* p = win + to[u] * win_slot;
 #pragma unroll
         for (int i = 0; i + 1 < W - 1; ++i) old[u][i + 1].store(p + (int64_t)i * a.C);
@@ -248,7 +247,7 @@ template <typename E, int W> __device__ __forceinline__ void short_sequence(cons
     for (int i = 0; i < CS_FEW; ++i) {
       if (t + i >= t1) break;
       conv_row<E, W, V>(k, row[H + i], hist).store(y + (int64_t)(t + i) * a.ys);
-      if (W == 1 || to[i] == -1) continue;
+      if (to[i] == -1) continue;
       if (to[i] < -1 || to[i] >= a.slots) {
         *a.err = ST_DEVICE;
         continue;
@@ -400,31 +399,29 @@ __global__ void __launch_bounds__(CS_THREADS, !MIXED ? 0 : sizeof(E) == 2 ? 6 : 
     }
     while (t < t0) take(&passed);   // the tokens of sequences that were refused
     walk(min(t1, max(hi, t0 + W - 1)));
-    if (W > 1) {
-      // the windows of the sequence's tokens, looked up CS_LOOK * 32 at a time
-      for (int s0 = a.slot_out ? t0 : t1 - 1; s0 < t1; s0 += CS_LOOK * 32) {
-        int to[CS_LOOK];
+    // the windows of the sequence's tokens, looked up CS_LOOK * 32 at a time
+    for (int s0 = a.slot_out ? t0 : t1 - 1; s0 < t1; s0 += CS_LOOK * 32) {
+      int to[CS_LOOK];
 #pragma unroll
-        for (int q = 0; q < CS_LOOK; ++q) {
-          const int s = s0 + q * 32 + lane;
-          to[q] = s >= t1 ? -1 : a.slot_out ? a.slot_out[s] : q + lane == 0 ? from : -1;
-        }
+      for (int q = 0; q < CS_LOOK; ++q) {
+        const int s = s0 + q * 32 + lane;
+        to[q] = s >= t1 ? -1 : a.slot_out ? a.slot_out[s] : q + lane == 0 ? from : -1;
+      }
 #pragma unroll
-        for (int q = 0; q < CS_LOOK; ++q) {
-          if (to[q] < -1 || to[q] >= a.slots) *a.err = ST_DEVICE;
-          for (unsigned hits = __ballot_sync(~0u, to[q] >= 0 && to[q] < a.slots); hits; hits &= hits - 1) {
-            const int i0 = __ffs(hits) - 1, first = s0 + q * 32 + i0 - t0 - (W - 2);
-            E* p = win + __shfl_sync(~0u, to[q], i0) * win_slot;
+      for (int q = 0; q < CS_LOOK; ++q) {
+        if (to[q] < -1 || to[q] >= a.slots) *a.err = ST_DEVICE;
+        for (unsigned hits = W > 1 ? __ballot_sync(~0u, to[q] >= 0 && to[q] < a.slots) : 0u; hits; hits &= hits - 1) {
+          const int i0 = __ffs(hits) - 1, first = s0 + q * 32 + i0 - t0 - (W - 2);
+          E* p = win + __shfl_sync(~0u, to[q], i0) * win_slot;
 #pragma unroll
-            for (int i = 0; i < W - 1; ++i) {
-              const int back = first + i;   // the row's place in the sequence; before it: the old window's
-              RawV<E, V> r;
-              if (back >= 0) r.load(x + (int64_t)(t0 + back) * a.xs);
+          for (int i = 0; i < W - 1; ++i) {
+            const int back = first + i;   // the row's place in the sequence; before it: the old window's
+            RawV<E, V> r;
+            if (back >= 0) r.load(x + (int64_t)(t0 + back) * a.xs);
 #pragma unroll
-              for (int j = 0; j < W - 1; ++j)
-                if (back + W - 1 == j) r = old[j];
-              if (live) r.store(p + (int64_t)i * a.C);
-            }
+            for (int j = 0; j < W - 1; ++j)
+              if (back + W - 1 == j) r = old[j];
+            if (live) r.store(p + (int64_t)i * a.C);
           }
         }
       }

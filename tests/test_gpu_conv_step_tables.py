@@ -73,3 +73,15 @@ def test_graph_replay_with_more_tokens_than_it_was_captured_for():
     assert gdn.gdn_device_status(err) == 7
     assert torch.equal(y[:360], want[0][:360]) and torch.equal(win[0], want[1][0])
     assert torch.equal(win[2].cpu(), x["window"][2])
+
+
+@pytest.mark.parametrize("lens", [[1, 1], [2, 2], [3, 40]])
+@pytest.mark.parametrize("slot", [2, -2])
+def test_width_one_reports_slots_outside_the_pool(lens, slot):
+    """A convolution of one tap keeps no window, but its tables are checked like any other's."""
+    x = make(lens, 16, 1, 2, "bf16", seed=26)
+    good = run(x, [0, 1], list(last_slots(lens, [0, 1])), cu=None if lens == [1, 1] else "dev")
+    assert good[2] == 0
+    out = last_slots(lens, [0, slot])
+    y, _, status = run(x, [0, 1], list(out), cu=None if lens == [1, 1] else "dev")
+    assert status == 7 and torch.equal(y, good[0])
