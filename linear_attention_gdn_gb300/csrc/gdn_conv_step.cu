@@ -41,7 +41,8 @@ constexpr int CS_LOOK = 4;        // slot numbers a lane has requested together
 constexpr int CS_ROUND = 7;       // CTAs an SM holds
 constexpr int CS_ROUND1 = 12;     // and of the kernel for single tokens
 constexpr int CS_LONG = 64;       // tokens of a long range
-constexpr int CS_MAXR = 256;      // tokens per range, at most
+constexpr int CS_MAXR = 256;      // tokens per range, at most, while the grid has rows for so many ranges:
+constexpr int CS_ROWS = 65535;
 
 struct ConvStepArgs {
   const void* x;
@@ -497,7 +498,8 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
     // sequences of up to 106 tokens: one round of 24 tokens 14 us, four of 6 23 us)
     const int64_t round = std::max<int64_t>(1, (int64_t)sm_count() * CS_ROUND / cols), one = (p->T + round - 1) / round;
     a.R = (int)(one <= CS_LONG ? one : std::min<int64_t>(CS_MAXR, std::max<int64_t>(CS_LONG, (one + 3) / 4)));
-    if (mixed) a.R = std::max(a.R, CS_SHORT);
+    if (mixed) a.R = std::max(a.R, CS_SHORT);   // (262,144 tokens at most: no more rows than the grid has)
+    else a.R = std::max(a.R, (int)((p->T + CS_ROWS - 1) / CS_ROWS));
     rows = (p->T + a.R - 1) / a.R + (mixed ? p->N : 0);
   } else {
     // one sequence a CTA column while the GPU holds them all, then two (64 of 10,240 channels: 4.1 us with one, 3.2
@@ -505,7 +507,6 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
     a.R = (int64_t)p->N * cols <= (int64_t)sm_count() * CS_ROUND1 * 128 / CS_THREADS1 ? 1 : 2;
     rows = std::min<int64_t>((p->N + a.R - 1) / a.R, std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols));
   }
-  if (rows > 65535) return GDN_ERR_UNSUPPORTED;   // grid.y: 16 M tokens, or fewer in very many columns
   const dim3 grid(cols, (unsigned)rows);
   prof_begin(K_CONV_STEP, stream);
   switch (p->dtype) {

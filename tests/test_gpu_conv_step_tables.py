@@ -85,3 +85,28 @@ def test_width_one_reports_slots_outside_the_pool(lens, slot):
     out = last_slots(lens, [0, slot])
     y, _, status = run(x, [0, 1], list(out), cu=None if lens == [1, 1] else "dev")
     assert status == 7 and torch.equal(y, good[0])
+
+
+def test_more_tokens_than_ranges_of_256():
+    """More tokens than 65,535 ranges (the rows of a grid) of 256 hold; the windows in place, y against FP64."""
+    import linear_attention_gdn_gb300 as gdn
+    W, C, T = 4, 8, 65535 * 256 + 257
+    cu = np.array([0, 1000, 1000, 7000001, T - 2, T], np.int32)
+    gen = torch.Generator(device="cuda").manual_seed(27)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, window = rnd(T, C).to(torch.bfloat16), rnd(5, W - 1, C).to(torch.bfloat16)
+    w, b = 0.5 * rnd(C, W), 0.1 * rnd(C)
+    y, win, err = torch.full_like(x, float("nan")), window.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_conv1d_step(gdn.conv_step_problem(T, 5, C, 5, W=W), x, w, b, win, y, err,
+                        cu_seqlens_dev=torch.from_numpy(cu).cuda())
+    assert gdn.gdn_device_status(err) == 0
+    for n in range(5):
+        a, e = int(cu[n]), int(cu[n + 1])
+        rows = torch.cat([window[n], x[a:e]]).double()
+        z = b.double() + sum(w[:, i].double() * rows[i:i + e - a] for i in range(W))
+        want = z * torch.sigmoid(z)
+        # W products and the sigmoid, in FP32, then one rounding to BF16
+        most = w.double().abs().sum(1) * rows.abs().max() + b.double().abs()
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -24 + 1.1 * (W + 12) * 2.0 ** -24 * most
+        assert ((y[a:e].double() - want).abs() <= tol).all(), n
+        assert torch.equal(win[n].double(), rows[e - a:])
