@@ -298,6 +298,7 @@ gdn_status gdn_kda_bwd(const gdn_problem *prob, const void *q, const void *k, co
  *              GDN_ERR_DEVICE for a slot outside the pool or bad cu_seqlens.  A sequence with a bad
  *              slot_in or bad bounds is skipped (its o rows keep what they held); a bad slot_out
  *              is not written to.  The call never clears the word.
+ *   (The tables and dev_err may start at any element: a view of a longer one.)
  * The states are read once and written once per slot_out, whatever the number of tokens; sums and
  * states are FP32.  Long prompts belong to gdn_fwd_states.
  * T up to 2^30 (else GDN_ERR_UNSUPPORTED, as for the two operators below).

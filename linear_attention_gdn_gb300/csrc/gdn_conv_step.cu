@@ -471,7 +471,7 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
   if (!dev_err) return GDN_ERR_INVALID_ARG;
   if (p->T == 0 || p->N == 0) return GDN_OK;
   if (!aligned16(x) || !aligned16(y) || !aligned16(w) || (b && !aligned16(b)) ||
-      (p->W > 1 && p->slots > 0 && !aligned16(window)))
+      (p->W > 1 && p->slots > 0 && !aligned16(window)) || !on_words(cu_dev, slot_in, slot_out, dev_err))
     return GDN_ERR_INVALID_ARG;
   a.x = x;
   a.w = w;

@@ -1,5 +1,6 @@
 // gdn_elem.cuh -- element types of the generation and q/k entry points: loads of 8 consecutive
-// values into FP32 and stores rounded to the type once, to nearest even.
+// values into FP32 and stores rounded to the type once, to nearest even; and the host's check of pointers to
+// 4-byte elements.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -10,6 +11,9 @@
 namespace gdn {
 
 __host__ __device__ constexpr int elem_bytes(int dtype) { return dtype == GDN_FP32 ? 4 : 2; }
+
+// tables, counters and weights lie on their elements' boundary (or are null): else a load faults
+template <typename... P> inline bool on_words(const P*... p) { return ((((uintptr_t)p & 3) == 0) && ...); }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }

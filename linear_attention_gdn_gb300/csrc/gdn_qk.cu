@@ -263,7 +263,7 @@ static gdn_status qk_args(const gdn_qk_problem* p, const void* q, const void* k,
                   : vectors(out[i], a->yt[i], a->yh[i], es));
   }
   if (p->rot > 0 && (!freq || ((uintptr_t)freq & 7) != 0)) return GDN_ERR_INVALID_ARG;
-  if (cu && p->N < 1) return GDN_ERR_INVALID_ARG;
+  if ((cu && p->N < 1) || !on_words(wq, wk, pos, cu)) return GDN_ERR_INVALID_ARG;
   a->w[0] = wq;
   a->w[1] = wk;
   a->freq = freq;

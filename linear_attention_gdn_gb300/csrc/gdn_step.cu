@@ -837,7 +837,7 @@ static gdn_status run_step(const gdn_step_problem* p, const void* q, const void*
   if (!err) return GDN_ERR_INVALID_ARG;
   if (p->T == 0 || p->N == 0) return GDN_OK;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(g) || !aligned16(beta) || !aligned16(o) ||
-      (p->slots > 0 && !aligned16(states)))
+      (p->slots > 0 && !aligned16(states)) || !on_words(cu, slot_in, slot_out, err))
     return GDN_ERR_INVALID_ARG;
   // By the sequences' heads and their mean length, which is all that the host knows of the lengths.  Few heads, for which
   // the chain from token to token is all: step_kernel with 8 columns a warp (one sequence of 64 tokens and 4 heads 20 us,
