@@ -55,8 +55,10 @@ __device__ __forceinline__ uint64_t turn_step(double f) {
                      : down > 0 ? (hi << (64 - down)) | (lo >> down) : down > -64 ? lo << -down : 0;
   return bits >> 63 ? 0 - t : t;
 }
-// m cos and m sin at position pos. FAST: within 2^-20, by the hardware's functions, for values that are then
-// rounded to 16 bits.
+// m cos and m sin at position pos. FAST: within 2^-20, by the hardware's functions, for 16-bit rows, whose values are then
+// rounded to 8 or 11 bits. The FP32 sums dwq and dwk of such rows are not, but their terms' errors are of either sign and add
+// up like the sum's own roundings: 32,768 tokens of 16 + 16 heads of 128, BF16, 2.1e-7 of the norm from FP64 (FP32 rows,
+// by sincospif, 1.9e-7; elementary FP32 operations 4.6e-7), 300 tokens of 8 + 2 heads 1.8e-7 (operations 1.5e-7).
 template <bool FAST>
 __device__ __forceinline__ void angle_cos_sin(uint64_t step, int pos, float m, float* c, float* s) {
   const uint64_t turn = step * (uint64_t)(int64_t)pos;

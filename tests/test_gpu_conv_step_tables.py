@@ -110,3 +110,31 @@ def test_more_tokens_than_ranges_of_256():
         tol = 2.0 ** -8 * want.abs() + 2.0 ** -24 + 1.1 * (W + 12) * 2.0 ** -24 * most
         assert ((y[a:e].double() - want).abs() <= tol).all(), n
         assert torch.equal(win[n].double(), rows[e - a:])
+
+
+@pytest.mark.parametrize("way", ["single", "short", "long"])
+def test_sigmoid_of_fp32_rows(way):
+    """One tap of one: y = z / (1 + exp(-z)) of the rows themselves, relative to y's own size down to z = -87.  In 2^-24: the
+    exponential's argument z log2(e) is rounded once, as is the constant (1.25 |z| of the exponential), the exponential 4,
+    the sum 1, the reciprocal 2, the product 1."""
+    T = 4096
+    lens = {"single": [1] * T, "short": [4] * (T // 4), "long": [T]}[way]
+    x = make(lens, 16, 1, len(lens), "fp32", bias=False, seed=28)
+    x["w"][:] = 1.0
+    x["x"] = torch.linspace(-87.0, 40.0, T * 16).reshape(T, 16)
+    y, _, status = run(x, None, None, cu=None if way == "single" else "dev")
+    z = x["x"].double()
+    want = z / (1.0 + torch.exp(-z))
+    assert status == 0
+    assert ((y.cpu().double() - want).abs() <= (1.25 * z.abs() + 8) * 2.0 ** -24 * want.abs()).all()
+
+
+def test_sigmoid_at_the_ends():
+    """Infinities and NaN as the formula has them; values below the exponential's range are zero."""
+    x = make([1] * 2, 8, 1, 2, "fp32", bias=False, seed=29)
+    x["w"][:] = 1.0
+    inf, nan = float("inf"), float("nan")
+    x["x"][:] = torch.tensor([inf, -inf, nan, -100.0, -3e38, 3e38, 0.0, -0.0])
+    y = run(x, None, None, cu=None)[0][0].cpu()
+    assert y[0] == inf and torch.isnan(y[1]) and torch.isnan(y[2]) and y[5] == x["x"][0, 5]
+    assert (y[[3, 4, 6, 7]] == 0).all()
