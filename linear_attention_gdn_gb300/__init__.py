@@ -409,7 +409,7 @@ def _entry(where):
     global _native
     if _native is None:
         if not os.path.exists(_build.CALL):
-            raise ImportError(f"_gdn_call.so not built ({_build.CALL}); run linear_attention_gdn_gb300.build.build()")
+            raise ImportError(f"_gdn_call not built ({_build.CALL}); run linear_attention_gdn_gb300.build.build()")
         spec = importlib.util.spec_from_file_location("_gdn_call", _build.CALL)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -4,7 +4,7 @@ Each .cu under csrc/ compiles to an object in parallel with
     nvcc -gencode arch=compute_103a,code=sm_103a -O3 -lineinfo
 and the objects link into one shared library exporting the C ABI of
 include/gdn.h.  csrc/gdn_call.c, the binding's argument marshalling, is a Python
-extension of its own (_gdn_call.so).  No torch, no cmake.
+extension of its own, named after the interpreter that it is built for.  No torch, no cmake.
 """
 from __future__ import annotations
 
@@ -20,7 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
-CALL = os.path.join(BUILD, "_gdn_call.so")
+CALL = os.path.join(BUILD, "_gdn_call" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
