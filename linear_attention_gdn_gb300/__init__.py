@@ -408,14 +408,26 @@ def _entry(where):
     """The address of an entry point; loads the library and the marshalling module at the first."""
     global _native
     if _native is None:
-        if not os.path.exists(_build.CALL):
-            raise ImportError(f"_gdn_call not built ({_build.CALL}); run linear_attention_gdn_gb300.build.build()")
-        spec = importlib.util.spec_from_file_location("_gdn_call", _build.CALL)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        _native = module.call
+        _native = _marshalling()
     _entries[where] = ctypes.cast(getattr(lib, where), ctypes.c_void_p).value
     return _entries[where]
+
+
+def _marshalling():
+    """The call of csrc/gdn_call.c, or where that could not be built for this interpreter, of its like."""
+    if not os.path.exists(_build.CALL):
+        return _through_ctypes
+    spec = importlib.util.spec_from_file_location("_gdn_call", _build.CALL)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module.call
+
+
+def _through_ctypes(entry, prob, size, stream, *pointers):
+    vp = ctypes.c_void_p
+    kinds = [vp] * (1 + len(pointers)) + ([] if size is None else [ctypes.c_size_t]) + [vp]
+    values = [prob, *map(_ptr, pointers)] + ([] if size is None else [size]) + [stream]
+    return ctypes.CFUNCTYPE(ctypes.c_int, *kinds)(entry)(*values)
 
 
 def _call(where, kind, prob, size, stream, *pointers):

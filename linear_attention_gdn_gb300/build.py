@@ -34,6 +34,16 @@ def _stale(out, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def call_job(force: bool = False):
+    """The command that builds the marshalling module, in a list; none where it is up to date, or where this interpreter
+    has no headers (the binding then marshals through ctypes).  By nvcc's host compiler, as the library."""
+    src, include = os.path.join(CSRC, "gdn_call.c"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")) or not (force or _stale(CALL, [src])):
+        return []
+    return [[NVCC, "-O2", "-shared", "-Xcompiler", "-fPIC", "-cudart", "none", "-I", include, src, "-o",
+             CALL + f".{os.getpid()}.tmp"]]
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -47,12 +57,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([NVCC, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
 
-    call_src = os.path.join(CSRC, "gdn_call.c")
-    if force or _stale(CALL, [call_src]):
-        jobs_call = [[os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
-                      call_src, "-o", CALL + f".{os.getpid()}.tmp"]]
-    else:
-        jobs_call = []
+    jobs_call = call_job(force)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
