@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(CS_THREADS, !MIXED ? 0 : sizeof(E) == 2 ? 6 : 
   const int64_t win_slot = (int64_t)(W - 1) * a.C;
   Taps<W, V> k;
   k.load(a, c0);
-  int n = a.cu ? sequence_of(a.cu, a.N, lo) : lo;
+  int n = sequence_of(a.cu, a.N, lo);
   // the next sequence from m on that begins before hi and is not short
   auto next_long = [&](int m) {
     for (; m < a.N; m += 32) {
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(CS_THREADS, !MIXED ? 0 : sizeof(E) == 2 ? 6 : 
   int t0, t1, from;
   bool skip;   // the sequence is refused
   auto enter = [&] {
-    t0 = a.cu ? a.cu[n] : n;
-    t1 = a.cu ? a.cu[n + 1] : n + 1;
+    t0 = a.cu[n];
+    t1 = a.cu[n + 1];
     if (t0 < 0 || t1 < t0 || t1 > a.T) t1 = t0;   // (reported apart)
     from = a.slot_in ? a.slot_in[n] : n;
     skip = from < -1 || from >= a.slots;
