@@ -300,8 +300,12 @@ gdn_status gdn_kda_bwd(const gdn_problem *prob, const void *q, const void *k, co
  *              is not written to.  The call never clears the word.
  *   (The tables and dev_err may start at any element: a view of a longer one.)
  * The states are read once and written once per slot_out, whatever the number of tokens; sums and
- * states are FP32.  Long prompts belong to gdn_fwd_states.
- * T up to 2^30 (else GDN_ERR_UNSUPPORTED, as for the two operators below).
+ * states are FP32.  Tokens outside cu_seqlens' range are no sequence's: their o rows keep what they held.
+ * Long prompts belong to gdn_fwd_states, whose chunks are faster from about 250 tokens a sequence on for one sequence
+ * of 4 or 16 value heads (256 tokens: 52 us, here 60), 130 for one of 48 (128 tokens: 46 us both), 64 for four of 48
+ * (50 us, here 58) and 32 for sixteen or more of 48 (sixteen: 97 us, here 96; of 64 tokens 97 and 162).  The
+ * per-channel rule has no chunked form that takes and gives states.
+ * T below 2^30 (else GDN_ERR_UNSUPPORTED, as for the two operators below).
  *
  * The kernels of gdn_step, gdn_kda_step, gdn_conv1d_step and gdn_qk_norm_rope_* are launched with programmatic stream
  * serialization: they may be placed while the kernel before them in the stream ends, and wait for it before they touch
@@ -357,7 +361,9 @@ gdn_status gdn_conv1d_step(const gdn_conv_step_problem *prob, const void *x, con
 
 /*
  * The norm of q and k per head with the position rotation in the same pass, for layers that put them
- * between the convolution and the rule (prob->l2norm is then 0 there), and its gradients.
+ * between the convolution and the rule, and its gradients.  The rule needs keys of about unit length: with GDN_NORM_L2 and
+ * weights near one its own l2norm may then be 0.  GDN_NORM_RMS leaves keys of length near sqrt(D), and GDN_NORM_NONE those
+ * that come in, with which the state would grow without bound: keep the rule's l2norm there.
  * For each token at position p and each head's row x of D values:
  *     x^ = x r,  r = 1 / sqrt(x.x / D + eps)  (GDN_NORM_RMS),  1 / sqrt(x.x + eps)  (GDN_NORM_L2),
  *          1  (GDN_NORM_NONE)
@@ -374,10 +380,11 @@ gdn_status gdn_conv1d_step(const gdn_conv_step_problem *prob, const void *x, con
  *              views of a packed row.  q_* and k_* describe q, k and (backward) dq, dk; qo_* and ko_*
  *              the outputs and (backward) dqo, dko.  The D values of a row are contiguous.
  *   HQ, HK     heads, either may be 0 (its pointers are then unused).
- * Forward: qo, ko; each may be its input (same strides).  Backward: dq, dk (each may be dqo, dko), and the
- * weights' gradients dwq, dwk [D] FP32 (each NULL: not wanted; not NULL with its w NULL is allowed), summed
+ * Forward: qo, ko; each may be its input (same strides).  Backward: dq, dk (each may be dqo, dko, same
+ * strides), and the weights' gradients dwq, dwk [D] FP32 (each NULL: not wanted; not NULL with its w NULL is allowed), summed
  * over all tokens and heads in a fixed order.  x must be what the forward read.
- * Any even rot <= D, any D <= 512, any alignment of at least the element's; sums in FP32.  The fast kernels take
+ * Any even rot <= D, any D <= 512, HQ + HK <= 65536 (beyond: GDN_ERR_UNSUPPORTED), any alignment of at least the
+ * element's; sums in FP32.  The fast kernels take
  * strides and pointers in whole 16 bytes, D a multiple of 8 up to 256 and, in the half layout, rot a multiple of 4; the
  * others are several times slower.
  * gdn_qk_workspace_bytes: the backward's scratch (16-byte aligned), for the partial sums of dwq and dwk.

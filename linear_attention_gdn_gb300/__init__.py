@@ -99,7 +99,8 @@ def conv_step_problem(T, N, C, slots, W=4, dtype=BF16, strides=(0, 0)) -> gdn_co
 
 def qk_problem(T, HQ, HK, D=128, rot=None, layout=ROPE_HALF, norm=NORM_RMS, eps=1e-6, mscale=1.0, N=0, dtype=BF16,
                q_strides=(0, 0), k_strides=(0, 0), qo_strides=(0, 0), ko_strides=(0, 0)) -> gdn_qk_problem:
-    """Strides: elements from token to token and from head to head (0: contiguous)."""
+    """Strides: elements from token to token and from head to head (0: contiguous).  In front of the rule: NORM_L2, or the
+    rule's own l2norm after any norm."""
     return gdn_qk_problem(int(T), int(N), int(HQ), int(HK), int(D), int(D if rot is None else rot), int(layout),
                           int(norm), _dtype(dtype), float(eps), float(mscale),
                           *(int(s) for pair in (q_strides, k_strides, qo_strides, ko_strides) for s in pair))

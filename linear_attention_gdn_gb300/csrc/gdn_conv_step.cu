@@ -38,8 +38,11 @@ constexpr int CS_FEW = 4;         // tokens of a short sequence that a thread ha
 constexpr int CS_SHORT = 16;      // tokens up to which a sequence of many is a thread's own
 constexpr int CS_MEAN = 8;        // where the mean is no more than so many
 constexpr int CS_LOOK = 4;        // slot numbers a lane has requested together
-constexpr int CS_ROUND = 7;       // CTAs an SM holds
-constexpr int CS_ROUND1 = 12;     // and of the kernel for single tokens
+// CTAs an SM that make a round: of the range kernel for 16-bit rows what it holds.  It holds 6 for FP32 rows (32 KiB of ring
+// each) and 6 or 4 of the mixed kernel, but with 6 ranges are as quick or slower there, too (9 FP32 sequences of up to
+// 693 tokens of 1,128 channels 9.4 us, with 7 8.9; 29 of up to 106 of 8,608 20.3 and 19.5; 64 of 1-4 of 10,240 6.8 both).
+constexpr int CS_ROUND = 7;
+constexpr int CS_ROUND1 = 12;     // that an SM holds of the kernel for single tokens
 constexpr int CS_LONG = 64;       // tokens of a long range
 constexpr int CS_MAXR = 256;      // tokens per range, at most, while the grid has rows for so many ranges:
 constexpr int CS_ROWS = 65535;
@@ -505,8 +508,8 @@ extern "C" gdn_status gdn_conv1d_step(const gdn_conv_step_problem* p, const void
     else a.R = std::max(a.R, (int)((p->T + CS_ROWS - 1) / CS_ROWS));
     rows = (p->T + a.R - 1) / a.R + (mixed ? p->N : 0);
   } else {
-    // one sequence a CTA column while the GPU holds them all, then two (64 of 10,240 channels: 4.1 us with one, 3.2
-    // with two), side by side as far as they give an SM 32 CTAs
+    // one sequence a CTA column while the GPU holds them all, then two (BF16, 10,240 channels, in a graph: 64 3.17 us
+    // with one, 3.07 with two; 512 13.1 and 13.4), side by side as far as they give an SM 32 CTAs
     a.R = (int64_t)p->N * cols <= (int64_t)sm_count() * CS_ROUND1 * 128 / CS_THREADS1 ? 1 : 2;
     rows = std::min<int64_t>((p->N + a.R - 1) / a.R, std::max<int64_t>(1, (int64_t)sm_count() * 32 / cols));
   }
