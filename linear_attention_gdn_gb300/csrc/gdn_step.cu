@@ -138,14 +138,14 @@ __global__ void __launch_bounds__(ST_WARPS * 32) step_token_kernel(const StepArg
       const float* gp = a.g + ((int64_t)t * a.HV + h) * D + r * 8;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float e = __expf(gp[(j & 7) + (j >> 3) * 64]);
+        const float e = expf(gp[(j & 7) + (j >> 3) * 64]);
         S[j].x *= e;
         S[j].y *= e;
         S[j].z *= e;
         S[j].w *= e;
       }
     } else {
-      const float e = __expf(a.g[(int64_t)t * a.HV + h]);
+      const float e = expf(a.g[(int64_t)t * a.HV + h]);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         S[j].x *= e;
@@ -233,7 +233,7 @@ template <typename E, bool KDA, int ROWL> struct StepToken {
 };
 
 // a few tokens: the next one's rows are requested a token ahead, and rows lie in pairs for the paired FP32 instructions
-// BUSY: registers for 12 and 16 warps an SM (64 sequences of 8 tokens 137 us with one decay a channel and 115 with one a
+// BUSY: registers for 12 and 16 warps an SM (64 sequences of 8 tokens 142 us with one decay a channel and 117 with one a
 // head; left to the compiler 177 and 125), where there are so many warps.
 template <typename E, bool KDA, int ROWL, bool BUSY>
 __global__ void __launch_bounds__(32, !BUSY ? 1 : KDA || sizeof(E) == 4 ? 12 : 16) step_kernel(const StepArgs a) {
@@ -300,19 +300,20 @@ __global__ void __launch_bounds__(32, !BUSY ? 1 : KDA || sizeof(E) == 4 ? 12 : 1
   request(t0, &x);
   E* op = static_cast<E*>(a.o) + ((int64_t)t0 * a.HV + h) * D + own;
   for (int t = t0; t < t1; ++t, op += (int64_t)a.HV * D) {
-    // decay: the fast exponential, for rows of any type, since states are FP32 whatever the rows are. It is off by up to 2 2^-24 of
-    // its value for |g| < 1 (0.4 too low on average), as much as the accurate one, and by up to 15 at g = -20, where the state
-    // is nothing next to what comes in.
+    // decay: not by the fast exponential, whose values just below one are 0.2 to 0.4 last places too low on average: that adds up
+    // over the tokens (256 of them: states 4.0e-7 of their columns' size from FP64, with this 1.4e-7, as with NumPy's FP32
+    // exponential; 586 ragged and 37 single tokens of the per-channel rule 105.7 and 25.9 us with it, with this 108.1 and
+    // 26.7; one decay a head within 1 %)
     if constexpr (KDA) {
 #pragma unroll
       for (int j = 0; j < L::PAIRS; ++j) {
         const float4 g = x.g[j >> 1];
-        const float2 e = j & 1 ? make_float2(__expf(g.z), __expf(g.w)) : make_float2(__expf(g.x), __expf(g.y));
+        const float2 e = j & 1 ? make_float2(expf(g.z), expf(g.w)) : make_float2(expf(g.x), expf(g.y));
 #pragma unroll
         for (int i = 0; i < 4; ++i) S[j][i] = __fmul2_rn(S[j][i], e);
       }
     } else {
-      const float e = __expf(x.g[0].x);
+      const float e = expf(x.g[0].x);
 #pragma unroll
       for (int j = 0; j < 4 * L::PAIRS; ++j) S[j >> 2][j & 3] = __fmul2_rn(S[j >> 2][j & 3], make_float2(e, e));
     }
@@ -489,10 +490,9 @@ __device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E
     x.get(q[s]);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) blk->v[s][lane + 32 * i] = s < len ? to_f32(raw.v[j + s][lane + 32 * i]) : 0.f;
-    // (the fast exponential, as in step_kernel)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      dec[s][i] = s >= len ? 1.f : KDA || i == 0 ? __expf(raw.g[j + s][KDA ? lane * 4 + i : 0]) : dec[s][0];
+      dec[s][i] = s >= len ? 1.f : KDA || i == 0 ? expf(raw.g[j + s][KDA ? lane * 4 + i : 0]) : dec[s][0];
   }
   const float beta = lane >= STB_BETA && lane - STB_BETA < len ? raw.beta[j + lane - STB_BETA] : 0.f;
   float sums[32];
@@ -544,7 +544,7 @@ __device__ __forceinline__ void prepare_block(const StepArgs& a, const StepRaw<E
 
 // Few sequences of unlike lengths are all on the GPU at once, and an SM's time is the sum of its CTAs': so the CTAs go by
 // falling length, and every second row of them over the SMs in the other direction (586 tokens in lengths
-// 0 .. 160 at HV = 48: 105 us, in the sequences' own order 127 us).
+// 0 .. 160 at HV = 48: 105 us, in the sequences' own order 127 us; with the accurate exponential 108).
 constexpr int STB_SORTED = 32;   // sequences that one warp ranks
 __device__ __forceinline__ int balanced_place(const StepArgs& a, int place, int places) {
   if (a.N > STB_SORTED) return place;
