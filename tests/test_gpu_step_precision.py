@@ -7,7 +7,7 @@ Two measures over all columns of all states (128 values each), and the same for 
              update 1.  The rule contracts (unit keys, beta at most 1), so it decays with the state:
              E_t = 40 U (|s_t| + |v_t|) + max(a_t) E_{t-1}.
   typical    The root of the mean square of (error / size) is at most 8 times that of the recurrence taken in FP32 by
-             NumPy: sums in another order, an exponential within two last places for half a one, and rows rounded to 16 bits.
+             NumPy: sums in another order, and room for a decay's exponential that is off by a few last places.
 A copy that keeps its state in 11 bits, or takes its products of 11 bits' operands, fails the second."""
 import numpy as np
 import pytest
