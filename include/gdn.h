@@ -437,6 +437,125 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_problem *prob, const void *q, const
 gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double original,
                                 double fast, double slow, double *freq, float *mscale);
 
+/*
+ * Linear attention with a fixed decay per value head (retention): the rule without its delta term,
+ *
+ *     S_t = a S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   a = exp(decay[h])
+ *
+ * over packed documents, forward, backward and, for generation, token by token on a pool of states (arXiv:2307.08621 gives
+ * the three forms).  q and k enter as they are: norms, rotations and feature maps are the caller's (gdn_qk_norm_rope_fwd).
+ *   q, k, v    rows of 128 values per head (H, H, HV heads; q/k head h / (HV/H) belongs to value head h), BF16, heads
+ *              contiguous, q_stride, k_stride, v_stride elements from token to token (0: contiguous), multiples of 8;
+ *              dq, dk, dv lie as q, k, v.  o, dO [T][HV][128] contiguous.
+ *   decay      [HV] FP32 log decays, <= 0 (-inf: nothing is kept); constants of the layer, without a gradient.
+ *   s_in       [N][HV][128][128] FP32 (S[dk][dv], the layout of gdn_fwd_states' and of the pools): the state each document
+ *              starts from; NULL: zero.
+ *   s_out      the state after each document's last token; NULL: not wanted.  An empty document passes s_in through.
+ *              It may be s_in.
+ *   ds_out, ds_in   the gradients of s_out (NULL: zero) and s_in (NULL: not wanted; may be ds_out).
+ *   dev_err    a device int, zero at first (gdn_device_status(dev_err) reads it, the call never clears it):
+ *              GDN_ERR_INVALID_ARG where the device copy of cu_seqlens has other bounds than the host's, whose documents are
+ *              then left out, GDN_ERR_TIMEOUT for a bounded wait that ran out.
+ * The forward needs nothing saved for the backward but its inputs: the backward walks the documents again.  Sums and
+ * states are FP32; the state keeps FP32's exactness, and is rounded to BF16 once, where it meets the rows.
+ * Inside a chunk of 128 tokens of a document, a value that is not finite also reaches the tokens before it; those of other
+ * documents, and rows outside cu_seqlens' range, reach none.
+ * Results are the same bits from run to run; dq and dk are sums over the value heads of a group in order.
+ * Outputs do not overlap inputs, but for the states as said.  T below 2^30 (else GDN_ERR_UNSUPPORTED).
+ * gdn_la_workspace_bytes: what the forward and the backward need (16-byte aligned; 0: nothing).
+ */
+typedef struct {
+    int64_t T;        /* total packed tokens (= cu_seqlens[N]) */
+    int32_t N;        /* documents (>= 1; empty ones allowed) */
+    int32_t H;        /* query/key heads */
+    int32_t HV;       /* value heads, a multiple of H */
+    int32_t dk;       /* must be 128 */
+    int32_t dv;       /* must be 128 */
+    float scale;      /* output scale */
+    int32_t segment;  /* 0: the planner decides where documents are cut into segments that run side by side;
+                         > 0: segments of so many chunks of 128 tokens */
+    int64_t q_stride, k_stride, v_stride;
+} gdn_la_problem;
+gdn_status gdn_la_workspace_bytes(const gdn_la_problem *prob, const int32_t *cu_seqlens_host, size_t *fwd_bytes,
+                                  size_t *bwd_bytes);
+gdn_status gdn_la_fwd(const gdn_la_problem *prob, const void *q, const void *k, const void *v, const float *decay,
+                      const int32_t *cu_seqlens_dev, const int32_t *cu_seqlens_host, const float *s_in, void *o,
+                      float *s_out, int32_t *dev_err, void *workspace, size_t ws_bytes, struct CUstream_st *stream);
+gdn_status gdn_la_bwd(const gdn_la_problem *prob, const void *q, const void *k, const void *v, const float *decay,
+                      const int32_t *cu_seqlens_dev, const int32_t *cu_seqlens_host, const float *s_in, const void *dO,
+                      const float *ds_out, void *dq, void *dk, void *dv, float *ds_in, int32_t *dev_err,
+                      void *workspace, size_t ws_bytes, struct CUstream_st *stream);
+/*
+ * The recurrent form: gdn_step's arguments and conventions, with decay [HV] in place of g and beta, and l2norm 0 (else
+ * GDN_ERR_UNSUPPORTED).  Types BF16, FP16, FP32.
+ */
+gdn_status gdn_la_step(const gdn_step_problem *prob, const void *q, const void *k, const void *v, const float *decay,
+                       const int32_t *cu_seqlens_dev, const int32_t *slot_in, const int32_t *slot_out, float *states,
+                       void *o, int32_t *dev_err, struct CUstream_st *stream);
+
+/*
+ * The root-mean-square norm in front of a layer, with the residual's addition, and its gradients.  For each of T rows of C:
+ *     h = x + r, rounded to the type (r NULL: h = x);   z = w h / sqrt(mean h^2 + eps)
+ *     y = z rounded to the type;   y8 = z / s in E4M3,   s = max |z| / 448 (at least 2^-100)
+ * with one s to `group` neighbouring values (32, 64 or 128, of which C is a multiple) or, with group 0, to a row.
+ *   x, r, h, y   `dtype`, x_stride, r_stride, h_stride, y_stride elements from row to row (0: C).  h may be x or r (same
+ *                stride), and NULL where r is; y, or y8 with scales, may be NULL.
+ *   y8           [T][C] bytes, contiguous, C apart;  scales [T][C / group] FP32 ([T] with group 0);  w [C] FP32.
+ * Backward, of y (what reads y8 takes its gradient to be z's): with h as the forward left it (h_stride), dy (y_stride) and
+ * dres (r_stride), the gradient that reaches h along the stream (NULL: none), dx (x_stride) is the gradient of x and of r, and
+ * dw [C] FP32 (NULL: not wanted) the weights', summed over the rows in a fixed order.  dx may be dy or dres (same stride).
+ * Sums in FP32.  Any C up to 2^20 (else GDN_ERR_UNSUPPORTED), any alignment of at least the element's; the fast kernels take
+ * C a multiple of 8 up to 16384 with strides and pointers in whole 16 bytes, the others are several times slower.
+ * gdn_add_norm_workspace_bytes: the backward's scratch (16-byte aligned; not needed without dw).
+ */
+typedef struct {
+    int64_t T;        /* rows; 0 writes only a zero dw */
+    int32_t C;        /* values of a row */
+    int32_t dtype;    /* GDN_BF16, GDN_FP16, GDN_FP32 */
+    int32_t group;    /* values to a scale of y8; 0: a row */
+    float eps;
+    int64_t x_stride, r_stride, h_stride, y_stride;
+} gdn_norm_problem;
+gdn_status gdn_add_norm_workspace_bytes(const gdn_norm_problem *prob, size_t *workspace_bytes);
+gdn_status gdn_add_norm_fwd(const gdn_norm_problem *prob, const void *x, const void *r, const float *w, void *h, void *y,
+                            void *y8, float *scales, struct CUstream_st *stream);
+gdn_status gdn_add_norm_bwd(const gdn_norm_problem *prob, const void *h, const float *w, const void *dy, const void *dres,
+                            void *dx, float *dw, void *workspace, size_t ws_bytes, struct CUstream_st *stream);
+
+/*
+ * The tables of a generation step (cu_seqlens, positions, slot_in, slot_out of the entry points above) from the requests'
+ * lengths, with the blocks of the states' pools handed out on the way; all on the GPU, so that a captured step goes on by
+ * itself.  A request keeps a state to every `block` tokens: block j's slot holds the state after the last token taken of
+ * j block .. (j+1) block - 1, so earlier blocks are what others with the same beginning can start from.  With `block` as long
+ * as the longest context a request has one slot.
+ *   lengths      [N] tokens that each request takes now; -1: it has ended, its blocks go back
+ *   context      [N] tokens it has taken before;  context_out [N]: after this step (0 where it has ended)
+ *   block_table  [N][max_blocks] slots of its blocks: ceil(context / block) are read, the new ones written behind them
+ *   free_list    [slots], free_count, free_count_out [1]: the slots that are free, taken from the end.  Blocks that go back
+ *                are put there first, in the order of requests and blocks, then new ones are taken, in that order.
+ *   cu_seqlens   [N+1];  positions [T] (NULL: not wanted), of each token, 0 past the last
+ *   slot_in      [N] slot of the state before the first token, -1: none yet
+ *   slot_out     [T] where the state after each token goes: its block's slot for the last token of a block and of this
+ *                step, else -1
+ * Where the tokens are more than T, or the blocks more than are free, the first request that does not fit and all after it
+ * take no tokens in this step: their entries of cu_seqlens repeat and their context stays.
+ * context_out may be context, free_count_out free_count (the call then works on the books in place).
+ * dev_err: GDN_ERR_DEVICE for a length below -1, a context or length past max_blocks * block (the request takes nothing and
+ * gives nothing back), a free_count outside the pool or more blocks given back than there are.
+ * N up to 16384 and max_blocks * block below 2^30 (else GDN_ERR_UNSUPPORTED).  The pointers may start at any element.
+ */
+typedef struct {
+    int32_t N;           /* requests */
+    int32_t T;           /* entries of positions and slot_out */
+    int32_t block;       /* tokens of a block */
+    int32_t max_blocks;  /* entries of a row of block_table */
+    int32_t slots;       /* states in the pool */
+} gdn_tables_problem;
+gdn_status gdn_step_tables(const gdn_tables_problem *prob, const int32_t *lengths, const int32_t *context,
+                           int32_t *context_out, int32_t *block_table, int32_t *free_list, const int32_t *free_count,
+                           int32_t *free_count_out, int32_t *cu_seqlens, int32_t *positions, int32_t *slot_in,
+                           int32_t *slot_out, int32_t *dev_err, struct CUstream_st *stream);
+
 /* Static description of a status code. */
 const char *gdn_status_string(gdn_status s);
 

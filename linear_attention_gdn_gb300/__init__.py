@@ -26,9 +26,11 @@ EXPORTS = ("gdn_saved_bytes", "gdn_fwd", "gdn_bwd", "gdn_ckpt_fwd_bwd", "gdn_sta
            "gdn_profile_read", "gdn_fwd_noalloc", "gdn_fwd_states", "gdn_bwd_states", "gdn_conv1d_workspace_bytes",
            "gdn_conv1d_fwd", "gdn_conv1d_bwd", "gdn_backward_tape_offsets", "gdn_kda_saved_bytes", "gdn_kda_fwd",
            "gdn_kda_bwd", "gdn_tensor_probe", "gdn_step", "gdn_kda_step", "gdn_conv1d_step", "gdn_qk_workspace_bytes",
-           "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd", "gdn_rope_frequencies")
+           "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd", "gdn_rope_frequencies", "gdn_la_workspace_bytes",
+           "gdn_la_fwd", "gdn_la_bwd", "gdn_la_step", "gdn_add_norm_workspace_bytes", "gdn_add_norm_fwd",
+           "gdn_add_norm_bwd", "gdn_step_tables")
 SAVED_FULL, SAVED_REPLAY = 0, 1   # gdn_problem.saved_form
-BF16, FP16, FP32 = 0, 1, 2        # dtype of the step and q/k problems
+BF16, FP16, FP32 = 0, 1, 2        # dtype of the step, q/k and norm problems
 ROPE_HALF, ROPE_PAIRS = 0, 1      # gdn_qk_problem.layout
 NORM_NONE, NORM_RMS, NORM_L2 = 0, 1, 2   # gdn_qk_problem.norm
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3   # scalings of gdn_rope_frequencies
@@ -77,6 +79,23 @@ class gdn_qk_problem(ctypes.Structure):
                 ("ko_token", ctypes.c_int64), ("ko_head", ctypes.c_int64)]
 
 
+class gdn_la_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("N", ctypes.c_int32), ("H", ctypes.c_int32), ("HV", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("scale", ctypes.c_float), ("segment", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class gdn_norm_problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("h_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64)]
+
+
+class gdn_tables_problem(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("T", ctypes.c_int32), ("block", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("slots", ctypes.c_int32)]
+
+
 def _dtype(dtype) -> int:
     """The library's number of an element type given as that number or as a torch dtype."""
     if isinstance(dtype, int):
@@ -104,6 +123,22 @@ def qk_problem(T, HQ, HK, D=128, rot=None, layout=ROPE_HALF, norm=NORM_RMS, eps=
     return gdn_qk_problem(int(T), int(N), int(HQ), int(HK), int(D), int(D if rot is None else rot), int(layout),
                           int(norm), _dtype(dtype), float(eps), float(mscale),
                           *(int(s) for pair in (q_strides, k_strides, qo_strides, ko_strides) for s in pair))
+
+
+def la_problem(T, N, H, HV, scale=128 ** -0.5, segment=0, strides=(0, 0, 0), dk=128, dv=128) -> gdn_la_problem:
+    """strides: elements from token to token of q, k and v (0: contiguous), and of their gradients."""
+    return gdn_la_problem(int(T), int(N), int(H), int(HV), int(dk), int(dv), float(scale), int(segment),
+                          *(int(s) for s in strides))
+
+
+def norm_problem(T, C, eps=1e-6, dtype=BF16, group=0, strides=(0, 0, 0, 0)) -> gdn_norm_problem:
+    """group: values to a scale of the 8-bit output (0: a row).  strides: elements from row to row of x, r, h and y (0:
+    contiguous)."""
+    return gdn_norm_problem(int(T), int(C), _dtype(dtype), int(group), float(eps), *(int(s) for s in strides))
+
+
+def tables_problem(N, T, block, max_blocks, slots) -> gdn_tables_problem:
+    return gdn_tables_problem(int(N), int(T), int(block), int(max_blocks), int(slots))
 
 
 def conv_problem(T, N, C, W=4) -> gdn_conv_problem:
@@ -159,6 +194,18 @@ def _load():
     L.gdn_rope_frequencies.argtypes = [ctypes.c_int32, f64, ctypes.c_int32, f64, f64, f64, f64, vp, f32p]
     for name in ("gdn_step", "gdn_kda_step", "gdn_conv1d_step", "gdn_qk_workspace_bytes", "gdn_qk_norm_rope_fwd",
                  "gdn_qk_norm_rope_bwd", "gdn_rope_frequencies"):
+        getattr(L, name).restype = ctypes.c_int
+    lp, mp, bp = (ctypes.POINTER(t) for t in (gdn_la_problem, gdn_norm_problem, gdn_tables_problem))
+    L.gdn_la_workspace_bytes.argtypes = [lp, i32p, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    L.gdn_la_fwd.argtypes = [lp] + [vp] * 11 + [sz, vp]
+    L.gdn_la_bwd.argtypes = [lp] + [vp] * 15 + [sz, vp]
+    L.gdn_la_step.argtypes = [sp] + [vp] * 11
+    L.gdn_add_norm_workspace_bytes.argtypes = [mp, ctypes.POINTER(sz)]
+    L.gdn_add_norm_fwd.argtypes = [mp] + [vp] * 8
+    L.gdn_add_norm_bwd.argtypes = [mp] + [vp] * 7 + [sz, vp]
+    L.gdn_step_tables.argtypes = [bp] + [vp] * 13
+    for name in ("gdn_la_workspace_bytes", "gdn_la_fwd", "gdn_la_bwd", "gdn_la_step", "gdn_add_norm_workspace_bytes",
+                 "gdn_add_norm_fwd", "gdn_add_norm_bwd", "gdn_step_tables"):
         getattr(L, name).restype = ctypes.c_int
     L.gdn_profile_enable.argtypes = [ctypes.c_int]
     L.gdn_profile_enable.restype = None
@@ -510,6 +557,79 @@ def gdn_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig
     _check(lib.gdn_rope_frequencies(int(rot), float(base), int(scaling), float(factor), float(original), float(fast),
                                     float(slow), _ptr(freq), ctypes.byref(m)), "gdn_rope_frequencies")
     return freq, m.value
+
+
+def gdn_la_workspace_bytes(prob, cu_seqlens_host):
+    """(forward's, backward's) bytes of workspace of the linear attention."""
+    cu, cup = _cu_host(cu_seqlens_host)
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib.gdn_la_workspace_bytes(ctypes.byref(prob), cup, ctypes.byref(f), ctypes.byref(b)), "gdn_la_workspace_bytes")
+    return f.value, b.value
+
+
+def _documents(prob, cu_seqlens_host, where):
+    """The host's cu_seqlens as the library reads it, and its address."""
+    cu = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int32))
+    if cu.ndim != 1 or cu.size < prob.N + 1:
+        raise ValueError(f"{where}: cu_seqlens_host has {cu.size} entries for {prob.N} documents")
+    return cu, cu.__array_interface__["data"][0]
+
+
+def _bytes(workspace, ws_bytes):
+    if ws_bytes is not None:
+        return ws_bytes
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def gdn_la_fwd(prob, q, k, v, decay, cu_seqlens_dev, cu_seqlens_host, s_in, o, s_out, dev_err, workspace, ws_bytes=None,
+               stream=None):
+    """Linear attention with a fixed decay per head: decay FP32 [HV]; s_in, s_out FP32 [N, HV, 128, 128] or None; dev_err a
+    device int32, zero at first; see include/gdn.h."""
+    cu, at = _documents(prob, cu_seqlens_host, "gdn_la_fwd")
+    _call("gdn_la_fwd", gdn_la_problem, prob, _bytes(workspace, ws_bytes), stream, q, k, v, decay, cu_seqlens_dev, at, s_in,
+          o, s_out, dev_err, workspace)
+
+
+def gdn_la_bwd(prob, q, k, v, decay, cu_seqlens_dev, cu_seqlens_host, s_in, dO, ds_out, dq, dk, dv, ds_in, dev_err,
+               workspace, ws_bytes=None, stream=None):
+    """Gradients of gdn_la_fwd: dq, dk, dv laid out as q, k, v; s_in as the forward's; ds_out, ds_in FP32
+    [N, HV, 128, 128] or None; see include/gdn.h."""
+    cu, at = _documents(prob, cu_seqlens_host, "gdn_la_bwd")
+    _call("gdn_la_bwd", gdn_la_problem, prob, _bytes(workspace, ws_bytes), stream, q, k, v, decay, cu_seqlens_dev, at, s_in,
+          dO, ds_out, dq, dk, dv, ds_in, dev_err, workspace)
+
+
+def gdn_la_step(prob, q, k, v, decay, states, o, dev_err, cu_seqlens_dev=None, slot_in=None, slot_out=None, stream=None):
+    """The recurrent form of gdn_la_fwd on a pool of states, FP32 [slots, HV, 128, 128]: prob is a step_problem with
+    l2norm=False; decay FP32 [HV]; see include/gdn.h."""
+    _call("gdn_la_step", gdn_step_problem, prob, None, stream, q, k, v, decay, cu_seqlens_dev, slot_in, slot_out, states, o,
+          dev_err)
+
+
+def gdn_add_norm_workspace_bytes(prob) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.gdn_add_norm_workspace_bytes(ctypes.byref(prob), ctypes.byref(n)), "gdn_add_norm_workspace_bytes")
+    return int(n.value)
+
+
+def gdn_add_norm_fwd(prob, x, r, w, h, y, y8=None, scales=None, stream=None):
+    """h = x + r and its root-mean-square norm: x, r, h, y [T, C] (r, h and y may be None); y8 E4M3 [T, C] with FP32 scales
+    [T, C / group]; w FP32 [C]; see include/gdn.h."""
+    _call("gdn_add_norm_fwd", gdn_norm_problem, prob, None, stream, x, r, w, h, y, y8, scales)
+
+
+def gdn_add_norm_bwd(prob, h, w, dy, dres, dx, dw, workspace, ws_bytes=None, stream=None):
+    """Gradients of gdn_add_norm_fwd: dres (or None) is what reaches h along the stream, dx the gradient of x and of r, dw
+    FP32 [C] or None (the workspace is then not needed); see include/gdn.h."""
+    _call("gdn_add_norm_bwd", gdn_norm_problem, prob, _bytes(workspace, ws_bytes), stream, h, w, dy, dres, dx, dw, workspace)
+
+
+def gdn_step_tables(prob, lengths, context, context_out, block_table, free_list, free_count, free_count_out, cu_seqlens,
+                    positions, slot_in, slot_out, dev_err, stream=None):
+    """The tables of a generation step from the requests' lengths, all int32 on the device, with blocks of the states' pool
+    handed out on the way; see include/gdn.h."""
+    _call("gdn_step_tables", gdn_tables_problem, prob, None, stream, lengths, context, context_out, block_table, free_list,
+          free_count, free_count_out, cu_seqlens, positions, slot_in, slot_out, dev_err)
 
 
 class Buffers:

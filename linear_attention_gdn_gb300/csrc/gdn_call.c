@@ -10,12 +10,12 @@
 #include <Python.h>
 #include <stddef.h>
 
-#define MOST 14
+#define MOST 15   // pointers
 
 typedef const void *P;
-typedef int (*entry9)(P, P, P, P, P, P, P, P, P, P, P);
-typedef int (*entry11)(P, P, P, P, P, P, P, P, P, P, P, P, P);
-typedef int (*entry14)(P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, size_t, P);
+#define P7 P, P, P, P, P, P, P
+#define A7 p[0], p[1], p[2], p[3], p[4], p[5], p[6]
+#define ENTRY(...) ((int (*)(P, __VA_ARGS__))entry)
 
 static PyObject *data_ptr_name;
 
@@ -41,24 +41,34 @@ static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   size_t size = 0;
   int status;
   (void)self;
-  if (count != 9 && count != 11 && count != 14)
-    return PyErr_Format(PyExc_TypeError, "call() takes 9, 11 or 14 pointers (%zd given)", count);
-  if ((count == 14) != (args[2] != Py_None)) return PyErr_Format(PyExc_TypeError, "a size goes with 14 pointers");
+  const int sized = n > 2 && args[2] != Py_None;
+  if (sized ? count != 7 && count != 11 && count != 14 && count != 15
+            : count != 7 && (count < 9 || count > 12))
+    return PyErr_Format(PyExc_TypeError, "call() takes 7 or 9 to 12 pointers, with a size 7, 11, 14 or 15 (%zd given)", count);
   if (!address(args[0], &entry) || !address(args[1], &prob) || !address(args[3], &stream)) return NULL;
-  if (args[2] != Py_None) {
+  if (sized) {
     size = PyLong_AsSize_t(args[2]);
     if (size == (size_t)-1 && PyErr_Occurred()) return NULL;
   }
   for (Py_ssize_t i = 0; i < count; ++i)
     if (!address(args[4 + i], &p[i])) return NULL;
   Py_BEGIN_ALLOW_THREADS
-  if (count == 9)
-    status = ((entry9)entry)(prob, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], stream);
-  else if (count == 11)
-    status = ((entry11)entry)(prob, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], stream);
-  else
-    status = ((entry14)entry)(prob, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], p[11], p[12],
-                              p[13], size, stream);
+  if (sized) switch (count) {
+    case 7: status = ENTRY(P7, size_t, P)(prob, A7, size, stream); break;
+    case 11: status = ENTRY(P7, P, P, P, P, size_t, P)(prob, A7, p[7], p[8], p[9], p[10], size, stream); break;
+    case 14:
+      status = ENTRY(P7, P7, size_t, P)(prob, A7, p[7], p[8], p[9], p[10], p[11], p[12], p[13], size, stream);
+      break;
+    default:
+      status = ENTRY(P7, P7, P, size_t, P)(prob, A7, p[7], p[8], p[9], p[10], p[11], p[12], p[13], p[14], size, stream);
+      break;
+  } else switch (count) {
+    case 7: status = ENTRY(P7, P)(prob, A7, stream); break;
+    case 9: status = ENTRY(P7, P, P, P)(prob, A7, p[7], p[8], stream); break;
+    case 10: status = ENTRY(P7, P, P, P, P)(prob, A7, p[7], p[8], p[9], stream); break;
+    case 11: status = ENTRY(P7, P, P, P, P, P)(prob, A7, p[7], p[8], p[9], p[10], stream); break;
+    default: status = ENTRY(P7, P, P, P, P, P, P)(prob, A7, p[7], p[8], p[9], p[10], p[11], stream); break;
+  }
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(status);
 }

@@ -1,0 +1,53 @@
+// gdn_la.cuh -- what the walk kernel, its launches and the host layer of the linear attention share.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+constexpr int LA_CH = 128;   // tokens of a chunk
+
+// How the segments of all documents are numbered: document d has max(1, ceil(chunks / len)) of them, in order.
+struct LaSegments {
+  const int* cu;   // [N+1] on the device
+  int N, len, total;   // chunks of a segment; segments as counted from the host's copy
+  int64_t T;
+};
+
+// One walk: out_r = sum over the tokens c that r sees of p_scale a^|r-c| (x_r . y_c) z_c  +  row_scale a^.. Z^T x_r, with
+// the state Z = sum of state_scale a^.. y_c z_c^T of the chunks before (forward) or behind (reverse).
+struct LaWalk {
+  CUtensorMap tx, ty, tz;
+  LaSegments seg;
+  const float* decay;     // [HV] log decays
+  int HV, gx, gy, gz;     // value heads to a head of x, y, z
+  float p_scale, row_scale, state_scale;
+  const float* init;      // states to start from, FP32 [.][HV][128][128], or null: zero
+  int init_segments;      // one a segment (else one a document)
+  int init_t;             // stored [z][y] (else [y][z])
+  float* sums;            // [segments][HV][y][z]: what each segment adds, for the carry (walks without output)
+  float* last;            // [N][HV][y][z]: the state that a document leaves, or null
+  void* out;              // BF16 rows of 128, or FP32
+  int64_t out_token, out_head;   // elements
+  int* err;
+};
+
+struct LaCarry {
+  LaSegments seg;
+  const float* decay;
+  int HV, init_t, reverse;
+  const float* init;   // [N][HV] or null
+  float* sums;         // in: what a segment adds; out: the state it starts from
+  int* err;
+};
+
+cudaError_t launch_la_walk(const LaWalk& a, bool reverse, int terms, bool f32, cudaStream_t s);
+cudaError_t launch_la_sums(const LaWalk& a, bool reverse, cudaStream_t s);
+cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s);
+// out[t][h] = sum over the G value heads of h, in order, of part[t][h G + i]
+cudaError_t launch_la_reduce(const float* part, void* out, int64_t T, int H, int G, int64_t out_token, cudaStream_t s);
+
+}  // namespace gdn

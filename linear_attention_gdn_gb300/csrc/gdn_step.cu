@@ -22,6 +22,7 @@
 #include "gdn_internal.h"
 #include "gdn_launch.cuh"
 #include "gdn_prof.h"
+#include "gdn_sequences.cuh"
 
 namespace gdn {
 
@@ -47,18 +48,6 @@ struct StepArgs {
   int N, H, HV, G, slots, l2norm, sms;
   float scale;
 };
-
-// bounds of sequence n's tokens; false (and the error word) where they are none
-__device__ __forceinline__ bool sequence_bounds(const int* cu, int n, int64_t T, int* t0, int* t1) {
-  if (!cu) {
-    *t0 = n;
-    *t1 = n + 1;
-    return true;
-  }
-  *t0 = cu[n];
-  *t1 = cu[n + 1];
-  return *t0 >= 0 && *t1 >= *t0 && *t1 <= T;
-}
 
 // What follows the sums of one token, the same in both kernels of single tokens: e = rk d of a column from its u, and
 // its output from S'^T q^ and e.
@@ -812,11 +801,6 @@ template <typename E, bool KDA> static bool launch_step(const StepArgs& a, bool 
     launch_chained(step_kernel<E, KDA, 8, true>, heads * StepLayout<8>::PARTS, 32, 0, s, a);
   }
   return true;
-}
-
-static bool step_stride(int64_t* s, int heads, int esize) {
-  if (*s == 0) *s = (int64_t)heads * D;
-  return *s >= (int64_t)heads * D && *s * esize % 16 == 0;
 }
 
 template <bool KDA>

@@ -1,0 +1,198 @@
+"""Linear attention with a fixed decay per head on the GPU: forward, backward and states against the FP64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_gdn_gb300 as gdn
+from tests.la_testutil import SCALE, expect, f64, make, on_gpu
+from tests.step_testutil import within
+
+pytestmark = pytest.mark.gpu
+
+
+def problem(x, d, segment=0):
+    return gdn.la_problem(len(x["q"]), len(x["cu"]) - 1, x["q"].shape[1], x["v"].shape[1], SCALE, segment,
+                          tuple(d[m].stride(0) for m in "qkv"))
+
+
+def run(x, d, segment=0, states=True, poison=float("nan"), stream=None):
+    """Every output, from buffers filled with poison."""
+    prob = problem(x, d, segment)
+    fill = lambda t: torch.full(t.shape, poison, dtype=t.dtype, device="cuda")  # noqa: E731
+    f, b = gdn.gdn_la_workspace_bytes(prob, x["cu"])
+    ws = torch.full((max(f, b, 16),), 255, dtype=torch.uint8, device="cuda")   # (all NaN)
+    r = dict(o=fill(d["dO"]), s_out=None, ds_in=None)
+    if states:
+        N, HV = len(x["cu"]) - 1, x["v"].shape[1]
+        r["s_out"], r["ds_in"] = (torch.full((N, HV, 128, 128), poison, device="cuda") for _ in range(2))
+    for m in "qkv":   # laid out as q, k, v, poison between the rows, too
+        flat = torch.full((d[m].shape[0] * d[m].stride(0) + 1,), poison, dtype=d[m].dtype, device="cuda")
+        r["d" + m] = flat.as_strided(d[m].shape, d[m].stride())
+    gdn.gdn_la_fwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], r["o"], r["s_out"], d["err"],
+                   ws, f, stream=stream)
+    ws.fill_(255)
+    gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], d["dO"], d["ds_out"], r["dq"],
+                   r["dk"], r["dv"], r["ds_in"], d["err"], ws, b, stream=stream)
+    assert gdn.gdn_device_status(d["err"]) == 0
+    return r
+
+
+def check(x, r):
+    want = expect(x, x["q"].shape[1], x["v"].shape[1])
+    for name, t in r.items():
+        if t is not None:
+            within(name, t, *want[name])
+
+
+CASES = [
+    ([1], 1, 1), ([2, 0, 1], 1, 2), ([0, 5], 2, 2), ([128], 1, 1), ([127, 129], 1, 3), ([256, 1], 2, 2), ([64, 200, 0, 33], 2, 6),
+    ([300], 1, 4), ([513, 140], 1, 1),
+]
+
+
+@pytest.mark.parametrize("lengths,H,HV", CASES)
+def test_documents(lengths, H, HV):
+    x = make(lengths, H, HV, seed=sum(lengths))
+    d = on_gpu(x)
+    check(x, run(x, d))
+
+
+@pytest.mark.parametrize("segment", [1, 2, 3])
+@pytest.mark.parametrize("lengths,H,HV", [([700], 1, 2), ([300, 0, 129, 1], 1, 1), ([128, 513], 2, 2)])
+def test_segments(lengths, H, HV, segment):
+    x = make(lengths, H, HV, seed=segment)
+    d = on_gpu(x)
+    check(x, run(x, d, segment))
+
+
+@pytest.mark.parametrize("segment", [0, 1])
+def test_without_states(segment):
+    x = make([200, 300], 1, 2, states=False)
+    d = on_gpu(x)
+    check(x, run(x, d, segment, states=False))
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-6, -2.0, -30.0, -1e9, float("-inf")])
+@pytest.mark.parametrize("segment", [0, 1])
+def test_decays(decay, segment):
+    x = make([290], 1, 1, seed=7, decay=decay)
+    d = on_gpu(x)
+    check(x, run(x, d, segment))
+
+
+@pytest.mark.parametrize("pad", [8, 128])
+def test_strided_rows(pad):
+    """Views of wider rows, in and out: what lies between is neither read nor written."""
+    x = make([140, 7], 2, 4, seed=pad)
+    d = on_gpu(x, pad)
+    r = run(x, d)
+    check(x, r)
+    for m in "qkv":
+        t = r["d" + m]
+        rest = t.as_strided((t.shape[0] - 1, pad), (t.stride(0), 1), t.shape[1] * 128)   # (the last row has none behind it)
+        assert rest.isnan().all()
+
+
+def test_views_of_one_packed_row():
+    H, HV, T = 1, 2, 150
+    x = make([T], H, HV, seed=3)
+    d = on_gpu(x)
+    rows = torch.cat([d["q"], d["k"], d["v"]], 1)
+    d["q"], d["k"], d["v"] = rows[:, :H], rows[:, H:2 * H], rows[:, 2 * H:]
+    check(x, run(x, d))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("segment", [0, 1])
+def test_other_documents_values_take_no_part(bad, segment):
+    """A document of infinite or NaN values changes no bit of those before and behind it, in its chunks' rows or not."""
+    lengths = [130, 70, 131]
+    x = make(lengths, 1, 2, seed=11)
+    clean = run(x, on_gpu(x), segment)
+    y = {m: t.clone() if torch.is_tensor(t) else t for m, t in x.items()}
+    for m in ("q", "k", "v", "dO"):
+        y[m][130:200] = bad
+    y["s_in"][1] = bad
+    got = run(y, on_gpu(y), segment)
+    for m, t in got.items():
+        if m in ("s_out", "ds_in"):
+            assert torch.equal(t[[0, 2]], clean[m][[0, 2]])
+        else:
+            assert torch.equal(t[:130], clean[m][:130]) and torch.equal(t[200:], clean[m][200:])
+
+
+@pytest.mark.parametrize("segment", [0, 2])
+def test_same_bits_again_and_in_place(segment):
+    x = make([400, 3], 1, 3, seed=2)
+    d = on_gpu(x)
+    first, second = run(x, d, segment), run(x, d, segment)
+    for m in first:
+        assert torch.equal(first[m], second[m])
+    prob = problem(x, d, segment)
+    f, b = gdn.gdn_la_workspace_bytes(prob, x["cu"])
+    ws = torch.empty(max(f, b, 16), dtype=torch.uint8, device="cuda")
+    states, grads = d["s_in"].clone(), d["ds_out"].clone()
+    o = torch.empty_like(first["o"])
+    gdn.gdn_la_fwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], states, o, states, d["err"], ws)
+    assert torch.equal(states, first["s_out"]) and torch.equal(o, first["o"])
+    gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], d["dO"], grads, first["dq"],
+                   first["dk"], first["dv"], grads, d["err"], ws)
+    assert torch.equal(grads, first["ds_in"])
+
+
+def test_no_tokens():
+    x = make([0, 0], 1, 2)
+    d = on_gpu(x)
+    r = run(x, d)
+    assert torch.equal(r["s_out"], d["s_in"]) and torch.equal(r["ds_in"], d["ds_out"])
+
+
+def test_a_wrong_device_copy_is_reported():
+    x = make([100, 60], 1, 1)
+    d = on_gpu(x)
+    for wrong in ([0, 100, 159], [0, 161, 160], [1, 100, 160], [0, -5, 160], [0, 100, 2 ** 30]):
+        prob = problem(x, d)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o = torch.empty_like(d["dO"])
+        gdn.gdn_la_fwd(prob, d["q"], d["k"], d["v"], d["decay"], torch.tensor(wrong, dtype=torch.int32, device="cuda"), x["cu"],
+                       None, o, None, err, None)
+        assert gdn.gdn_device_status(err) == 1
+
+
+def test_other_stream_and_graph():
+    x = make([260, 50], 1, 2, seed=4)
+    d = on_gpu(x)
+    want = run(x, d, 1)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = run(x, d, 1, stream=s)
+    s.synchronize()
+    for m in want:
+        assert torch.equal(want[m], got[m])
+    prob = problem(x, d, 1)
+    f, _ = gdn.gdn_la_workspace_bytes(prob, x["cu"])
+    ws = torch.empty(f, dtype=torch.uint8, device="cuda")
+    o, s_out = torch.empty_like(want["o"]), torch.empty_like(want["s_out"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_la_fwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], o, s_out, d["err"], ws)
+    for _ in range(2):
+        o.fill_(float("nan"))
+        s_out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want["o"]) and torch.equal(s_out, want["s_out"])
+
+
+def test_gradients_are_differences():
+    """The forward is linear in v, so a forward of a step in v is an exact difference: its product with dO is dv's with
+    the step.  Both sides are sums of values whose roundings are independent, each at most its tolerance off: within six
+    times the root of the sum of their squares."""
+    x = make([150], 1, 2, states=False, seed=9)
+    y = dict(x, v=torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(1)).bfloat16())
+    r, moved = run(x, on_gpu(x), states=False), run(y, on_gpu(y), states=False)
+    dO, step = f64(x["dO"]), f64(y["v"])
+    left, right = (f64(moved["o"]) * dO).sum(), (f64(r["dv"]) * step).sum()
+    off = ((expect(y, 1, 2)["o"][1] * dO) ** 2).sum() + ((expect(x, 1, 2)["dv"][1] * step) ** 2).sum()
+    assert abs(left - right) <= 6 * np.sqrt(off)
