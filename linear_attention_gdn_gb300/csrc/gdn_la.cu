@@ -6,11 +6,13 @@
 //   reverse  dv: x, y, z = k, q, dO;    dk : v, dO, q     (r sees c >= r; Z is the gradient behind the chunk)
 //
 // A CTA walks one segment of a document for one value head.  Per chunk, on the tensor cores:
-//   QK[r][c] = x_r . y_c;  Oi = x Z;  P = decayed, masked QK;  Op = P z;  dZ[z][y] = z^T (decayed y);  out = a^.. Oi + Op
-// P goes back to TMEM as the left operand.  The state is FP32 in registers (thread: one row z, 64 columns y), rounded to
-// BF16 once for the product with x.  The decayed y is given to the product as a sum of BF16 terms, so that the
-// state keeps FP32's exactness: two terms (2^-17) where only BF16 results come of it, three (2^-25) where the state itself
-// is handed out.
+//   QK[r][c] = x_r . y_c;  O = x Z;  dZ[y][z] = (decayed y)^T z;  P = decayed, masked QK;  O = a^.. O + P z
+// P and the decayed y go to TMEM as left operands, so that shared memory, which all operands pass, is read least.  The state
+// is FP32 in registers (thread: one row y, 64 columns z), rounded to BF16 once for the product with x.  The decayed y is given
+// to the product as a sum of BF16 terms, so that the state keeps FP32's exactness: two terms (2^-17) where only BF16 results
+// come of it, three (2^-25) where the state itself is handed out.
+// Two sets of warps work side by side: one makes P, scales O and writes it out, the other makes the decayed y, a quarter of
+// a chunk at a time in a ring, and carries the state on; so the tensor cores have dZ to do while P is made.
 // Documents whose chains are too few or too long are cut into segments: la_walk without output first sums what each adds,
 // la_carry_kernel turns the sums into the states they start from.
 #include <cuda_bf16.h>
@@ -22,14 +24,18 @@
 
 namespace gdn {
 
-constexpr int LA_WORK = 256;                 // threads that compute: two warpgroups, 64 columns each
-constexpr int LA_THREADS = LA_WORK + 64;     // and a warp each for the MMAs and the loads
+constexpr int LA_SET = 256;                  // threads of a set: two warpgroups, 64 columns each
+constexpr int LA_THREADS = 2 * LA_SET + 128; // and a warp each for the MMAs and the loads
+// Registers a thread, of the 96 that the CTA is launched with: 256 x 96 + 256 x 120 + 128 x 48 = 640 x 96
+constexpr int LA_REG_B = 120, LA_REG_CTRL = 48;
 constexpr int LA_TILE = LA_CH * D * 2;       // 32 KB
-constexpr int LA_STAGE = 3 * LA_TILE;
-constexpr int LA_ZS = 2 * LA_STAGE;          // the state as BF16 [z][y]; then a term of the decayed y
+constexpr int LA_STAGE = 3 * LA_TILE;        // y, x, z; z then has the output on its way out (FP32: x and z)
+constexpr int LA_Y = 0, LA_X = LA_TILE, LA_Z = 2 * LA_TILE;
+constexpr int LA_ZS = 2 * LA_STAGE;          // the state as BF16 [y][z]
 constexpr int LA_SMEM = LA_ZS + LA_TILE + 1024;
-// TMEM columns
-constexpr int LT_QK = 0, LT_OI = 128, LT_OP = 256, LT_DZ = 384;
+// TMEM columns: QK, then P in the halves' first 32; O; dZ; the ring of decayed y
+constexpr int LT_QK = 0, LT_O = 128, LT_DZ = 256, LT_Y = 384;
+constexpr int LA_Q = 32;                     // tokens of a quarter: 16 columns a term
 constexpr float LA_LEAST = -1e4f;   // log decays below it: nothing is left of it either, and no product is NaN
 
 // a^n: the product's rounding error is put back, so that far powers are as exact as near ones
@@ -49,6 +55,7 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
   const int lane = threadIdx.x & 31;
   int before = 0;
   bool found = false, good = true;
+#pragma unroll 1
   for (int d0 = 0; d0 < s.N; d0 += 32) {
     const int d = d0 + lane;
     int n = 0, a = 0, b = 0;
@@ -81,11 +88,36 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
   return found;
 }
 
-// waits up to about a second, whatever the error word holds from earlier calls
+// Waits, but no longer than about a second more once many tries have gone by, whatever the error word holds from earlier calls.
+// Small on purpose: waits are everywhere, and the kernel's speed is lost as soon as its code leaves the instruction cache (196 KB
+// of it: a chunk in 12,000 cycles).
 __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_drain(bar, parity)) return true;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 0x3fff) == 0) {
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 1000000000ull) break;
+    }
+  }
   atomicCAS(err, 0, ST_TIMEOUT);
   return false;
+}
+
+// barrier over one set that also tells whether all of it is well
+__device__ __forceinline__ bool la_set_well(int id, bool v) {
+  asm volatile("" ::: "memory");
+  v = bar_and(id, LA_SET, v);
+  asm volatile("" ::: "memory");
+  return v;
 }
 
 __device__ __forceinline__ void la_tile(uint8_t* dst, const CUtensorMap* map, int head, int row, uint64_t* bar) {
@@ -93,18 +125,45 @@ __device__ __forceinline__ void la_tile(uint8_t* dst, const CUtensorMap* map, in
   tma_load_3d(dst + LA_TILE / 2, map, 64, head, row, bar);
 }
 
+__device__ __forceinline__ void la_prefetch(const CUtensorMap* map, int head, int row) {
+  tma_prefetch_3d(map, 0, head, row);
+  tma_prefetch_3d(map, 64, head, row);
+}
+
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// BF16 by cutting off: the upper halves of two values, and what is left of one below its upper half (none of infinities,
+// whose place in the sum the upper half has)
+__device__ __forceinline__ uint32_t uppers(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float below(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+// 16 lanes x 8 columns: register 2 m + i of a lane goes to the TMEM lane (lane / 4) + 8 i, column 4 m + lane % 4
+__device__ __forceinline__ void tmem_st_16lanes(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]));
+}
+
+// byte offset of the 16-byte piece c16 (of 32) of row r in an FP32 [128][128] tile, swizzled as the BF16 ones
+__device__ __forceinline__ uint32_t la_f32(int r, int c16) {
+  return (uint32_t)((c16 >> 3) * (LA_CH * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+}
 
 template <bool OUT, bool REV, int TERMS, bool F32>
 __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_constant__ LaWalk a) {
   chain_kernel();
+  constexpr int SLOTS = 128 / (16 * TERMS);   // of the ring
   extern __shared__ uint8_t la_raw[];
   uint8_t* sm = smem_align1024(la_raw);
-  __shared__ uint64_t full[2], empty[2], bar_qk, bar_oi, bar_p, bar_op, bar_dz, bar_z;
+  // a tile is asked for again as soon as it has been used: y by QK and the decayed y, x by O, z at the end of its chunk
+  __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[SLOTS];
+  __shared__ uint64_t bar_qk, bar_oi, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
   __shared__ int go_s;
-  __shared__ alignas(16) float pw[LA_CH + 4], back[32];   // a^d; a^(31-j): the columns of a block seen from its last
+  // a^d; a^(31-j): the columns of a block seen from its last; the decayed y's factors of a whole chunk
+  __shared__ alignas(16) float pw[LA_CH + 4], back[32], fy[LA_CH];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.HV, want = blockIdx.x / a.HV;
 
@@ -119,19 +178,30 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       place_s = p;
       go_s = go;
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     tmem_alloc(&tmem_slot, 512);
-  } else if (warp == 9 && lane == 0) {
+  } else if (warp == 17 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&full_y[i], 1);
+      mbar_init(&full_x[i], 1);
+      mbar_init(&full_z[i], 1);
+      mbar_init(&empty_y[i], OUT ? LA_SET + 1 : LA_SET);
+      mbar_init(&empty_x[i], F32 ? 2 : 1);
+      mbar_init(&empty_z[i], OUT ? 2 : 1);
+    }
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&y_full[i], LA_SET);
+      mbar_init(&y_empty[i], 1);
     }
     mbar_init(&bar_qk, 1);
     mbar_init(&bar_oi, 1);
-    mbar_init(&bar_p, LA_WORK);
+    mbar_init(&bar_p, LA_SET);
     mbar_init(&bar_op, 1);
+    mbar_init(&bar_o, LA_SET);
     mbar_init(&bar_dz, 1);
-    mbar_init(&bar_z, LA_WORK);
+    mbar_init(&bar_dz_read, LA_SET);
+    mbar_init(&bar_z, LA_SET);
+    mbar_init(&bar_init, LA_SET);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const float g = [&] {
@@ -139,7 +209,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     return x < LA_LEAST ? LA_LEAST : x;
   }();
   if (tid <= LA_CH) pw[tid] = la_power(g, (float)tid);
-  if (tid < 32) back[tid] = la_power(g, (float)(31 - tid));
+  if (tid >= 256 && tid < 256 + 32) back[tid - 256] = la_power(g, (float)(31 - (tid - 256)));
+  if (tid >= 384 && tid < 384 + LA_CH) {
+    const int c = tid - 384;
+    fy[c] = a.state_scale * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c));
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -149,124 +223,149 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   const int nch = go_s ? min(chunks - c0, a.seg.len) : 0;
   const bool keep = !OUT || (a.last && (REV ? p.index == 0 : p.index + 1 == p.count));   // the state at the end is wanted
   const bool from = OUT && a.init;
+  const bool staged = from && !a.init_t;   // the first state comes by way of the second stage
   // the i-th chunk of the walk: its first token, and how many
   auto first = [&](int i) { return p.t0 + (c0 + (REV ? nch - 1 - i : i)) * LA_CH; };
   auto tokens = [&](int i) { return min(LA_CH, p.t1 - first(i)); };
 
-  if (!go_s) {
-    // nothing to walk
-  } else if (warp == 9) {
-    // ---- loads ----
-    if (lane == 0) {
-      int loaded = 0;
-      for (int i = 0; i < nch; ++i) {
-        const int b = i & 1;
-        if (i >= 2 && !la_wait(&empty[b], ((i >> 1) & 1) ^ 1, a.err)) break;
+  if (warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_CTRL));
+    if (warp == 17 && lane == 0 && go_s) {
+      // ---- loads ----
+      bool live = true;
+      int ny = 0, nx = 0, nz = 0;   // asked for
+#pragma unroll 1
+      for (int i = 0; i < nch && live; ++i) {
+        const int b = i & 1, t = first(i);
+        const uint32_t free = ((i >> 1) & 1) ^ 1;
         uint8_t* st = sm + b * LA_STAGE;
-        const int t = first(i);
-        mbar_expect_tx(&full[b], OUT ? LA_STAGE : 2 * LA_TILE);
-        la_tile(st + LA_TILE, &a.ty, h / a.gy, t, &full[b]);
-        if (OUT) la_tile(st, &a.tx, h / a.gx, t, &full[b]);
-        la_tile(st + 2 * LA_TILE, &a.tz, h / a.gz, t, &full[b]);
-        ++loaded;
+        if (i == 1 && staged && !(live = la_wait(&bar_init, 0, a.err))) break;
+        if (i >= 2 && !(live = la_wait(&empty_y[b], free, a.err))) break;
+        mbar_expect_tx(&full_y[b], LA_TILE);
+        la_tile(st + LA_Y, &a.ty, h / a.gy, t, &full_y[b]);
+        ++ny;
+        if (OUT) {
+          if (i >= 2 && !(live = la_wait(&empty_x[b], free, a.err))) break;
+          mbar_expect_tx(&full_x[b], LA_TILE);
+          la_tile(st + LA_X, &a.tx, h / a.gx, t, &full_x[b]);
+          ++nx;
+        }
+        if (i >= 2 && !(live = la_wait(&empty_z[b], free, a.err))) break;
+        mbar_expect_tx(&full_z[b], LA_TILE);
+        la_tile(st + LA_Z, &a.tz, h / a.gz, t, &full_z[b]);
+        ++nz;
+        if (i + 2 < nch) {   // until their tiles are free, the next rows come as far as L2
+          const int ahead = first(i + 2);
+          la_prefetch(&a.ty, h / a.gy, ahead);
+          if (OUT) la_prefetch(&a.tx, h / a.gx, ahead);
+          la_prefetch(&a.tz, h / a.gz, ahead);
+        }
       }
       // whatever happened: what was asked for lands before the CTA ends
-      for (int i = max(0, loaded - 2); i < loaded; ++i) mbar_drain(&full[i & 1], (i >> 1) & 1);
+#pragma unroll 1
+      for (int i = max(0, ny - 2); i < ny; ++i) mbar_drain(&full_y[i & 1], (i >> 1) & 1);
+#pragma unroll 1
+      for (int i = max(0, nx - 2); i < nx; ++i) mbar_drain(&full_x[i & 1], (i >> 1) & 1);
+#pragma unroll 1
+      for (int i = max(0, nz - 2); i < nz; ++i) mbar_drain(&full_z[i & 1], (i >> 1) & 1);
     }
-  } else if (warp == 8) {
-    // ---- MMAs ----
-    const uint32_t zs = smem_u32(sm + LA_ZS);
-    bool live = true;
-    for (int i = 0; i < nch && live; ++i) {
-      const int b = i & 1;
-      const uint32_t x = smem_u32(sm + b * LA_STAGE), y = x + LA_TILE, z = y + LA_TILE;
-      const bool add = keep || i + 1 < nch;
-      if (!(live = la_wait(&full[b], (i >> 1) & 1, a.err))) break;
-      if (OUT) {
+    if (warp == 16 && go_s) {
+      // ---- MMAs ----
+      const uint32_t zs = smem_u32(sm + LA_ZS);
+      bool live = true;
+      auto pairs = [&](int i) {   // QK of chunk i
+        const uint32_t st = smem_u32(sm + (i & 1) * LA_STAGE);
+        if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1, a.err) && la_wait(&full_x[i & 1], (i >> 1) & 1, a.err))) return;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ss_w(tb + LT_QK, desc_k(x, LA_CH, ks), desc_k(y, LA_CH, ks), idesc(128, 128, 0, 0), ks > 0);
+          mma_ss_w(tb + LT_QK, desc_k(st + LA_X, LA_CH, ks), desc_k(st + LA_Y, LA_CH, ks), idesc(128, 128, 0, 0), ks > 0);
         mma_commit_w(&bar_qk);
-        if (!(live = la_wait(&bar_z, i & 1, a.err))) break;
-        tc_fence_after();
-        if (i > 0 || from) {
+        mma_commit_w(&empty_y[i & 1]);
+      };
+      if (OUT && nch > 0) pairs(0);
+#pragma unroll 1
+      for (int i = 0; i < nch && live; ++i) {
+        const int b = i & 1;
+        const uint32_t x = smem_u32(sm + b * LA_STAGE + LA_X), z = smem_u32(sm + b * LA_STAGE + LA_Z);
+        const bool add = keep || i + 1 < nch;
+        auto quarter = [&](int q) {   // of dZ
+          const int n = i * 4 + q, slot = n % SLOTS;
+          if (!live || !(live = la_wait(&y_full[slot], (n / SLOTS) & 1, a.err))) return;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+              mma_ts_w(tb + LT_DZ, tb + LT_Y + (slot * TERMS + k) * 16 + ks * 8, desc_mn(z, LA_CH, q * 2 + ks),
+                       idesc(128, 128, 0, 1), q + k + ks > 0);
+          mma_commit_w(&y_empty[slot]);
+        };
+        if (add) {
+          if (i > 0 && !(live = la_wait(&bar_dz_read, (i - 1) & 1, a.err))) break;
+          if (!(live = la_wait(&full_z[b], (i >> 1) & 1, a.err))) break;
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) quarter(q);
+        }
+        if (OUT && live) {
+          if (!(live = la_wait(&bar_z, i & 1, a.err))) break;
+          if (i > 0 && !(live = la_wait(&bar_o, (i - 1) & 1, a.err))) break;
+          tc_fence_after();
+          if (i > 0 || from) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ss_w(tb + LT_O, desc_k(x, LA_CH, ks), desc_mn(zs, D, ks), idesc(128, 128, 0, 1), ks > 0);
+          }
+          mma_commit_w(&bar_oi);
+          mma_commit_w(&empty_x[b]);
+        }
+        if (add && live) {
+#pragma unroll 1
+          for (int q = 2; q < 4; ++q) quarter(q);
+          mma_commit_w(&bar_dz);
+        }
+        if (OUT && live) {
+          if (!(live = la_wait(&bar_p, i & 1, a.err) && la_wait(&full_z[b], (i >> 1) & 1, a.err))) break;
+          tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ss_w(tb + LT_OI, desc_k(x, LA_CH, ks), desc_k(zs, D, ks), idesc(128, 128, 0, 0), ks > 0);
+            mma_ts_w(tb + LT_O, tb + LT_QK + (ks >> 2) * 64 + (ks & 3) * 8, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
+                     ks > 0 || i > 0 || from);
+          mma_commit_w(&bar_op);
         }
-        mma_commit_w(&bar_oi);
+        mma_commit_w(&empty_z[b]);
+        if (OUT && live && i + 1 < nch) pairs(i + 1);
       }
-      if (!(live = la_wait(&bar_p, i & 1, a.err))) break;
-      tc_fence_after();
-      if (OUT) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts_w(tb + LT_OP, tb + LT_QK + (ks >> 2) * 64 + (ks & 3) * 8, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
-                   ks > 0);
-        mma_commit_w(&bar_op);
-      }
-      if (add) {
-        const uint32_t term[3] = {y, x, zs};
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k)
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ss_w(tb + LT_DZ, desc_mn(z, LA_CH, ks), desc_mn(term[k], LA_CH, ks), idesc(128, 128, 1, 1),
-                     k + ks > 0);
-      }
-      mma_commit_w(&bar_dz);
-      mma_commit_w(&empty[b]);
     }
-  } else {
-    // ---- the rest: this thread's row (of tokens, or of the state) and its 64 columns ----
-    const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
-    const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
-    uint8_t* zs = sm + LA_ZS;
-    float S[64];   // Z[z = row][y = col + j]
-    {
-      const float* src = nullptr;
-      if (from) src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
-      if (!src) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = 0.f;
-      } else if (a.init_t) {
-#pragma unroll
-        for (int j = 0; j < 64; j += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src + row * D + col + j);
-          S[j] = v.x, S[j + 1] = v.y, S[j + 2] = v.z, S[j + 3] = v.w;
+  } else if (warp < 8) {
+    // ---- set A: this thread's row of tokens and its 64 columns of P and O ----
+    if (OUT && go_s) {
+      const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
+      const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
+      bool live = true;
+      auto sent = [&](int i) {   // chunk i's output has left its tiles
+        bulk_wait_read();
+        mbar_arrive(&empty_z[i & 1]);
+        if (F32) mbar_arrive(&empty_x[i & 1]);
+      };
+#pragma unroll 1
+      for (int i = 0; i < nch && live; ++i) {
+        const int b = i & 1, L = tokens(i), t = first(i);
+        const bool state = i > 0 || from;
+        uint8_t* z = sm + b * LA_STAGE + LA_Z;
+        uint8_t* out = sm + b * LA_STAGE + (F32 ? LA_X : LA_Z);
+        do {   // (a wait that runs out ends the walk for the whole set, below)
+        if (L < LA_CH) {
+          if (!(live = la_wait(&full_z[b], (i >> 1) & 1, a.err))) break;
+          // rows past the document's end are another's, or none: what they hold takes no part
+#pragma unroll 1
+          for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_SET)
+            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = src[(col + j) * D + row];
-      }
-    }
-    auto put_state = [&](int j) {   // the columns j .. j+7 as BF16
-      *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col + j) >> 3, D)) =
-          make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
-                     pack_bf16(S[j + 6], S[j + 7]));
-    };
-    if (OUT && nch > 0) {
-#pragma unroll
-      for (int j = 0; j < 64; j += 8) put_state(j);
-      fence_async_smem();
-      mbar_arrive(&bar_z);
-    }
-    bool live = true;
-    for (int i = 0; i < nch && live; ++i) {
-      const int b = i & 1, L = tokens(i), t = first(i);
-      const bool add = keep || i + 1 < nch, state = i > 0 || from;
-      uint8_t *x = sm + b * LA_STAGE, *y = x + LA_TILE, *z = y + LA_TILE;
-      if (!(live = la_wait(&full[b], (i >> 1) & 1, a.err))) break;
-      if (L < LA_CH) {
-        // rows past the document's end are another's, or none: what they hold takes no part
-        for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_WORK)
-          *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      if (OUT) {
         if (!(live = la_wait(&bar_qk, i & 1, a.err))) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int m = 0; m < 2; ++m) {   // blocks of 32 columns: seen, not seen, or on the diagonal, as a warp's rows lie
           const int blk = wg * 2 + m;
           uint32_t w[16];
@@ -306,104 +405,224 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           tmem_st8(tl + LT_QK + wg * 64 + m * 16, w);
           tmem_st8(tl + LT_QK + wg * 64 + m * 16 + 8, w + 8);
         }
+        if (tid == 0 && i > 0) sent(i - 1);
+        if (!(live = la_wait(&bar_oi, i & 1, a.err))) break;
+        if (state) {   // O so far is the state's: a^.. of it stays
+          tc_fence_after();
+          const float f = a.row_scale * pw[REV ? max(L - 1 - row, 0) : row + 1];
+#pragma unroll 1
+          for (int j = 0; j < 64; j += 16) {
+            float v[16];
+            tmem_ld16(tl + LT_O + col + j, v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] *= f;
+            tmem_st16(tl + LT_O + col + j, v);
+          }
+        }
         tmem_wait_st();
         tc_fence_before();
-        // y and x have been read, and the state
-        if (!(live = la_wait(&bar_oi, i & 1, a.err))) break;
-      }
-      if (add) {
-#pragma unroll 2
-        for (int k = tid; k < LA_CH * 16; k += LA_WORK) {
-          const int c = k >> 4;
-          const uint32_t at = sw_chunk(c, k & 15, LA_CH);
-          const uint4 u = *reinterpret_cast<const uint4*>(y + at);
-          uint32_t w[4] = {u.x, u.y, u.z, u.w}, mid[4] = {0u, 0u, 0u, 0u}, low[4] = {0u, 0u, 0u, 0u};
-          if (c < L) {
-            const float f = a.state_scale * pw[REV ? c + 1 : L - 1 - c];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float v0 = f * __uint_as_float(w[j] << 16), v1 = f * __uint_as_float(w[j] & 0xffff0000u);
-              w[j] = pack_bf16(v0, v1);
-              v0 -= __uint_as_float(w[j] << 16);
-              v1 -= __uint_as_float(w[j] & 0xffff0000u);
-              mid[j] = pack_bf16(v0, v1);
-              if (TERMS == 3)
-                low[j] = pack_bf16(v0 - __uint_as_float(mid[j] << 16), v1 - __uint_as_float(mid[j] & 0xffff0000u));
-            }
-          } else {
-            w[0] = w[1] = w[2] = w[3] = 0u;
-          }
-          *reinterpret_cast<uint4*>(y + at) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(x + at) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-          if (TERMS == 3) *reinterpret_cast<uint4*>(zs + at) = make_uint4(low[0], low[1], low[2], low[3]);
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(&bar_p);
-      if (OUT) {
+        mbar_arrive(&bar_p);
         if (!(live = la_wait(&bar_op, i & 1, a.err))) break;
         tc_fence_after();
-        const float f = a.row_scale * pw[REV ? max(L - 1 - row, 0) : row + 1];
-        const int64_t at = (int64_t)(t + row) * a.out_token + h * a.out_head + col;
+        // out by way of z, which has been read (FP32: x and z)
+#pragma unroll 1
+        for (int j = 0; j < 64; j += 32) {
+          float v[32];
+          tmem_ld32(tl + LT_O + col + j, v);
+          if (F32) {
 #pragma unroll
-        for (int j = 0; j < 64; j += 16) {
-          float v[16];
-          if (state) {
-            uint32_t inter[16], intra[16];
-            tmem_ld16_async(tl + LT_OI + col + j, inter);
-            tmem_ld16_async(tl + LT_OP + col + j, intra);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = fmaf(f, __uint_as_float(inter[k]), __uint_as_float(intra[k]));
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(out + la_f32(row, (col + j) / 4 + k)) =
+                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           } else {
-            tmem_ld16(tl + LT_OP + col + j, v);
-          }
-          if (row < L) {
-            if (F32) {
-              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + j);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            } else {
-              uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + j);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                o[k] = make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
-                                  pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
-            }
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(out + sw_chunk(row, (col + j) / 8 + k, LA_CH)) =
+                  make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
+                             pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
           }
         }
-      }
-      if (!(live = la_wait(&bar_dz, i & 1, a.err))) break;
-      tc_fence_after();
-      if (add) {
-        const float f = pw[L];
-#pragma unroll
-        for (int j = 0; j < 64; j += 16) {
-          float v[16];
-          tmem_ld16(tl + LT_DZ + col + j, v);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) S[j + k] = fmaf(f, S[j + k], v[k]);
-          if (OUT && i + 1 < nch) {
-            put_state(j);
-            put_state(j + 8);
-          }
-        }
-      }
-      tc_fence_before();
-      if (OUT && i + 1 < nch) {
+        tc_fence_before();
+        mbar_arrive(&bar_o);
         fence_async_smem();
-        mbar_arrive(&bar_z);
+        } while (false);
+        if (!(live = la_set_well(1, live))) break;
+        if (L == LA_CH) {
+          if (tid == 0) {
+            for (int k = 0; k < (F32 ? 4 : 2); ++k)
+              tma_store_3d(&a.to, out + k * (LA_TILE / 2), k * (F32 ? 32 : 64), h, t);
+            bulk_commit();
+          }
+        } else {   // the rows behind are another document's
+#pragma unroll 1
+          for (int k = tid; k < L * (F32 ? 32 : 16); k += LA_SET) {
+            if (F32)
+              *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)(t + (k >> 5)) * a.out_token + h * a.out_head +
+                                         (k & 31) * 4) = *reinterpret_cast<const float4*>(out + la_f32(k >> 5, k & 31));
+            else
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)(t + (k >> 4)) * a.out_token +
+                                        h * a.out_head + (k & 15) * 8) =
+                  *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
+          }
+          la_set_well(1, true);
+        }
+        if (tid == 0 && i + 1 == nch) bulk_wait_all();
       }
     }
-    if (keep && live) {
-      float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)want * a.HV + h) * (D * D);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_B));
+    if (go_s) {
+    // ---- set B: this thread's row y of the state and its 64 columns z; of the decayed y, its column and half the tokens ----
+    const int me = tid - LA_SET, wg = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
+    const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
+    uint8_t* zs = sm + LA_ZS;
+    uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
+    float S[64];
+    if (from) {
+      const float* src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
+      if (a.init_t) {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) dst[(col + j) * D + row] = S[j];
+        for (int j = 0; j < 64; ++j) S[j] = src[(col + j) * D + row];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int e = k * LA_SET + me;
+          *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
+        }
+        la_set_well(2, true);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 16 + k));
+          S[4 * k] = v.x, S[4 * k + 1] = v.y, S[4 * k + 2] = v.z, S[4 * k + 3] = v.w;
+        }
+        fence_async_smem();
+        mbar_arrive(&bar_init);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 64; ++j) S[j] = 0.f;
+    }
+    auto put_state = [&] {   // as BF16
+#pragma unroll
+      for (int j = 0; j < 64; j += 8)
+        *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col + j) >> 3, D)) =
+            make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
+                       pack_bf16(S[j + 6], S[j + 7]));
+      fence_async_smem();
+      mbar_arrive(&bar_z);
+    };
+    if (OUT && nch > 0) put_state();
+    bool live = true;
+    // The decayed y of 16 tokens of quarter q of chunk i, in terms.  A transposing load gives a lane the tokens 2 (lane % 4) and
+    // the next of the column lane / 4 of each 8 x 8 block, which is also how a store of 16 TMEM lanes takes them.
+    auto quarter = [&](int i, int q) {
+      const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i), t0 = q * LA_Q + wg * 16, pair = (lane & 3) * 2;
+      uint32_t y[8];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int c8 = quad * 4 + m * 2 + ((lane >> 3) & 1), r = t0 + (lane >> 4) * 8 + (lane & 7);
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(y[4 * m]), "=r"(y[4 * m + 1]), "=r"(y[4 * m + 2]), "=r"(y[4 * m + 3])
+                     : "r"(smem_u32(sm + (i & 1) * LA_STAGE + LA_Y) + sw_chunk(r, c8, LA_CH))
+                     : "memory");
+      }
+      float2 f[2];   // of this lane's tokens in the first and the last 8
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int c = t0 + m * 8 + pair;
+        if (L == LA_CH) {
+          f[m] = *reinterpret_cast<const float2*>(fy + c);
+        } else {
+          f[m].x = c < L ? a.state_scale * pw[REV ? c + 1 : L - 1 - c] : 0.f;
+          f[m].y = c + 1 < L ? a.state_scale * pw[REV ? c + 2 : L - 2 - c] : 0.f;
+          // what the rows past the end hold takes no part
+          const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
+          y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
+        }
+      }
+      // terms cut off 8 bits at a time, so that three are the whole value, and no conversion is needed
+      uint32_t w[TERMS][8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 d = f[(k >> 1) & 1];
+        float v0 = d.x * __uint_as_float(y[k] << 16), v1 = d.y * __uint_as_float(y[k] & 0xffff0000u);
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e) {
+          w[e][k] = uppers(v0, v1);
+          v0 = below(v0);
+          v1 = below(v1);
+        }
+      }
+      if (n >= SLOTS && !(live = la_wait(&y_empty[slot], ((n / SLOTS) & 1) ^ 1, a.err))) return;
+      tc_fence_after();
+      const uint32_t to = tl + LT_Y + slot * TERMS * 16 + wg * 8;
+#pragma unroll
+      for (int e = 0; e < TERMS; ++e) {
+        tmem_st_16lanes(to + e * 16, w[e]);
+        tmem_st_16lanes(to + e * 16 + (16u << 16), w[e] + 4);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&y_full[slot]);
+    };
+    // The quarters one after the other; each chunk's state after the next chunk's first two, which need nothing of it.
+    const int adds = keep ? nch : max(nch - 1, 0);   // chunks that add to the state
+#pragma unroll 1
+    for (int n = 0; n < 4 * adds + (adds > 0 ? 2 : 0) && live; ++n) {
+      const int i = n >> 2, q = n & 3;
+      if (i < adds) {
+        if (q == 0) {
+          if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1, a.err))) break;
+          const int L = tokens(i);
+          if (L < LA_CH) {
+            if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1, a.err))) break;
+            uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
+#pragma unroll 1
+            for (int k = L * 16 + me; k < LA_CH * 16; k += LA_SET)
+              *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+            fence_async_smem();
+          }
+        }
+        quarter(i, q);
+        if (q == 3) mbar_arrive(&empty_y[i & 1]);
+      }
+      if (q != 1 || i == 0 || !live) continue;
+      if (!(live = la_wait(&bar_dz, (i - 1) & 1, a.err))) break;
+      tc_fence_after();
+      const float f = pw[tokens(i - 1)];
+#pragma unroll
+      for (int j = 0; j < 64; j += 16) {
+        float v[16];
+        tmem_ld16(tl + LT_DZ + col + j, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) S[j + k] = fmaf(f, S[j + k], v[k]);
+      }
+      tc_fence_before();
+      mbar_arrive(&bar_dz_read);
+      if (OUT && i < nch) put_state();
+    }
+    if (keep) {
+      // by way of the other stage's y and x than the last chunk's, which have been used
+      if (live && nch > 1)
+        live = F32 ? la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1, a.err) : la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1, a.err);
+      uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) = make_float4(S[4 * k], S[4 * k + 1], S[4 * k + 2], S[4 * k + 3]);
+      if (la_set_well(2, live)) {
+        float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)want * a.HV + h) * (D * D);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int e = k * LA_SET + me;
+          *reinterpret_cast<float4*>(dst + e * 4) = *reinterpret_cast<const float4*>(way + la_f32(e >> 5, e & 31));
+        }
+      }
+    }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tb, 512);
+  if (warp == 16) tmem_dealloc(tb, 512);
 }
 
 // Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.

@@ -20,7 +20,7 @@ struct LaSegments {
 // One walk: out_r = sum over the tokens c that r sees of p_scale a^|r-c| (x_r . y_c) z_c  +  row_scale a^.. Z^T x_r, with
 // the state Z = sum of state_scale a^.. y_c z_c^T of the chunks before (forward) or behind (reverse).
 struct LaWalk {
-  CUtensorMap tx, ty, tz;
+  CUtensorMap tx, ty, tz, to;
   LaSegments seg;
   const float* decay;     // [HV] log decays
   int HV, gx, gy, gz;     // value heads to a head of x, y, z

@@ -12,6 +12,8 @@ namespace gdn {
 
 bool make_tmap_strided(CUtensorMap* m, const void* base, int64_t T, int heads, int64_t token, int rows);
 
+bool make_tmap_f32(CUtensorMap* m, const void* base, int64_t T, int heads, int rows);
+
 struct LaPlan {
   int len, total;   // chunks of a segment, segments
   bool split;       // some document has more than one
@@ -137,6 +139,8 @@ struct LaCall {
     w.out_token = token;
     w.out_head = head;
     w.last = last;
+    if (p->T > 0) ok = f32 ? make_tmap_f32(&w.to, out, p->T, p->HV, LA_CH) : make_tmap_strided(&w.to, out, p->T, p->HV, token, LA_CH);
+    if (!ok) return;
     prof_begin(K_LA_WALK, s);
     check(launch_la_walk(w, reverse, last ? 3 : 2, f32, s));
     prof_end(K_LA_WALK, s);
