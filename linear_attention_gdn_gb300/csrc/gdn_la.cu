@@ -24,10 +24,11 @@
 
 namespace gdn {
 
-constexpr int LA_SET = 256;                  // threads of a set: two warpgroups, 64 columns each
-constexpr int LA_THREADS = 2 * LA_SET + 128; // and a warp each for the MMAs and the loads
-// Registers a thread, of the 96 that the CTA is launched with: 256 x 96 + 256 x 120 + 128 x 48 = 640 x 96
-constexpr int LA_REG_B = 120, LA_REG_CTRL = 48;
+constexpr int LA_A = 256, LA_B = 512;        // threads of the sets: 64 columns of O each, 32 of the state
+constexpr int LA_THREADS = LA_A + LA_B + 128; // and a warp each for the MMAs and the loads
+constexpr int LA_MMA = (LA_A + LA_B) / 32, LA_LOAD = LA_MMA + 1;   // those warps
+// Registers a thread, of the 72 that the CTA is launched with: 256 x 88 + 512 x 72 + 128 x 40 = 896 x 72
+constexpr int LA_REG_A = 88, LA_REG_CTRL = 40;
 constexpr int LA_TILE = LA_CH * D * 2;       // 32 KB
 constexpr int LA_STAGE = 3 * LA_TILE;        // y, x, z; z then has the output on its way out (FP32: x and z)
 constexpr int LA_Y = 0, LA_X = LA_TILE, LA_Z = 2 * LA_TILE;
@@ -88,34 +89,32 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
   return found;
 }
 
-// Waits, but no longer than about a second more once many tries have gone by, whatever the error word holds from earlier calls.
-// Small on purpose: waits are everywhere, and the kernel's speed is lost as soon as its code leaves the instruction cache (196 KB
-// of it: a chunk in 12,000 cycles).
-__device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity, int* err) {
-  uint64_t t0 = 0;
+// Waits, but not for ever: 2^20 tries, about a second; false if they run out.  Small on purpose, as are the loops below:
+// the kernel's speed is lost as soon as its code leaves the instruction cache (196 KB of it: a chunk in 12,000 cycles).
+__device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
 #pragma unroll 1
-  for (uint32_t i = 1;; ++i) {
-    uint32_t done;
+  for (uint32_t i = 0; i < 1u << 20; ++i) {
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
-    if (done) return true;
-    if ((i & 0x3fff) == 0) {
-      const uint64_t now = globaltimer();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > 1000000000ull) break;
-    }
+    if (done) break;
   }
-  atomicCAS(err, 0, ST_TIMEOUT);
-  return false;
+  return done;
+}
+
+// A warp's arrival: one for its 32 threads (counted one by one they queue at the barrier's word: 256 take 500 cycles).
+__device__ __forceinline__ void la_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // barrier over one set that also tells whether all of it is well
-__device__ __forceinline__ bool la_set_well(int id, bool v) {
+template <int ID, int N> __device__ __forceinline__ bool la_set_well(bool v) {
   asm volatile("" ::: "memory");
-  v = bar_and(id, LA_SET, v);
+  v = bar_and(ID, N, v);
   asm volatile("" ::: "memory");
   return v;
 }
@@ -134,10 +133,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 
 // BF16 by cutting off: the upper halves of two values, and what is left of one below its upper half (none of infinities,
 // whose place in the sum the upper half has)
-__device__ __forceinline__ uint32_t uppers(float lo, float hi) {
-  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+__device__ __forceinline__ uint32_t uppers(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
 }
-__device__ __forceinline__ float below(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+__device__ __forceinline__ float2 below(float2 x) {
+  const float2 top = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+  return __ffma2_rn(top, make_float2(-1.f, -1.f), x);
+}
 
 // 16 lanes x 8 columns: register 2 m + i of a lane goes to the TMEM lane (lane / 4) + 8 i, column 4 m + lane % 4
 __device__ __forceinline__ void tmem_st_16lanes(uint32_t addr, const uint32_t* v) {
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   extern __shared__ uint8_t la_raw[];
   uint8_t* sm = smem_align1024(la_raw);
   // a tile is asked for again as soon as it has been used: y by QK and the decayed y, x by O, z at the end of its chunk
-  __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[SLOTS];
+  __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[4];
   __shared__ uint64_t bar_qk, bar_oi, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
@@ -178,30 +180,30 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       place_s = p;
       go_s = go;
     }
-  } else if (warp == 16) {
+  } else if (warp == LA_MMA) {
     tmem_alloc(&tmem_slot, 512);
-  } else if (warp == 17 && lane == 0) {
+  } else if (warp == LA_LOAD && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full_y[i], 1);
       mbar_init(&full_x[i], 1);
       mbar_init(&full_z[i], 1);
-      mbar_init(&empty_y[i], OUT ? LA_SET + 1 : LA_SET);
+      mbar_init(&empty_y[i], LA_B / 32 + (OUT ? 1 : 0));
       mbar_init(&empty_x[i], F32 ? 2 : 1);
       mbar_init(&empty_z[i], OUT ? 2 : 1);
     }
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&y_full[i], LA_SET);
-      mbar_init(&y_empty[i], 1);
+      mbar_init(&y_full[i], 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&y_empty[i], 1);
     mbar_init(&bar_qk, 1);
     mbar_init(&bar_oi, 1);
-    mbar_init(&bar_p, LA_SET);
+    mbar_init(&bar_p, LA_A / 32);
     mbar_init(&bar_op, 1);
-    mbar_init(&bar_o, LA_SET);
+    mbar_init(&bar_o, LA_A / 32);
     mbar_init(&bar_dz, 1);
-    mbar_init(&bar_dz_read, LA_SET);
-    mbar_init(&bar_z, LA_SET);
-    mbar_init(&bar_init, LA_SET);
+    mbar_init(&bar_dz_read, LA_B / 32);
+    mbar_init(&bar_z, LA_B / 32);
+    mbar_init(&bar_init, LA_B / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const float g = [&] {
@@ -223,34 +225,34 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   const int nch = go_s ? min(chunks - c0, a.seg.len) : 0;
   const bool keep = !OUT || (a.last && (REV ? p.index == 0 : p.index + 1 == p.count));   // the state at the end is wanted
   const bool from = OUT && a.init;
+  bool live = true;   // no wait has run out
   const bool staged = from && !a.init_t;   // the first state comes by way of the second stage
   // the i-th chunk of the walk: its first token, and how many
   auto first = [&](int i) { return p.t0 + (c0 + (REV ? nch - 1 - i : i)) * LA_CH; };
   auto tokens = [&](int i) { return min(LA_CH, p.t1 - first(i)); };
 
-  if (warp >= 16) {
+  if (warp >= LA_MMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_CTRL));
-    if (warp == 17 && lane == 0 && go_s) {
+    if (warp == LA_LOAD && lane == 0 && go_s) {
       // ---- loads ----
-      bool live = true;
       int ny = 0, nx = 0, nz = 0;   // asked for
 #pragma unroll 1
       for (int i = 0; i < nch && live; ++i) {
         const int b = i & 1, t = first(i);
         const uint32_t free = ((i >> 1) & 1) ^ 1;
         uint8_t* st = sm + b * LA_STAGE;
-        if (i == 1 && staged && !(live = la_wait(&bar_init, 0, a.err))) break;
-        if (i >= 2 && !(live = la_wait(&empty_y[b], free, a.err))) break;
+        if (i == 1 && staged && !(live = la_wait(&bar_init, 0))) break;
+        if (i >= 2 && !(live = la_wait(&empty_y[b], free))) break;
         mbar_expect_tx(&full_y[b], LA_TILE);
         la_tile(st + LA_Y, &a.ty, h / a.gy, t, &full_y[b]);
         ++ny;
         if (OUT) {
-          if (i >= 2 && !(live = la_wait(&empty_x[b], free, a.err))) break;
+          if (i >= 2 && !(live = la_wait(&empty_x[b], free))) break;
           mbar_expect_tx(&full_x[b], LA_TILE);
           la_tile(st + LA_X, &a.tx, h / a.gx, t, &full_x[b]);
           ++nx;
         }
-        if (i >= 2 && !(live = la_wait(&empty_z[b], free, a.err))) break;
+        if (i >= 2 && !(live = la_wait(&empty_z[b], free))) break;
         mbar_expect_tx(&full_z[b], LA_TILE);
         la_tile(st + LA_Z, &a.tz, h / a.gz, t, &full_z[b]);
         ++nz;
@@ -269,13 +271,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 #pragma unroll 1
       for (int i = max(0, nz - 2); i < nz; ++i) mbar_drain(&full_z[i & 1], (i >> 1) & 1);
     }
-    if (warp == 16 && go_s) {
+    if (warp == LA_MMA && go_s) {
       // ---- MMAs ----
       const uint32_t zs = smem_u32(sm + LA_ZS);
-      bool live = true;
       auto pairs = [&](int i) {   // QK of chunk i
         const uint32_t st = smem_u32(sm + (i & 1) * LA_STAGE);
-        if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1, a.err) && la_wait(&full_x[i & 1], (i >> 1) & 1, a.err))) return;
+        if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1) && la_wait(&full_x[i & 1], (i >> 1) & 1))) return;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         const bool add = keep || i + 1 < nch;
         auto quarter = [&](int q) {   // of dZ
           const int n = i * 4 + q, slot = n % SLOTS;
-          if (!live || !(live = la_wait(&y_full[slot], (n / SLOTS) & 1, a.err))) return;
+          if (!live || !(live = la_wait(&y_full[slot], (n / SLOTS) & 1))) return;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < TERMS; ++k)
@@ -299,17 +300,17 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
             for (int ks = 0; ks < 2; ++ks)
               mma_ts_w(tb + LT_DZ, tb + LT_Y + (slot * TERMS + k) * 16 + ks * 8, desc_mn(z, LA_CH, q * 2 + ks),
                        idesc(128, 128, 0, 1), q + k + ks > 0);
-          mma_commit_w(&y_empty[slot]);
+          mma_commit_w(&y_empty[q]);
         };
         if (add) {
-          if (i > 0 && !(live = la_wait(&bar_dz_read, (i - 1) & 1, a.err))) break;
-          if (!(live = la_wait(&full_z[b], (i >> 1) & 1, a.err))) break;
+          if (i > 0 && !(live = la_wait(&bar_dz_read, (i - 1) & 1))) break;
+          if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) quarter(q);
         }
         if (OUT && live) {
-          if (!(live = la_wait(&bar_z, i & 1, a.err))) break;
-          if (i > 0 && !(live = la_wait(&bar_o, (i - 1) & 1, a.err))) break;
+          if (!(live = la_wait(&bar_z, i & 1))) break;
+          if (i > 0 && !(live = la_wait(&bar_o, (i - 1) & 1))) break;
           tc_fence_after();
           if (i > 0 || from) {
 #pragma unroll
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           mma_commit_w(&bar_dz);
         }
         if (OUT && live) {
-          if (!(live = la_wait(&bar_p, i & 1, a.err) && la_wait(&full_z[b], (i >> 1) & 1, a.err))) break;
+          if (!(live = la_wait(&bar_p, i & 1) && la_wait(&full_z[b], (i >> 1) & 1))) break;
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
@@ -337,12 +338,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         if (OUT && live && i + 1 < nch) pairs(i + 1);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < LA_A / 32) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_A));
     // ---- set A: this thread's row of tokens and its 64 columns of P and O ----
     if (OUT && go_s) {
       const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
       const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
-      bool live = true;
       auto sent = [&](int i) {   // chunk i's output has left its tiles
         bulk_wait_read();
         mbar_arrive(&empty_z[i & 1]);
@@ -356,73 +357,76 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         uint8_t* out = sm + b * LA_STAGE + (F32 ? LA_X : LA_Z);
         do {   // (a wait that runs out ends the walk for the whole set, below)
         if (L < LA_CH) {
-          if (!(live = la_wait(&full_z[b], (i >> 1) & 1, a.err))) break;
+          if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
           // rows past the document's end are another's, or none: what they hold takes no part
 #pragma unroll 1
-          for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_SET)
+          for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_A)
             *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
         }
-        if (!(live = la_wait(&bar_qk, i & 1, a.err))) break;
+        if (!(live = la_wait(&bar_qk, i & 1))) break;
         tc_fence_after();
+        // blocks of 32 columns are seen, not seen, or on the diagonal, as a warp's rows lie; 16 columns at a time
 #pragma unroll 1
-        for (int m = 0; m < 2; ++m) {   // blocks of 32 columns: seen, not seen, or on the diagonal, as a warp's rows lie
-          const int blk = wg * 2 + m;
-          uint32_t w[16];
-          const bool seen = REV ? blk >= quad : blk <= quad;
-          if (seen) {
-            float v[32];
-            tmem_ld32(tl + LT_QK + blk * 32, v);
+        for (int m = 0; m < 4; ++m) {
+          const int c = wg * 64 + m * 16, blk = c >> 5, in = c & 31;
+          uint32_t w[8];
+          if (REV ? blk >= quad : blk <= quad) {
+            float v[16];
+            tmem_ld16(tl + LT_QK + c, v);
             if (blk != quad) {
               const float far = a.p_scale * (REV ? pw[blk * 32 - row] : pw[row - blk * 32 - 31]);
               const float2 f = make_float2(far, far);
-              const float4* near = reinterpret_cast<const float4*>(REV ? pw : back);
+              const float4* near = reinterpret_cast<const float4*>((REV ? pw : back) + in);
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
+              for (int j = 0; j < 16; j += 4) {
                 const float4 n = near[j >> 2];
                 const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), f));
-                const float2 s = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), f));
-                v[j] = u.x, v[j + 1] = u.y, v[j + 2] = s.x, v[j + 3] = s.y;
+                const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), f));
+                v[j] = u.x, v[j + 1] = u.y, v[j + 2] = x.x, v[j + 3] = x.y;
               }
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const int d = REV ? j - lane : lane - j;
+              for (int j = 0; j < 16; ++j) {
+                const int d = REV ? in + j - lane : lane - in - j;
                 v[j] = d >= 0 ? v[j] * (a.p_scale * pw[max(d, 0)]) : 0.f;
               }
             }
             if (REV && L < LA_CH) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (blk * 32 + j >= L) v[j] = 0.f;
+              for (int j = 0; j < 16; ++j)
+                if (c + j >= L) v[j] = 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = 0u;
+            for (int j = 0; j < 8; ++j) w[j] = 0u;
           }
-          tmem_st8(tl + LT_QK + wg * 64 + m * 16, w);
-          tmem_st8(tl + LT_QK + wg * 64 + m * 16 + 8, w + 8);
+          tmem_st8(tl + LT_QK + wg * 64 + m * 8, w);
         }
         if (tid == 0 && i > 0) sent(i - 1);
-        if (!(live = la_wait(&bar_oi, i & 1, a.err))) break;
+        if (!(live = la_wait(&bar_oi, i & 1))) break;
         if (state) {   // O so far is the state's: a^.. of it stays
           tc_fence_after();
           const float f = a.row_scale * pw[REV ? max(L - 1 - row, 0) : row + 1];
 #pragma unroll 1
-          for (int j = 0; j < 64; j += 16) {
-            float v[16];
-            tmem_ld16(tl + LT_O + col + j, v);
+          for (int j = 0; j < 64; j += 32) {
+            float v[32];
+            tmem_ld32(tl + LT_O + col + j, v);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] *= f;
+            for (int k = 0; k < 32; k += 2) {
+              const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
+              v[k] = u.x, v[k + 1] = u.y;
+            }
             tmem_st16(tl + LT_O + col + j, v);
+            tmem_st16(tl + LT_O + col + j + 16, v + 16);
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar_p);
-        if (!(live = la_wait(&bar_op, i & 1, a.err))) break;
+        la_arrive(&bar_p);
+        if (!(live = la_wait(&bar_op, i & 1))) break;
         tc_fence_after();
         // out by way of z, which has been read (FP32: x and z)
 #pragma unroll 1
@@ -443,10 +447,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           }
         }
         tc_fence_before();
-        mbar_arrive(&bar_o);
+        la_arrive(&bar_o);
         fence_async_smem();
         } while (false);
-        if (!(live = la_set_well(1, live))) break;
+        if (!(live = la_set_well<1, LA_A>(live))) break;
         if (L == LA_CH) {
           if (tid == 0) {
             for (int k = 0; k < (F32 ? 4 : 2); ++k)
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           }
         } else {   // the rows behind are another document's
 #pragma unroll 1
-          for (int k = tid; k < L * (F32 ? 32 : 16); k += LA_SET) {
+          for (int k = tid; k < L * (F32 ? 32 : 16); k += LA_A) {
             if (F32)
               *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)(t + (k >> 5)) * a.out_token + h * a.out_head +
                                          (k & 31) * 4) = *reinterpret_cast<const float4*>(out + la_f32(k >> 5, k & 31));
@@ -464,165 +468,170 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
                                         h * a.out_head + (k & 15) * 8) =
                   *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
           }
-          la_set_well(1, true);
+          la_set_well<1, LA_A>(true);
         }
         if (tid == 0 && i + 1 == nch) bulk_wait_all();
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_B));
     if (go_s) {
-    // ---- set B: this thread's row y of the state and its 64 columns z; of the decayed y, its column and half the tokens ----
-    const int me = tid - LA_SET, wg = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
+    // ---- set B: this thread's row y of the state and its 32 columns z; of the decayed y, a quarter of the tokens ----
+    const int me = tid - LA_A, wg = me >> 7, quad = warp & 3, row = quad * 32 + lane, col = wg * 32;
     const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
     uint8_t* zs = sm + LA_ZS;
     uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
-    float S[64];
+    float2 S[16];
     if (from) {
       const float* src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
       if (a.init_t) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) S[j] = src[(col + j) * D + row];
+        for (int j = 0; j < 16; ++j) S[j] = make_float2(src[(col + 2 * j) * D + row], src[(col + 2 * j + 1) * D + row]);
       } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int e = k * LA_SET + me;
+        for (int k = 0; k < 8; ++k) {
+          const int e = k * LA_B + me;
           *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
         }
-        la_set_well(2, true);
+        la_set_well<2, LA_B>(true);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 16 + k));
-          S[4 * k] = v.x, S[4 * k + 1] = v.y, S[4 * k + 2] = v.z, S[4 * k + 3] = v.w;
+        for (int k = 0; k < 8; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 8 + k));
+          S[2 * k] = make_float2(v.x, v.y);
+          S[2 * k + 1] = make_float2(v.z, v.w);
         }
         fence_async_smem();
-        mbar_arrive(&bar_init);
+        la_arrive(&bar_init);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 64; ++j) S[j] = 0.f;
+      for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
     }
     auto put_state = [&] {   // as BF16
 #pragma unroll
-      for (int j = 0; j < 64; j += 8)
-        *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col + j) >> 3, D)) =
-            make_uint4(pack_bf16(S[j], S[j + 1]), pack_bf16(S[j + 2], S[j + 3]), pack_bf16(S[j + 4], S[j + 5]),
-                       pack_bf16(S[j + 6], S[j + 7]));
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col >> 3) + (j >> 2), D)) =
+            make_uint4(pack_bf16(S[j].x, S[j].y), pack_bf16(S[j + 1].x, S[j + 1].y), pack_bf16(S[j + 2].x, S[j + 2].y),
+                       pack_bf16(S[j + 3].x, S[j + 3].y));
       fence_async_smem();
-      mbar_arrive(&bar_z);
+      la_arrive(&bar_z);
     };
     if (OUT && nch > 0) put_state();
-    bool live = true;
-    // The decayed y of 16 tokens of quarter q of chunk i, in terms.  A transposing load gives a lane the tokens 2 (lane % 4) and
-    // the next of the column lane / 4 of each 8 x 8 block, which is also how a store of 16 TMEM lanes takes them.
+    // The decayed y of quarter q of chunk i, in terms, by one warpgroup while the others make the next ones.  A transposing
+    // load gives a lane the tokens 2 (lane % 4) and the next of the column lane / 4 of each 8 x 8 block, which is also how a
+    // store of 16 TMEM lanes takes them.
     auto quarter = [&](int i, int q) {
-      const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i), t0 = q * LA_Q + wg * 16, pair = (lane & 3) * 2;
-      uint32_t y[8];
+      const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i);
+      const uint32_t to = tl + LT_Y + slot * TERMS * 16;
+      // (of the quarter that had the slot before; so that each warpgroup sees every phase of the one barrier it waits for)
+      if (n >= SLOTS && !(live = la_wait(&y_empty[(q - SLOTS) & 3], ((n - SLOTS) >> 2) & 1))) return;
+      tc_fence_after();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {   // 16 tokens
+        const int t0 = q * LA_Q + half * 16, pair = (lane & 3) * 2;
+        uint32_t y[8];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int c8 = quad * 4 + m * 2 + ((lane >> 3) & 1), r = t0 + (lane >> 4) * 8 + (lane & 7);
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(y[4 * m]), "=r"(y[4 * m + 1]), "=r"(y[4 * m + 2]), "=r"(y[4 * m + 3])
-                     : "r"(smem_u32(sm + (i & 1) * LA_STAGE + LA_Y) + sw_chunk(r, c8, LA_CH))
-                     : "memory");
-      }
-      float2 f[2];   // of this lane's tokens in the first and the last 8
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int c = t0 + m * 8 + pair;
-        if (L == LA_CH) {
-          f[m] = *reinterpret_cast<const float2*>(fy + c);
-        } else {
-          f[m].x = c < L ? a.state_scale * pw[REV ? c + 1 : L - 1 - c] : 0.f;
-          f[m].y = c + 1 < L ? a.state_scale * pw[REV ? c + 2 : L - 2 - c] : 0.f;
-          // what the rows past the end hold takes no part
-          const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
-          y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
+        for (int m = 0; m < 2; ++m) {
+          const int c8 = quad * 4 + m * 2 + ((lane >> 3) & 1), r = t0 + (lane >> 4) * 8 + (lane & 7);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(y[4 * m]), "=r"(y[4 * m + 1]), "=r"(y[4 * m + 2]), "=r"(y[4 * m + 3])
+                       : "r"(smem_u32(sm + (i & 1) * LA_STAGE + LA_Y) + sw_chunk(r, c8, LA_CH))
+                       : "memory");
         }
-      }
-      // terms cut off 8 bits at a time, so that three are the whole value, and no conversion is needed
-      uint32_t w[TERMS][8];
+        float2 f[2];   // of this lane's tokens in the first and the last 8
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float2 d = f[(k >> 1) & 1];
-        float v0 = d.x * __uint_as_float(y[k] << 16), v1 = d.y * __uint_as_float(y[k] & 0xffff0000u);
+        for (int m = 0; m < 2; ++m) {
+          const int c = t0 + m * 8 + pair;
+          if (L == LA_CH) {
+            f[m] = *reinterpret_cast<const float2*>(fy + c);
+          } else {
+            f[m].x = c < L ? a.state_scale * pw[REV ? c + 1 : L - 1 - c] : 0.f;
+            f[m].y = c + 1 < L ? a.state_scale * pw[REV ? c + 2 : L - 2 - c] : 0.f;
+            // what the rows past the end hold takes no part
+            const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
+            y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
+          }
+        }
+        // terms cut off 8 bits at a time, so that three are the whole value, and no conversion is needed
+        uint32_t w[TERMS][8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 d = f[(k >> 1) & 1];
+          float2 v = mul2(d, make_float2(__uint_as_float(y[k] << 16), __uint_as_float(y[k] & 0xffff0000u)));
+#pragma unroll
+          for (int e = 0; e < TERMS; ++e) {
+            w[e][k] = uppers(v);
+            v = below(v);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < TERMS; ++e) {
-          w[e][k] = uppers(v0, v1);
-          v0 = below(v0);
-          v1 = below(v1);
+          tmem_st_16lanes(to + e * 16 + half * 8, w[e]);
+          tmem_st_16lanes(to + e * 16 + half * 8 + (16u << 16), w[e] + 4);
         }
-      }
-      if (n >= SLOTS && !(live = la_wait(&y_empty[slot], ((n / SLOTS) & 1) ^ 1, a.err))) return;
-      tc_fence_after();
-      const uint32_t to = tl + LT_Y + slot * TERMS * 16 + wg * 8;
-#pragma unroll
-      for (int e = 0; e < TERMS; ++e) {
-        tmem_st_16lanes(to + e * 16, w[e]);
-        tmem_st_16lanes(to + e * 16 + (16u << 16), w[e] + 4);
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&y_full[slot]);
+      la_arrive(&y_full[slot]);
     };
-    // The quarters one after the other; each chunk's state after the next chunk's first two, which need nothing of it.
+    // This warpgroup's quarter of each chunk, then the state after the chunk before, which the quarter does not need; but
+    // those whose place in the ring another quarter of the same chunk has first, which waits for that state, after the state.
     const int adds = keep ? nch : max(nch - 1, 0);   // chunks that add to the state
+    const int early = wg < SLOTS && adds > 0 ? 1 : 0;
 #pragma unroll 1
-    for (int n = 0; n < 4 * adds + (adds > 0 ? 2 : 0) && live; ++n) {
-      const int i = n >> 2, q = n & 3;
+    for (int i = 0; i < adds + early && live; ++i) {
       if (i < adds) {
-        if (q == 0) {
-          if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1, a.err))) break;
-          const int L = tokens(i);
-          if (L < LA_CH) {
-            if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1, a.err))) break;
-            uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
+        if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
+        const int L = tokens(i);
+        if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
+          if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
+          uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
 #pragma unroll 1
-            for (int k = L * 16 + me; k < LA_CH * 16; k += LA_SET)
-              *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
-            fence_async_smem();
-          }
+          for (int k = max(L, wg * LA_Q) * 16 + (me & 127); k < (wg + 1) * LA_Q * 16; k += 128)
+            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();
         }
-        quarter(i, q);
-        if (q == 3) mbar_arrive(&empty_y[i & 1]);
+        quarter(i, wg);
+        la_arrive(&empty_y[i & 1]);
       }
-      if (q != 1 || i == 0 || !live) continue;
-      if (!(live = la_wait(&bar_dz, (i - 1) & 1, a.err))) break;
+      const int done = i - early;
+      if (done < 0 || !live) continue;
+      if (!(live = la_wait(&bar_dz, done & 1))) break;
       tc_fence_after();
-      const float f = pw[tokens(i - 1)];
+      const float f = pw[tokens(done)];
+      uint32_t v[2][16];
+      tmem_ld16_async(tl + LT_DZ + col, v[0]);
+      tmem_ld16_async(tl + LT_DZ + col + 16, v[1]);
+      tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 64; j += 16) {
-        float v[16];
-        tmem_ld16(tl + LT_DZ + col + j, v);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) S[j + k] = fmaf(f, S[j + k], v[k]);
-      }
+      for (int k = 0; k < 16; ++k)
+        S[k] = __ffma2_rn(make_float2(f, f), S[k], make_float2(__uint_as_float(v[k >> 3][2 * (k & 7)]), __uint_as_float(v[k >> 3][2 * (k & 7) + 1])));
       tc_fence_before();
-      mbar_arrive(&bar_dz_read);
-      if (OUT && i < nch) put_state();
+      la_arrive(&bar_dz_read);
+      if (OUT && done + 1 < nch) put_state();
     }
     if (keep) {
       // by way of the other stage's y and x than the last chunk's, which have been used
       if (live && nch > 1)
-        live = F32 ? la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1, a.err) : la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1, a.err);
+        live = F32 ? la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1) : la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1);
       uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) = make_float4(S[4 * k], S[4 * k + 1], S[4 * k + 2], S[4 * k + 3]);
-      if (la_set_well(2, live)) {
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<float4*>(way + la_f32(row, wg * 8 + k)) = make_float4(S[2 * k].x, S[2 * k].y, S[2 * k + 1].x, S[2 * k + 1].y);
+      if (la_set_well<2, LA_B>(live)) {
         float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)want * a.HV + h) * (D * D);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int e = k * LA_SET + me;
+        for (int k = 0; k < 8; ++k) {
+          const int e = k * LA_B + me;
           *reinterpret_cast<float4*>(dst + e * 4) = *reinterpret_cast<const float4*>(way + la_f32(e >> 5, e & 31));
         }
       }
     }
     }
   }
+  if (!live) atomicCAS(a.err, 0, ST_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) tmem_dealloc(tb, 512);
+  if (warp == LA_MMA) tmem_dealloc(tb, 512);
 }
 
 // Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.
