@@ -10,9 +10,10 @@
 // P and the decayed y go to TMEM as left operands, so that shared memory, which all operands pass, is read least.  The state
 // is FP32 in registers (thread: one row y, 64 columns z), rounded to BF16 once for the product with x.  The decayed y is given
 // to the product as a sum of BF16 terms, so that the state keeps FP32's exactness: two terms (2^-17) where only BF16 results
-// come of it, three (2^-25) where the state itself is handed out.
-// Two sets of warps work side by side: one makes P, scales O and writes it out, the other makes the decayed y, a quarter of
-// a chunk at a time in a ring, and carries the state on; so the tensor cores have dZ to do while P is made.
+// come of it, four (2^-25) where the state itself is handed out.  Both come from the packed BF16 multiply-add, whose one rounding
+// the next one recovers, in 3 and 5 instructions a pair of values.
+// Three sets of warps work side by side: one makes P, scales O and writes it out, one makes the decayed y, a quarter of a
+// chunk at a time in a ring, one carries the state on; so the tensor cores have dZ to do while P is made.
 // Documents whose chains are too few or too long are cut into segments: la_walk without output first sums what each adds,
 // la_carry_kernel turns the sums into the states they start from.
 #include <cuda_bf16.h>
@@ -24,11 +25,11 @@
 
 namespace gdn {
 
-constexpr int LA_A = 256, LA_B = 512;        // threads of the sets: 64 columns of O each, 32 of the state
-constexpr int LA_THREADS = LA_A + LA_B + 128; // and a warp each for the MMAs and the loads
-constexpr int LA_MMA = (LA_A + LA_B) / 32, LA_LOAD = LA_MMA + 1;   // those warps
-// Registers a thread, of the 72 that the CTA is launched with: 256 x 88 + 512 x 72 + 128 x 40 = 896 x 72
-constexpr int LA_REG_A = 88, LA_REG_CTRL = 40;
+constexpr int LA_SET = 256;                   // threads of each of the three sets: two warpgroups
+constexpr int LA_THREADS = 3 * LA_SET + 128;  // and a warp each for the MMAs and the loads
+constexpr int LA_MMA = 3 * LA_SET / 32, LA_LOAD = LA_MMA + 1;   // those warps
+// Registers a thread, of the 72 that the CTA is launched with: 256 x (80 + 56 + 96) + 128 x 40 = 896 x 72
+constexpr int LA_REG_OUT = 80, LA_REG_Y = 56, LA_REG_STATE = 96, LA_REG_CTRL = 40;
 constexpr int LA_TILE = LA_CH * D * 2;       // 32 KB
 constexpr int LA_STAGE = 3 * LA_TILE;        // y, x, z; z then has the output on its way out (FP32: x and z)
 constexpr int LA_Y = 0, LA_X = LA_TILE, LA_Z = 2 * LA_TILE;
@@ -131,14 +132,25 @@ __device__ __forceinline__ void la_prefetch(const CUtensorMap* map, int head, in
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
-// BF16 by cutting off: the upper halves of two values, and what is left of one below its upper half (none of infinities,
-// whose place in the sum the upper half has)
-__device__ __forceinline__ uint32_t uppers(float2 x) {
-  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+// pairs of BF16 values: products and sums rounded once
+__device__ __forceinline__ uint32_t bf_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
-__device__ __forceinline__ float2 below(float2 x) {
-  const float2 top = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
-  return __ffma2_rn(top, make_float2(-1.f, -1.f), x);
+__device__ __forceinline__ uint32_t bf_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// a pair of FP32 values as three pairs of BF16 whose sums they are (to 2^-24)
+__device__ __forceinline__ void la_parts(float lo, float hi, uint32_t* part) {
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+    part[e] = pack_bf16(lo, hi);
+    lo -= __uint_as_float(part[e] << 16);
+    hi -= __uint_as_float(part[e] & 0xffff0000u);
+  }
 }
 
 // 16 lanes x 8 columns: register 2 m + i of a lane goes to the TMEM lane (lane / 4) + 8 i, column 4 m + lane % 4
@@ -164,8 +176,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
   __shared__ int go_s;
-  // a^d; a^(31-j): the columns of a block seen from its last; the decayed y's factors of a whole chunk
-  __shared__ alignas(16) float pw[LA_CH + 4], back[32], fy[LA_CH];
+  // a^d; a^(31-j): the columns of a block seen from its last; the decayed y's factors in a whole chunk, in parts
+  __shared__ alignas(16) float pw[LA_CH + 4], back[32];
+  __shared__ uint32_t fy[3][LA_CH / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.HV, want = blockIdx.x / a.HV;
 
@@ -187,7 +200,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&full_y[i], 1);
       mbar_init(&full_x[i], 1);
       mbar_init(&full_z[i], 1);
-      mbar_init(&empty_y[i], LA_B / 32 + (OUT ? 1 : 0));
+      mbar_init(&empty_y[i], LA_SET / 32 + (OUT ? 1 : 0));
       mbar_init(&empty_x[i], F32 ? 2 : 1);
       mbar_init(&empty_z[i], OUT ? 2 : 1);
     }
@@ -197,13 +210,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     for (int i = 0; i < 4; ++i) mbar_init(&y_empty[i], 1);
     mbar_init(&bar_qk, 1);
     mbar_init(&bar_oi, 1);
-    mbar_init(&bar_p, LA_A / 32);
+    mbar_init(&bar_p, LA_SET / 32);
     mbar_init(&bar_op, 1);
-    mbar_init(&bar_o, LA_A / 32);
+    mbar_init(&bar_o, LA_SET / 32);
     mbar_init(&bar_dz, 1);
-    mbar_init(&bar_dz_read, LA_B / 32);
-    mbar_init(&bar_z, LA_B / 32);
-    mbar_init(&bar_init, LA_B / 32);
+    mbar_init(&bar_dz_read, LA_SET / 32);
+    mbar_init(&bar_z, LA_SET / 32);
+    mbar_init(&bar_init, LA_SET / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const float g = [&] {
@@ -212,9 +225,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   }();
   if (tid <= LA_CH) pw[tid] = la_power(g, (float)tid);
   if (tid >= 256 && tid < 256 + 32) back[tid - 256] = la_power(g, (float)(31 - (tid - 256)));
-  if (tid >= 384 && tid < 384 + LA_CH) {
-    const int c = tid - 384;
-    fy[c] = a.state_scale * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c));
+  if (tid >= 384 && tid < 384 + LA_CH / 2) {
+    const int c = (tid - 384) * 2;
+    uint32_t part[3];
+    la_parts(a.state_scale * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c)),
+             a.state_scale * la_power(g, (float)(REV ? c + 2 : LA_CH - 2 - c)), part);
+#pragma unroll
+    for (int e = 0; e < 3; ++e) fy[e][c >> 1] = part[e];
   }
   tc_fence_before();
   __syncthreads();
@@ -225,6 +242,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   const int nch = go_s ? min(chunks - c0, a.seg.len) : 0;
   const bool keep = !OUT || (a.last && (REV ? p.index == 0 : p.index + 1 == p.count));   // the state at the end is wanted
   const bool from = OUT && a.init;
+  const int adds = keep ? nch : max(nch - 1, 0);   // chunks that add to the state
   bool live = true;   // no wait has run out
   const bool staged = from && !a.init_t;   // the first state comes by way of the second stage
   // the i-th chunk of the walk: its first token, and how many
@@ -338,9 +356,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         if (OUT && live && i + 1 < nch) pairs(i + 1);
       }
     }
-  } else if (warp < LA_A / 32) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_A));
-    // ---- set A: this thread's row of tokens and its 64 columns of P and O ----
+  } else if (warp < LA_SET / 32) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_OUT));
+    // ---- P and O: this thread's row of tokens and its 64 columns ----
     if (OUT && go_s) {
       const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
       const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
@@ -360,7 +378,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
           // rows past the document's end are another's, or none: what they hold takes no part
 #pragma unroll 1
-          for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_A)
+          for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_SET)
             *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
           fence_async_smem();
         }
@@ -450,7 +468,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         la_arrive(&bar_o);
         fence_async_smem();
         } while (false);
-        if (!(live = la_set_well<1, LA_A>(live))) break;
+        if (!(live = la_set_well<1, LA_SET>(live))) break;
         if (L == LA_CH) {
           if (tid == 0) {
             for (int k = 0; k < (F32 ? 4 : 2); ++k)
@@ -459,7 +477,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           }
         } else {   // the rows behind are another document's
 #pragma unroll 1
-          for (int k = tid; k < L * (F32 ? 32 : 16); k += LA_A) {
+          for (int k = tid; k < L * (F32 ? 32 : 16); k += LA_SET) {
             if (F32)
               *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)(t + (k >> 5)) * a.out_token + h * a.out_head +
                                          (k & 31) * 4) = *reinterpret_cast<const float4*>(out + la_f32(k >> 5, k & 31));
@@ -468,63 +486,21 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
                                         h * a.out_head + (k & 15) * 8) =
                   *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
           }
-          la_set_well<1, LA_A>(true);
+          la_set_well<1, LA_SET>(true);
         }
         if (tid == 0 && i + 1 == nch) bulk_wait_all();
       }
     }
-  } else {
-    if (go_s) {
-    // ---- set B: this thread's row y of the state and its 32 columns z; of the decayed y, a quarter of the tokens ----
-    const int me = tid - LA_A, wg = me >> 7, quad = warp & 3, row = quad * 32 + lane, col = wg * 32;
+  } else if (warp < 2 * LA_SET / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_Y));
+    // ---- the decayed y: a warpgroup the even quarters, the other the odd ones; a warp 32 columns of y ----
+    const int me = tid - LA_SET, wg = me >> 7, quad = warp & 3;
     const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
-    uint8_t* zs = sm + LA_ZS;
-    uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
-    float2 S[16];
-    if (from) {
-      const float* src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
-      if (a.init_t) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) S[j] = make_float2(src[(col + 2 * j) * D + row], src[(col + 2 * j + 1) * D + row]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int e = k * LA_B + me;
-          *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
-        }
-        la_set_well<2, LA_B>(true);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 8 + k));
-          S[2 * k] = make_float2(v.x, v.y);
-          S[2 * k + 1] = make_float2(v.z, v.w);
-        }
-        fence_async_smem();
-        la_arrive(&bar_init);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) S[j] = make_float2(0.f, 0.f);
-    }
-    auto put_state = [&] {   // as BF16
-#pragma unroll
-      for (int j = 0; j < 16; j += 4)
-        *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col >> 3) + (j >> 2), D)) =
-            make_uint4(pack_bf16(S[j].x, S[j].y), pack_bf16(S[j + 1].x, S[j + 1].y), pack_bf16(S[j + 2].x, S[j + 2].y),
-                       pack_bf16(S[j + 3].x, S[j + 3].y));
-      fence_async_smem();
-      la_arrive(&bar_z);
-    };
-    if (OUT && nch > 0) put_state();
-    // The decayed y of quarter q of chunk i, in terms, by one warpgroup while the others make the next ones.  A transposing
-    // load gives a lane the tokens 2 (lane % 4) and the next of the column lane / 4 of each 8 x 8 block, which is also how a
-    // store of 16 TMEM lanes takes them.
+    // Quarter q of chunk i, in terms.  A transposing load gives a lane the tokens 2 (lane % 4) and the next of the column
+    // lane / 4 of each 8 x 8 block, which is also how a store of 16 TMEM lanes takes them.
     auto quarter = [&](int i, int q) {
       const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i);
       const uint32_t to = tl + LT_Y + slot * TERMS * 16;
-      // (of the quarter that had the slot before; so that each warpgroup sees every phase of the one barrier it waits for)
-      if (n >= SLOTS && !(live = la_wait(&y_empty[(q - SLOTS) & 3], ((n - SLOTS) >> 2) & 1))) return;
-      tc_fence_after();
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {   // 16 tokens
         const int t0 = q * LA_Q + half * 16, pair = (lane & 3) * 2;
@@ -537,31 +513,42 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
                        : "r"(smem_u32(sm + (i & 1) * LA_STAGE + LA_Y) + sw_chunk(r, c8, LA_CH))
                        : "memory");
         }
-        float2 f[2];   // of this lane's tokens in the first and the last 8
+        // the decays of this lane's tokens in the first and the last 8, as three BF16 parts each
+        uint32_t f[2][3];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int c = t0 + m * 8 + pair;
           if (L == LA_CH) {
-            f[m] = *reinterpret_cast<const float2*>(fy + c);
+#pragma unroll
+            for (int e = 0; e < (TERMS > 2 ? 3 : 2); ++e) f[m][e] = fy[e][c >> 1];
           } else {
-            f[m].x = c < L ? a.state_scale * pw[REV ? c + 1 : L - 1 - c] : 0.f;
-            f[m].y = c + 1 < L ? a.state_scale * pw[REV ? c + 2 : L - 2 - c] : 0.f;
+            la_parts(c < L ? a.state_scale * pw[REV ? c + 1 : L - 1 - c] : 0.f,
+                     c + 1 < L ? a.state_scale * pw[REV ? c + 2 : L - 2 - c] : 0.f, f[m]);
             // what the rows past the end hold takes no part
             const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
             y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
           }
         }
-        // terms cut off 8 bits at a time, so that three are the whole value, and no conversion is needed
+        // The products in BF16 parts, without a rounding left out: y f1 and what its rounding left (exact: 16 bits), then y f2
+        // added to that, or, for a state that is handed out, y f2 and what its rounding left with y f3.
         uint32_t w[TERMS][8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float2 d = f[(k >> 1) & 1];
-          float2 v = mul2(d, make_float2(__uint_as_float(y[k] << 16), __uint_as_float(y[k] & 0xffff0000u)));
-#pragma unroll
-          for (int e = 0; e < TERMS; ++e) {
-            w[e][k] = uppers(v);
-            v = below(v);
+          const uint32_t* d = f[(k >> 1) & 1];
+          w[0][k] = bf_mul(y[k], d[0]);
+          const uint32_t left = bf_fma(y[k], d[0], w[0][k] ^ 0x80008000u);
+          if (TERMS == 2) {
+            w[1][k] = bf_fma(y[k], d[1], left);
+          } else {
+            w[1][k] = left;
+            w[2][k] = bf_mul(y[k], d[1]);
+            w[TERMS - 1][k] = bf_fma(y[k], d[2], bf_fma(y[k], d[1], w[2][k] ^ 0x80008000u));
           }
+        }
+        if (half == 0) {
+          // (of the quarter that had the slot before; so that each warpgroup sees every phase of the one barrier it waits for)
+          if (n >= SLOTS && !(live = la_wait(&y_empty[(q - SLOTS) & 3], ((n - SLOTS) >> 2) & 1))) return;
+          tc_fence_after();
         }
 #pragma unroll
         for (int e = 0; e < TERMS; ++e) {
@@ -573,41 +560,84 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       tc_fence_before();
       la_arrive(&y_full[slot]);
     };
-    // This warpgroup's quarter of each chunk, then the state after the chunk before, which the quarter does not need; but
-    // those whose place in the ring another quarter of the same chunk has first, which waits for that state, after the state.
-    const int adds = keep ? nch : max(nch - 1, 0);   // chunks that add to the state
-    const int early = wg < SLOTS && adds > 0 ? 1 : 0;
+    const int quarters = go_s ? 2 * adds : 0;
 #pragma unroll 1
-    for (int i = 0; i < adds + early && live; ++i) {
-      if (i < adds) {
-        if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
-        const int L = tokens(i);
-        if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
-          if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
-          uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
+    for (int m = 0; m < quarters && live; ++m) {
+      const int i = m >> 1, q = (m & 1) * 2 + wg;
+      if (q < 2 && !(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
+      const int L = tokens(i);
+      if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
+        if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
+        uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
 #pragma unroll 1
-          for (int k = max(L, wg * LA_Q) * 16 + (me & 127); k < (wg + 1) * LA_Q * 16; k += 128)
-            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
-          fence_async_smem();
-        }
-        quarter(i, wg);
-        la_arrive(&empty_y[i & 1]);
+        for (int k = max(L, q * LA_Q) * 16 + (me & 127); k < (q + 1) * LA_Q * 16; k += 128)
+          *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
       }
-      const int done = i - early;
-      if (done < 0 || !live) continue;
-      if (!(live = la_wait(&bar_dz, done & 1))) break;
-      tc_fence_after();
-      const float f = pw[tokens(done)];
-      uint32_t v[2][16];
-      tmem_ld16_async(tl + LT_DZ + col, v[0]);
-      tmem_ld16_async(tl + LT_DZ + col + 16, v[1]);
-      tmem_wait_ld();
+      quarter(i, q);
+      if (q >= 2) la_arrive(&empty_y[i & 1]);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_STATE));
+    // ---- the state: this thread's row y and its 64 columns z ----
+    if (go_s) {
+    const int me = tid - 2 * LA_SET, wg = me >> 7, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
+    const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
+    uint8_t* zs = sm + LA_ZS;
+    uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
+    float2 S[32];
+    if (from) {
+      const float* src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
+      if (a.init_t) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        S[k] = __ffma2_rn(make_float2(f, f), S[k], make_float2(__uint_as_float(v[k >> 3][2 * (k & 7)]), __uint_as_float(v[k >> 3][2 * (k & 7) + 1])));
+        for (int j = 0; j < 32; ++j) S[j] = make_float2(src[(col + 2 * j) * D + row], src[(col + 2 * j + 1) * D + row]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int e = k * LA_SET + me;
+          *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
+        }
+        la_set_well<2, LA_SET>(true);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 16 + k));
+          S[2 * k] = make_float2(v.x, v.y);
+          S[2 * k + 1] = make_float2(v.z, v.w);
+        }
+        fence_async_smem();
+        la_arrive(&bar_init);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
+    }
+    auto put_state = [&] {   // as BF16
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col >> 3) + (j >> 2), D)) =
+            make_uint4(pack_bf16(S[j].x, S[j].y), pack_bf16(S[j + 1].x, S[j + 1].y), pack_bf16(S[j + 2].x, S[j + 2].y),
+                       pack_bf16(S[j + 3].x, S[j + 3].y));
+      fence_async_smem();
+      la_arrive(&bar_z);
+    };
+    if (OUT && nch > 0) put_state();
+#pragma unroll 1
+    for (int i = 0; i < adds && live; ++i) {
+      if (!(live = la_wait(&bar_dz, i & 1))) break;
+      tc_fence_after();
+      const float f = pw[tokens(i)];
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        uint32_t v[16];
+        tmem_ld16_async(tl + LT_DZ + col + 2 * j, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          S[j + k] = __ffma2_rn(make_float2(f, f), S[j + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+      }
       tc_fence_before();
       la_arrive(&bar_dz_read);
-      if (OUT && done + 1 < nch) put_state();
+      if (OUT && i + 1 < nch) put_state();
     }
     if (keep) {
       // by way of the other stage's y and x than the last chunk's, which have been used
@@ -615,13 +645,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         live = F32 ? la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1) : la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1);
       uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        *reinterpret_cast<float4*>(way + la_f32(row, wg * 8 + k)) = make_float4(S[2 * k].x, S[2 * k].y, S[2 * k + 1].x, S[2 * k + 1].y);
-      if (la_set_well<2, LA_B>(live)) {
+      for (int k = 0; k < 16; ++k)
+        *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) = make_float4(S[2 * k].x, S[2 * k].y, S[2 * k + 1].x, S[2 * k + 1].y);
+      if (la_set_well<2, LA_SET>(live)) {
         float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)want * a.HV + h) * (D * D);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int e = k * LA_B + me;
+        for (int k = 0; k < 16; ++k) {
+          const int e = k * LA_SET + me;
           *reinterpret_cast<float4*>(dst + e * 4) = *reinterpret_cast<const float4*>(way + la_f32(e >> 5, e & 31));
         }
       }
@@ -725,14 +755,14 @@ template <bool OUT, bool REV, int TERMS, bool F32> static cudaError_t launch_wal
 cudaError_t launch_la_walk(const LaWalk& a, bool reverse, int terms, bool f32, cudaStream_t s) {
   if (reverse) {
     if (f32) return launch_walk<true, true, 2, true>(a, s);
-    return terms == 3 ? launch_walk<true, true, 3, false>(a, s) : launch_walk<true, true, 2, false>(a, s);
+    return terms == 4 ? launch_walk<true, true, 4, false>(a, s) : launch_walk<true, true, 2, false>(a, s);
   }
   if (f32) return launch_walk<true, false, 2, true>(a, s);
-  return terms == 3 ? launch_walk<true, false, 3, false>(a, s) : launch_walk<true, false, 2, false>(a, s);
+  return terms == 4 ? launch_walk<true, false, 4, false>(a, s) : launch_walk<true, false, 2, false>(a, s);
 }
 
 cudaError_t launch_la_sums(const LaWalk& a, bool reverse, cudaStream_t s) {
-  return reverse ? launch_walk<false, true, 3, false>(a, s) : launch_walk<false, false, 3, false>(a, s);
+  return reverse ? launch_walk<false, true, 4, false>(a, s) : launch_walk<false, false, 4, false>(a, s);
 }
 
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s) {

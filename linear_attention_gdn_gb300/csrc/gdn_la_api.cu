@@ -142,7 +142,7 @@ struct LaCall {
     if (p->T > 0) ok = f32 ? make_tmap_f32(&w.to, out, p->T, p->HV, LA_CH) : make_tmap_strided(&w.to, out, p->T, p->HV, token, LA_CH);
     if (!ok) return;
     prof_begin(K_LA_WALK, s);
-    check(launch_la_walk(w, reverse, last ? 3 : 2, f32, s));
+    check(launch_la_walk(w, reverse, last ? 4 : 2, f32, s));
     prof_end(K_LA_WALK, s);
   }
   void reduce(const float* part, void* out, int64_t token) {
