@@ -26,8 +26,8 @@
 namespace gdn {
 
 constexpr int LA_SET = 256;                   // threads of each of the three sets: two warpgroups
-constexpr int LA_THREADS = 3 * LA_SET + 128;  // and a warp each for the MMAs and the loads
-constexpr int LA_MMA = 3 * LA_SET / 32, LA_LOAD = LA_MMA + 1;   // those warps
+constexpr int LA_THREADS = 3 * LA_SET + 128;  // and a warp each for the loads and two streams of MMAs
+constexpr int LA_MMA = 3 * LA_SET / 32, LA_LOAD = LA_MMA + 1, LA_DZ = LA_MMA + 2;   // those warps
 // Registers a thread, of the 72 that the CTA is launched with: 256 x (80 + 56 + 96) + 128 x 40 = 896 x 72
 constexpr int LA_REG_OUT = 80, LA_REG_Y = 56, LA_REG_STATE = 96, LA_REG_CTRL = 40;
 constexpr int LA_TILE = LA_CH * D * 2;       // 32 KB
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   uint8_t* sm = smem_align1024(la_raw);
   // a tile is asked for again as soon as it has been used: y by QK and the decayed y, x by O, z at the end of its chunk
   __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[4];
+  __shared__ uint64_t dz_used[2];   // (dZ may be a chunk ahead of the output, which so needs a barrier to each stage)
   __shared__ uint64_t bar_qk, bar_oi, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
@@ -200,9 +201,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&full_y[i], 1);
       mbar_init(&full_x[i], 1);
       mbar_init(&full_z[i], 1);
+      mbar_init(&dz_used[i], 1);
       mbar_init(&empty_y[i], LA_SET / 32 + (OUT ? 1 : 0));
       mbar_init(&empty_x[i], F32 ? 2 : 1);
-      mbar_init(&empty_z[i], OUT ? 2 : 1);
+      mbar_init(&empty_z[i], OUT ? 3 : 1);
     }
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&y_full[i], 4);
@@ -289,71 +291,64 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 #pragma unroll 1
       for (int i = max(0, nz - 2); i < nz; ++i) mbar_drain(&full_z[i & 1], (i >> 1) & 1);
     }
-    if (warp == LA_MMA && go_s) {
-      // ---- MMAs ----
+    // ---- the products, in two streams that wait for different things: QK, x Z and P z here ----
+    if (OUT && warp == LA_MMA && go_s) {
       const uint32_t zs = smem_u32(sm + LA_ZS);
-      auto pairs = [&](int i) {   // QK of chunk i
-        const uint32_t st = smem_u32(sm + (i & 1) * LA_STAGE);
-        if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1) && la_wait(&full_x[i & 1], (i >> 1) & 1))) return;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss_w(tb + LT_QK, desc_k(st + LA_X, LA_CH, ks), desc_k(st + LA_Y, LA_CH, ks), idesc(128, 128, 0, 0), ks > 0);
-        mma_commit_w(&bar_qk);
-        mma_commit_w(&empty_y[i & 1]);
-      };
-      if (OUT && nch > 0) pairs(0);
 #pragma unroll 1
       for (int i = 0; i < nch && live; ++i) {
         const int b = i & 1;
-        const uint32_t x = smem_u32(sm + b * LA_STAGE + LA_X), z = smem_u32(sm + b * LA_STAGE + LA_Z);
-        const bool add = keep || i + 1 < nch;
-        auto quarter = [&](int q) {   // of dZ
-          const int n = i * 4 + q, slot = n % SLOTS;
-          if (!live || !(live = la_wait(&y_full[slot], (n / SLOTS) & 1))) return;
-          tc_fence_after();
+        const uint32_t par = (i >> 1) & 1, st = smem_u32(sm + b * LA_STAGE), x = st + LA_X, z = st + LA_Z;
+        if (!(live = la_wait(&full_y[b], par) && la_wait(&full_x[b], par))) break;
+        tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < TERMS; ++k)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-              mma_ts_w(tb + LT_DZ, tb + LT_Y + (slot * TERMS + k) * 16 + ks * 8, desc_mn(z, LA_CH, q * 2 + ks),
-                       idesc(128, 128, 0, 1), q + k + ks > 0);
-          mma_commit_w(&y_empty[q]);
-        };
-        if (add) {
-          if (i > 0 && !(live = la_wait(&bar_dz_read, (i - 1) & 1))) break;
-          if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
-#pragma unroll 1
-          for (int q = 0; q < 2; ++q) quarter(q);
-        }
-        if (OUT && live) {
-          if (!(live = la_wait(&bar_z, i & 1))) break;
-          if (i > 0 && !(live = la_wait(&bar_o, (i - 1) & 1))) break;
-          tc_fence_after();
-          if (i > 0 || from) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_ss_w(tb + LT_O, desc_k(x, LA_CH, ks), desc_mn(zs, D, ks), idesc(128, 128, 0, 1), ks > 0);
-          }
-          mma_commit_w(&bar_oi);
-          mma_commit_w(&empty_x[b]);
-        }
-        if (add && live) {
-#pragma unroll 1
-          for (int q = 2; q < 4; ++q) quarter(q);
-          mma_commit_w(&bar_dz);
-        }
-        if (OUT && live) {
-          if (!(live = la_wait(&bar_p, i & 1) && la_wait(&full_z[b], (i >> 1) & 1))) break;
-          tc_fence_after();
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss_w(tb + LT_QK, desc_k(x, LA_CH, ks), desc_k(st + LA_Y, LA_CH, ks), idesc(128, 128, 0, 0), ks > 0);
+        mma_commit_w(&bar_qk);
+        mma_commit_w(&empty_y[b]);
+        if (!(live = la_wait(&bar_z, i & 1))) break;
+        if (i > 0 && !(live = la_wait(&bar_o, (i - 1) & 1))) break;
+        tc_fence_after();
+        if (i > 0 || from) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ts_w(tb + LT_O, tb + LT_QK + (ks >> 2) * 64 + (ks & 3) * 8, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
-                     ks > 0 || i > 0 || from);
-          mma_commit_w(&bar_op);
+            mma_ss_w(tb + LT_O, desc_k(x, LA_CH, ks), desc_mn(zs, D, ks), idesc(128, 128, 0, 1), ks > 0);
         }
+        mma_commit_w(&bar_oi);
+        mma_commit_w(&empty_x[b]);
+        if (!(live = la_wait(&bar_p, i & 1) && la_wait(&full_z[b], par))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts_w(tb + LT_O, tb + LT_QK + (ks >> 2) * 64 + (ks & 3) * 8, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
+                   ks > 0 || i > 0 || from);
+        mma_commit_w(&bar_op);
         mma_commit_w(&empty_z[b]);
-        if (OUT && live && i + 1 < nch) pairs(i + 1);
+      }
+    }
+    // ---- and dZ here ----
+    if (warp == LA_DZ && go_s) {
+#pragma unroll 1
+      for (int n = 0; n < 4 * adds && live; ++n) {
+        const int i = n >> 2, q = n & 3, slot = n % SLOTS;
+        const uint32_t z = smem_u32(sm + (i & 1) * LA_STAGE + LA_Z);
+        if (q == 0) {
+          if (i > 0 && !(live = la_wait(&bar_dz_read, (i - 1) & 1))) break;
+          if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
+        }
+        if (!(live = la_wait(&y_full[slot], (n / SLOTS) & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            mma_ts_w(tb + LT_DZ, tb + LT_Y + (slot * TERMS + k) * 16 + ks * 8, desc_mn(z, LA_CH, q * 2 + ks),
+                     idesc(128, 128, 0, 1), q + k + ks > 0);
+        mma_commit_w(&y_empty[q]);
+        if (q == 3) {
+          mma_commit_w(&bar_dz);
+          mma_commit_w(&dz_used[i & 1]);
+          mma_commit_w(&empty_z[i & 1]);
+        }
       }
     }
   } else if (warp < LA_SET / 32) {
@@ -444,9 +439,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         tmem_wait_st();
         tc_fence_before();
         la_arrive(&bar_p);
-        if (!(live = la_wait(&bar_op, i & 1))) break;
+        if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&dz_used[b], (i >> 1) & 1)))) break;
         tc_fence_after();
-        // out by way of z, which has been read (FP32: x and z)
+        // out by way of z, which has been read by both products (FP32: x and z)
 #pragma unroll 1
         for (int j = 0; j < 64; j += 32) {
           float v[32];
@@ -637,12 +632,15 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       }
       tc_fence_before();
       la_arrive(&bar_dz_read);
-      if (OUT && i + 1 < nch) put_state();
+      if (OUT && i + 1 < nch) {
+        if (!(live = la_wait(&bar_oi, i & 1))) break;   // the state before has been used
+        put_state();
+      }
     }
     if (keep) {
       // by way of the other stage's y and x than the last chunk's, which have been used
       if (live && nch > 1)
-        live = F32 ? la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1) : la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1);
+        live = la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1) && (!OUT || la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1));
       uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
 #pragma unroll
       for (int k = 0; k < 16; ++k)

@@ -46,7 +46,7 @@ def check(x, r):
 
 CASES = [
     ([1], 1, 1), ([2, 0, 1], 1, 2), ([0, 5], 2, 2), ([128], 1, 1), ([127, 129], 1, 3), ([256, 1], 2, 2), ([64, 200, 0, 33], 2, 6),
-    ([300], 1, 4), ([513, 140], 1, 1),
+    ([300], 1, 4), ([513, 140], 1, 1), ([1409], 1, 2),
 ]
 
 
@@ -58,16 +58,17 @@ def test_documents(lengths, H, HV):
 
 
 @pytest.mark.parametrize("segment", [1, 2, 3])
-@pytest.mark.parametrize("lengths,H,HV", [([700], 1, 2), ([300, 0, 129, 1], 1, 1), ([128, 513], 2, 2)])
+@pytest.mark.parametrize("lengths,H,HV", [([700], 1, 2), ([300, 0, 129, 1], 1, 1), ([128, 513], 2, 2), ([1290], 1, 1)])
 def test_segments(lengths, H, HV, segment):
     x = make(lengths, H, HV, seed=segment)
     d = on_gpu(x)
     check(x, run(x, d, segment))
 
 
-@pytest.mark.parametrize("segment", [0, 1])
-def test_without_states(segment):
-    x = make([200, 300], 1, 2, states=False)
+@pytest.mark.parametrize("segment", [0, 1, 5])
+@pytest.mark.parametrize("lengths", [[200, 300], [1500, 1]])
+def test_without_states(segment, lengths):
+    x = make(lengths, 1, 2, states=False)
     d = on_gpu(x)
     check(x, run(x, d, segment, states=False))
 
