@@ -38,6 +38,7 @@ constexpr int LA_SMEM = LA_ZS + LA_TILE + 1024;
 // TMEM columns: QK, then P in the halves' first 32; O; dZ; the ring of decayed y
 constexpr int LT_QK = 0, LT_O = 128, LT_DZ = 256, LT_Y = 384;
 constexpr int LA_Q = 32;                     // tokens of a quarter: 16 columns a term
+constexpr float LA_COLUMNS = -0.43f;   // (128 times it: 2^-79)
 constexpr float LA_LEAST = -1e4f;   // log decays below it: nothing is left of it either, and no product is NaN
 
 // a^n: the product's rounding error is put back, so that far powers are as exact as near ones
@@ -173,12 +174,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   // a tile is asked for again as soon as it has been used: y by QK and the decayed y, x by O, z at the end of its chunk
   __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[4];
   __shared__ uint64_t dz_used[2];   // (dZ may be a chunk ahead of the output, which so needs a barrier to each stage)
-  __shared__ uint64_t bar_qk, bar_oi, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
+  __shared__ uint64_t bar_oi[2];   // (nor does the output wait for it in every chunk)
+  __shared__ uint64_t bar_qk, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
   __shared__ int go_s;
-  // a^d; a^(31-j): the columns of a block seen from its last; the decayed y's factors in a whole chunk, in parts
-  __shared__ alignas(16) float pw[LA_CH + 4], back[32];
+  // a^d; P's factors where they go by columns alone (the first half's); the decayed y's factors in a whole chunk, in parts
+  __shared__ alignas(16) float pw[LA_CH + 4], wcol[LA_CH / 2];
   __shared__ uint32_t fy[3][LA_CH / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.HV, want = blockIdx.x / a.HV;
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&full_x[i], 1);
       mbar_init(&full_z[i], 1);
       mbar_init(&dz_used[i], 1);
+      mbar_init(&bar_oi[i], 1);
       mbar_init(&empty_y[i], LA_SET / 32 + (OUT ? 1 : 0));
       mbar_init(&empty_x[i], F32 ? 2 : 1);
       mbar_init(&empty_z[i], OUT ? 3 : 1);
@@ -211,7 +214,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     }
     for (int i = 0; i < 4; ++i) mbar_init(&y_empty[i], 1);
     mbar_init(&bar_qk, 1);
-    mbar_init(&bar_oi, 1);
     mbar_init(&bar_p, LA_SET / 32);
     mbar_init(&bar_op, 1);
     mbar_init(&bar_o, LA_SET / 32);
@@ -226,7 +228,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     return x < LA_LEAST ? LA_LEAST : x;
   }();
   if (tid <= LA_CH) pw[tid] = la_power(g, (float)tid);
-  if (tid >= 256 && tid < 256 + 32) back[tid - 256] = la_power(g, (float)(31 - (tid - 256)));
+  // Where a^-128 is no more than 2^80, a^(r-c) is a^-(c+1) in P and a^(r+1) on O, the state's part with it, at the end.
+  const bool columns = g >= LA_COLUMNS && a.row_scale != 0.f;
+  if (tid >= 256 && tid < 256 + LA_CH / 2 && columns) {
+    const int c = tid - 256;
+    wcol[c] = a.p_scale / a.row_scale * la_power(g, (float)(REV ? c + 1 - LA_CH : -c - 1));
+  }
   if (tid >= 384 && tid < 384 + LA_CH / 2) {
     const int c = (tid - 384) * 2;
     uint32_t part[3];
@@ -313,13 +320,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           for (int ks = 0; ks < 8; ++ks)
             mma_ss_w(tb + LT_O, desc_k(x, LA_CH, ks), desc_mn(zs, D, ks), idesc(128, 128, 0, 1), ks > 0);
         }
-        mma_commit_w(&bar_oi);
+        mma_commit_w(&bar_oi[b]);
         mma_commit_w(&empty_x[b]);
         if (!(live = la_wait(&bar_p, i & 1) && la_wait(&full_z[b], par))) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts_w(tb + LT_O, tb + LT_QK + (ks >> 2) * 64 + (ks & 3) * 8, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
+          mma_ts_w(tb + LT_O, tb + LT_QK + ks * 16, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
                    ks > 0 || i > 0 || from);
         mma_commit_w(&bar_op);
         mma_commit_w(&empty_z[b]);
@@ -357,6 +364,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     if (OUT && go_s) {
       const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
       const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
+      const float half = columns ? la_power(g, REV ? 64.f : -64.f) : 1.f;
       auto sent = [&](int i) {   // chunk i's output has left its tiles
         bulk_wait_read();
         mbar_arrive(&empty_z[i & 1]);
@@ -379,36 +387,40 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         }
         if (!(live = la_wait(&bar_qk, i & 1))) break;
         tc_fence_after();
-        // blocks of 32 columns are seen, not seen, or on the diagonal, as a warp's rows lie; 16 columns at a time
+        // Blocks of 32 columns are seen, not seen, or on the diagonal, as a warp's rows lie; 16 columns at a time, the two
+        // warpgroups in turn.  P goes where the same 16 columns of QK were.
+        const bool plain = columns && !(REV && L < LA_CH);
 #pragma unroll 1
         for (int m = 0; m < 4; ++m) {
-          const int c = wg * 64 + m * 16, blk = c >> 5, in = c & 31;
+          const int c = m * 32 + wg * 16;
           uint32_t w[8];
-          if (REV ? blk >= quad : blk <= quad) {
+          if (REV ? m >= quad : m <= quad) {
             float v[16];
             tmem_ld16(tl + LT_QK + c, v);
-            if (blk != quad) {
-              const float far = a.p_scale * (REV ? pw[blk * 32 - row] : pw[row - blk * 32 - 31]);
-              const float2 f = make_float2(far, far);
-              const float4* near = reinterpret_cast<const float4*>((REV ? pw : back) + in);
+            if (plain) {
+              const float4* near = reinterpret_cast<const float4*>(wcol + (c & 63));
+              const float2 h = m < 2 ? make_float2(1.f, 1.f) : make_float2(half, half);
 #pragma unroll
               for (int j = 0; j < 16; j += 4) {
                 const float4 n = near[j >> 2];
-                const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), f));
-                const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), f));
+                const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), h));
+                const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), h));
                 v[j] = u.x, v[j + 1] = u.y, v[j + 2] = x.x, v[j + 3] = x.y;
               }
             } else {
+              const int far = REV ? c - row : row - c;   // tokens between this row and the first column, or seen from it
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int d = REV ? in + j - lane : lane - in - j;
-                v[j] = d >= 0 ? v[j] * (a.p_scale * pw[max(d, 0)]) : 0.f;
+              for (int j = 0; j < 16; ++j) v[j] *= a.p_scale * pw[max(REV ? far + j : far - j, 0)];
+              if (REV && L < LA_CH) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (c + j >= L) v[j] = 0.f;
               }
             }
-            if (REV && L < LA_CH) {
+            if (m == quad) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (c + j >= L) v[j] = 0.f;
+                if (REV ? wg * 16 + j < lane : wg * 16 + j > lane) v[j] = 0.f;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
@@ -416,24 +428,20 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = 0u;
           }
-          tmem_st8(tl + LT_QK + wg * 64 + m * 8, w);
+          tmem_st8(tl + LT_QK + c, w);
         }
         if (tid == 0 && i > 0) sent(i - 1);
-        if (!(live = la_wait(&bar_oi, i & 1))) break;
-        if (state) {   // O so far is the state's: a^.. of it stays
+        const float f = a.row_scale * pw[REV ? max(L - 1 - row, 0) : row + 1];
+        if (state && !plain) {   // O so far is the state's: a^.. of it stays
+          if (!(live = la_wait(&bar_oi[b], (i >> 1) & 1))) break;
           tc_fence_after();
-          const float f = a.row_scale * pw[REV ? max(L - 1 - row, 0) : row + 1];
 #pragma unroll 1
-          for (int j = 0; j < 64; j += 32) {
-            float v[32];
-            tmem_ld32(tl + LT_O + col + j, v);
+          for (int j = 0; j < 64; j += 16) {
+            float v[16];
+            tmem_ld16(tl + LT_O + col + j, v);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
-              v[k] = u.x, v[k + 1] = u.y;
-            }
+            for (int k = 0; k < 16; ++k) v[k] *= f;
             tmem_st16(tl + LT_O + col + j, v);
-            tmem_st16(tl + LT_O + col + j + 16, v + 16);
           }
         }
         tmem_wait_st();
@@ -446,6 +454,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         for (int j = 0; j < 64; j += 32) {
           float v[32];
           tmem_ld32(tl + LT_O + col + j, v);
+          if (plain) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
+              v[k] = u.x, v[k + 1] = u.y;
+            }
+          }
           if (F32) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -633,7 +648,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       tc_fence_before();
       la_arrive(&bar_dz_read);
       if (OUT && i + 1 < nch) {
-        if (!(live = la_wait(&bar_oi, i & 1))) break;   // the state before has been used
+        if (!(live = la_wait(&bar_oi[i & 1], (i >> 1) & 1))) break;   // the state before has been used
         put_state();
       }
     }
