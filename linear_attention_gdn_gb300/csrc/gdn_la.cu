@@ -26,8 +26,8 @@
 namespace gdn {
 
 constexpr int LA_SET = 256;                   // threads of each of the three sets: two warpgroups
-constexpr int LA_THREADS = 3 * LA_SET + 128;  // and a warp each for the loads and two streams of MMAs
-constexpr int LA_MMA = 3 * LA_SET / 32, LA_LOAD = LA_MMA + 1, LA_DZ = LA_MMA + 2;   // those warps
+constexpr int LA_THREADS = 3 * LA_SET + 128;  // and a warp each for the loads, two streams of MMAs, the sums' output
+constexpr int LA_MMA = 3 * LA_SET / 32, LA_LOAD = LA_MMA + 1, LA_DZ = LA_MMA + 2, LA_SUM = LA_MMA + 3;   // those warps
 // Registers a thread, of the 72 that the CTA is launched with: 256 x (80 + 56 + 96) + 128 x 40 = 896 x 72
 constexpr int LA_REG_OUT = 80, LA_REG_Y = 56, LA_REG_STATE = 96, LA_REG_CTRL = 40;
 constexpr int LA_TILE = LA_CH * D * 2;       // 32 KB
@@ -38,7 +38,7 @@ constexpr int LA_SMEM = LA_ZS + LA_TILE + 1024;
 // TMEM columns: QK, then P in the halves' first 32; O; dZ; the ring of decayed y
 constexpr int LT_QK = 0, LT_O = 128, LT_DZ = 256, LT_Y = 384;
 constexpr int LA_Q = 32;                     // tokens of a quarter: 16 columns a term
-constexpr float LA_COLUMNS = -0.43f;   // (128 times it: 2^-79)
+constexpr float LA_COLUMNS = -0.92f;   // (64 times it: 2^-85)
 constexpr float LA_LEAST = -1e4f;   // log decays below it: nothing is left of it either, and no product is NaN
 
 // a^n: the product's rounding error is put back, so that far powers are as exact as near ones
@@ -52,12 +52,12 @@ struct LaPlace {
   int t0, t1;              // the document's tokens
 };
 
-// Segment number `want` by one warp; false if there is none.  The whole list is walked if `check`: false, too, if it does
-// not have the length that the host counted.
+// Segment number `want` by one warp; false if there is none, or if the documents up to it are not in order.  If `check`, the
+// whole list is walked, and *sound tells whether it is in order and as long as the host counted it.
 __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool check, LaPlace* out, bool* sound) {
   const int lane = threadIdx.x & 31;
   int before = 0;
-  bool found = false, good = true;
+  bool found = false, good = true, there = false;
 #pragma unroll 1
   for (int d0 = 0; d0 < s.N; d0 += 32) {
     const int d = d0 + lane;
@@ -74,20 +74,22 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
       const int x = __shfl_up_sync(~0u, sum, o);
       if (lane >= o) sum += x;
     }
+    good = __all_sync(~0u, good);
     const unsigned at = __ballot_sync(~0u, n > 0 && want >= before + sum - n && want < before + sum);
-    if (at && !found) {
+    if (at && !there) {
       const int l = __ffs(at) - 1;
       out->doc = d0 + l;
       out->index = want - before - __shfl_sync(~0u, sum - n, l);
       out->count = __shfl_sync(~0u, n, l);
       out->t0 = __shfl_sync(~0u, a, l);
       out->t1 = __shfl_sync(~0u, b, l);
-      found = true;
+      there = true;
+      found = good;
       if (!check) break;
     }
     before += __shfl_sync(~0u, sum, 31);
   }
-  *sound = __all_sync(~0u, good) && (!check || before == s.total);
+  *sound = good && (!check || before == s.total);
   return found;
 }
 
@@ -111,6 +113,38 @@ __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void la_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The same for a barrier that other CTAs of the cluster arrive at, and such an arrival.
+__device__ __forceinline__ bool la_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+#pragma unroll 1
+  for (uint32_t i = 0; i < 1u << 20; ++i) {
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) break;
+  }
+  return done;
+}
+__device__ __forceinline__ uint32_t la_remote(uint32_t at, uint32_t rank) {
+  uint32_t to;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(rank));
+  return to;
+}
+__device__ __forceinline__ void la_arrive_at(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(la_remote(smem_u32(bar), rank)) : "memory");
+}
+// adds a box of FP32 to memory
+__device__ __forceinline__ void la_tma_add(const CUtensorMap* map, const void* ssrc, int x, int y, int z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(ssrc))
+               : "memory");
+}
+__device__ __forceinline__ void la_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // barrier over one set that also tells whether all of it is well
@@ -165,7 +199,7 @@ __device__ __forceinline__ uint32_t la_f32(int r, int c16) {
   return (uint32_t)((c16 >> 3) * (LA_CH * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
 }
 
-template <bool OUT, bool REV, int TERMS, bool F32>
+template <bool OUT, bool REV, int TERMS, bool SUM>
 __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_constant__ LaWalk a) {
   chain_kernel();
   constexpr int SLOTS = 128 / (16 * TERMS);   // of the ring
@@ -175,6 +209,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[4];
   __shared__ uint64_t dz_used[2];   // (dZ may be a chunk ahead of the output, which so needs a barrier to each stage)
   __shared__ uint64_t bar_oi[2];   // (nor does the output wait for it in every chunk)
+  __shared__ uint64_t part_full[2], part_empty[2];   // SUM: this head's part of a chunk is there; has been added
+  __shared__ uint64_t sum_full[2], sum_free[2];      // the heads before have been added; the next head knows
   __shared__ uint64_t bar_qk, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
@@ -188,10 +224,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   if (warp == 0) {
     LaPlace p;
     bool sound;
-    const bool found = la_find(a.seg, want, blockIdx.x == 0, &p, &sound);
+    const bool found = la_find(a.seg, want, blockIdx.x == 0, &p, &sound);   // (the cluster's CTAs find the same)
     if (!sound && lane == 0) atomicCAS(a.err, 0, GDN_ERR_INVALID_ARG);
     // without output: the segment that is last in the walk adds to none
-    const bool go = found && sound && (OUT || (REV ? p.index > 0 : p.index + 1 < p.count));
+    const bool go = found && (OUT || (REV ? p.index > 0 : p.index + 1 < p.count));
     if (lane == 0) {
       place_s = p;
       go_s = go;
@@ -206,8 +242,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&dz_used[i], 1);
       mbar_init(&bar_oi[i], 1);
       mbar_init(&empty_y[i], LA_SET / 32 + (OUT ? 1 : 0));
-      mbar_init(&empty_x[i], F32 ? 2 : 1);
-      mbar_init(&empty_z[i], OUT ? 3 : 1);
+      mbar_init(&empty_x[i], 1);
+      mbar_init(&empty_z[i], !OUT ? 1 : SUM ? 2 : 3);
+      mbar_init(&part_full[i], 1);
+      mbar_init(&part_empty[i], 1);
+      mbar_init(&sum_full[i], 1);   // (the heads' order)
+      mbar_init(&sum_free[i], 1);
     }
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&y_full[i], 4);
@@ -227,23 +267,26 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     const float x = a.decay[h];
     return x < LA_LEAST ? LA_LEAST : x;
   }();
+  // Where a^-64 is no more than 2^85, a^(r-c) is a^(63-c) in P and a^(r-63) on O at the end, and the state's part comes by
+  // a state that is held as a^64 of it, without a pass over O between (a chunk 2.5 us, with it 6.2).
+  const bool columns = OUT && g >= LA_COLUMNS && a.row_scale != 0.f;
+  const float held = columns ? la_power(g, 64.f) : 1.f;
   if (tid <= LA_CH) pw[tid] = la_power(g, (float)tid);
-  // Where a^-128 is no more than 2^80, a^(r-c) is a^-(c+1) in P and a^(r+1) on O, the state's part with it, at the end.
-  const bool columns = g >= LA_COLUMNS && a.row_scale != 0.f;
   if (tid >= 256 && tid < 256 + LA_CH / 2 && columns) {
     const int c = tid - 256;
-    wcol[c] = a.p_scale / a.row_scale * la_power(g, (float)(REV ? c + 1 - LA_CH : -c - 1));
+    wcol[c] = a.p_scale / a.row_scale * la_power(g, (float)(REV ? c - 63 : 63 - c));
   }
   if (tid >= 384 && tid < 384 + LA_CH / 2) {
     const int c = (tid - 384) * 2;
     uint32_t part[3];
-    la_parts(a.state_scale * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c)),
-             a.state_scale * la_power(g, (float)(REV ? c + 2 : LA_CH - 2 - c)), part);
+    la_parts(a.state_scale * held * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c)),
+             a.state_scale * held * la_power(g, (float)(REV ? c + 2 : LA_CH - 2 - c)), part);
 #pragma unroll
     for (int e = 0; e < 3; ++e) fy[e][c >> 1] = part[e];
   }
   tc_fence_before();
   __syncthreads();
+  if (SUM) la_cluster_sync();
   tc_fence_after();
   const uint32_t tb = tmem_slot;
   const LaPlace p = place_s;
@@ -275,6 +318,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         ++ny;
         if (OUT) {
           if (i >= 2 && !(live = la_wait(&empty_x[b], free))) break;
+          if (SUM && i >= 2 && !(live = la_wait(&part_empty[b], free))) break;
           mbar_expect_tx(&full_x[b], LA_TILE);
           la_tile(st + LA_X, &a.tx, h / a.gx, t, &full_x[b]);
           ++nx;
@@ -332,6 +376,47 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         mma_commit_w(&empty_z[b]);
       }
     }
+    // ---- SUM: the parts go out, each head's added to those before it, by the memory system but in the heads' order ----
+    if (SUM && warp == LA_SUM && go_s) {
+      uint32_t rank;
+      asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+      const int head = h / a.cluster;
+      const bool more = (int)rank + 1 < a.cluster;
+#pragma unroll 1
+      for (int i = 0; i < nch && live; ++i) {
+        const int b = i & 1, L = tokens(i), t = first(i);
+        const uint32_t par = (i >> 1) & 1;
+        const uint8_t* tile = sm + b * LA_STAGE + LA_X;
+        if (!(live = la_wait(&part_full[b], par))) break;
+        if (rank > 0 && !(live = la_wait_cluster(&sum_full[b], par))) break;
+        if (rank == 0 && L < LA_CH) {   // the rows behind are another document's; to them the other heads add zeros
+          float* o = static_cast<float*>(a.out) + (int64_t)t * a.out_token + head * a.out_head;
+#pragma unroll 1
+          for (int k = lane; k < L * 32; k += 32)
+            *reinterpret_cast<float4*>(o + (k >> 5) * a.out_token + (k & 31) * 4) =
+                *reinterpret_cast<const float4*>(tile + la_f32(k >> 5, k & 31));
+        } else if (lane == 0) {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            if (rank == 0) tma_store_3d(&a.to, tile + k * (LA_TILE / 2), k * 32, head, t);
+            else la_tma_add(&a.to, tile + k * (LA_TILE / 2), k * 32, head, t);
+          }
+          bulk_commit();
+          bulk_wait_read();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&part_empty[b]);
+        if (more) {
+          if (lane == 0) bulk_wait_all();
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+          if (i >= 2 && !(live = la_wait_cluster(&sum_free[b], par ^ 1))) break;
+          __syncwarp();
+          if (lane == 0) la_arrive_at(&sum_full[b], rank + 1);
+        }
+        if (rank > 0 && lane == 0) la_arrive_at(&sum_free[b], rank - 1);
+      }
+      if (lane == 0) bulk_wait_all();
+    }
     // ---- and dZ here ----
     if (warp == LA_DZ && go_s) {
 #pragma unroll 1
@@ -365,17 +450,19 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
       const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
       const float half = columns ? la_power(g, REV ? 64.f : -64.f) : 1.f;
+      // O's factor: of this row in a whole chunk, as P goes by columns; else of the state's part
+      const float whole = columns ? a.row_scale * la_power(g, (float)(REV ? 63 - row : row - 63)) : 0.f;
+      const float back = columns ? a.row_scale * la_power(g, -64.f) : a.row_scale;
       auto sent = [&](int i) {   // chunk i's output has left its tiles
         bulk_wait_read();
         mbar_arrive(&empty_z[i & 1]);
-        if (F32) mbar_arrive(&empty_x[i & 1]);
       };
 #pragma unroll 1
       for (int i = 0; i < nch && live; ++i) {
         const int b = i & 1, L = tokens(i), t = first(i);
         const bool state = i > 0 || from;
         uint8_t* z = sm + b * LA_STAGE + LA_Z;
-        uint8_t* out = sm + b * LA_STAGE + (F32 ? LA_X : LA_Z);
+        uint8_t* out = sm + b * LA_STAGE + (SUM ? LA_X : LA_Z);
         do {   // (a wait that runs out ends the walk for the whole set, below)
         if (L < LA_CH) {
           if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
@@ -430,8 +517,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           }
           tmem_st8(tl + LT_QK + c, w);
         }
-        if (tid == 0 && i > 0) sent(i - 1);
-        const float f = a.row_scale * pw[REV ? max(L - 1 - row, 0) : row + 1];
+        if (!SUM && tid == 0 && i > 0) sent(i - 1);
+        const float f = plain ? whole : back * pw[REV ? max(L - 1 - row, 0) : row + 1];
         if (state && !plain) {   // O so far is the state's: a^.. of it stays
           if (!(live = la_wait(&bar_oi[b], (i >> 1) & 1))) break;
           tc_fence_after();
@@ -449,19 +536,22 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         la_arrive(&bar_p);
         if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&dz_used[b], (i >> 1) & 1)))) break;
         tc_fence_after();
-        // out by way of z, which has been read by both products (FP32: x and z)
+        // out by way of z, which has been read by both products (SUM: the FP32 part by x and z)
 #pragma unroll 1
         for (int j = 0; j < 64; j += 32) {
           float v[32];
           tmem_ld32(tl + LT_O + col + j, v);
-          if (plain) {
+          if (SUM && row >= L) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0.f;
+          } else if (plain) {
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
               v[k] = u.x, v[k + 1] = u.y;
             }
           }
-          if (F32) {
+          if (SUM) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               *reinterpret_cast<float4*>(out + la_f32(row, (col + j) / 4 + k)) =
@@ -479,26 +569,23 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         fence_async_smem();
         } while (false);
         if (!(live = la_set_well<1, LA_SET>(live))) break;
-        if (L == LA_CH) {
+        if (SUM) {
+          if (tid == 0) mbar_arrive(&part_full[b]);
+        } else if (L == LA_CH) {
           if (tid == 0) {
-            for (int k = 0; k < (F32 ? 4 : 2); ++k)
-              tma_store_3d(&a.to, out + k * (LA_TILE / 2), k * (F32 ? 32 : 64), h, t);
+            tma_store_3d(&a.to, out, 0, h, t);
+            tma_store_3d(&a.to, out + LA_TILE / 2, 64, h, t);
             bulk_commit();
           }
         } else {   // the rows behind are another document's
 #pragma unroll 1
-          for (int k = tid; k < L * (F32 ? 32 : 16); k += LA_SET) {
-            if (F32)
-              *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)(t + (k >> 5)) * a.out_token + h * a.out_head +
-                                         (k & 31) * 4) = *reinterpret_cast<const float4*>(out + la_f32(k >> 5, k & 31));
-            else
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)(t + (k >> 4)) * a.out_token +
-                                        h * a.out_head + (k & 15) * 8) =
-                  *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
-          }
+          for (int k = tid; k < L * 16; k += LA_SET)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)(t + (k >> 4)) * a.out_token +
+                                      h * a.out_head + (k & 15) * 8) =
+                *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
           la_set_well<1, LA_SET>(true);
         }
-        if (tid == 0 && i + 1 == nch) bulk_wait_all();
+        if (!SUM && tid == 0 && i + 1 == nch) bulk_wait_all();
       }
     }
   } else if (warp < 2 * LA_SET / 32) {
@@ -532,8 +619,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 #pragma unroll
             for (int e = 0; e < (TERMS > 2 ? 3 : 2); ++e) f[m][e] = fy[e][c >> 1];
           } else {
-            la_parts(c < L ? a.state_scale * pw[REV ? c + 1 : L - 1 - c] : 0.f,
-                     c + 1 < L ? a.state_scale * pw[REV ? c + 2 : L - 2 - c] : 0.f, f[m]);
+            la_parts(c < L ? a.state_scale * held * pw[REV ? c + 1 : L - 1 - c] : 0.f,
+                     c + 1 < L ? a.state_scale * held * pw[REV ? c + 2 : L - 2 - c] : 0.f, f[m]);
             // what the rows past the end hold takes no part
             const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
             y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
@@ -570,37 +657,40 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       tc_fence_before();
       la_arrive(&y_full[slot]);
     };
-    const int quarters = go_s ? 2 * adds : 0;
+    const int steps = go_s ? adds : 0;
 #pragma unroll 1
-    for (int m = 0; m < quarters && live; ++m) {
-      const int i = m >> 1, q = (m & 1) * 2 + wg;
-      if (q < 2 && !(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
+    for (int i = 0; i < steps && live; ++i) {
+      if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
       const int L = tokens(i);
-      if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
-        if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
-        uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
 #pragma unroll 1
-        for (int k = max(L, q * LA_Q) * 16 + (me & 127); k < (q + 1) * LA_Q * 16; k += 128)
-          *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
-        fence_async_smem();
+      for (int q = wg; q < 4 && live; q += 2) {
+        if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
+          if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
+          uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
+#pragma unroll 1
+          for (int k = max(L, q * LA_Q) * 16 + (me & 127); k < (q + 1) * LA_Q * 16; k += 128)
+            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();
+        }
+        quarter(i, q);
       }
-      quarter(i, q);
-      if (q >= 2) la_arrive(&empty_y[i & 1]);
+      la_arrive(&empty_y[i & 1]);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_STATE));
-    // ---- the state: this thread's row y and its 64 columns z ----
+    // ---- the state (held: so many times it): this thread's row y and its 64 columns z ----
     if (go_s) {
     const int me = tid - 2 * LA_SET, wg = me >> 7, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
     const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
     uint8_t* zs = sm + LA_ZS;
     uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
+    const float times = nch > 0 ? held : 1.f;   // (an empty document's passes through as it is)
     float2 S[32];
     if (from) {
       const float* src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
       if (a.init_t) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = make_float2(src[(col + 2 * j) * D + row], src[(col + 2 * j + 1) * D + row]);
+        for (int j = 0; j < 32; ++j) S[j] = make_float2(times * src[(col + 2 * j) * D + row], times * src[(col + 2 * j + 1) * D + row]);
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -611,8 +701,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 16 + k));
-          S[2 * k] = make_float2(v.x, v.y);
-          S[2 * k + 1] = make_float2(v.z, v.w);
+          S[2 * k] = make_float2(times * v.x, times * v.y);
+          S[2 * k + 1] = make_float2(times * v.z, times * v.w);
         }
         fence_async_smem();
         la_arrive(&bar_init);
@@ -656,10 +746,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       // by way of the other stage's y and x than the last chunk's, which have been used
       if (live && nch > 1)
         live = la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1) && (!OUT || la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1));
+      const float free = columns && nch > 0 ? la_power(g, -64.f) : 1.f;
       uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) = make_float4(S[2 * k].x, S[2 * k].y, S[2 * k + 1].x, S[2 * k + 1].y);
+        *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) =
+            make_float4(free * S[2 * k].x, free * S[2 * k].y, free * S[2 * k + 1].x, free * S[2 * k + 1].y);
       if (la_set_well<2, LA_SET>(live)) {
         float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)want * a.HV + h) * (D * D);
 #pragma unroll
@@ -675,6 +767,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   if (warp == LA_MMA) tmem_dealloc(tb, 512);
+  if (SUM) la_cluster_sync();   // (whatever happened: none reads the shared memory of one that has ended)
 }
 
 // Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.
@@ -758,24 +851,38 @@ __global__ void __launch_bounds__(256) la_reduce_kernel(const float* part, __nv_
   }
 }
 
-template <bool OUT, bool REV, int TERMS, bool F32> static cudaError_t launch_walk(const LaWalk& a, cudaStream_t s) {
-  const auto kernel = la_walk_kernel<OUT, REV, TERMS, F32>;
+template <bool OUT, bool REV, int TERMS, bool SUM> static cudaError_t launch_walk(const LaWalk& a, cudaStream_t s) {
+  const auto kernel = la_walk_kernel<OUT, REV, TERMS, SUM>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LA_SMEM);
   if (e != cudaSuccess) return e;
-  return launch_chained(kernel, dim3((unsigned)a.seg.total * a.HV), dim3(LA_THREADS), LA_SMEM, s, a);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.seg.total * a.HV);
+  cfg.blockDim = dim3(LA_THREADS);
+  cfg.dynamicSmemBytes = LA_SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = SUM ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-cudaError_t launch_la_walk(const LaWalk& a, bool reverse, int terms, bool f32, cudaStream_t s) {
+cudaError_t launch_la_walk(const LaWalk& a, bool reverse, bool exact, bool sum, cudaStream_t s) {
   if (reverse) {
-    if (f32) return launch_walk<true, true, 2, true>(a, s);
-    return terms == 4 ? launch_walk<true, true, 4, false>(a, s) : launch_walk<true, true, 2, false>(a, s);
+    if (sum) return launch_walk<true, true, 2, true>(a, s);
+    return exact ? launch_walk<true, true, 4, false>(a, s) : launch_walk<true, true, 2, false>(a, s);
   }
-  if (f32) return launch_walk<true, false, 2, true>(a, s);
-  return terms == 4 ? launch_walk<true, false, 4, false>(a, s) : launch_walk<true, false, 2, false>(a, s);
+  if (sum) return launch_walk<true, false, 2, true>(a, s);
+  return exact ? launch_walk<true, false, 4, false>(a, s) : launch_walk<true, false, 2, false>(a, s);
 }
 
-cudaError_t launch_la_sums(const LaWalk& a, bool reverse, cudaStream_t s) {
-  return reverse ? launch_walk<false, true, 4, false>(a, s) : launch_walk<false, false, 4, false>(a, s);
+cudaError_t launch_la_sums(const LaWalk& a, bool reverse, bool exact, cudaStream_t s) {
+  if (reverse) return exact ? launch_walk<false, true, 4, false>(a, s) : launch_walk<false, true, 2, false>(a, s);
+  return exact ? launch_walk<false, false, 4, false>(a, s) : launch_walk<false, false, 2, false>(a, s);
 }
 
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s) {

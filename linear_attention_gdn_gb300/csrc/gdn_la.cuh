@@ -30,8 +30,9 @@ struct LaWalk {
   int init_t;             // stored [z][y] (else [y][z])
   float* sums;            // [segments][HV][y][z]: what each segment adds, for the carry (walks without output)
   float* last;            // [N][HV][y][z]: the state that a document leaves, or null
-  void* out;              // BF16 rows of 128, or FP32
+  void* out;              // BF16 rows of 128, or FP32 of walks that sum
   int64_t out_token, out_head;   // elements
+  int cluster;            // walks that sum: the value heads of a cluster, whose outputs come to one output head
   int* err;
 };
 
@@ -44,10 +45,11 @@ struct LaCarry {
   int* err;
 };
 
-cudaError_t launch_la_walk(const LaWalk& a, bool reverse, int terms, bool f32, cudaStream_t s);
-cudaError_t launch_la_sums(const LaWalk& a, bool reverse, cudaStream_t s);
+// exact: the state is handed out, and keeps FP32's exactness; else it only goes into BF16 results
+cudaError_t launch_la_walk(const LaWalk& a, bool reverse, bool exact, bool sum, cudaStream_t s);
+cudaError_t launch_la_sums(const LaWalk& a, bool reverse, bool exact, cudaStream_t s);
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s);
-// out[t][h] = sum over the G value heads of h, in order, of part[t][h G + i]
+// out[t][h] = sum over G parts, in order, of part[t][h G + i]
 cudaError_t launch_la_reduce(const float* part, void* out, int64_t T, int H, int G, int64_t out_token, cudaStream_t s);
 
 }  // namespace gdn

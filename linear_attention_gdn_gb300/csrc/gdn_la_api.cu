@@ -12,6 +12,13 @@ namespace gdn {
 
 bool make_tmap_strided(CUtensorMap* m, const void* base, int64_t T, int heads, int64_t token, int rows);
 
+// Of G value heads, how many a cluster adds up: 8 at most, and all clusters as many.
+static int la_cluster(int G) {
+  int c = 8;
+  while (G % c) --c;
+  return c;
+}
+
 bool make_tmap_f32(CUtensorMap* m, const void* base, int64_t T, int heads, int rows);
 
 struct LaPlan {
@@ -73,6 +80,11 @@ static size_t la_states(const gdn_la_problem* p, const LaPlan& plan) {
   return plan.split ? (size_t)plan.total * p->HV * STATE_F32 * sizeof(float) : 0;
 }
 
+// FP32 sums of dq or dk over the value heads of each cluster
+static size_t la_parts(const gdn_la_problem* p) {
+  return p->HV > p->H ? (size_t)p->T * (p->HV / la_cluster(p->HV / p->H)) * 128 * sizeof(float) : 0;
+}
+
 static bool la_stride(int64_t* s, int heads) {
   if (*s == 0) *s = (int64_t)heads * 128;
   return *s >= (int64_t)heads * 128 && *s % 8 == 0 && *s < (int64_t)1 << 38;
@@ -116,12 +128,12 @@ struct LaCall {
   }
   void check(cudaError_t e) { ok = ok && e == cudaSuccess; }
   // the states that the segments start from, by y and z as set
-  void carried(bool reverse, const float* init, int init_t, float* sums) {
+  void carried(bool reverse, bool exact, const float* init, int init_t, float* sums) {
     if (!ok) return;
     w.sums = sums;
     w.init = nullptr;
     prof_begin(K_LA_SUMS, s);
-    check(launch_la_sums(w, reverse, s));
+    check(launch_la_sums(w, reverse, exact, s));
     prof_end(K_LA_SUMS, s);
     const LaCarry c = {w.seg, w.decay, w.HV, init_t, reverse, init, sums, w.err};
     prof_begin(K_LA_CARRY, s);
@@ -133,22 +145,37 @@ struct LaCall {
     w.init_segments = one_a_segment;
     w.init_t = init_t;
   }
-  void walk(bool reverse, bool f32, void* out, int64_t token, int64_t head, float* last) {
-    if (!ok) return;
+  // to rows of the value heads, `token` elements apart
+  void walk(bool reverse, void* out, int64_t token, float* last) {
     w.out = out;
     w.out_token = token;
-    w.out_head = head;
+    w.out_head = 128;
     w.last = last;
-    if (p->T > 0) ok = f32 ? make_tmap_f32(&w.to, out, p->T, p->HV, LA_CH) : make_tmap_strided(&w.to, out, p->T, p->HV, token, LA_CH);
+    w.cluster = 1;
+    if (p->T > 0) ok = ok && make_tmap_strided(&w.to, out, p->T, p->HV, token, LA_CH);
     if (!ok) return;
     prof_begin(K_LA_WALK, s);
-    check(launch_la_walk(w, reverse, last ? 4 : 2, f32, s));
+    check(launch_la_walk(w, reverse, last != nullptr, false, s));
     prof_end(K_LA_WALK, s);
   }
-  void reduce(const float* part, void* out, int64_t token) {
+  // to rows of the q/k heads, the sums over their value heads: in FP32 by clusters of them, then rounded (and added up where
+  // there are several clusters)
+  void walk_summed(bool reverse, void* out, int64_t token, float* part) {
+    const int G = p->HV / p->H, C = la_cluster(G);
+    if (G == 1) return walk(reverse, out, token, nullptr);
+    w.last = nullptr;
+    w.cluster = C;
+    w.out = part;
+    w.out_token = (int64_t)p->HV / C * 128;
+    w.out_head = 128;
+    if (p->T > 0) ok = ok && make_tmap_f32(&w.to, part, p->T, p->HV / C, LA_CH);
+    if (!ok) return;
+    prof_begin(K_LA_WALK, s);
+    check(launch_la_walk(w, reverse, false, true, s));
+    prof_end(K_LA_WALK, s);
     if (!ok || p->T == 0) return;
     prof_begin(K_LA_REDUCE, s);
-    check(launch_la_reduce(part, out, p->T, p->H, p->HV / p->H, token, s));
+    check(launch_la_reduce(part, out, p->T, p->H, G / C, token, s));
     prof_end(K_LA_REDUCE, s);
   }
 };
@@ -165,7 +192,7 @@ gdn_status gdn_la_workspace_bytes(const gdn_la_problem* p, const int32_t* cu_hos
   if (st != GDN_OK) return st;
   if (!fwd_bytes || !bwd_bytes) return GDN_ERR_INVALID_ARG;
   *fwd_bytes = la_states(p, plan);
-  *bwd_bytes = 2 * la_states(p, plan) + (p->HV > p->H ? (size_t)p->T * p->HV * 128 * sizeof(float) : 0);
+  *bwd_bytes = 2 * la_states(p, plan) + la_parts(p);
   return GDN_OK;
 }
 
@@ -188,10 +215,10 @@ gdn_status gdn_la_fwd(const gdn_la_problem* p, const void* q, const void* k, con
   c.scales(p->scale, p->scale, 1.f);
   c.start(s_in, 0, 0);
   if (plan.split) {
-    c.carried(false, s_in, 0, static_cast<float*>(workspace));
+    c.carried(false, s_out != nullptr, s_in, 0, static_cast<float*>(workspace));
     c.start(static_cast<float*>(workspace), 1, 0);
   }
-  c.walk(false, false, o, (int64_t)p->HV * 128, 128, s_out);
+  c.walk(false, o, (int64_t)p->HV * 128, s_out);
   return c.ok ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -215,37 +242,33 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
   if (ws_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
   if (p->T == 0 && !ds_in) return GDN_OK;
   const LaTensor tq = {q, p->H, qs}, tk = {k, p->H, ks}, tv = {v, p->HV, vs}, td = {dO, p->HV, (int64_t)p->HV * 128};
-  const int G = p->HV / p->H;
   float* states = static_cast<float*>(workspace);
   const size_t values = la_states(p, plan) / sizeof(float);
   float *wstates = states + values, *part = wstates + values;
-  const int64_t part_token = (int64_t)p->HV * 128;
   LaCall c(p, plan, decay, cu_dev, dev_err, stream);
   // dv, and the gradients of the states; Z[dk][dv]
   c.tensors(tk, tq, td);
   c.scales(p->scale, 1.f, p->scale);
   c.start(ds_out, 0, 0);
   if (plan.split) {
-    c.carried(true, ds_out, 0, wstates);
+    c.carried(true, ds_in != nullptr, ds_out, 0, wstates);
     c.start(wstates, 1, 0);
   }
-  c.walk(true, false, dv, vs, 128, ds_in);
+  c.walk(true, dv, vs, ds_in);
   if (p->T == 0) return c.ok ? GDN_OK : GDN_ERR_CUDA;
   // dk, by the same states seen from the other side
   c.tensors(tv, td, tq);
   c.start(plan.split ? wstates : ds_out, plan.split, 1);
-  c.walk(true, G > 1, G > 1 ? (void*)part : dk, G > 1 ? part_token : ks, 128, nullptr);
-  if (G > 1) c.reduce(part, dk, ks);
+  c.walk_summed(true, dk, ks, part);
   // dq; Z[dv][dk], the state before each chunk
   c.tensors(td, tv, tk);
   c.scales(p->scale, p->scale, 1.f);
   c.start(s_in, 0, 1);
   if (plan.split) {
-    c.carried(false, s_in, 1, states);
+    c.carried(false, false, s_in, 1, states);
     c.start(states, 1, 0);
   }
-  c.walk(false, G > 1, G > 1 ? (void*)part : dq, G > 1 ? part_token : qs, 128, nullptr);
-  if (G > 1) c.reduce(part, dq, qs);
+  c.walk_summed(false, dq, qs, part);
   return c.ok ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -47,6 +47,7 @@ def check(x, r):
 CASES = [
     ([1], 1, 1), ([2, 0, 1], 1, 2), ([0, 5], 2, 2), ([128], 1, 1), ([127, 129], 1, 3), ([256, 1], 2, 2), ([64, 200, 0, 33], 2, 6),
     ([300], 1, 4), ([513, 140], 1, 1), ([1409], 1, 2),
+    ([200, 70], 1, 8), ([150], 1, 11), ([300, 5], 1, 16), ([140], 2, 14),
 ]
 
 
@@ -73,7 +74,7 @@ def test_without_states(segment, lengths):
     check(x, run(x, d, segment, states=False))
 
 
-@pytest.mark.parametrize("decay", [0.0, -1e-6, -2.0, -30.0, -1e9, float("-inf")])
+@pytest.mark.parametrize("decay", [0.0, -1e-6, -0.3, -0.91, -0.93, -2.0, -30.0, -1e9, float("-inf")])
 @pytest.mark.parametrize("segment", [0, 1])
 def test_decays(decay, segment):
     x = make([290], 1, 1, seed=7, decay=decay)

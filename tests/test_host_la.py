@@ -43,15 +43,16 @@ def test_la_bad_problems(call, prob, cu, code):
     for n in names for v in (None, P + 8)] + [
     (c, x) for c in (fwd, bwd) for x in (dict(decay=None), dict(decay=P + 2), dict(cu_dev=None), dict(cu_dev=P + 1),
                                          dict(err=None), dict(s_in=P + 4))] + [
-    (fwd, dict(s_out=P + 8)), (bwd, dict(ds_out=P + 4)), (bwd, dict(ds_in=P + 8)), (bwd, dict(ws=None))])
+    (fwd, dict(s_out=P + 8)), (bwd, dict(ds_out=P + 4)), (bwd, dict(ds_in=P + 8))])
 def test_la_bad_arguments(call, change):
     refused(1, *call(gdn.la_problem(**LA), **change))
 
 
 def test_la_workspace():
     one = gdn.la_problem(**LA)
-    assert gdn.gdn_la_workspace_bytes(one, CU) == (0, 5 * 2 * 512)   # the group's parts
-    assert gdn.gdn_la_workspace_bytes(gdn.la_problem(5, 2, 2, 2), CU) == (0, 0)
+    # FP32 sums over the value heads of a group, or as many of them as one cluster takes
+    for H, HV, heads in ((1, 2, 1), (2, 2, 0), (1, 8, 1), (2, 32, 4), (1, 11, 11)):
+        assert gdn.gdn_la_workspace_bytes(gdn.la_problem(5, 2, H, HV), CU) == (0, 5 * heads * 512)
     cu = [0, 300, 300, 301]
     cut = gdn.la_problem(301, 3, 2, 2, segment=2)                    # segments: 2, 1, 1
     f, b = gdn.gdn_la_workspace_bytes(cut, cu)
@@ -59,6 +60,7 @@ def test_la_workspace():
     refused(3, *fwd(cut, np.array(cu, np.int32), ws_bytes=f - 1))
     refused(3, *bwd(cut, np.array(cu, np.int32), ws_bytes=b - 1))
     refused(1, *fwd(cut, np.array(cu, np.int32), ws=P + 8))
+    refused(1, *bwd(cut, np.array(cu, np.int32), ws=None))
     with pytest.raises(ValueError):
         gdn.gdn_la_fwd(one, *[P] * 5, CU[:2], P, P, P, P, P, 0, stream=0)
 
