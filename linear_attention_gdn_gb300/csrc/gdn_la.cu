@@ -49,18 +49,20 @@ __device__ __forceinline__ float la_power(float g, float n) {
 
 struct LaPlace {
   int doc, index, count;   // segment `index` of the document's `count`
+  int segment;             // its number among all
   int t0, t1;              // the document's tokens
 };
 
-// Segment number `want` by one warp; false if there is none, or if the documents up to it are not in order.  If `check`, the
-// whole list is walked, and *sound tells whether it is in order and as long as the host counted it.
+// The segment of place `want` by one warp; false if there is none, or if the documents up to it are not in order.  If `check`,
+// the whole list is walked, and *sound tells whether it is in order and as long as the host counted it.  Up to 32 documents
+// give their segments by falling length, so that no long one begins when the others end (12 prompts of up to 4,096 tokens).
 __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool check, LaPlace* out, bool* sound) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   bool found = false, good = true, there = false;
 #pragma unroll 1
   for (int d0 = 0; d0 < s.N; d0 += 32) {
-    const int d = d0 + lane;
+    int d = d0 + lane;
     int n = 0, a = 0, b = 0;
     if (d < s.N) {
       a = s.cu[d];
@@ -68,18 +70,40 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
       if (a < 0 || b < a || b > s.T || (d == 0 && a != 0) || (d == s.N - 1 && b != s.T)) good = false, b = a = 0;
       n = max(1, ((b - a + LA_CH - 1) / LA_CH + s.len - 1) / s.len);
     }
-    int sum = n;
+    auto sums = [&](int x) {   // inclusive, over the lanes
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(~0u, sum, o);
-      if (lane >= o) sum += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+      }
+      return x;
+    };
+    int first = before + sums(n) - n, place = first;   // of the document's segments: their number, their place
+    if (s.N <= 32) {
+      const int key = d < s.N ? min(b - a, s.len * LA_CH) : -1;
+      int rank = 0, from = 0;
+#pragma unroll 4
+      for (int i = 0; i < 32; ++i) {
+        const int other = __shfl_sync(~0u, key, i);
+        rank += other > key || (other == key && i < lane);
+      }
+#pragma unroll 4
+      for (int i = 0; i < 32; ++i)
+        if (__shfl_sync(~0u, rank, i) == lane) from = i;
+      d = from;
+      n = __shfl_sync(~0u, n, from);
+      a = __shfl_sync(~0u, a, from);
+      b = __shfl_sync(~0u, b, from);
+      first = __shfl_sync(~0u, first, from);
+      place = sums(n) - n;
     }
     good = __all_sync(~0u, good);
-    const unsigned at = __ballot_sync(~0u, n > 0 && want >= before + sum - n && want < before + sum);
+    const unsigned at = __ballot_sync(~0u, n > 0 && want >= place && want < place + n);
     if (at && !there) {
       const int l = __ffs(at) - 1;
-      out->doc = d0 + l;
-      out->index = want - before - __shfl_sync(~0u, sum - n, l);
+      out->doc = __shfl_sync(~0u, d, l);
+      out->index = want - __shfl_sync(~0u, place, l);
+      out->segment = __shfl_sync(~0u, first, l) + out->index;
       out->count = __shfl_sync(~0u, n, l);
       out->t0 = __shfl_sync(~0u, a, l);
       out->t1 = __shfl_sync(~0u, b, l);
@@ -87,7 +111,7 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
       found = good;
       if (!check) break;
     }
-    before += __shfl_sync(~0u, sum, 31);
+    before += __shfl_sync(~0u, sums(n), 31);
   }
   *sound = good && (!check || before == s.total);
   return found;
@@ -202,16 +226,19 @@ __device__ __forceinline__ uint32_t la_f32(int r, int c16) {
 template <bool OUT, bool REV, int TERMS, bool SUM>
 __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_constant__ LaWalk a) {
   chain_kernel();
-  constexpr int SLOTS = 128 / (16 * TERMS);   // of the ring
+  constexpr int SLOTS = OUT ? 128 / (16 * TERMS) : 4;   // of the ring
+  // without output there is room for the ring of a whole chunk and for a second dZ, made while the first is read
+  constexpr int T_Y = OUT ? LT_Y : 256;
+  auto t_dz = [](int i) { return OUT ? LT_DZ : (i & 1) * 128; };
   extern __shared__ uint8_t la_raw[];
   uint8_t* sm = smem_align1024(la_raw);
   // a tile is asked for again as soon as it has been used: y by QK and the decayed y, x by O, z at the end of its chunk
   __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[4];
-  __shared__ uint64_t dz_used[2];   // (dZ may be a chunk ahead of the output, which so needs a barrier to each stage)
-  __shared__ uint64_t bar_oi[2];   // (nor does the output wait for it in every chunk)
+  // (by the chunk's parity: dZ may be a chunk ahead of those that wait for it, and these do not all wait in every chunk)
+  __shared__ uint64_t bar_dz[2], dz_read[2], bar_oi[2];
   __shared__ uint64_t part_full[2], part_empty[2];   // SUM: this head's part of a chunk is there; has been added
   __shared__ uint64_t sum_full[2], sum_free[2];      // the heads before have been added; the next head knows
-  __shared__ uint64_t bar_qk, bar_p, bar_op, bar_o, bar_dz, bar_dz_read, bar_z, bar_init;
+  __shared__ uint64_t bar_qk, bar_p, bar_op, bar_o, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
   __shared__ int go_s;
@@ -239,7 +266,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&full_y[i], 1);
       mbar_init(&full_x[i], 1);
       mbar_init(&full_z[i], 1);
-      mbar_init(&dz_used[i], 1);
+      mbar_init(&bar_dz[i], 1);
+      mbar_init(&dz_read[i], LA_SET / 32);
       mbar_init(&bar_oi[i], 1);
       mbar_init(&empty_y[i], LA_SET / 32 + (OUT ? 1 : 0));
       mbar_init(&empty_x[i], 1);
@@ -257,8 +285,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     mbar_init(&bar_p, LA_SET / 32);
     mbar_init(&bar_op, 1);
     mbar_init(&bar_o, LA_SET / 32);
-    mbar_init(&bar_dz, 1);
-    mbar_init(&bar_dz_read, LA_SET / 32);
     mbar_init(&bar_z, LA_SET / 32);
     mbar_init(&bar_init, LA_SET / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -424,7 +450,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         const int i = n >> 2, q = n & 3, slot = n % SLOTS;
         const uint32_t z = smem_u32(sm + (i & 1) * LA_STAGE + LA_Z);
         if (q == 0) {
-          if (i > 0 && !(live = la_wait(&bar_dz_read, (i - 1) & 1))) break;
+          const int last = OUT ? i - 1 : i - 2;   // chunk whose dZ was where this one's goes
+          if (last >= 0 && !(live = la_wait(&dz_read[last & 1], (last >> 1) & 1))) break;
           if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
         }
         if (!(live = la_wait(&y_full[slot], (n / SLOTS) & 1))) break;
@@ -433,12 +460,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         for (int k = 0; k < TERMS; ++k)
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
-            mma_ts_w(tb + LT_DZ, tb + LT_Y + (slot * TERMS + k) * 16 + ks * 8, desc_mn(z, LA_CH, q * 2 + ks),
+            mma_ts_w(tb + t_dz(i), tb + T_Y + (slot * TERMS + k) * 16 + ks * 8, desc_mn(z, LA_CH, q * 2 + ks),
                      idesc(128, 128, 0, 1), q + k + ks > 0);
         mma_commit_w(&y_empty[q]);
         if (q == 3) {
-          mma_commit_w(&bar_dz);
-          mma_commit_w(&dz_used[i & 1]);
+          mma_commit_w(&bar_dz[i & 1]);
           mma_commit_w(&empty_z[i & 1]);
         }
       }
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         tmem_wait_st();
         tc_fence_before();
         la_arrive(&bar_p);
-        if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&dz_used[b], (i >> 1) & 1)))) break;
+        if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&bar_dz[b], (i >> 1) & 1)))) break;
         tc_fence_after();
         // out by way of z, which has been read by both products (SUM: the FP32 part by x and z)
 #pragma unroll 1
@@ -597,7 +623,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     // lane / 4 of each 8 x 8 block, which is also how a store of 16 TMEM lanes takes them.
     auto quarter = [&](int i, int q) {
       const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i);
-      const uint32_t to = tl + LT_Y + slot * TERMS * 16;
+      const uint32_t to = tl + T_Y + slot * TERMS * 16;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {   // 16 tokens
         const int t0 = q * LA_Q + half * 16, pair = (lane & 3) * 2;
@@ -687,7 +713,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     const float times = nch > 0 ? held : 1.f;   // (an empty document's passes through as it is)
     float2 S[32];
     if (from) {
-      const float* src = a.init + ((int64_t)(a.init_segments ? want : p.doc) * a.HV + h) * (D * D);
+      const float* src = a.init + ((int64_t)(a.init_segments ? p.segment : p.doc) * a.HV + h) * (D * D);
       if (a.init_t) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) S[j] = make_float2(times * src[(col + 2 * j) * D + row], times * src[(col + 2 * j + 1) * D + row]);
@@ -723,20 +749,20 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     if (OUT && nch > 0) put_state();
 #pragma unroll 1
     for (int i = 0; i < adds && live; ++i) {
-      if (!(live = la_wait(&bar_dz, i & 1))) break;
+      if (!(live = la_wait(&bar_dz[i & 1], (i >> 1) & 1))) break;
       tc_fence_after();
       const float f = pw[tokens(i)];
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         uint32_t v[16];
-        tmem_ld16_async(tl + LT_DZ + col + 2 * j, v);
+        tmem_ld16_async(tl + t_dz(i) + col + 2 * j, v);
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           S[j + k] = __ffma2_rn(make_float2(f, f), S[j + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
       }
       tc_fence_before();
-      la_arrive(&bar_dz_read);
+      la_arrive(&dz_read[i & 1]);
       if (OUT && i + 1 < nch) {
         if (!(live = la_wait(&bar_oi[i & 1], (i >> 1) & 1))) break;   // the state before has been used
         put_state();
@@ -753,7 +779,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) =
             make_float4(free * S[2 * k].x, free * S[2 * k].y, free * S[2 * k + 1].x, free * S[2 * k + 1].y);
       if (la_set_well<2, LA_SET>(live)) {
-        float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)want * a.HV + h) * (D * D);
+        float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)p.segment * a.HV + h) * (D * D);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int e = k * LA_SET + me;
@@ -771,7 +797,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 }
 
 // Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.
-constexpr int LC_THREADS = 256, LC_PARTS = D * D / (4 * LC_THREADS), LC_AHEAD = 8;
+constexpr int LC_THREADS = 256, LC_PARTS = D * D / (4 * LC_THREADS), LC_AHEAD = 16;
 
 __global__ void __launch_bounds__(LC_THREADS) la_carry_kernel(const LaCarry a) {
   chain_kernel();
