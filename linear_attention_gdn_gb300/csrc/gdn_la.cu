@@ -10,8 +10,8 @@
 // P and the decayed y go to TMEM as left operands, so that shared memory, which all operands pass, is read least.  The state
 // is FP32 in registers (thread: one row y, 64 columns z), rounded to BF16 once for the product with x.  The decayed y is given
 // to the product as a sum of BF16 terms, so that the state keeps FP32's exactness: two terms (2^-17) where only BF16 results
-// come of it, four (2^-25) where the state itself is handed out.  Both come from the packed BF16 multiply-add, whose one rounding
-// the next one recovers, in 3 and 5 instructions a pair of values.
+// come of it, by the packed BF16 multiply-add, whose rounding the next one recovers (3 instructions a pair of values); three, the
+// whole FP32 product 8 bits at a time, where the state itself is handed out.
 // Three sets of warps work side by side: one makes P, scales O and writes it out, one makes the decayed y, a quarter of a
 // chunk at a time in a ring, one carries the state on; so the tensor cores have dZ to do while P is made.
 // Documents whose chains are too few or too long are cut into segments: la_walk without output first sums what each adds,
@@ -202,14 +202,18 @@ __device__ __forceinline__ uint32_t bf_fma(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-// a pair of FP32 values as three pairs of BF16 whose sums they are (to 2^-24)
-__device__ __forceinline__ void la_parts(float lo, float hi, uint32_t* part) {
-#pragma unroll
-  for (int e = 0; e < 3; ++e) {
-    part[e] = pack_bf16(lo, hi);
-    lo -= __uint_as_float(part[e] << 16);
-    hi -= __uint_as_float(part[e] & 0xffff0000u);
-  }
+// a pair of FP32 values as two pairs of BF16 whose sums they are (to 2^-17)
+__device__ __forceinline__ void la_parts(float2 v, uint32_t (&part)[2]) {
+  part[0] = pack_bf16(v.x, v.y);
+  part[1] = pack_bf16(v.x - __uint_as_float(part[0] << 16), v.y - __uint_as_float(part[0] & 0xffff0000u));
+}
+// BF16 by cutting off: the upper halves of two values, and what is left of them below
+__device__ __forceinline__ uint32_t uppers(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+__device__ __forceinline__ float2 below(float2 x) {
+  const float2 top = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u), __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+  return __ffma2_rn(top, make_float2(-1.f, -1.f), x);
 }
 
 // 16 lanes x 8 columns: register 2 m + i of a lane goes to the TMEM lane (lane / 4) + 8 i, column 4 m + lane % 4
@@ -242,9 +246,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
   __shared__ int go_s;
-  // a^d; P's factors where they go by columns alone (the first half's); the decayed y's factors in a whole chunk, in parts
+  // a^d; P's factors where they go by columns alone (the first half's); the decayed y's factors in a whole chunk
   __shared__ alignas(16) float pw[LA_CH + 4], wcol[LA_CH / 2];
-  __shared__ uint32_t fy[3][LA_CH / 2];
+  __shared__ uint32_t fy[2][LA_CH / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.HV, want = blockIdx.x / a.HV;
 
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&bar_dz[i], 1);
       mbar_init(&dz_read[i], LA_SET / 32);
       mbar_init(&bar_oi[i], 1);
-      mbar_init(&empty_y[i], LA_SET / 32 + (OUT ? 1 : 0));
+      mbar_init(&empty_y[i], OUT ? LA_SET / 32 + 1 : 2 * LA_SET / 32);
       mbar_init(&empty_x[i], 1);
       mbar_init(&empty_z[i], !OUT ? 1 : SUM ? 2 : 3);
       mbar_init(&part_full[i], 1);
@@ -304,11 +308,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   }
   if (tid >= 384 && tid < 384 + LA_CH / 2) {
     const int c = (tid - 384) * 2;
-    uint32_t part[3];
-    la_parts(a.state_scale * held * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c)),
-             a.state_scale * held * la_power(g, (float)(REV ? c + 2 : LA_CH - 2 - c)), part);
-#pragma unroll
-    for (int e = 0; e < 3; ++e) fy[e][c >> 1] = part[e];
+    const float2 f = make_float2(a.state_scale * held * la_power(g, (float)(REV ? c + 1 : LA_CH - 1 - c)),
+                                 a.state_scale * held * la_power(g, (float)(REV ? c + 2 : LA_CH - 2 - c)));
+    uint32_t part[2] = {__float_as_uint(f.x), __float_as_uint(f.y)};
+    if (TERMS == 2) la_parts(f, part);
+    fy[0][c >> 1] = part[0];
+    fy[1][c >> 1] = part[1];
   }
   tc_fence_before();
   __syncthreads();
@@ -326,6 +331,99 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   // the i-th chunk of the walk: its first token, and how many
   auto first = [&](int i) { return p.t0 + (c0 + (REV ? nch - 1 - i : i)) * LA_CH; };
   auto tokens = [&](int i) { return min(LA_CH, p.t1 - first(i)); };
+
+  // ---- the decayed y, by one warpgroup the quarters q0, q0 + qs, ..; a warp 32 columns of y ----
+  auto make_y = [&](int q0, int qs) {
+    const int quad = warp & 3;
+    const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
+    // Quarter q of chunk i, in terms.  A transposing load gives a lane the tokens 2 (lane % 4) and the next of the column
+    // lane / 4 of each 8 x 8 block, which is also how a store of 16 TMEM lanes takes them.
+    auto quarter = [&](int i, int q) {
+      const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i);
+      const uint32_t to = tl + T_Y + slot * TERMS * 16;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {   // 16 tokens
+        const int t0 = q * LA_Q + half * 16, pair = (lane & 3) * 2;
+        uint32_t y[8];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int c8 = quad * 4 + m * 2 + ((lane >> 3) & 1), r = t0 + (lane >> 4) * 8 + (lane & 7);
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(y[4 * m]), "=r"(y[4 * m + 1]), "=r"(y[4 * m + 2]), "=r"(y[4 * m + 3])
+                       : "r"(smem_u32(sm + (i & 1) * LA_STAGE + LA_Y) + sw_chunk(r, c8, LA_CH))
+                       : "memory");
+        }
+        // The decays of this lane's tokens in the first and the last 8 as two BF16 parts each, or, for a state that is
+        // handed out, in FP32; and the products in BF16 parts: y f1 and what its rounding left (exact: 16 bits) with y f2; or
+        // the FP32 product's three times 8 bits.
+        uint32_t w[TERMS][8];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int c = t0 + m * 8 + pair;
+          float2 f;
+          uint32_t part[2];
+          if (L == LA_CH) {
+            if (TERMS == 2) part[0] = fy[0][c >> 1], part[1] = fy[1][c >> 1];
+            else f = make_float2(__uint_as_float(fy[0][c >> 1]), __uint_as_float(fy[1][c >> 1]));
+          } else {
+            f.x = c < L ? a.state_scale * held * pw[REV ? c + 1 : L - 1 - c] : 0.f;
+            f.y = c + 1 < L ? a.state_scale * held * pw[REV ? c + 2 : L - 2 - c] : 0.f;
+            la_parts(f, part);
+            // what the rows past the end hold takes no part
+            const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
+            y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 2 * m + (e & 1) + (e >> 1) * 4;
+            if (TERMS == 2) {
+              w[0][k] = bf_mul(y[k], part[0]);
+              w[1][k] = bf_fma(y[k], part[1], bf_fma(y[k], part[0], w[0][k] ^ 0x80008000u));
+            } else {
+              float2 v = mul2(f, make_float2(__uint_as_float(y[k] << 16), __uint_as_float(y[k] & 0xffff0000u)));
+#pragma unroll
+              for (int n = 0; n < TERMS; ++n) {
+                w[n][k] = uppers(v);
+                v = below(v);
+              }
+            }
+          }
+        }
+        if (half == 0) {
+          // (of the quarter that had the slot before; so that each warpgroup sees every phase of the one barrier it waits for)
+          if (n >= SLOTS && !(live = la_wait(&y_empty[(q - SLOTS) & 3], ((n - SLOTS) >> 2) & 1))) return;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int e = 0; e < TERMS; ++e) {
+          tmem_st_16lanes(to + e * 16 + half * 8, w[e]);
+          tmem_st_16lanes(to + e * 16 + half * 8 + (16u << 16), w[e] + 4);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      la_arrive(&y_full[slot]);
+    };
+    const int steps = go_s ? adds : 0;
+#pragma unroll 1
+    for (int i = 0; i < steps && live; ++i) {
+      if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
+      const int L = tokens(i);
+#pragma unroll 1
+      for (int q = q0; q < 4 && live; q += qs) {
+        if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
+          if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
+          uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
+#pragma unroll 1
+          for (int k = max(L, q * LA_Q) * 16 + (tid & 127); k < (q + 1) * LA_Q * 16; k += 128)
+            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_async_smem();
+        }
+        quarter(i, q);
+      }
+      la_arrive(&empty_y[i & 1]);
+    }
+  };
 
   if (warp >= LA_MMA) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_CTRL));
@@ -471,8 +569,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     }
   } else if (warp < LA_SET / 32) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_OUT));
-    // ---- P and O: this thread's row of tokens and its 64 columns ----
-    if (OUT && go_s) {
+    // ---- P and O: this thread's row of tokens and its 64 columns (without output: half of the quarters, too) ----
+    if (!OUT) {
+      make_y((tid >> 7) & 1, 4);
+    } else if (go_s) {
       const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
       const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
       const float half = columns ? la_power(g, REV ? 64.f : -64.f) : 1.f;
@@ -616,92 +716,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     }
   } else if (warp < 2 * LA_SET / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_Y));
-    // ---- the decayed y: a warpgroup the even quarters, the other the odd ones; a warp 32 columns of y ----
-    const int me = tid - LA_SET, wg = me >> 7, quad = warp & 3;
-    const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
-    // Quarter q of chunk i, in terms.  A transposing load gives a lane the tokens 2 (lane % 4) and the next of the column
-    // lane / 4 of each 8 x 8 block, which is also how a store of 16 TMEM lanes takes them.
-    auto quarter = [&](int i, int q) {
-      const int n = i * 4 + q, slot = n % SLOTS, L = tokens(i);
-      const uint32_t to = tl + T_Y + slot * TERMS * 16;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {   // 16 tokens
-        const int t0 = q * LA_Q + half * 16, pair = (lane & 3) * 2;
-        uint32_t y[8];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int c8 = quad * 4 + m * 2 + ((lane >> 3) & 1), r = t0 + (lane >> 4) * 8 + (lane & 7);
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(y[4 * m]), "=r"(y[4 * m + 1]), "=r"(y[4 * m + 2]), "=r"(y[4 * m + 3])
-                       : "r"(smem_u32(sm + (i & 1) * LA_STAGE + LA_Y) + sw_chunk(r, c8, LA_CH))
-                       : "memory");
-        }
-        // the decays of this lane's tokens in the first and the last 8, as three BF16 parts each
-        uint32_t f[2][3];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int c = t0 + m * 8 + pair;
-          if (L == LA_CH) {
-#pragma unroll
-            for (int e = 0; e < (TERMS > 2 ? 3 : 2); ++e) f[m][e] = fy[e][c >> 1];
-          } else {
-            la_parts(c < L ? a.state_scale * held * pw[REV ? c + 1 : L - 1 - c] : 0.f,
-                     c + 1 < L ? a.state_scale * held * pw[REV ? c + 2 : L - 2 - c] : 0.f, f[m]);
-            // what the rows past the end hold takes no part
-            const uint32_t mask = (c < L ? 0xffffu : 0u) | (c + 1 < L ? 0xffff0000u : 0u);
-            y[2 * m] &= mask, y[2 * m + 1] &= mask, y[4 + 2 * m] &= mask, y[5 + 2 * m] &= mask;
-          }
-        }
-        // The products in BF16 parts, without a rounding left out: y f1 and what its rounding left (exact: 16 bits), then y f2
-        // added to that, or, for a state that is handed out, y f2 and what its rounding left with y f3.
-        uint32_t w[TERMS][8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t* d = f[(k >> 1) & 1];
-          w[0][k] = bf_mul(y[k], d[0]);
-          const uint32_t left = bf_fma(y[k], d[0], w[0][k] ^ 0x80008000u);
-          if (TERMS == 2) {
-            w[1][k] = bf_fma(y[k], d[1], left);
-          } else {
-            w[1][k] = left;
-            w[2][k] = bf_mul(y[k], d[1]);
-            w[TERMS - 1][k] = bf_fma(y[k], d[2], bf_fma(y[k], d[1], w[2][k] ^ 0x80008000u));
-          }
-        }
-        if (half == 0) {
-          // (of the quarter that had the slot before; so that each warpgroup sees every phase of the one barrier it waits for)
-          if (n >= SLOTS && !(live = la_wait(&y_empty[(q - SLOTS) & 3], ((n - SLOTS) >> 2) & 1))) return;
-          tc_fence_after();
-        }
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e) {
-          tmem_st_16lanes(to + e * 16 + half * 8, w[e]);
-          tmem_st_16lanes(to + e * 16 + half * 8 + (16u << 16), w[e] + 4);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      la_arrive(&y_full[slot]);
-    };
-    const int steps = go_s ? adds : 0;
-#pragma unroll 1
-    for (int i = 0; i < steps && live; ++i) {
-      if (!(live = la_wait(&full_y[i & 1], (i >> 1) & 1))) break;
-      const int L = tokens(i);
-#pragma unroll 1
-      for (int q = wg; q < 4 && live; q += 2) {
-        if (L < LA_CH) {   // z of the rows past the end, as far as this quarter's products read them
-          if (!(live = la_wait(&full_z[i & 1], (i >> 1) & 1))) break;
-          uint8_t* z = sm + (i & 1) * LA_STAGE + LA_Z;
-#pragma unroll 1
-          for (int k = max(L, q * LA_Q) * 16 + (me & 127); k < (q + 1) * LA_Q * 16; k += 128)
-            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
-          fence_async_smem();
-        }
-        quarter(i, q);
-      }
-      la_arrive(&empty_y[i & 1]);
-    }
+    if (OUT) make_y((tid >> 7) & 1, 2);
+    else make_y(2 + ((tid >> 7) & 1), 4);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_STATE));
     // ---- the state (held: so many times it): this thread's row y and its 64 columns z ----
@@ -900,15 +916,15 @@ template <bool OUT, bool REV, int TERMS, bool SUM> static cudaError_t launch_wal
 cudaError_t launch_la_walk(const LaWalk& a, bool reverse, bool exact, bool sum, cudaStream_t s) {
   if (reverse) {
     if (sum) return launch_walk<true, true, 2, true>(a, s);
-    return exact ? launch_walk<true, true, 4, false>(a, s) : launch_walk<true, true, 2, false>(a, s);
+    return exact ? launch_walk<true, true, 3, false>(a, s) : launch_walk<true, true, 2, false>(a, s);
   }
   if (sum) return launch_walk<true, false, 2, true>(a, s);
-  return exact ? launch_walk<true, false, 4, false>(a, s) : launch_walk<true, false, 2, false>(a, s);
+  return exact ? launch_walk<true, false, 3, false>(a, s) : launch_walk<true, false, 2, false>(a, s);
 }
 
 cudaError_t launch_la_sums(const LaWalk& a, bool reverse, bool exact, cudaStream_t s) {
-  if (reverse) return exact ? launch_walk<false, true, 4, false>(a, s) : launch_walk<false, true, 2, false>(a, s);
-  return exact ? launch_walk<false, false, 4, false>(a, s) : launch_walk<false, false, 2, false>(a, s);
+  if (reverse) return exact ? launch_walk<false, true, 3, false>(a, s) : launch_walk<false, true, 2, false>(a, s);
+  return exact ? launch_walk<false, false, 3, false>(a, s) : launch_walk<false, false, 2, false>(a, s);
 }
 
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s) {
