@@ -3,7 +3,9 @@
 // The states of a request lie in blocks of B tokens: block j's slot holds the state after the last of the tokens
 // jB .. (j+1)B - 1 that has been taken.  All of it is sums over the requests in their order (tokens taken, blocks needed,
 // blocks given back) and then one write a token, so it is one kernel of one cluster: every CTA works the sums out
-// for itself in shared memory, and they share the writes.  Bound by the latency of its few dependent steps.
+// for itself in shared memory, and they share the writes.  Bound by the latency of its few dependent steps (64 requests of a
+// token each: 5.4 us).  Where tokens are many, a second kernel writes theirs from the first one's tables (2,000 requests, 60,000
+// tokens; by the one cluster 21 us).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -16,9 +18,11 @@
 
 namespace gdn {
 
-constexpr int TB_THREADS = 1024, TB_MOST = 16384;   // requests
+constexpr int TB_THREADS = 1024, TB_MOST = 16384;   // threads of a CTA; requests
+constexpr int TB_SMALL = 256;      // threads where requests and tokens are no more than that
+constexpr int TB_KEPT = 8192;      // so many requests' lengths and contexts are kept in shared memory, too
 constexpr int TB_CLUSTER = 8;      // CTAs where there is more to write than
-constexpr int TB_ALONE = 4096;     // so many tokens and blocks
+constexpr int TB_ALONE = 4096;     // so many tokens or requests; the tokens are then a second kernel's
 
 struct StepTableArgs {
   const int* lengths;
@@ -34,15 +38,15 @@ struct StepTableArgs {
   int* slot_out;
   int* err;
   int N, T, block, row, slots;
+  int apart;   // the tokens' tables are the second kernel's
 };
 
 struct Request {
   int take, held, need, back;   // tokens; blocks held, needed, given back
 };
 
-__device__ __forceinline__ Request request_of(const StepTableArgs& a, int n, bool* bad) {
+__device__ __forceinline__ Request request_of(const StepTableArgs& a, int len, int ctx, bool* bad) {
   Request r = {0, 0, 0, 0};
-  const int len = a.lengths[n], ctx = a.context[n];
   const int64_t after = (int64_t)ctx + max(len, 0);
   if (len < -1 || ctx < 0 || after > (int64_t)a.row * a.block) {
     *bad = true;
@@ -58,26 +62,44 @@ __device__ __forceinline__ Request request_of(const StepTableArgs& a, int n, boo
   return r;
 }
 
-// inclusive sums over the CTA's threads; `total` of all of them
-__device__ __forceinline__ int64_t over_cta(int64_t v, int64_t* words, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(~0u, v, d);
-    if (lane >= d) v += x;
+// the request whose part of a running sum (sum[n] <= e < sum[n + 1]) the element e is
+__device__ __forceinline__ int owner_of(const int* sum, int N, int e) {
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sum[mid] <= e) lo = mid;
+    else hi = mid;
   }
-  __syncthreads();
-  if (lane == 31) words[warp] = v;
-  __syncthreads();
-  int64_t w = words[lane];
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(~0u, w, d);
-    if (lane >= d) w += x;
+  return lo;
+}
+
+// position and slot of token t of request n, whose tokens end before `end`; first: its position is t more than that
+__device__ __forceinline__ void write_token(const StepTableArgs& a, int t, int tokens, int n, int first, int end) {
+  int pos = 0, slot = -1;
+  if (t < tokens) {
+    pos = first + t;
+    if (t == end - 1 || pos % a.block == a.block - 1) slot = __ldcg(a.blocks + (int64_t)n * a.row + pos / a.block);
   }
-  *total = __shfl_sync(~0u, w, 31);
-  const int64_t before = __shfl_sync(~0u, w, (warp + 31) & 31);
-  return v + (warp ? before : 0);
+  if (a.positions) a.positions[t] = pos;
+  a.slot_out[t] = slot;
+}
+
+// the tokens' tables from the requests': a request that has taken tokens had so many fewer before
+__global__ void __launch_bounds__(TB_THREADS) step_tokens_kernel(const StepTableArgs a) {
+  chain_kernel();
+  extern __shared__ int tb_smem[];
+  const int* cu = a.cu;
+  if (a.N <= TB_KEPT) {
+    for (int n = threadIdx.x; n <= a.N; n += blockDim.x) tb_smem[n] = __ldcg(a.cu + n);
+    __syncthreads();
+    cu = tb_smem;
+  }
+  const int tokens = cu[a.N];
+  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < a.T; t += gridDim.x * blockDim.x) {
+    const int n = t < tokens ? owner_of(cu, a.N, t) : 0;
+    const int end = t < tokens ? cu[n + 1] : 0;
+    write_token(a, t, tokens, n, t < tokens ? __ldcg(a.context_out + n) - end : 0, end);
+  }
 }
 
 __global__ void __launch_bounds__(TB_THREADS) step_tables_kernel(const StepTableArgs a) {
@@ -86,112 +108,118 @@ __global__ void __launch_bounds__(TB_THREADS) step_tables_kernel(const StepTable
   extern __shared__ int tb_smem[];
   int *start = tb_smem, *fresh = start + a.N + 1, *given = fresh + a.N + 1;   // tokens, new blocks, returned blocks before
   __shared__ int64_t words[3][32];
+  __shared__ int first_s;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
-  const int lane = threadIdx.x & 31, warp = rank * (TB_THREADS / 32) + (threadIdx.x >> 5), warps = ctas * (TB_THREADS / 32);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int me = rank * blockDim.x + threadIdx.x, all = ctas * blockDim.x;
+  const int *lengths = a.lengths, *context = a.context;
+  if (a.N <= TB_KEPT) {
+    int *l = given + a.N + 1, *c = l + a.N;
+    for (int n = threadIdx.x; n < a.N; n += blockDim.x) l[n] = a.lengths[n], c[n] = a.context[n];   // (read again by the same thread first)
+    lengths = l;
+    context = c;
+  }
   bool bad = false;
   int64_t held = *a.free_count;
   if (held < 0 || held > a.slots) {
     bad = true;
     held = 0;
   }
-  // blocks that come back
-  int64_t back = 0, take = 0, need = 0, all;
-  for (int n0 = 0; n0 < a.N; n0 += TB_THREADS) {
+  if (threadIdx.x == 0) start[0] = fresh[0] = given[0] = 0, first_s = a.N;
+  // running sums of the tokens, the blocks needed and the blocks that come back (past 2^31, as much: it fits nowhere)
+  int64_t before[3] = {0, 0, 0};
+  for (int n0 = 0; n0 < a.N; n0 += blockDim.x) {
     const int n = n0 + threadIdx.x;
-    const Request r = n < a.N ? request_of(a, n, &bad) : Request{0, 0, 0, 0};
-    const int64_t sum = over_cta(r.back, words[0], &all);
-    if (n < a.N) given[n] = (int)min(back + sum - r.back, (int64_t)INT32_MAX);
-    back += all;
+    const Request r = n < a.N ? request_of(a, lengths[n], context[n], &bad) : Request{0, 0, 0, 0};
+    int64_t v[3] = {r.take, r.need, r.back};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, v[i], d);
+        if (lane >= d) v[i] += x;
+      }
+    __syncthreads();
+    if (lane == 31)
+      for (int i = 0; i < 3; ++i) words[i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      int64_t w = lane < warps ? words[i][lane] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, w, d);
+        if (lane >= d) w += x;
+      }
+      const int64_t up = __shfl_sync(~0u, w, (warp + 31) & 31), total = __shfl_sync(~0u, w, 31);
+      v[i] += before[i] + (warp ? up : 0);
+      before[i] += total;
+    }
+    if (n < a.N) {
+      start[n + 1] = (int)min(v[0], (int64_t)INT32_MAX);
+      fresh[n + 1] = (int)min(v[1], (int64_t)INT32_MAX);
+      given[n + 1] = (int)min(v[2], (int64_t)INT32_MAX);
+    }
   }
+  int64_t back = before[2];
   if (held + back > a.slots) {   // (more than there are: some were not this pool's)
     bad = true;
     back = a.slots - held;
   }
   const int64_t top = held + back;
-  // Those that fit take their tokens and blocks: the first that does not, and all after it, wait.  The sums only
-  // grow, so each request sees for itself.
-  for (int n0 = 0; n0 < a.N; n0 += TB_THREADS) {
-    const int n = n0 + threadIdx.x;
-    const Request r = n < a.N ? request_of(a, n, &bad) : Request{0, 0, 0, 0};
-    const int64_t st = over_cta(r.take, words[1], &all) + take;
-    take += all;
-    const int64_t sn = over_cta(r.need, words[2], &all) + need;
-    need += all;
-    const bool fits = st <= a.T && sn <= top;
-    // (of those that wait, the sums before them, which no later one passes: what the last that fits leaves)
-    if (n < a.N) {
-      start[n + 1] = fits ? (int)st : -1;
-      fresh[n + 1] = fits ? (int)sn : -1;
-    }
-  }
-  if (threadIdx.x == 0) start[0] = fresh[0] = 0;
-  __syncthreads();
-  // the first that waits, by the sums that were not kept
-  __shared__ int first_s;
-  if (threadIdx.x == 0) first_s = a.N;
-  __syncthreads();
-  for (int n = threadIdx.x; n < a.N; n += TB_THREADS)
-    if (start[n + 1] < 0) atomicMin(&first_s, n);
-  __syncthreads();
-  const int fit = first_s;
-  const int tokens = start[fit], taken = fresh[fit];
-  __syncthreads();
-  for (int n = fit + threadIdx.x; n < a.N; n += TB_THREADS) {
-    start[n + 1] = tokens;
-    fresh[n + 1] = taken;
-  }
-  __syncthreads();
   if (bad && rank == 0) *a.err = ST_DEVICE;
+  __syncthreads();
+  // The first request that does not fit, and all after it, wait.
+  if (before[0] > a.T || before[1] > top) {
+    for (int n = threadIdx.x; n < a.N; n += blockDim.x)
+      if (start[n + 1] > a.T || fresh[n + 1] > top) atomicMin(&first_s, n);
+    __syncthreads();
+    const int fit = first_s, t = start[fit], f = fresh[fit];
+    __syncthreads();
+    for (int n = fit + threadIdx.x; n < a.N; n += blockDim.x) start[n + 1] = t, fresh[n + 1] = f;
+    __syncthreads();
+  }
+  const int tokens = start[a.N], taken = fresh[a.N];
   // returned blocks on top of the free ones
-  for (int n = warp; n < a.N; n += warps) {
-    bool b = false;
-    const Request r = request_of(a, n, &b);
-    const int64_t at = held + given[n];
-    for (int j = lane; j < r.back; j += 32)
-      if (at + j < a.slots) a.free_list[at + j] = a.blocks[(int64_t)n * a.row + j];
+  if (back > 0) {
+    for (int e = me; e < back; e += all) {
+      const int n = owner_of(given, a.N, e);
+      a.free_list[held + e] = a.blocks[(int64_t)n * a.row + (e - given[n])];
+    }
+    cluster.sync();
   }
-  cluster.sync();
   // new ones from there
-  for (int n = warp; n < a.N; n += warps) {
-    const int count = fresh[n + 1] - fresh[n];
-    if (count <= 0) continue;
-    bool b = false;
-    const Request r = request_of(a, n, &b);
-    for (int j = lane; j < count; j += 32)
-      a.blocks[(int64_t)n * a.row + r.held + j] = __ldcg(a.free_list + (top - 1 - fresh[n] - j));
+  if (taken > 0) {
+    for (int e = me; e < taken; e += all) {
+      const int n = owner_of(fresh, a.N, e);
+      const int held_n = (int)(((int64_t)context[n] + a.block - 1) / a.block);
+      a.blocks[(int64_t)n * a.row + held_n + (e - fresh[n])] = __ldcg(a.free_list + (top - 1 - e));
+    }
+    cluster.sync();
   }
-  cluster.sync();
-  for (int n = rank * TB_THREADS + threadIdx.x; n < a.N; n += ctas * TB_THREADS) {
-    const int ctx = a.context[n];
+  for (int n = me; n < a.N; n += all) {
     bool b = false;
-    const Request r = request_of(a, n, &b);
+    const int ctx = context[n];
+    const Request r = request_of(a, lengths[n], ctx, &b);
     a.slot_in[n] = r.held > 0 && r.back == 0 ? __ldcg(a.blocks + (int64_t)n * a.row + (ctx - 1) / a.block) : -1;
     a.cu[n + 1] = start[n + 1];
   }
-  if (rank == 0 && threadIdx.x == 0) a.cu[0] = 0;
-  for (int t = rank * TB_THREADS + threadIdx.x; t < a.T; t += ctas * TB_THREADS) {
-    int pos = 0, slot = -1;
-    if (t < tokens) {
-      int lo = 0, hi = a.N;   // start[lo] <= t < start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      pos = a.context[lo] + t - start[lo];
-      if (t == start[lo + 1] - 1 || pos % a.block == a.block - 1) slot = __ldcg(a.blocks + (int64_t)lo * a.row + pos / a.block);
+  if (me == 0) a.cu[0] = 0;
+  if (!a.apart) {
+    for (int t = me; t < a.T; t += all) {
+      const int n = t < tokens ? owner_of(start, a.N, t) : 0;
+      write_token(a, t, tokens, n, t < tokens ? context[n] - start[n] : 0, t < tokens ? start[n + 1] : 0);
     }
-    if (a.positions) a.positions[t] = pos;
-    a.slot_out[t] = slot;
   }
   cluster.sync();   // all has been read: the books may be the ones that go on
-  for (int n = rank * TB_THREADS + threadIdx.x; n < a.N; n += ctas * TB_THREADS) {
+  for (int n = me; n < a.N; n += all) {
     bool b = false;
-    request_of(a, n, &b);
-    a.context_out[n] = a.lengths[n] == -1 && !b ? 0 : a.context[n] + start[n + 1] - start[n];
+    const int len = lengths[n], ctx = context[n];
+    request_of(a, len, ctx, &b);
+    a.context_out[n] = len == -1 && !b ? 0 : ctx + start[n + 1] - start[n];
   }
-  if (rank == 0 && threadIdx.x == 0) *a.free_count_out = (int)top - taken;
+  if (me == 0) *a.free_count_out = (int)top - taken;
 }
 
 }  // namespace gdn
@@ -209,12 +237,14 @@ extern "C" gdn_status gdn_step_tables(const gdn_tables_problem* p, const int32_t
   if ((p->N > 0 && p->max_blocks > 0 && !blocks) || (p->slots > 0 && !free_list) || (p->T > 0 && !slot_out)) return GDN_ERR_INVALID_ARG;
   if (!on_words(lengths, context, context_out, blocks, free_list, positions, slot_in, slot_out)) return GDN_ERR_INVALID_ARG;
   const StepTableArgs a = {lengths, context, context_out, blocks, free_list, free_count, free_count_out, cu, positions, slot_in,
-                           slot_out, err, p->N, p->T, p->block, p->max_blocks, p->slots};
-  const int bytes = (3 * p->N + 3) * (int)sizeof(int);
+                           slot_out, err, p->N, p->T, p->block, p->max_blocks, p->slots, p->T > TB_ALONE};
+  const int bytes = ((p->N <= TB_KEPT ? 5 : 3) * p->N + 3) * (int)sizeof(int);
+  static_assert(3 * TB_MOST >= 5 * TB_KEPT, "the larger need is what is asked for");
   if (cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (3 * TB_MOST + 3) * (int)sizeof(int)) !=
       cudaSuccess)
     return GDN_ERR_CUDA;
   const int ctas = p->T > TB_ALONE || p->N > TB_ALONE ? TB_CLUSTER : 1;
+  const int threads = p->T <= TB_SMALL && p->N <= TB_SMALL ? TB_SMALL : TB_THREADS;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -223,13 +253,18 @@ extern "C" gdn_status gdn_step_tables(const gdn_tables_problem* p, const int32_t
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(TB_THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   prof_begin(K_STEP_TABLES, stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, step_tables_kernel, a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, step_tables_kernel, a);
+  if (e == cudaSuccess && a.apart) {
+    const int need = (p->T + TB_THREADS - 1) / TB_THREADS, most = 2 * sm_count();
+    e = launch_chained(step_tokens_kernel, dim3(need < most ? need : most), dim3(TB_THREADS),
+                       p->N <= TB_KEPT ? (p->N + 1) * sizeof(int) : 0, stream, a);
+  }
   prof_end(K_STEP_TABLES, stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
