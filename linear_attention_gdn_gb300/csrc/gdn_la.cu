@@ -38,7 +38,7 @@ constexpr int LA_SMEM = LA_ZS + LA_TILE + 1024;
 // TMEM columns: QK, then P in the halves' first 32; O; dZ; the ring of decayed y
 constexpr int LT_QK = 0, LT_O = 128, LT_DZ = 256, LT_Y = 384;
 constexpr int LA_Q = 32;                     // tokens of a quarter: 16 columns a term
-constexpr float LA_COLUMNS = -0.92f;   // (64 times it: 2^-85)
+constexpr float LA_COLUMNS = -0.7f;   // (64 times it: 2^-65, which leaves P z as much of FP32's range)
 constexpr float LA_LEAST = -1e4f;   // log decays below it: nothing is left of it either, and no product is NaN
 
 // a^n: the product's rounding error is put back, so that far powers are as exact as near ones
@@ -117,12 +117,12 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
   return found;
 }
 
-// Waits, but not for ever: 2^20 tries, about a second; false if they run out.  Small on purpose, as are the loops below:
+// Waits, but not for ever: 2^18 tries of up to 4 us each, about a second; false if they run out.  Small on purpose, as are the loops below:
 // the kernel's speed is lost as soon as its code leaves the instruction cache (196 KB of it: a chunk in 12,000 cycles).
 __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
 #pragma unroll 1
-  for (uint32_t i = 0; i < 1u << 20; ++i) {
+  for (uint32_t i = 0; i < 1u << 18; ++i) {
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
@@ -143,7 +143,7 @@ __device__ __forceinline__ void la_arrive(uint64_t* bar) {
 __device__ __forceinline__ bool la_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t done;
 #pragma unroll 1
-  for (uint32_t i = 0; i < 1u << 20; ++i) {
+  for (uint32_t i = 0; i < 1u << 18; ++i) {
     asm volatile(
         "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     const float x = a.decay[h];
     return x < LA_LEAST ? LA_LEAST : x;
   }();
-  // Where a^-64 is no more than 2^85, a^(r-c) is a^(63-c) in P and a^(r-63) on O at the end, and the state's part comes by
+  // Where a^-64 is no more than 2^65, a^(r-c) is a^(63-c) in P and a^(r-63) on O at the end, and the state's part comes by
   // a state that is held as a^64 of it, without a pass over O between (a chunk 2.5 us, with it 6.2).
   const bool columns = OUT && g >= LA_COLUMNS && a.row_scale != 0.f;
   const float held = columns ? la_power(g, 64.f) : 1.f;

@@ -74,12 +74,44 @@ def test_without_states(segment, lengths):
     check(x, run(x, d, segment, states=False))
 
 
-@pytest.mark.parametrize("decay", [0.0, -1e-6, -0.3, -0.91, -0.93, -2.0, -30.0, -1e9, float("-inf")])
+@pytest.mark.parametrize("decay", [0.0, -1e-6, -0.3, -0.69, -0.71, -2.0, -30.0, -1e9, float("-inf")])
 @pytest.mark.parametrize("segment", [0, 1])
 def test_decays(decay, segment):
     x = make([290], 1, 1, seed=7, decay=decay)
     d = on_gpu(x)
     check(x, run(x, d, segment))
+
+
+@pytest.mark.parametrize("decay", [-0.001, -0.69, -2.0])
+@pytest.mark.parametrize("size", [1e-6, 3e4])
+def test_sizes_of_values(size, decay):
+    """Small and large values: the tolerances are relative to what is added up."""
+    x = make([200], 1, 2, seed=13, decay=decay)
+    for m in ("q", "k", "v", "dO"):
+        x[m] = (x[m].float() * size).bfloat16()
+    for m in ("s_in", "ds_out"):
+        x[m] = x[m] * size * size
+    check(x, run(x, on_gpu(x)))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.5, 4.0])
+def test_scales(scale):
+    x = make([200], 1, 2, seed=14)
+    d = on_gpu(x)
+    one = run(x, d)
+    prob = gdn.la_problem(200, 1, 1, 2, scale)
+    o, dv = torch.empty_like(one["o"]), torch.empty_like(one["dv"])
+    dq, dk = torch.empty_like(one["dq"]), torch.empty_like(one["dk"])
+    ws = torch.empty(max(16, *gdn.gdn_la_workspace_bytes(prob, x["cu"])), dtype=torch.uint8, device="cuda")
+    gdn.gdn_la_fwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], o, None, d["err"], ws)
+    gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], d["dO"], None, dq, dk, dv, None, d["err"], ws)
+    zero = torch.zeros_like(d["s_in"])
+    y = dict(x, ds_out=zero.cpu())
+    r = run(y, on_gpu(y))
+    for got, want in ((o, one["o"]), (dq, r["dq"]), (dk, r["dk"]), (dv, r["dv"])):
+        w = f64(want) * (scale / SCALE)
+        # the same sums, rounded at other places: three roundings of each part, as in `expect`, on either side
+        assert np.abs(f64(got) - w).max() <= 6 * 2.0 ** -8 * np.abs(w).max() + 1e-30
 
 
 @pytest.mark.parametrize("pad", [8, 128])
