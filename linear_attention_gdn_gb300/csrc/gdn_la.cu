@@ -79,19 +79,20 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
       return x;
     };
     int first = before + sums(n) - n, place = first;   // of the document's segments: their number, their place
-    if (s.N <= 32) {
+    if (s.N > 1 && s.N <= 32) {
       const int key = d < s.N ? min(b - a, s.len * LA_CH) : -1;
       int rank = 0, from = 0;
 #pragma unroll 4
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < s.N; ++i) {
         const int other = __shfl_sync(~0u, key, i);
         rank += other > key || (other == key && i < lane);
       }
 #pragma unroll 4
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < s.N; ++i)
         if (__shfl_sync(~0u, rank, i) == lane) from = i;
       d = from;
       n = __shfl_sync(~0u, n, from);
+      if (lane >= s.N) n = 0;
       a = __shfl_sync(~0u, a, from);
       b = __shfl_sync(~0u, b, from);
       first = __shfl_sync(~0u, first, from);
@@ -229,7 +230,7 @@ __device__ __forceinline__ uint32_t la_f32(int r, int c16) {
 
 template <bool OUT, bool REV, int TERMS, bool SUM>
 __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_constant__ LaWalk a) {
-  chain_kernel();
+  dependents_may_launch();
   constexpr int SLOTS = OUT ? 128 / (16 * TERMS) : 4;   // of the ring
   // without output there is room for the ring of a whole chunk and for a second dZ, made while the first is read
   constexpr int T_Y = OUT ? LT_Y : 256;
@@ -252,18 +253,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.HV, want = blockIdx.x / a.HV;
 
-  if (warp == 0) {
-    LaPlace p;
-    bool sound;
-    const bool found = la_find(a.seg, want, blockIdx.x == 0, &p, &sound);   // (the cluster's CTAs find the same)
-    if (!sound && lane == 0) atomicCAS(a.err, 0, GDN_ERR_INVALID_ARG);
-    // without output: the segment that is last in the walk adds to none
-    const bool go = found && (OUT || (REV ? p.index > 0 : p.index + 1 < p.count));
-    if (lane == 0) {
-      place_s = p;
-      go_s = go;
-    }
-  } else if (warp == LA_MMA) {
+  // what touches no memory, while the kernel before ends
+  if (warp == LA_MMA) {
     tmem_alloc(&tmem_slot, 512);
   } else if (warp == LA_LOAD && lane == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -292,6 +283,24 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     mbar_init(&bar_z, LA_SET / 32);
     mbar_init(&bar_init, LA_SET / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == LA_DZ && lane == 0) {
+    const CUtensorMap* maps[4] = {&a.tx, &a.ty, &a.tz, &a.to};
+#pragma unroll
+    for (int i = OUT ? 0 : 1; i < (OUT && !SUM ? 4 : 3); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[i]) : "memory");
+  }
+  previous_kernel_done();
+  if (warp == 0) {
+    LaPlace p;
+    bool sound;
+    const bool found = la_find(a.seg, want, blockIdx.x == 0, &p, &sound);   // (the cluster's CTAs find the same)
+    if (!sound && lane == 0) atomicCAS(a.err, 0, GDN_ERR_INVALID_ARG);
+    // without output: the segment that is last in the walk adds to none
+    const bool go = found && (OUT || (REV ? p.index > 0 : p.index + 1 < p.count));
+    if (lane == 0) {
+      place_s = p;
+      go_s = go;
+    }
   }
   const float g = [&] {
     const float x = a.decay[h];
