@@ -458,6 +458,8 @@ gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
  *              then left out, GDN_ERR_TIMEOUT for a bounded wait that ran out.
  * The forward needs nothing saved for the backward but its inputs: the backward walks the documents again.  Sums and
  * states are FP32; the state keeps FP32's exactness, and is rounded to BF16 once, where it meets the rows.
+ * Heads with decays down to -0.7 are held up to 2^65 times larger or smaller on the way: in them, products (q . k) v and states
+ * above 1e16 can overflow, and those below 1e-18 lose bits.
  * Inside a chunk of 128 tokens of a document, a value that is not finite also reaches the tokens before it; those of other
  * documents, and rows outside cu_seqlens' range, reach none.
  * Results are the same bits from run to run; dq and dk are sums over the value heads of a group in order.

@@ -16,6 +16,13 @@
 // chunk at a time in a ring, one carries the state on; so the tensor cores have dZ to do while P is made.
 // Documents whose chains are too few or too long are cut into segments: la_walk without output first sums what each adds,
 // la_carry_kernel turns the sums into the states they start from.
+//
+// What bounds it: a chunk is 12.6 MFLOP of products (6 of 128^3, dZ's twice or three times) and 128 KB to and from memory, and
+// takes a CTA 2.45 us at 1.9 GHz (3 documents of 8,192 tokens, 48 heads of their own: 6.5 TB/s, 96% of a plain copy's rate;
+// 32,768 tokens: 6.8 TB/s).  By the counters the tensor cores work 47% of the time, the warps issue 54%, and the path from shared
+// memory and TMEM is near its limit.  Where heads share q and k, memory has less to do and the chunk's time stays (12 prompts
+// of 30,054 tokens in all, 48 heads on 16: 266 us, 59% of the copy rate).  Shorter chunks need more passes of the state
+// through shared memory per token, longer ones do not fit the tiles.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +42,7 @@ constexpr int LA_STAGE = 3 * LA_TILE;        // y, x, z; z then has the output o
 constexpr int LA_Y = 0, LA_X = LA_TILE, LA_Z = 2 * LA_TILE;
 constexpr int LA_ZS = 2 * LA_STAGE;          // the state as BF16 [y][z]
 constexpr int LA_SMEM = LA_ZS + LA_TILE + 1024;
-// TMEM columns: QK, then P in the halves' first 32; O; dZ; the ring of decayed y
+// TMEM columns: QK, each 16 of them then P in their first 8; O; dZ; the ring of decayed y
 constexpr int LT_QK = 0, LT_O = 128, LT_DZ = 256, LT_Y = 384;
 constexpr int LA_Q = 32;                     // tokens of a quarter: 16 columns a term
 constexpr float LA_COLUMNS = -0.7f;   // (64 times it: 2^-65, which leaves P z as much of FP32's range)
@@ -118,8 +125,9 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
   return found;
 }
 
-// Waits, but not for ever: 2^18 tries of up to 4 us each, about a second; false if they run out.  Small on purpose, as are the loops below:
-// the kernel's speed is lost as soon as its code leaves the instruction cache (196 KB of it: a chunk in 12,000 cycles).
+// Waits, but not for ever: 2^18 tries of up to 4 us each, about a second; false if they run out.  Small on purpose, as are the
+// loops below: the kernel's speed is lost as soon as its code leaves the instruction cache (with the waits and loops unrolled it
+// had 196 KB, and a chunk took 12,000 cycles; now 4,700).
 __device__ __forceinline__ bool la_wait(uint64_t* bar, uint32_t parity) {
   uint32_t done;
 #pragma unroll 1
@@ -599,109 +607,109 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         uint8_t* z = sm + b * LA_STAGE + LA_Z;
         uint8_t* out = sm + b * LA_STAGE + (SUM ? LA_X : LA_Z);
         do {   // (a wait that runs out ends the walk for the whole set, below)
-        if (L < LA_CH) {
-          if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
-          // rows past the document's end are another's, or none: what they hold takes no part
+          if (L < LA_CH) {
+            if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
+            // rows past the document's end are another's, or none: what they hold takes no part
 #pragma unroll 1
-          for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_SET)
-            *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
-          fence_async_smem();
-        }
-        if (!(live = la_wait(&bar_qk, i & 1))) break;
-        tc_fence_after();
-        // Blocks of 32 columns are seen, not seen, or on the diagonal, as a warp's rows lie; 16 columns at a time, the two
-        // warpgroups in turn.  P goes where the same 16 columns of QK were.
-        const bool plain = columns && !(REV && L < LA_CH);
+            for (int k = L * 16 + tid; k < LA_CH * 16; k += LA_SET)
+              *reinterpret_cast<uint4*>(z + sw_chunk(k >> 4, k & 15, LA_CH)) = make_uint4(0u, 0u, 0u, 0u);
+            fence_async_smem();
+          }
+          if (!(live = la_wait(&bar_qk, i & 1))) break;
+          tc_fence_after();
+          // Blocks of 32 columns are seen, not seen, or on the diagonal, as a warp's rows lie; 16 columns at a time, the two
+          // warpgroups in turn.  P goes where the same 16 columns of QK were.
+          const bool plain = columns && !(REV && L < LA_CH);
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-          const int c = m * 32 + wg * 16;
-          uint32_t w[8];
-          if (REV ? m >= quad : m <= quad) {
-            float v[16];
-            tmem_ld16(tl + LT_QK + c, v);
-            if (plain) {
-              const float4* near = reinterpret_cast<const float4*>(wcol + (c & 63));
-              const float2 h = m < 2 ? make_float2(1.f, 1.f) : make_float2(half, half);
+          for (int m = 0; m < 4; ++m) {
+            const int c = m * 32 + wg * 16;
+            uint32_t w[8];
+            if (REV ? m >= quad : m <= quad) {
+              float v[16];
+              tmem_ld16(tl + LT_QK + c, v);
+              if (plain) {
+                const float4* near = reinterpret_cast<const float4*>(wcol + (c & 63));
+                const float2 h = m < 2 ? make_float2(1.f, 1.f) : make_float2(half, half);
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 n = near[j >> 2];
-                const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), h));
-                const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), h));
-                v[j] = u.x, v[j + 1] = u.y, v[j + 2] = x.x, v[j + 3] = x.y;
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 n = near[j >> 2];
+                  const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), h));
+                  const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), h));
+                  v[j] = u.x, v[j + 1] = u.y, v[j + 2] = x.x, v[j + 3] = x.y;
+                }
+              } else {
+                const int far = REV ? c - row : row - c;   // tokens between this row and the first column, or seen from it
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] *= a.p_scale * pw[max(REV ? far + j : far - j, 0)];
+                if (REV && L < LA_CH) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    if (c + j >= L) v[j] = 0.f;
+                }
               }
-            } else {
-              const int far = REV ? c - row : row - c;   // tokens between this row and the first column, or seen from it
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] *= a.p_scale * pw[max(REV ? far + j : far - j, 0)];
-              if (REV && L < LA_CH) {
+              if (m == quad) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                  if (c + j >= L) v[j] = 0.f;
+                  if (REV ? wg * 16 + j < lane : wg * 16 + j > lane) v[j] = 0.f;
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = 0u;
+            }
+            tmem_st8(tl + LT_QK + c, w);
+          }
+          if (!SUM && tid == 0 && i > 0) sent(i - 1);
+          const float f = plain ? whole : back * pw[REV ? max(L - 1 - row, 0) : row + 1];
+          if (state && !plain) {   // O so far is the state's: a^.. of it stays
+            if (!(live = la_wait(&bar_oi[b], (i >> 1) & 1))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 16) {
+              float v[16];
+              tmem_ld16(tl + LT_O + col + j, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] *= f;
+              tmem_st16(tl + LT_O + col + j, v);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          la_arrive(&bar_p);
+          if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&bar_dz[b], (i >> 1) & 1)))) break;
+          tc_fence_after();
+          // out by way of z, which has been read by both products (SUM: the FP32 part by x and z)
+#pragma unroll 1
+          for (int j = 0; j < 64; j += 32) {
+            float v[32];
+            tmem_ld32(tl + LT_O + col + j, v);
+            if (SUM && row >= L) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            } else if (plain) {
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
+                v[k] = u.x, v[k + 1] = u.y;
               }
             }
-            if (m == quad) {
+            if (SUM) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (REV ? wg * 16 + j < lane : wg * 16 + j > lane) v[j] = 0.f;
-            }
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<float4*>(out + la_f32(row, (col + j) / 4 + k)) =
+                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 0u;
-          }
-          tmem_st8(tl + LT_QK + c, w);
-        }
-        if (!SUM && tid == 0 && i > 0) sent(i - 1);
-        const float f = plain ? whole : back * pw[REV ? max(L - 1 - row, 0) : row + 1];
-        if (state && !plain) {   // O so far is the state's: a^.. of it stays
-          if (!(live = la_wait(&bar_oi[b], (i >> 1) & 1))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int j = 0; j < 64; j += 16) {
-            float v[16];
-            tmem_ld16(tl + LT_O + col + j, v);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] *= f;
-            tmem_st16(tl + LT_O + col + j, v);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        la_arrive(&bar_p);
-        if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&bar_dz[b], (i >> 1) & 1)))) break;
-        tc_fence_after();
-        // out by way of z, which has been read by both products (SUM: the FP32 part by x and z)
-#pragma unroll 1
-        for (int j = 0; j < 64; j += 32) {
-          float v[32];
-          tmem_ld32(tl + LT_O + col + j, v);
-          if (SUM && row >= L) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0.f;
-          } else if (plain) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
-              v[k] = u.x, v[k + 1] = u.y;
+              for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4*>(out + sw_chunk(row, (col + j) / 8 + k, LA_CH)) =
+                    make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
+                               pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
             }
           }
-          if (SUM) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(out + la_f32(row, (col + j) / 4 + k)) =
-                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(out + sw_chunk(row, (col + j) / 8 + k, LA_CH)) =
-                  make_uint4(pack_bf16(v[8 * k], v[8 * k + 1]), pack_bf16(v[8 * k + 2], v[8 * k + 3]),
-                             pack_bf16(v[8 * k + 4], v[8 * k + 5]), pack_bf16(v[8 * k + 6], v[8 * k + 7]));
-          }
-        }
-        tc_fence_before();
-        la_arrive(&bar_o);
-        fence_async_smem();
+          tc_fence_before();
+          la_arrive(&bar_o);
+          fence_async_smem();
         } while (false);
         if (!(live = la_set_well<1, LA_SET>(live))) break;
         if (SUM) {
@@ -720,8 +728,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
                 *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
           la_set_well<1, LA_SET>(true);
         }
-        if (!SUM && tid == 0 && i + 1 == nch) bulk_wait_all();
       }
+      if (!SUM && tid == 0) bulk_wait_all();
     }
   } else if (warp < 2 * LA_SET / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_Y));
@@ -731,87 +739,87 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LA_REG_STATE));
     // ---- the state (held: so many times it): this thread's row y and its 64 columns z ----
     if (go_s) {
-    const int me = tid - 2 * LA_SET, wg = me >> 7, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
-    const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
-    uint8_t* zs = sm + LA_ZS;
-    uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
-    const float times = nch > 0 ? held : 1.f;   // (an empty document's passes through as it is)
-    float2 S[32];
-    if (from) {
-      const float* src = a.init + ((int64_t)(a.init_segments ? p.segment : p.doc) * a.HV + h) * (D * D);
-      if (a.init_t) {
+      const int me = tid - 2 * LA_SET, wg = me >> 7, quad = warp & 3, row = quad * 32 + lane, col = wg * 64;
+      const uint32_t tl = tb + ((uint32_t)(quad * 32) << 16);
+      uint8_t* zs = sm + LA_ZS;
+      uint8_t* tile = sm + LA_STAGE;   // FP32 [128][128] for the first and the last state
+      const float times = nch > 0 ? held : 1.f;   // (an empty document's passes through as it is)
+      float2 S[32];
+      if (from) {
+        const float* src = a.init + ((int64_t)(a.init_segments ? p.segment : p.doc) * a.HV + h) * (D * D);
+        if (a.init_t) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = make_float2(times * src[(col + 2 * j) * D + row], times * src[(col + 2 * j + 1) * D + row]);
+          for (int j = 0; j < 32; ++j) S[j] = make_float2(times * src[(col + 2 * j) * D + row], times * src[(col + 2 * j + 1) * D + row]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = k * LA_SET + me;
+            *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
+          }
+          la_set_well<2, LA_SET>(true);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 16 + k));
+            S[2 * k] = make_float2(times * v.x, times * v.y);
+            S[2 * k + 1] = make_float2(times * v.z, times * v.w);
+          }
+          fence_async_smem();
+          la_arrive(&bar_init);
+        }
       } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int e = k * LA_SET + me;
-          *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
-        }
-        la_set_well<2, LA_SET>(true);
+        for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
+      }
+      auto put_state = [&] {   // as BF16
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(tile + la_f32(row, wg * 16 + k));
-          S[2 * k] = make_float2(times * v.x, times * v.y);
-          S[2 * k + 1] = make_float2(times * v.z, times * v.w);
-        }
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col >> 3) + (j >> 2), D)) =
+              make_uint4(pack_bf16(S[j].x, S[j].y), pack_bf16(S[j + 1].x, S[j + 1].y), pack_bf16(S[j + 2].x, S[j + 2].y),
+                         pack_bf16(S[j + 3].x, S[j + 3].y));
         fence_async_smem();
-        la_arrive(&bar_init);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) S[j] = make_float2(0.f, 0.f);
-    }
-    auto put_state = [&] {   // as BF16
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<uint4*>(zs + sw_chunk(row, (col >> 3) + (j >> 2), D)) =
-            make_uint4(pack_bf16(S[j].x, S[j].y), pack_bf16(S[j + 1].x, S[j + 1].y), pack_bf16(S[j + 2].x, S[j + 2].y),
-                       pack_bf16(S[j + 3].x, S[j + 3].y));
-      fence_async_smem();
-      la_arrive(&bar_z);
-    };
-    if (OUT && nch > 0) put_state();
+        la_arrive(&bar_z);
+      };
+      if (OUT && nch > 0) put_state();
 #pragma unroll 1
-    for (int i = 0; i < adds && live; ++i) {
-      if (!(live = la_wait(&bar_dz[i & 1], (i >> 1) & 1))) break;
-      tc_fence_after();
-      const float f = pw[tokens(i)];
+      for (int i = 0; i < adds && live; ++i) {
+        if (!(live = la_wait(&bar_dz[i & 1], (i >> 1) & 1))) break;
+        tc_fence_after();
+        const float f = pw[tokens(i)];
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint32_t v[16];
-        tmem_ld16_async(tl + t_dz(i) + col + 2 * j, v);
-        tmem_wait_ld();
+        for (int j = 0; j < 32; j += 8) {
+          uint32_t v[16];
+          tmem_ld16_async(tl + t_dz(i) + col + 2 * j, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          S[j + k] = __ffma2_rn(make_float2(f, f), S[j + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
-      }
-      tc_fence_before();
-      la_arrive(&dz_read[i & 1]);
-      if (OUT && i + 1 < nch) {
-        if (!(live = la_wait(&bar_oi[i & 1], (i >> 1) & 1))) break;   // the state before has been used
-        put_state();
-      }
-    }
-    if (keep) {
-      // by way of the other stage's y and x than the last chunk's, which have been used
-      if (live && nch > 1)
-        live = la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1) && (!OUT || la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1));
-      const float free = columns && nch > 0 ? la_power(g, -64.f) : 1.f;
-      uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) =
-            make_float4(free * S[2 * k].x, free * S[2 * k].y, free * S[2 * k + 1].x, free * S[2 * k + 1].y);
-      if (la_set_well<2, LA_SET>(live)) {
-        float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)p.segment * a.HV + h) * (D * D);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int e = k * LA_SET + me;
-          *reinterpret_cast<float4*>(dst + e * 4) = *reinterpret_cast<const float4*>(way + la_f32(e >> 5, e & 31));
+          for (int k = 0; k < 8; ++k)
+            S[j + k] = __ffma2_rn(make_float2(f, f), S[j + k], make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])));
+        }
+        tc_fence_before();
+        la_arrive(&dz_read[i & 1]);
+        if (OUT && i + 1 < nch) {
+          if (!(live = la_wait(&bar_oi[i & 1], (i >> 1) & 1))) break;   // the state before has been used
+          put_state();
         }
       }
-    }
+      if (keep) {
+        // by way of the other stage's y and x than the last chunk's, which have been used
+        if (live && nch > 1)
+          live = la_wait(&empty_y[nch & 1], ((nch - 2) >> 1) & 1) && (!OUT || la_wait(&empty_x[nch & 1], ((nch - 2) >> 1) & 1));
+        const float free = columns && nch > 0 ? la_power(g, -64.f) : 1.f;
+        uint8_t* way = nch > 0 && ((nch - 1) & 1) ? sm : tile;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          *reinterpret_cast<float4*>(way + la_f32(row, wg * 16 + k)) =
+              make_float4(free * S[2 * k].x, free * S[2 * k].y, free * S[2 * k + 1].x, free * S[2 * k + 1].y);
+        if (la_set_well<2, LA_SET>(live)) {
+          float* dst = OUT ? a.last + ((int64_t)p.doc * a.HV + h) * (D * D) : a.sums + ((int64_t)p.segment * a.HV + h) * (D * D);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int e = k * LA_SET + me;
+            *reinterpret_cast<float4*>(dst + e * 4) = *reinterpret_cast<const float4*>(way + la_f32(e >> 5, e & 31));
+          }
+        }
+      }
     }
   }
   if (!live) atomicCAS(a.err, 0, ST_TIMEOUT);

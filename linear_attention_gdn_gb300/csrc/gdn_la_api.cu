@@ -39,8 +39,9 @@ static int64_t segments_of(const gdn_la_problem* p, const int32_t* cu, int len) 
 // The cut into segments.  A walk of one segment and head is a CTA, one to an SM; its time is its chunks (2.5 us each) and what
 // begins and ends it (5.4 us).  Cutting costs a second pass over two of the four tensors, about 0.8 of the walk, and the carry
 // between.  So documents stay whole unless the longest is the better part of the time, and then the number of pieces is
-// taken for which the rounds of CTAs are estimated to end first (one document of 32,768 tokens and 16 heads: whole 645 us, in 19
-// pieces, two rounds of CTAs, 190, in 9, one round, 160).
+// taken for which the rounds of CTAs are estimated to end first (one document of 32,768 tokens and 16 heads: whole 668 us, in 19
+// pieces, two rounds of CTAs, 179, in 9, one round, 157; of 8,192 and 48 heads: whole 178, in 3 pieces 124, in 8 161; of 2,048:
+// whole 53, in 2 pieces 63).
 static gdn_status la_plan(const gdn_la_problem* p, const int32_t* cu, LaPlan* plan) {
   if (!p || !cu) return GDN_ERR_INVALID_ARG;
   if (p->N < 1 || p->T < 0 || p->H < 1 || p->HV < 1 || p->segment < 0) return GDN_ERR_INVALID_ARG;
@@ -63,7 +64,7 @@ static gdn_status la_plan(const gdn_la_problem* p, const int32_t* cu, LaPlan* pl
       return (work + LA_BEGIN * ctas) / sms + 0.5 * (len + LA_BEGIN);
     };
     double best = time(most, p->N);
-    for (int parts = 2; parts <= most; parts += 1 + parts / 8) {
+    for (int parts = 2; parts <= most; parts += 1 + parts / 16) {
       const int len = (most + parts - 1) / parts;
       const double t = 1.8 * time(len, segments_of(p, cu, len)) + 4;
       if (t < best) {
