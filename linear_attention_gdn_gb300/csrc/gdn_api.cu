@@ -324,7 +324,7 @@ static const char* const kKernelNames[K_NUM] = {
     "kda_out_kernel",     "kda_grad_kernel",    "walk_order_kernel",
     "step_kernel",        "kda_step_kernel",    "conv_step_kernel",   "qk_fwd_kernel",
     "qk_bwd_kernel(+reduce)", "la_walk_kernel", "la_walk_kernel(sums)", "la_carry_kernel",
-    "la_reduce_kernel",   "la_step_kernel",     "norm_fwd_kernel",    "norm_bwd_kernel(+reduce)",
+    "la_round_kernel",    "la_step_kernel",     "norm_fwd_kernel",    "norm_bwd_kernel(+reduce)",
     "step_tables_kernel"};
 struct ProfRec {
   int id;

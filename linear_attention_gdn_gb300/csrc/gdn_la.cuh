@@ -32,7 +32,12 @@ struct LaWalk {
   float* last;            // [N][HV][y][z]: the state that a document leaves, or null
   void* out;              // BF16 rows of 128, or FP32 of walks that sum
   int64_t out_token, out_head;   // elements
-  int cluster;            // walks that sum: the value heads of a cluster, whose outputs come to one output head
+  // Walks that sum: over the `group` value heads of an output head
+  int group;
+  int* counts;            // [chunks][output heads]: count + how many heads have been added
+  int count;
+  int* ticket;            // numbers the CTAs as they begin
+  int64_t clear;          // walks that do not sum: of counts and the tickets behind them, so many are cleared
   int* err;
 };
 
@@ -49,7 +54,7 @@ struct LaCarry {
 cudaError_t launch_la_walk(const LaWalk& a, bool reverse, bool exact, bool sum, cudaStream_t s);
 cudaError_t launch_la_sums(const LaWalk& a, bool reverse, bool exact, cudaStream_t s);
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s);
-// out[t][h] = sum over G parts, in order, of part[t][h G + i]
-cudaError_t launch_la_reduce(const float* part, void* out, int64_t T, int H, int G, int64_t out_token, cudaStream_t s);
+// out[t][h] = part[t][h], rounded
+cudaError_t launch_la_round(const float* part, void* out, int64_t T, int H, int64_t out_token, cudaStream_t s);
 
 }  // namespace gdn

@@ -12,13 +12,6 @@ namespace gdn {
 
 bool make_tmap_strided(CUtensorMap* m, const void* base, int64_t T, int heads, int64_t token, int rows);
 
-// Of G value heads, how many a cluster adds up: 8 at most, and all clusters as many.
-static int la_cluster(int G) {
-  int c = 8;
-  while (G % c) --c;
-  return c;
-}
-
 bool make_tmap_f32(CUtensorMap* m, const void* base, int64_t T, int heads, int rows);
 
 constexpr double LA_BEGIN = 2.2;   // of a walk, in chunks
@@ -84,10 +77,10 @@ static size_t la_states(const gdn_la_problem* p, const LaPlan& plan) {
   return plan.split ? (size_t)plan.total * p->HV * STATE_F32 * sizeof(float) : 0;
 }
 
-// FP32 sums of dq or dk over the value heads of each cluster
-static size_t la_parts(const gdn_la_problem* p) {
-  return p->HV > p->H ? (size_t)p->T * (p->HV / la_cluster(p->HV / p->H)) * 128 * sizeof(float) : 0;
-}
+// FP32 sums of dq or dk over the value heads of a group, and behind them the counts of added heads and two tickets
+static size_t la_parts(const gdn_la_problem* p) { return p->HV > p->H ? (size_t)p->T * p->H * 128 * sizeof(float) : 0; }
+static int64_t la_counts(const gdn_la_problem* p) { return p->HV > p->H ? (p->T / LA_CH + p->N + 1) * p->H : 0; }
+static size_t la_sum_bytes(const gdn_la_problem* p) { return la_parts(p) + (p->HV > p->H ? la_counts(p) + 2 : 0) * sizeof(int); }
 
 static bool la_stride(int64_t* s, int heads) {
   if (*s == 0) *s = (int64_t)heads * 128;
@@ -155,31 +148,38 @@ struct LaCall {
     w.out_token = token;
     w.out_head = 128;
     w.last = last;
-    w.cluster = 1;
     if (p->T > 0) ok = ok && make_tmap_strided(&w.to, out, p->T, p->HV, token, LA_CH);
     if (!ok) return;
     prof_begin(K_LA_WALK, s);
     check(launch_la_walk(w, reverse, last != nullptr, false, s));
     prof_end(K_LA_WALK, s);
   }
-  // to rows of the q/k heads, the sums over their value heads: in FP32 by clusters of them, then rounded (and added up where
-  // there are several clusters)
+  // where walks that sum do so
+  void summing(float* part) {
+    if (p->HV == p->H) return;
+    w.group = p->HV / p->H;
+    w.counts = reinterpret_cast<int*>(part + la_parts(p) / sizeof(float));
+    w.ticket = w.counts + la_counts(p);
+    w.clear = la_counts(p) + 2;
+  }
+  // to rows of the q/k heads, the sums over their value heads: in FP32, then rounded
   void walk_summed(bool reverse, void* out, int64_t token, float* part) {
-    const int G = p->HV / p->H, C = la_cluster(G);
-    if (G == 1) return walk(reverse, out, token, nullptr);
+    if (p->HV == p->H) return walk(reverse, out, token, nullptr);
     w.last = nullptr;
-    w.cluster = C;
     w.out = part;
-    w.out_token = (int64_t)p->HV / C * 128;
+    w.out_token = (int64_t)p->H * 128;
     w.out_head = 128;
-    if (p->T > 0) ok = ok && make_tmap_f32(&w.to, part, p->T, p->HV / C, LA_CH);
+    if (p->T > 0) ok = ok && make_tmap_f32(&w.to, part, p->T, p->H, LA_CH);
     if (!ok) return;
     prof_begin(K_LA_WALK, s);
     check(launch_la_walk(w, reverse, false, true, s));
     prof_end(K_LA_WALK, s);
-    if (!ok || p->T == 0) return;
+    w.count += w.group;   // the next such walk's counts go on, and it has its own ticket
+    w.ticket += 1;
+    w.clear = 0;
+    if (!ok) return;
     prof_begin(K_LA_REDUCE, s);
-    check(launch_la_reduce(part, out, p->T, p->H, G / C, token, s));
+    check(launch_la_round(part, out, p->T, p->H, token, s));
     prof_end(K_LA_REDUCE, s);
   }
 };
@@ -196,7 +196,7 @@ gdn_status gdn_la_workspace_bytes(const gdn_la_problem* p, const int32_t* cu_hos
   if (st != GDN_OK) return st;
   if (!fwd_bytes || !bwd_bytes) return GDN_ERR_INVALID_ARG;
   *fwd_bytes = la_states(p, plan);
-  *bwd_bytes = 2 * la_states(p, plan) + la_parts(p);
+  *bwd_bytes = 2 * la_states(p, plan) + la_sum_bytes(p);
   return GDN_OK;
 }
 
@@ -250,6 +250,7 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
   const size_t values = la_states(p, plan) / sizeof(float);
   float *wstates = states + values, *part = wstates + values;
   LaCall c(p, plan, decay, cu_dev, dev_err, stream);
+  c.summing(part);
   // dv, and the gradients of the states; Z[dk][dv]
   c.tensors(tk, tq, td);
   c.scales(p->scale, 1.f, p->scale);

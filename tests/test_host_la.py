@@ -50,9 +50,10 @@ def test_la_bad_arguments(call, change):
 
 def test_la_workspace():
     one = gdn.la_problem(**LA)
-    # FP32 sums over the value heads of a group, or as many of them as one cluster takes
-    for H, HV, heads in ((1, 2, 1), (2, 2, 0), (1, 8, 1), (2, 32, 4), (1, 11, 11)):
-        assert gdn.gdn_la_workspace_bytes(gdn.la_problem(5, 2, H, HV), CU) == (0, 5 * heads * 512)
+    # FP32 sums over the value heads of a group, the counts of heads that are in them, two tickets
+    for H, HV in ((1, 2), (2, 2), (1, 8), (2, 32), (1, 11)):
+        b = 0 if H == HV else 5 * H * 512 + (0 + 2 + 1) * H * 4 + 8
+        assert gdn.gdn_la_workspace_bytes(gdn.la_problem(5, 2, H, HV), CU) == (0, b)
     cu = [0, 300, 300, 301]
     cut = gdn.la_problem(301, 3, 2, 2, segment=2)                    # segments: 2, 1, 1
     f, b = gdn.gdn_la_workspace_bytes(cut, cu)
