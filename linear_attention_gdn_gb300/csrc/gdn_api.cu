@@ -254,20 +254,6 @@ bool make_tmap_strided(CUtensorMap* m, const void* base, int64_t T, int heads, i
   return r == CUDA_SUCCESS;
 }
 
-// [T][heads][128] FP32, boxes of 32 values and `rows` tokens
-bool make_tmap_f32(CUtensorMap* m, const void* base, int64_t T, int heads, int rows) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)std::max<int64_t>(T, 1)};
-  cuuint64_t strides[2] = {128 * 4, (cuuint64_t)heads * 128 * 4};
-  cuuint32_t box[3] = {32, 1, (cuuint32_t)rows};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 bool make_tmap_g(CUtensorMap* m, const float* base, int64_t T, int heads) {
   auto fn = encode_fn();
   if (!fn) return false;
@@ -324,8 +310,7 @@ static const char* const kKernelNames[K_NUM] = {
     "kda_out_kernel",     "kda_grad_kernel",    "walk_order_kernel",
     "step_kernel",        "kda_step_kernel",    "conv_step_kernel",   "qk_fwd_kernel",
     "qk_bwd_kernel(+reduce)", "la_walk_kernel", "la_walk_kernel(sums)", "la_carry_kernel",
-    "la_round_kernel",    "la_step_kernel",     "norm_fwd_kernel",    "norm_bwd_kernel(+reduce)",
-    "step_tables_kernel"};
+    "la_step_kernel",     "norm_fwd_kernel",    "norm_bwd_kernel(+reduce)", "step_tables_kernel"};
 struct ProfRec {
   int id;
   cudaEvent_t e0, e1;

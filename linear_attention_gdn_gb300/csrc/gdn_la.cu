@@ -148,7 +148,7 @@ __device__ __forceinline__ void la_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// A count in memory that another CTA raises; about a second, too.
+// A count in memory that another CTA raises (2^20 tries: about a second, too).
 __device__ __forceinline__ bool la_wait_count(const int* count, int least) {
 #pragma unroll 1
   for (uint32_t i = 0; i < 1u << 20; ++i) {
@@ -159,12 +159,21 @@ __device__ __forceinline__ bool la_wait_count(const int* count, int least) {
   }
   return false;
 }
-// adds a box of FP32 to memory
-__device__ __forceinline__ void la_tma_add(const CUtensorMap* map, const void* ssrc, int x, int y, int z) {
-  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-               "r"(x), "r"(y), "r"(z), "r"(smem_u32(ssrc))
+// a tile of a sum to memory, added to what is there, and back
+__device__ __forceinline__ void la_bulk_store(float* dst, const void* ssrc, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(ssrc)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void la_bulk_add(float* dst, const void* ssrc, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(ssrc)),
+               "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void la_bulk_load(void* sdst, const float* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(sdst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // barrier over one set that also tells whether all of it is well
 template <int ID, int N> __device__ __forceinline__ bool la_set_well(bool v) {
   asm volatile("" ::: "memory");
@@ -221,6 +230,11 @@ __device__ __forceinline__ uint32_t la_f32(int r, int c16) {
   return (uint32_t)((c16 >> 3) * (LA_CH * 128) + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
 }
 
+// the same where a warp's 32 rows lie side by side, and the first 32 of each 64 columns in the first half
+__device__ __forceinline__ uint32_t la_part(int r, int c16) {
+  return (uint32_t)((((c16 & 8) << 1) + ((c16 & 16) >> 1) + (c16 & 7)) * LA_CH + r) * 16;
+}
+
 template <bool OUT, bool REV, int TERMS, bool SUM>
 __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_constant__ LaWalk a) {
   dependents_may_launch();
@@ -234,7 +248,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   __shared__ uint64_t full_y[2], full_x[2], full_z[2], empty_y[2], empty_x[2], empty_z[2], y_full[SLOTS], y_empty[4];
   // (by the chunk's parity: dZ may be a chunk ahead of those that wait for it, and these do not all wait in every chunk)
   __shared__ uint64_t bar_dz[2], dz_read[2], bar_oi[2];
-  __shared__ uint64_t part_full[2], part_empty[2];   // SUM: this head's part of a chunk is there; has been added
+  // SUM: this head's part is there, may be loaded over; the sum of the heads before it, by halves
+  __shared__ uint64_t part_full[2], part_empty[2], part_in[2][2];
   __shared__ uint64_t bar_qk, bar_p, bar_op, bar_o, bar_z, bar_init;
   __shared__ uint32_t tmem_slot;
   __shared__ LaPlace place_s;
@@ -256,7 +271,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       mbar_init(&bar_oi[i], 1);
       mbar_init(&empty_y[i], OUT ? LA_SET / 32 + 1 : 2 * LA_SET / 32);
       mbar_init(&empty_x[i], 1);
-      mbar_init(&empty_z[i], !OUT ? 1 : SUM ? 2 : 3);
+      mbar_init(&empty_z[i], OUT ? 3 : 1);
+      mbar_init(&part_in[0][i], 1);
+      mbar_init(&part_in[1][i], 1);
       mbar_init(&part_full[i], 1);
       mbar_init(&part_empty[i], 1);
     }
@@ -275,7 +292,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   if (warp == LA_DZ && lane == 0) {
     const CUtensorMap* maps[4] = {&a.tx, &a.ty, &a.tz, &a.to};
 #pragma unroll
-    for (int i = OUT ? 0 : 1; i < (OUT && !SUM ? 4 : 3); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[i]) : "memory");
+    for (int i = OUT ? 0 : 1; i < (OUT ? 4 : 3); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[i]) : "memory");
   }
   previous_kernel_done();
   // SUM: in the order in which CTAs begin, so that what a head waits for has begun before it, whatever runs side by side
@@ -286,6 +303,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     number = h_s;
   }
   const int h = number % a.HV, want = number / a.HV;
+  const int head = SUM ? h / a.group : h, rank = SUM ? h % a.group : 0;
+  const bool ends = !SUM || rank + 1 == a.group;   // (the last head of a group has the sum)
   if (warp == 0) {
     LaPlace p;
     bool sound;
@@ -441,12 +460,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         uint8_t* st = sm + b * LA_STAGE;
         if (i == 1 && staged && !(live = la_wait(&bar_init, 0))) break;
         if (i >= 2 && !(live = la_wait(&empty_y[b], free))) break;
+        if (SUM && i >= 2 && !(live = la_wait(&part_empty[b], free))) break;
         mbar_expect_tx(&full_y[b], LA_TILE);
         la_tile(st + LA_Y, &a.ty, h / a.gy, t, &full_y[b]);
         ++ny;
         if (OUT) {
           if (i >= 2 && !(live = la_wait(&empty_x[b], free))) break;
-          if (SUM && i >= 2 && !(live = la_wait(&part_empty[b], free))) break;
           mbar_expect_tx(&full_x[b], LA_TILE);
           la_tile(st + LA_X, &a.tx, h / a.gx, t, &full_x[b]);
           ++nx;
@@ -504,46 +523,44 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         mma_commit_w(&empty_z[b]);
       }
     }
-    // ---- SUM: the parts go out, each head's added to those before it, by the memory system but in the heads' order ----
-    if (SUM && warp == LA_SUM && go_s) {
-      const int head = h / a.group, rank = h % a.group;
+    // ---- SUM: the parts go out from where y and x were, each head's added to those before it, by the memory system but in the
+    // heads' order; the last head has the sum before it come in there ----
+    if (SUM && warp == LA_SUM && lane == 0 && go_s) {
+      // the chunk's number (no two documents' chunks have the same), whose tile, and how many heads are in it
+      auto place = [&](int i) { return ((int64_t)p.t0 / LA_CH + p.doc + (first(i) - p.t0) / LA_CH) * (a.HV / a.group) + head; };
+      int in = 0;   // halves asked for
 #pragma unroll 1
       for (int i = 0; i < nch && live; ++i) {
-        const int b = i & 1, L = tokens(i), t = first(i);
-        const uint8_t* tile = sm + b * LA_STAGE + LA_X;
-        // the chunk's number (no two documents' chunks have the same), and how many heads have been added there
-        int* count = a.counts + ((int64_t)p.t0 / LA_CH + p.doc + (t - p.t0) / LA_CH) * (a.HV / a.group) + head;
-        if (!(live = la_wait(&part_full[b], (i >> 1) & 1))) break;
-        if (rank > 0) {
-          if (!(live = la_wait_count(count, a.count + rank))) break;
-          asm volatile("fence.proxy.async.global;" ::: "memory");
-        }
-        if (rank == 0 && L < LA_CH) {   // the rows behind are another document's; to them the other heads add zeros
-          float* o = static_cast<float*>(a.out) + (int64_t)t * a.out_token + head * a.out_head;
+        const int b = i & 1;
+        const uint32_t par = (i >> 1) & 1;
+        uint8_t* tile = sm + b * LA_STAGE + LA_Y;
+        float* to = a.sums + place(i) * (LA_CH * D);
+        int* count = a.counts + place(i);
+        if (ends) {
+          if (!(live = la_wait_count(count, a.count + rank) && (i >= adds || la_wait(&empty_y[b], par)))) break;
 #pragma unroll 1
-          for (int k = lane; k < L * 32; k += 32)
-            *reinterpret_cast<float4*>(o + (k >> 5) * a.out_token + (k & 31) * 4) =
-                *reinterpret_cast<const float4*>(tile + la_f32(k >> 5, k & 31));
-        } else if (lane == 0) {
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            if (rank == 0) tma_store_3d(&a.to, tile + k * (LA_TILE / 2), k * 32, head, t);
-            else la_tma_add(&a.to, tile + k * (LA_TILE / 2), k * 32, head, t);
+          for (int k = 0; k < 2; ++k) {
+            if ((k || i >= adds) && !(live = la_wait(&empty_x[b], par))) break;
+            asm volatile("fence.proxy.async;" ::: "memory");
+            mbar_expect_tx(&part_in[k][b], LA_TILE);
+            la_bulk_load(tile + k * LA_TILE, to + k * (LA_CH * D / 2), LA_TILE, &part_in[k][b]);
+            ++in;
           }
-          bulk_commit();
-          bulk_wait_read();
+          continue;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&part_empty[b]);
-        if (rank + 1 < a.group) {
-          if (lane == 0) bulk_wait_all();
-          asm volatile("fence.proxy.async.global;" ::: "memory");
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(count), "r"(a.count + rank + 1) : "memory");
-        }
+        if (!(live = la_wait(&part_full[b], par) && (rank == 0 || la_wait_count(count, a.count + rank)))) break;
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        if (rank == 0) la_bulk_store(to, tile, 2 * LA_TILE);
+        else la_bulk_add(to, tile, 2 * LA_TILE);
+        bulk_commit();
+        bulk_wait_read();
+        mbar_arrive(&part_empty[b]);
+        bulk_wait_all();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(count), "r"(a.count + rank + 1) : "memory");
       }
-      if (lane == 0) bulk_wait_all();
+#pragma unroll 1
+      for (int i = max(0, in - 4); i < in; ++i) mbar_drain(&part_in[i & 1][(i >> 1) & 1], (i >> 2) & 1);
     }
     // ---- and dZ here ----
     if (warp == LA_DZ && go_s) {
@@ -592,7 +609,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         const int b = i & 1, L = tokens(i), t = first(i);
         const bool state = i > 0 || from;
         uint8_t* z = sm + b * LA_STAGE + LA_Z;
-        uint8_t* out = sm + b * LA_STAGE + (SUM ? LA_X : LA_Z);
+        uint8_t* out = sm + b * LA_STAGE + LA_Z;
+        uint8_t* part = sm + b * LA_STAGE + LA_Y;   // SUM
         do {   // (a wait that runs out ends the walk for the whole set, below)
           if (L < LA_CH) {
             if (!(live = la_wait(&full_z[b], (i >> 1) & 1))) break;
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
             }
             tmem_st8(tl + LT_QK + c, w);
           }
-          if (!SUM && tid == 0 && i > 0) sent(i - 1);
+          if (tid == 0 && i > 0) sent(i - 1);
           const float f = plain ? whole : back * pw[REV ? max(L - 1 - row, 0) : row + 1];
           if (state && !plain) {   // O so far is the state's: a^.. of it stays
             if (!(live = la_wait(&bar_oi[b], (i >> 1) & 1))) break;
@@ -666,26 +684,30 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           la_arrive(&bar_p);
           if (!(live = la_wait(&bar_op, i & 1) && (i >= adds || la_wait(&bar_dz[b], (i >> 1) & 1)))) break;
           tc_fence_after();
-          // out by way of z, which has been read by both products (SUM: the FP32 part by x and z)
+          // out by way of z, which has been read by both products (a part of a sum by y and x)
 #pragma unroll 1
           for (int j = 0; j < 64; j += 32) {
             float v[32];
+            if (SUM && ends && !(live = la_wait(&part_in[j >> 5][b], (i >> 1) & 1))) break;
             tmem_ld32(tl + LT_O + col + j, v);
-            if (SUM && row >= L) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = 0.f;
-            } else if (plain) {
+            if (plain) {
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
                 const float2 u = mul2(make_float2(v[k], v[k + 1]), make_float2(f, f));
                 v[k] = u.x, v[k + 1] = u.y;
               }
             }
-            if (SUM) {
+            float4* at = reinterpret_cast<float4*>(part + la_part(row, (col + j) / 4));
+            if (SUM && ends) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4*>(out + la_f32(row, (col + j) / 4 + k)) =
-                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 8; ++k) {
+                const float4 n = at[k * LA_CH];
+                v[4 * k] += n.x, v[4 * k + 1] += n.y, v[4 * k + 2] += n.z, v[4 * k + 3] += n.w;
+              }
+            }
+            if (!ends) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) at[k * LA_CH] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             } else {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
@@ -699,24 +721,23 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           fence_async_smem();
         } while (false);
         if (!(live = la_set_well<1, LA_SET>(live))) break;
-        if (SUM) {
-          if (tid == 0) mbar_arrive(&part_full[b]);
-        } else if (L == LA_CH) {
+        if (SUM && tid == 0) mbar_arrive(ends ? &part_empty[b] : &part_full[b]);
+        if (!ends) continue;
+        if (L == LA_CH) {
           if (tid == 0) {
-            tma_store_3d(&a.to, out, 0, h, t);
-            tma_store_3d(&a.to, out + LA_TILE / 2, 64, h, t);
+            tma_store_3d(&a.to, out, 0, head, t);
+            tma_store_3d(&a.to, out + LA_TILE / 2, 64, head, t);
             bulk_commit();
           }
         } else {   // the rows behind are another document's
 #pragma unroll 1
           for (int k = tid; k < L * 16; k += LA_SET)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)(t + (k >> 4)) * a.out_token +
-                                      h * a.out_head + (k & 15) * 8) =
-                *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)(t + (k >> 4)) * a.out_token + head * D +
+                                      (k & 15) * 8) = *reinterpret_cast<const uint4*>(out + sw_chunk(k >> 4, k & 15, LA_CH));
           la_set_well<1, LA_SET>(true);
         }
       }
-      if (!SUM && tid == 0) bulk_wait_all();
+      if (tid == 0) bulk_wait_all();
     }
   } else if (warp < 2 * LA_SET / 32) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LA_REG_Y));
@@ -881,19 +902,6 @@ __global__ void __launch_bounds__(LC_THREADS) la_carry_kernel(const LaCarry a) {
   }
 }
 
-// The sums over the value heads as BF16 (65,536 tokens and 16 heads: 805 MB in 123 us).
-__global__ void __launch_bounds__(256) la_round_kernel(const float* part, __nv_bfloat16* out, int64_t items, int H,
-                                                       int64_t out_token) {
-  chain_kernel();
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < items; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t th = i >> 4;   // token, head
-    const float4* p = reinterpret_cast<const float4*>(part) + i * 2;
-    const float4 u = p[0], v = p[1];
-    *reinterpret_cast<uint4*>(out + th / H * out_token + th % H * D + (i & 15) * 8) =
-        make_uint4(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w), pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  }
-}
-
 template <bool OUT, bool REV, int TERMS, bool SUM> static cudaError_t launch_walk(const LaWalk& a, cudaStream_t s) {
   const auto kernel = la_walk_kernel<OUT, REV, TERMS, SUM>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LA_SMEM);
@@ -917,13 +925,6 @@ cudaError_t launch_la_sums(const LaWalk& a, bool reverse, bool exact, cudaStream
 
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s) {
   return launch_chained(la_carry_kernel, dim3((unsigned)(a.seg.N * a.HV * LC_PARTS)), dim3(LC_THREADS), 0, s, a);
-}
-
-cudaError_t launch_la_round(const float* part, void* out, int64_t T, int H, int64_t out_token, cudaStream_t s) {
-  const int64_t items = T * H * 16;
-  const int64_t blocks = (items + 255) / 256;
-  return launch_chained(la_round_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, part,
-                        static_cast<__nv_bfloat16*>(out), items, H, out_token);
 }
 
 }  // namespace gdn

@@ -28,10 +28,11 @@ struct LaWalk {
   const float* init;      // states to start from, FP32 [.][HV][128][128], or null: zero
   int init_segments;      // one a segment (else one a document)
   int init_t;             // stored [z][y] (else [y][z])
-  float* sums;            // [segments][HV][y][z]: what each segment adds, for the carry (walks without output)
+  float* sums;            // [segments][HV][y][z]: what each segment adds, for the carry (walks without output);
+                          // [chunks][output heads][32][128 rows][4]: heads' sums (walks that sum)
   float* last;            // [N][HV][y][z]: the state that a document leaves, or null
-  void* out;              // BF16 rows of 128, or FP32 of walks that sum
-  int64_t out_token, out_head;   // elements
+  void* out;              // BF16 rows of 128, heads side by side
+  int64_t out_token;      // elements
   // Walks that sum: over the `group` value heads of an output head
   int group;
   int* counts;            // [chunks][output heads]: count + how many heads have been added
@@ -54,7 +55,4 @@ struct LaCarry {
 cudaError_t launch_la_walk(const LaWalk& a, bool reverse, bool exact, bool sum, cudaStream_t s);
 cudaError_t launch_la_sums(const LaWalk& a, bool reverse, bool exact, cudaStream_t s);
 cudaError_t launch_la_carry(const LaCarry& a, cudaStream_t s);
-// out[t][h] = part[t][h], rounded
-cudaError_t launch_la_round(const float* part, void* out, int64_t T, int H, int64_t out_token, cudaStream_t s);
-
 }  // namespace gdn

@@ -12,8 +12,6 @@ namespace gdn {
 
 bool make_tmap_strided(CUtensorMap* m, const void* base, int64_t T, int heads, int64_t token, int rows);
 
-bool make_tmap_f32(CUtensorMap* m, const void* base, int64_t T, int heads, int rows);
-
 constexpr double LA_BEGIN = 2.2;   // of a walk, in chunks
 
 struct LaPlan {
@@ -77,9 +75,10 @@ static size_t la_states(const gdn_la_problem* p, const LaPlan& plan) {
   return plan.split ? (size_t)plan.total * p->HV * STATE_F32 * sizeof(float) : 0;
 }
 
-// FP32 sums of dq or dk over the value heads of a group, and behind them the counts of added heads and two tickets
-static size_t la_parts(const gdn_la_problem* p) { return p->HV > p->H ? (size_t)p->T * p->H * 128 * sizeof(float) : 0; }
+// Sums of dq or dk over the value heads of a group: a FP32 tile for each chunk and q/k head (a document's chunks begin at
+// t0 / 128 + its number, so that none share one), behind them the counts of heads that are in each and two tickets.
 static int64_t la_counts(const gdn_la_problem* p) { return p->HV > p->H ? (p->T / LA_CH + p->N + 1) * p->H : 0; }
+static size_t la_parts(const gdn_la_problem* p) { return (size_t)la_counts(p) * LA_CH * 128 * sizeof(float); }
 static size_t la_sum_bytes(const gdn_la_problem* p) { return la_parts(p) + (p->HV > p->H ? la_counts(p) + 2 : 0) * sizeof(int); }
 
 static bool la_stride(int64_t* s, int heads) {
@@ -146,7 +145,6 @@ struct LaCall {
   void walk(bool reverse, void* out, int64_t token, float* last) {
     w.out = out;
     w.out_token = token;
-    w.out_head = 128;
     w.last = last;
     if (p->T > 0) ok = ok && make_tmap_strided(&w.to, out, p->T, p->HV, token, LA_CH);
     if (!ok) return;
@@ -162,14 +160,14 @@ struct LaCall {
     w.ticket = w.counts + la_counts(p);
     w.clear = la_counts(p) + 2;
   }
-  // to rows of the q/k heads, the sums over their value heads: in FP32, then rounded
+  // to rows of the q/k heads, the sums over their value heads
   void walk_summed(bool reverse, void* out, int64_t token, float* part) {
     if (p->HV == p->H) return walk(reverse, out, token, nullptr);
     w.last = nullptr;
-    w.out = part;
-    w.out_token = (int64_t)p->H * 128;
-    w.out_head = 128;
-    if (p->T > 0) ok = ok && make_tmap_f32(&w.to, part, p->T, p->H, LA_CH);
+    w.sums = part;
+    w.out = out;
+    w.out_token = token;
+    if (p->T > 0) ok = ok && make_tmap_strided(&w.to, out, p->T, p->H, token, LA_CH);
     if (!ok) return;
     prof_begin(K_LA_WALK, s);
     check(launch_la_walk(w, reverse, false, true, s));
@@ -177,10 +175,6 @@ struct LaCall {
     w.count += w.group;   // the next such walk's counts go on, and it has its own ticket
     w.ticket += 1;
     w.clear = 0;
-    if (!ok) return;
-    prof_begin(K_LA_REDUCE, s);
-    check(launch_la_round(part, out, p->T, p->H, token, s));
-    prof_end(K_LA_REDUCE, s);
   }
 };
 

@@ -10,7 +10,7 @@ enum KernelId {
   K_TABLES_SCAN = 0, K_TABLES_FILL, K_PREP, K_FWD_WALK, K_FWD_MERGE, K_FWD_SCAN,
   K_CHECK_SAVED, K_BWD_WALK, K_BWD_MERGE, K_BWD_SCAN, K_GRAD, K_PASS, K_CONV_FWD, K_CONV_BWD, K_VNEW,
   K_KDA_PREP, K_KDA_OUT, K_KDA_GRAD, K_WALK_ORDER, K_STEP, K_KDA_STEP, K_CONV_STEP,
-  K_QK_FWD, K_QK_BWD, K_LA_WALK, K_LA_SUMS, K_LA_CARRY, K_LA_REDUCE, K_LA_STEP, K_NORM_FWD, K_NORM_BWD,
+  K_QK_FWD, K_QK_BWD, K_LA_WALK, K_LA_SUMS, K_LA_CARRY, K_LA_STEP, K_NORM_FWD, K_NORM_BWD,
   K_STEP_TABLES, K_NUM
 };
 void prof_begin(int id, cudaStream_t s);
