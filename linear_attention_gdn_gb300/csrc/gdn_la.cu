@@ -26,6 +26,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "gdn_common.cuh"
 #include "gdn_la.cuh"
 #include "gdn_launch.cuh"
@@ -45,6 +47,7 @@ constexpr int LA_SMEM = LA_ZS + LA_TILE + 1024;
 // TMEM columns: QK, each 16 of them then P in their first 8; O; dZ; the ring of decayed y
 constexpr int LT_QK = 0, LT_O = 128, LT_DZ = 256, LT_Y = 384;
 constexpr int LA_Q = 32;                     // tokens of a quarter: 16 columns a term
+constexpr int LA_SHORT = 64;                 // tokens of a chunk whose P has two terms, in as many products as a whole one's
 constexpr float LA_COLUMNS = -0.7f;   // (64 times it: 2^-65, which leaves P z as much of FP32's range)
 constexpr float LA_LEAST = -1e4f;   // log decays below it: nothing is left of it either, and no product is NaN
 
@@ -513,11 +516,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         }
         mma_commit_w(&bar_oi[b]);
         mma_commit_w(&empty_x[b]);
+        // (P's second terms meet the same rows of z as the first)
+        const uint32_t upper = z + (tokens(i) <= LA_SHORT ? 0 : LA_SHORT * 128);
         if (!(live = la_wait(&bar_p, i & 1) && la_wait(&full_z[b], par))) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ts_w(tb + LT_O, tb + LT_QK + ks * 16, desc_mn(z, LA_CH, ks), idesc(128, 128, 0, 1),
+          mma_ts_w(tb + LT_O, tb + LT_QK + ks * 16, desc_mn(ks < 4 ? z : upper, LA_CH, ks & 3), idesc(128, 128, 0, 1),
                    ks > 0 || i > 0 || from);
         mma_commit_w(&bar_op);
         mma_commit_w(&empty_z[b]);
@@ -623,48 +628,63 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           if (!(live = la_wait(&bar_qk, i & 1))) break;
           tc_fence_after();
           // Blocks of 32 columns are seen, not seen, or on the diagonal, as a warp's rows lie; 16 columns at a time, the two
-          // warpgroups in turn.  P goes where the same 16 columns of QK were.
+          // warpgroups in turn.  P goes where the same 16 columns of QK were.  Up to 64 tokens: with what its rounding left
+          // behind, in the other columns.
           const bool plain = columns && !(REV && L < LA_CH);
+          auto pairs = [&](auto few) {
+            constexpr bool SHORT = decltype(few)::value;
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            const int c = m * 32 + wg * 16;
-            uint32_t w[8];
-            if (REV ? m >= quad : m <= quad) {
+            for (int m = 0; m < (SHORT ? 2 : 4); ++m) {
+              const int c = m * 32 + wg * 16;
+              uint32_t w[8];
               float v[16];
-              tmem_ld16(tl + LT_QK + c, v);
-              if (plain) {
-                const float4* near = reinterpret_cast<const float4*>(wcol + (c & 63));
-                const float2 h = m < 2 ? make_float2(1.f, 1.f) : make_float2(half, half);
+              if (REV ? m >= quad : m <= quad) {
+                tmem_ld16(tl + LT_QK + c, v);
+                if (plain) {
+                  const float4* near = reinterpret_cast<const float4*>(wcol + (c & 63));
+                  const float2 h = m < 2 ? make_float2(1.f, 1.f) : make_float2(half, half);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  const float4 n = near[j >> 2];
-                  const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), h));
-                  const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), h));
-                  v[j] = u.x, v[j + 1] = u.y, v[j + 2] = x.x, v[j + 3] = x.y;
+                  for (int j = 0; j < 16; j += 4) {
+                    const float4 n = near[j >> 2];
+                    const float2 u = mul2(make_float2(v[j], v[j + 1]), mul2(make_float2(n.x, n.y), h));
+                    const float2 x = mul2(make_float2(v[j + 2], v[j + 3]), mul2(make_float2(n.z, n.w), h));
+                    v[j] = u.x, v[j + 1] = u.y, v[j + 2] = x.x, v[j + 3] = x.y;
+                  }
+                } else {
+                  const int far = REV ? c - row : row - c;   // tokens between this row and the first column, or seen from it
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[j] *= a.p_scale * pw[max(REV ? far + j : far - j, 0)];
+                  if (REV && L < LA_CH) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                      if (c + j >= L) v[j] = 0.f;
+                  }
                 }
-              } else {
-                const int far = REV ? c - row : row - c;   // tokens between this row and the first column, or seen from it
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] *= a.p_scale * pw[max(REV ? far + j : far - j, 0)];
-                if (REV && L < LA_CH) {
+                if (m == quad) {
 #pragma unroll
                   for (int j = 0; j < 16; ++j)
-                    if (c + j >= L) v[j] = 0.f;
+                    if (REV ? wg * 16 + j < lane : wg * 16 + j > lane) v[j] = 0.f;
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 0u;
+                if (SHORT)
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[j] = 0.f;
               }
-              if (m == quad) {
+              tmem_st8(tl + LT_QK + c, w);
+              if (SHORT) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  if (REV ? wg * 16 + j < lane : wg * 16 + j > lane) v[j] = 0.f;
+                for (int j = 0; j < 8; ++j)
+                  w[j] = pack_bf16(v[2 * j] - __uint_as_float(w[j] << 16), v[2 * j + 1] - __uint_as_float(w[j] & 0xffff0000u));
+                tmem_st8(tl + LT_QK + LA_SHORT + c, w);
               }
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) w[j] = 0u;
             }
-            tmem_st8(tl + LT_QK + c, w);
-          }
+          };
+          if (L <= LA_SHORT) pairs(std::true_type());
+          else pairs(std::false_type());
           if (tid == 0 && i > 0) sent(i - 1);
           const float f = plain ? whole : back * pw[REV ? max(L - 1 - row, 0) : row + 1];
           if (state && !plain) {   // O so far is the state's: a^.. of it stays

@@ -376,8 +376,11 @@ struct NormShape {
   int vpt, threads, warp, ctas;
 };
 
-// Rows in pieces of 8 values: few enough for a warp (up to 4 a lane), else a CTA, 1 a thread where there are no more rows than
-// SMs and only latency counts, 2 as far as its threads go, else 4 (20,000 rows of 12,288, forward: 2 pieces 368 us, 4 526).
+// Rows in pieces of 8 values.  Up to 64 pieces a warp takes a row.  From there to 128 a CTA does, whose rows come in whole (60,000
+// BF16 rows of 1,024: 77 us, by warps 94; 100 of them 2.2 and 2.8), unless its last round is far from full (3,000 rows: 6.0 us,
+// by warps 4.2) or the rows are FP32, forward (60,000: 176 us, by warps 150).  Longer ones: forward 1 piece a thread where there
+// are no more rows than SMs and only latency counts (64 of 4,096: 2.5 us, 2 pieces 2.8), 2 as far as its threads go, else 4
+// (20,000 rows of 12,288: 2 pieces 368 us, 4 526).
 static NormShape norm_shape(const gdn_norm_problem* p, bool fast, bool back) {
   NormShape s = {fast, 0, 0, 0, 0};
   const int64_t sms = sm_count();
@@ -388,7 +391,13 @@ static NormShape norm_shape(const gdn_norm_problem* p, bool fast, bool back) {
     s.ctas = (int)(p->T < sms * 4 ? p->T : sms * 4);
     return s;
   }
-  if (pieces <= 128) {
+  auto round_of = [&](int vpt, int threads) {   // CTAs, by the kernels' registers (FP32 rows of 4,096 in 1 1/3: 395 us for 309)
+    const int resident = back || vpt == 4 ? 512 : p->dtype == GDN_FP32 && vpt == 2 ? 768 : 1024;
+    return sms * (resident / threads > 0 ? resident / threads : 1);
+  };
+  const int64_t small = round_of(2, 64);
+  const bool even = p->T <= small || (p->T + small - 1) / small * small * 20 <= p->T * 23;
+  if (pieces <= 64 || (pieces <= 128 && (!even || (!back && p->dtype == GDN_FP32 && p->T > sms)))) {
     s.warp = 1;
     s.vpt = pieces <= 32 ? 1 : pieces <= 64 ? 2 : 4;
     s.threads = 128;
@@ -397,11 +406,9 @@ static NormShape norm_shape(const gdn_norm_problem* p, bool fast, bool back) {
     return s;
   }
   const int two = !back && p->dtype != GDN_FP32 ? 2048 : 1024;   // pieces
-  s.vpt = p->T <= sms && pieces <= 1024 ? 1 : pieces <= two ? 2 : 4;
+  s.vpt = !back && p->T <= sms && pieces <= 1024 ? 1 : pieces <= two ? 2 : 4;
   s.threads = ((pieces + s.vpt - 1) / s.vpt + 31) / 32 * 32;
-  // one round of CTAs, by the kernels' registers (FP32 rows of 4,096 in 1 1/3: 395 us for 309)
-  const int resident = back || s.vpt == 4 ? 512 : p->dtype == GDN_FP32 && s.vpt == 2 ? 768 : 1024;
-  const int64_t most = sms * (resident / s.threads > 0 ? resident / s.threads : 1);
+  const int64_t most = round_of(s.vpt, s.threads);
   s.ctas = (int)(p->T < most ? p->T : most);
   return s;
 }
