@@ -230,3 +230,44 @@ def test_gradients_are_differences():
     left, right = (f64(moved["o"]) * dO).sum(), (f64(r["dv"]) * step).sum()
     off = ((expect(y, 1, 2)["o"][1] * dO) ** 2).sum() + ((expect(x, 1, 2)["dv"][1] * step) ** 2).sum()
     assert abs(left - right) <= 6 * np.sqrt(off)
+
+
+@pytest.mark.parametrize("lengths,H,HV", [([1], 1, 1), ([3, 0, 1], 1, 1), ([1, 1, 2, 5], 2, 6), ([17, 64], 1, 2), ([33, 128 + 7], 1, 1)])
+def test_short_chunks_are_rounded_once(lengths, H, HV):
+    """Chunks of up to 64 tokens give the pairs' factors in two BF16 terms, so without a state before them only the result
+    is rounded.  With x the result before its rounding and w the exact one, |bf(x) - x| <= |bf(w) - x|, so
+    |bf(x) - w| <= |bf(w) - w| + 2 |x - w|; |x - w| <= 2^-16 of the sums of absolute values A: the terms' 2^-17, and 2^-17 for
+    the FP32 sums and products (under 64 operations, each 2^-23 or 2^-24)."""
+    x = make(lengths, H, HV, states=False, seed=5)
+    d = on_gpu(x)
+    r = run(x, d, states=False)
+    want, G, outside = expect(x, H, HV), HV // H, 0
+    bf = lambda t: torch.from_numpy(t).to(torch.bfloat16).double().numpy()  # noqa: E731
+    for m in ("o", "dq", "dk", "dv"):
+        got, w = f64(r[m].cpu()), want[m][0]
+        once = np.zeros(w.shape)   # with the factors rounded
+        for i, n in enumerate(lengths):
+            a, b = int(x["cu"][i]), int(x["cu"][i + 1])
+            if not 0 < n <= 64:
+                continue
+            A = np.zeros((n,) + w.shape[1:])
+            for h in range(HV):
+                Q, K, V, DO = (f64(x[c])[a:b, h // G if c in "qk" else h] for c in ("q", "k", "v", "dO"))
+                g = float(x["decay"][h])
+                t = np.arange(n)
+                decay = np.where(t[:, None] >= t, SCALE * np.exp(g * np.maximum(t[:, None] - t, 0)), 0.0)
+                if m == "o":
+                    X, Y, Z, D = Q, K, V, decay
+                elif m == "dv":
+                    X, Y, Z, D = K, Q, DO, decay.T
+                elif m == "dq":
+                    X, Y, Z, D = DO, V, K, decay
+                else:
+                    X, Y, Z, D = V, DO, Q, decay.T
+                j = h if m in ("o", "dv") else h // G
+                A[:, j] += (D * (np.abs(X) @ np.abs(Y).T)) @ np.abs(Z)
+                once[a:b, j] += bf(D * (X @ Y.T)) @ Z
+            near = np.abs(bf(w[a:b]) - w[a:b]) + 2.0 ** -15 * A
+            assert (np.abs(got[a:b] - w[a:b]) <= near).all()
+            outside += int((np.abs(bf(once[a:b]) - w[a:b]) > near).sum())
+    assert outside   # factors of one term would not do
