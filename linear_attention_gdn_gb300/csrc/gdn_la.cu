@@ -17,12 +17,15 @@
 // Documents whose chains are too few or too long are cut into segments: la_walk without output first sums what each adds,
 // la_carry_kernel turns the sums into the states they start from.
 //
-// What bounds it: a chunk is 12.6 MFLOP of products (6 of 128^3, dZ's twice or three times) and 128 KB to and from memory, and
-// takes a CTA 2.45 us at 1.9 GHz (3 documents of 8,192 tokens, 48 heads of their own: 6.5 TB/s, 96% of a plain copy's rate;
-// 32,768 tokens: 6.8 TB/s).  By the counters the tensor cores work 47% of the time, the warps issue 54%, and the path from shared
-// memory and TMEM is near its limit.  Where heads share q and k, memory has less to do and the chunk's time stays (12 prompts
-// of 30,054 tokens in all, 48 heads on 16: 266 us, 59% of the copy rate).  Shorter chunks need more passes of the state
-// through shared memory per token, longer ones do not fit the tiles.
+// Heads of a group share q and k: dq and dk are sums over them.  Each head is a CTA; the first stores its part of a chunk, the
+// next add theirs by the memory system, the last loads the sum before it and writes the result, each when the one before has
+// (3 documents of 8,192 tokens, 48 heads on 16: a walk with sums 252 us, without 167).
+//
+// What bounds it: a chunk is 12.6 MFLOP of products (6 of 128^3; dZ two or three times) and 128 KB to and from memory, and
+// takes a CTA 2.5 to 2.9 us (3 documents of 8,192 tokens, 48 heads of their own: 185 us, 6.5 TB/s, 96% of a plain copy's rate;
+// of 32,768 tokens 699 us, 6.9 TB/s).  By the counters the tensor cores work half of the time and the warps issue 56%: it is the
+// chain from QK to the output of one chunk, of which the next chunk's can overlap all but P.  Where heads share q and k, memory
+// has less to do and the chunk's time stays (12 prompts of 30,054 tokens in all, 48 heads on 16: 266 us, 59% of the copy rate).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -858,7 +861,8 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   if (warp == LA_MMA) tmem_dealloc(tb, 512);
 }
 
-// Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.
+// Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.  Bound by the latency of its loads,
+// 16 segments ahead (9 of 16 heads: 10 us alone, most of it the launch).
 constexpr int LC_THREADS = 256, LC_PARTS = D * D / (4 * LC_THREADS), LC_AHEAD = 16;
 
 __global__ void __launch_bounds__(LC_THREADS) la_carry_kernel(const LaCarry a) {
