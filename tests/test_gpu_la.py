@@ -271,3 +271,69 @@ def test_short_chunks_are_rounded_once(lengths, H, HV):
             assert (np.abs(got[a:b] - w[a:b]) <= near).all()
             outside += int((np.abs(bf(once[a:b]) - w[a:b]) > near).sum())
     assert outside   # factors of one term would not do
+
+
+@pytest.mark.parametrize("N,H,HV,most", [(40, 1, 8, 140), (21, 1, 16, 300), (3, 2, 128, 150)])
+def test_groups_of_more_heads_than_run_side_by_side(N, H, HV, most):
+    """320 to 384 CTAs whose heads add up in order, on fewer SMs, by falling length or, past 32 documents, in their order."""
+    lengths = np.random.RandomState(N).randint(0, most, N).tolist()
+    x = make(lengths, H, HV, states=False, seed=N)
+    d = on_gpu(x)
+    first = run(x, d, states=False)
+    check(x, first)
+    again = run(x, d, states=False)
+    for m in ("dq", "dk", "dv"):
+        assert torch.equal(first[m], again[m])
+
+
+def test_two_backward_passes_at_once():
+    """On two streams, each with its workspace, and then both captured in graphs with one workspace that run in turn."""
+    xs = [make([200, 90, 0, 300], 1, 6, seed=s) for s in (31, 32)]
+    ds = [on_gpu(x) for x in xs]
+    want = [run(x, d) for x, d in zip(xs, ds)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    probs = [problem(x, d) for x, d in zip(xs, ds)]
+    b = gdn.gdn_la_workspace_bytes(probs[0], xs[0]["cu"])[1]
+    ws = [torch.empty(b, dtype=torch.uint8, device="cuda") for _ in xs]
+    got = [{m: torch.empty_like(w[m]) for m in ("dq", "dk", "dv", "ds_in")} for w in want]
+
+    def call(i, w, stream=None):
+        d, g = ds[i], got[i]
+        gdn.gdn_la_bwd(probs[i], d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], xs[i]["cu"], d["s_in"], d["dO"], d["ds_out"],
+                       g["dq"], g["dk"], g["dv"], g["ds_in"], d["err"], w, b, stream=stream)
+
+    def same():
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for m in g:
+                assert torch.equal(g[m], w[m])
+                g[m].fill_(float("nan"))
+        assert all(gdn.gdn_device_status(d["err"]) == 0 for d in ds)
+
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in (0, 1):
+            call(i, ws[i], streams[i])
+    same()
+    graphs = [torch.cuda.CUDAGraph() for _ in xs]
+    for i in (0, 1):
+        with torch.cuda.graph(graphs[i]):
+            call(i, ws[0])
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    same()
+
+
+def test_a_wrong_device_copy_is_reported_by_the_backward():
+    x = make([100, 60], 1, 3)
+    d = on_gpu(x)
+    prob = problem(x, d)
+    ws = torch.empty(gdn.gdn_la_workspace_bytes(prob, x["cu"])[1], dtype=torch.uint8, device="cuda")
+    for wrong in ([0, 100, 159], [0, 161, 160], [1, 100, 160], [0, -5, 160], [0, 100, 2 ** 30]):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = [torch.empty_like(d[m]) for m in "qkv"]
+        gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], torch.tensor(wrong, dtype=torch.int32, device="cuda"), x["cu"],
+                       None, d["dO"], None, *out, None, err, ws)
+        assert gdn.gdn_device_status(err) == 1
+    check(x, run(x, d))   # and nothing is left behind
