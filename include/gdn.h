@@ -465,7 +465,7 @@ gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
  * Results are the same bits from run to run; dq and dk are sums over the value heads of a group in order.
  * Outputs do not overlap inputs, but for the states as said.  T below 2^30 (else GDN_ERR_UNSUPPORTED).
  * gdn_la_workspace_bytes: what the forward and the backward need (16-byte aligned; 0: nothing).
- *     The backward of groups (HV > H) takes 64 KiB to each begun chunk of 128 tokens of a document and q/k head; documents
+ *     The backward of groups (HV > H) takes 128 KiB to each begun chunk of 128 tokens of a document and q/k head; documents
  *     that are cut, 64 KiB (the backward 128) to a segment and value head.
  */
 typedef struct {

@@ -60,6 +60,9 @@ __device__ __forceinline__ float la_power(float g, float n) {
   return fmaf(e, fmaf(g, n, -p), e);
 }
 
+// from L2 in kernels that may follow another without waiting
+template <bool L2, typename T> __device__ __forceinline__ T la_load(const T* p) { return L2 ? __ldcg(p) : *p; }
+
 struct LaPlace {
   int doc, index, count;   // segment `index` of the document's `count`
   int segment;             // its number among all
@@ -69,7 +72,7 @@ struct LaPlace {
 // The segment of place `want` by one warp; false if there is none, or if the documents up to it are not in order.  If `check`,
 // the whole list is walked, and *sound tells whether it is in order and as long as the host counted it.  Up to 32 documents
 // give their segments by falling length, so that no long one begins when the others end (12 prompts of up to 4,096 tokens).
-__device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool check, LaPlace* out, bool* sound) {
+template <bool L2> __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool check, LaPlace* out, bool* sound) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   bool found = false, good = true, there = false;
@@ -78,8 +81,8 @@ __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool chec
     int d = d0 + lane;
     int n = 0, a = 0, b = 0;
     if (d < s.N) {
-      a = s.cu[d];
-      b = s.cu[d + 1];
+      a = la_load<L2>(s.cu + d);
+      b = la_load<L2>(s.cu + d + 1);
       if (a < 0 || b < a || b > s.T || (d == 0 && a != 0) || (d == s.N - 1 && b != s.T)) good = false, b = a = 0;
       n = max(1, ((b - a + LA_CH - 1) / LA_CH + s.len - 1) / s.len);
     }
@@ -243,7 +246,8 @@ __device__ __forceinline__ uint32_t la_part(int r, int c16) {
 
 template <bool OUT, bool REV, int TERMS, bool SUM>
 __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_constant__ LaWalk a) {
-  dependents_may_launch();
+  constexpr bool LEADS = OUT && REV && !SUM, FOLLOWS = OUT && TERMS == 2;   // (which may)
+  if (!LEADS || !a.leads) dependents_may_launch();
   constexpr int SLOTS = OUT ? 128 / (16 * TERMS) : 4;   // of the ring
   // without output there is room for the ring of a whole chunk and for a second dZ, made while the first is read
   constexpr int T_Y = OUT ? LT_Y : 256;
@@ -300,7 +304,13 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
 #pragma unroll
     for (int i = OUT ? 0 : 1; i < (OUT ? 4 : 3); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[i]) : "memory");
   }
-  previous_kernel_done();
+  if (!FOLLOWS || !a.follows) previous_kernel_done();   // (else the kernels before it, but one, have ended; what is read comes from L2)
+  if (LEADS && a.clear) {   // for the walks behind
+    for (int64_t i = (int64_t)blockIdx.x * LA_THREADS + tid; i < a.clear; i += (int64_t)gridDim.x * LA_THREADS) a.counts[i] = 0;
+    __threadfence();
+    __syncthreads();
+  }
+  if (LEADS && a.leads) dependents_may_launch();
   // SUM: in the order in which CTAs begin, so that what a head waits for has begun before it, whatever runs side by side
   int number = blockIdx.x;
   if (SUM) {
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
   if (warp == 0) {
     LaPlace p;
     bool sound;
-    const bool found = la_find(a.seg, want, number == 0, &p, &sound);   // (all heads find the same)
+    const bool found = la_find<FOLLOWS>(a.seg, want, number == 0, &p, &sound);   // (all heads find the same)
     if (!sound && lane == 0) atomicCAS(a.err, 0, GDN_ERR_INVALID_ARG);
     // without output: the segment that is last in the walk adds to none
     const bool go = found && (OUT || (REV ? p.index > 0 : p.index + 1 < p.count));
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     }
   }
   const float g = [&] {
-    const float x = a.decay[h];
+    const float x = la_load<FOLLOWS>(a.decay + h);
     return x < LA_LEAST ? LA_LEAST : x;
   }();
   // Where a^-64 is no more than 2^65, a^(r-c) is a^(63-c) in P and a^(r-63) on O at the end, and the state's part comes by
@@ -545,7 +555,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         float* to = a.sums + place(i) * (LA_CH * D);
         int* count = a.counts + place(i);
         if (ends) {
-          if (!(live = la_wait_count(count, a.count + rank) && (i >= adds || la_wait(&empty_y[b], par)))) break;
+          if (!(live = la_wait_count(count, rank) && (i >= adds || la_wait(&empty_y[b], par)))) break;
 #pragma unroll 1
           for (int k = 0; k < 2; ++k) {
             if ((k || i >= adds) && !(live = la_wait(&empty_x[b], par))) break;
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
           }
           continue;
         }
-        if (!(live = la_wait(&part_full[b], par) && (rank == 0 || la_wait_count(count, a.count + rank)))) break;
+        if (!(live = la_wait(&part_full[b], par) && (rank == 0 || la_wait_count(count, rank)))) break;
         asm volatile("fence.proxy.async.global;" ::: "memory");
         if (rank == 0) la_bulk_store(to, tile, 2 * LA_TILE);
         else la_bulk_add(to, tile, 2 * LA_TILE);
@@ -565,7 +575,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         mbar_arrive(&part_empty[b]);
         bulk_wait_all();
         asm volatile("fence.proxy.async.global;" ::: "memory");
-        asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(count), "r"(a.count + rank + 1) : "memory");
+        asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(count), "r"(rank + 1) : "memory");
       }
 #pragma unroll 1
       for (int i = max(0, in - 4); i < in; ++i) mbar_drain(&part_in[i & 1][(i >> 1) & 1], (i >> 2) & 1);
@@ -780,12 +790,12 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         const float* src = a.init + ((int64_t)(a.init_segments ? p.segment : p.doc) * a.HV + h) * (D * D);
         if (a.init_t) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) S[j] = make_float2(times * src[(col + 2 * j) * D + row], times * src[(col + 2 * j + 1) * D + row]);
+          for (int j = 0; j < 32; ++j) S[j] = make_float2(times * la_load<FOLLOWS>(src + (col + 2 * j) * D + row), times * la_load<FOLLOWS>(src + (col + 2 * j + 1) * D + row));
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int e = k * LA_SET + me;
-            *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = *reinterpret_cast<const float4*>(src + e * 4);
+            *reinterpret_cast<float4*>(tile + la_f32(e >> 5, e & 31)) = la_load<FOLLOWS>(reinterpret_cast<const float4*>(src + e * 4));
           }
           la_set_well<2, LA_SET>(true);
 #pragma unroll
@@ -853,12 +863,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
       }
     }
   }
-  if (!SUM && a.clear)   // for the walks behind
-    for (int64_t i = (int64_t)blockIdx.x * LA_THREADS + tid; i < a.clear; i += (int64_t)gridDim.x * LA_THREADS) a.counts[i] = 0;
   if (!live) atomicCAS(a.err, 0, ST_TIMEOUT);
   tc_fence_before();
   __syncthreads();
   if (warp == LA_MMA) tmem_dealloc(tb, 512);
+  if (FOLLOWS && a.follows && blockIdx.x == gridDim.x - 1) previous_kernel_done();   // (the kernel does not end before it)
 }
 
 // Z of each segment of a document from the sums, in the walk's order; a thread takes 4 values.  Bound by the latency of its loads,

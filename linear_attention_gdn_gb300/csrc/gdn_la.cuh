@@ -35,10 +35,12 @@ struct LaWalk {
   int64_t out_token;      // elements
   // Walks that sum: over the `group` value heads of an output head
   int group;
-  int* counts;            // [chunks][output heads]: count + how many heads have been added
-  int count;
+  int* counts;            // [chunks][output heads]: heads that have been added
   int* ticket;            // numbers the CTAs as they begin
-  int64_t clear;          // walks that do not sum: of counts and the tickets behind them, so many are cleared
+  int64_t clear;          // walks that lead: of counts on, so many are cleared
+  // Walks that need nothing of one another fill the SMs that the one before leaves: `leads`: the next kernel may begin when
+  // all CTAs of this one run, and all before it has ended; `follows`: begins then, and does not end before it.
+  int leads, follows;
   int* err;
 };
 

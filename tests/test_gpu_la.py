@@ -174,6 +174,23 @@ def test_same_bits_again_and_in_place(segment):
     assert torch.equal(grads, first["ds_in"])
 
 
+@pytest.mark.parametrize("HV", [1, 3])
+@pytest.mark.parametrize("segment", [0, 1])
+def test_state_gradients_in_place_leave_the_others(segment, HV):
+    """ds_in over ds_out: dk, which needs ds_out too, has what it has with buffers of their own."""
+    x = make([200, 0, 140], 1, HV, seed=3)
+    d = on_gpu(x)
+    want = run(x, d, segment)
+    prob = problem(x, d, segment)
+    ws = torch.empty(max(16, gdn.gdn_la_workspace_bytes(prob, x["cu"])[1]), dtype=torch.uint8, device="cuda")
+    grads, got = d["ds_out"].clone(), {m: torch.full_like(want[m], float("nan")) for m in ("dq", "dk", "dv")}
+    gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], d["dO"], grads, got["dq"],
+                   got["dk"], got["dv"], grads, d["err"], ws)
+    assert gdn.gdn_device_status(d["err"]) == 0 and torch.equal(grads, want["ds_in"])
+    for m in got:
+        assert torch.equal(got[m], want[m]), m
+
+
 def test_no_tokens():
     x = make([0, 0], 1, 2)
     d = on_gpu(x)

@@ -50,9 +50,9 @@ def test_la_bad_arguments(call, change):
 
 def test_la_workspace():
     one = gdn.la_problem(**LA)
-    # FP32 sums over the value heads of a group, a tile to a chunk, the counts of heads that are in them, two tickets
+    # FP32 sums of dq and dk over the value heads of a group: a tile to a chunk, the counts of heads that are in them, a ticket
     for H, HV in ((1, 2), (2, 2), (1, 8), (2, 32), (1, 11)):
-        b = 0 if H == HV else (0 + 2 + 1) * H * (65536 + 4) + 8
+        b = 0 if H == HV else 2 * ((0 + 2 + 1) * H * (65536 + 4) + 4)
         assert gdn.gdn_la_workspace_bytes(gdn.la_problem(5, 2, H, HV), CU) == (0, b)
     cu = [0, 300, 300, 301]
     cut = gdn.la_problem(301, 3, 2, 2, segment=2)                    # segments: 2, 1, 1
