@@ -7,10 +7,13 @@
 //
 // Bound by the bytes: each row is read once and stays in registers (8 values a thread at a time, VPT such pieces) while its
 // sums go round.  Short rows belong to a warp, longer ones to a CTA.  65,536 rows of 4,096 BF16 values, both outputs: 375 us, 95%
-// of a plain copy's rate; backward 365 us, 87%.
+// of a plain copy's rate; backward 333 us, 95%.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "gdn.h"
+#include "gdn_common.cuh"
 #include "gdn_elem.cuh"
 #include "gdn_internal.h"
 #include "gdn_launch.cuh"
@@ -161,15 +164,11 @@ __global__ void __launch_bounds__(WARP ? 128 : VPT * sizeof(E) <= 4 ? 1024 : 512
   }
 }
 
-template <typename E, int VPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : VPT == 1 ? 1024 : 512) norm_bwd_kernel(const NormArgs a) {
+// Rows of a warp, backward: the next is asked for a row ahead, as far as there are registers for it.
+template <typename E, int VPT> __global__ void __launch_bounds__(128) norm_bwd_kernel(const NormArgs a) {
   chain_kernel();
-  __shared__ float words[2][32];
-  const int pieces = a.C >> 3, step = WARP ? 32 : blockDim.x, me = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t rows = WARP ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
-  const int64_t first = WARP ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  // The next row is asked for a row ahead, as far as there are registers for it (4 pieces of 16 bits, a row ahead: 863 us for
-  // 65,536 rows of 4,096, 2 pieces 372).
+  const int pieces = a.C >> 3, step = 32, me = threadIdx.x & 31;
+  const int64_t rows = (int64_t)gridDim.x * (blockDim.x >> 5), first = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   constexpr bool AHEAD = VPT * sizeof(E) <= 4;
   Raw8<E> nh[VPT], ng[VPT], na[VPT];
   float dw[VPT][8];
@@ -210,20 +209,8 @@ __global__ void __launch_bounds__(WARP ? 128 : VPT == 1 ? 1024 : 512) norm_bwd_k
       }
     }
     if (AHEAD) request(t + rows);
-    float mean;
-    if (WARP) {
-      ss = over_warp<false>(ss);
-      mean = over_warp<false>(sg);
-    } else {   // both sums in one go
-      ss = over_warp<false>(ss);
-      sg = over_warp<false>(sg);
-      const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-      __syncthreads();
-      if (lane == 0) words[0][threadIdx.x >> 5] = ss, words[1][threadIdx.x >> 5] = sg;
-      __syncthreads();
-      ss = over_warp<false>(lane < warps ? words[0][lane] : 0.f);
-      mean = over_warp<false>(lane < warps ? words[1][lane] : 0.f);
-    }
+    ss = over_warp<false>(ss);
+    float mean = over_warp<false>(sg);
     const float rho = norm_inverse(ss, a.C, a.eps);
     mean = mean * rho / (float)a.C;   // of g and the normed h
 #pragma unroll
@@ -252,33 +239,142 @@ __global__ void __launch_bounds__(WARP ? 128 : VPT == 1 ? 1024 : 512) norm_bwd_k
     }
   }
   if (!a.partial) return;
-  // this CTA's part of dw; its warps' (rows of a warp each) one after the other
-  if (WARP) {
-    extern __shared__ float sums[];   // [warps][C]
+  // this CTA's part of dw: its warps' one after the other
+  extern __shared__ float sums[];   // [warps][C]
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int p = me + i * 32;
-      if (p < pieces)
+  for (int i = 0; i < VPT; ++i) {
+    const int p = me + i * 32;
+    if (p < pieces)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[(threadIdx.x >> 5) * a.C + p * 8 + j] = dw[i][j];
+      for (int j = 0; j < 8; ++j) sums[(threadIdx.x >> 5) * a.C + p * 8 + j] = dw[i][j];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
+    float v = 0.f;
+    for (int n = 0; n < (int)(blockDim.x >> 5); ++n) v += sums[n * a.C + c];
+    a.partial[(int64_t)blockIdx.x * a.C + c] = v;
+  }
+}
+
+// Rows of a CTA, backward.  The rows ahead are copied to shared memory, so many that an SM's CTAs have some 200 KB on the way,
+// and not to registers, so that three CTAs of 256 threads fit (65,536 rows of 4,096 BF16 values 333 us, 95% of a plain copy's
+// rate; two 363; with one row ahead in registers 365).  A thread's copies are its own to read: no barrier but for the sums.  Its
+// 8 VPT values are words of 16 bytes a whole CTA's width apart: the copies pass the L1, and would fetch sectors twice (30,517
+// FP32 rows: 300 us; words in pairs 485; without rows ahead 416).
+template <typename E, int VPT> struct NormAhead {
+  static constexpr int U = 16 / (int)sizeof(E), N = 8 * VPT / U;   // values of a word, words of a thread's row
+  static constexpr int ROWS = N == 2 ? 3 : 8 / N;
+  static constexpr int BYTES = ROWS * 3 * N * 16;   // a thread
+};
+template <typename E> struct NormWord : Raw8<E> {};
+template <> struct NormWord<float> {
+  float4 u;
+  __device__ __forceinline__ void get(float (&v)[4]) const { v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w; }
+  __device__ __forceinline__ void put(const float (&v)[4]) { u = make_float4(v[0], v[1], v[2], v[3]); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+};
+
+template <typename E, int VPT> __global__ void __launch_bounds__(512) norm_bwd_rows_kernel(const NormArgs a) {
+  chain_kernel();
+  using Ahead = NormAhead<E, VPT>;
+  constexpr int U = Ahead::U, N = Ahead::N;
+  constexpr bool KEEP = VPT <= 2;   // the weights stay in registers
+  extern __shared__ uint4 ahead[];
+  __shared__ float words[2][32];
+  const int all = a.C / U, step = blockDim.x, me = threadIdx.x, lane = me & 31, warps = blockDim.x >> 5;
+  const int64_t rows = gridDim.x;
+  auto slot = [&](int stage, int stream, int i) { return ahead + ((stage * 3 + stream) * N + i) * step + me; };
+  auto request = [&](int stage, int64_t row) {
+    if (row < a.T) {
+      const E* from[3] = {static_cast<const E*>(a.x) + row * a.xs, static_cast<const E*>(a.dy) + row * a.hs,
+                          a.r ? static_cast<const E*>(a.r) + row * a.rs : nullptr};
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (me + i * step < all && from[k])
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot(stage, k, i))),
+                         "l"(from[k] + (me + i * step) * U)
+                         : "memory");
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
-      float s = 0.f;
-      for (int k = 0; k < (int)(blockDim.x >> 5); ++k) s += sums[k * a.C + c];
-      a.partial[(int64_t)blockIdx.x * a.C + c] = s;
-    }
-  } else {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch = [&](int stage, int stream, int i, float (&v)[U]) {
+    NormWord<E> x;
+    *reinterpret_cast<uint4*>(&x) = *slot(stage, stream, i);
+    x.get(v);
+  };
+  float dw[N][U], kept[KEEP ? N : 1][U];
+  auto weights = [&](int i, float (&w)[U]) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int p = me + i * step;
-      if (p < pieces) {
-        float4* d = reinterpret_cast<float4*>(a.partial + (int64_t)blockIdx.x * a.C + p * 8);
-        d[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-        d[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    for (int j = 0; j < U; j += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(a.w + (me + i * step) * U + j);
+      w[j] = x.x, w[j + 1] = x.y, w[j + 2] = x.z, w[j + 3] = x.w;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) dw[i][j] = 0.f;
+    if (KEEP && me + i * step < all) weights(i, kept[KEEP ? i : 0]);
+  }
+  int64_t t = blockIdx.x;
+#pragma unroll
+  for (int k = 0; k < Ahead::ROWS; ++k) request(k, t + k * rows);
+  for (int stage = 0; t < a.T; t += rows, stage = stage + 1 == Ahead::ROWS ? 0 : stage + 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(Ahead::ROWS - 1) : "memory");
+    float ss = 0.f, sg = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (me + i * step < all) {
+        float h[U], g[U], w[U];
+        fetch(stage, 0, i, h);
+        fetch(stage, 1, i, g);
+        if (!KEEP) weights(i, w);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          ss = fmaf(h[j], h[j], ss);
+          sg = fmaf(g[j] * (KEEP ? kept[KEEP ? i : 0][j] : w[j]), h[j], sg);
+        }
       }
     }
+    ss = over_warp<false>(ss);
+    sg = over_warp<false>(sg);
+    __syncthreads();
+    if (lane == 0) words[0][me >> 5] = ss, words[1][me >> 5] = sg;
+    __syncthreads();
+    ss = over_warp<false>(lane < warps ? words[0][lane] : 0.f);
+    sg = over_warp<false>(lane < warps ? words[1][lane] : 0.f);
+    const float rho = norm_inverse(ss, a.C, a.eps), mean = sg * rho / (float)a.C;   // of g and the normed h
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (me + i * step < all) {
+        float h[U], g[U], along[U], w[U];
+        fetch(stage, 0, i, h);
+        fetch(stage, 1, i, g);
+        if (a.r) fetch(stage, 2, i, along);
+        if (!KEEP) weights(i, w);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const float xhat = h[j] * rho;
+          dw[i][j] = fmaf(g[j], xhat, dw[i][j]);
+          h[j] = rho * fmaf(-xhat, mean, g[j] * (KEEP ? kept[KEEP ? i : 0][j] : w[j])) + (a.r ? along[j] : 0.f);
+        }
+        NormWord<E> out;
+        out.put(h);
+        out.store(static_cast<E*>(a.y) + t * a.ys + (me + i * step) * U);
+      }
+    }
+    request(stage, t + Ahead::ROWS * rows);
   }
+  if (!a.partial) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i)   // this CTA's part of dw
+    if (me + i * step < all)
+#pragma unroll
+      for (int j = 0; j < U; j += 4)
+        *reinterpret_cast<float4*>(a.partial + (int64_t)blockIdx.x * a.C + (me + i * step) * U + j) =
+            make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
 }
 
 // Rows of any length, stride and alignment: a CTA a row, a value at a time, the row read again for each use.
@@ -392,8 +488,11 @@ static NormShape norm_shape(const gdn_norm_problem* p, bool fast, bool back) {
     s.ctas = (int)(p->T < sms * 4 ? p->T : sms * 4);
     return s;
   }
-  auto round_of = [&](int vpt, int threads) {   // CTAs, by the kernels' registers (FP32 rows of 4,096 in 1 1/3: 395 us for 309)
-    const int resident = back || vpt == 4 ? 512 : p->dtype == GDN_FP32 && vpt == 2 ? 768 : 1024;
+  // One round of CTAs, by the kernels' registers (FP32 rows of 4,096 in 1 1/3: 395 us for 309) and shared memory; backward 16-bit
+  // rows 768 threads an SM (30,000 rows of 1,536 70 us, with 512 84), the shortest 512 (60,000 of 1,024 92 us, with 768 110).
+  auto round_of = [&](int vpt, int threads) {
+    const bool fp32 = p->dtype == GDN_FP32;
+    const int resident = vpt == 4 || (back && (fp32 || threads < 96)) ? 512 : back || (fp32 && vpt == 2) ? 768 : 1024;
     return sms * (resident / threads > 0 ? resident / threads : 1);
   };
   const int64_t small = round_of(2, 64);
@@ -435,18 +534,32 @@ static bool on_elements(const void* p, int es) { return p && (uintptr_t)p % es =
 
 template <typename E, bool BACK> static cudaError_t norm_run(const NormArgs& a, const NormShape& s, cudaStream_t st) {
   const dim3 grid(s.ctas), block(s.threads);
-  const size_t smem = BACK && s.warp && a.partial ? (size_t)(s.threads / 32) * a.C * sizeof(float) : 0;
-#define GDN_NORM(V, W) return launch_chained(BACK ? norm_bwd_kernel<E, V, W> : norm_fwd_kernel<E, V, W>, grid, block, smem, st, a)
   if (!s.fast) return launch_chained(BACK ? norm_bwd_general_kernel<E> : norm_fwd_general_kernel<E>, grid, block, 0, st, a);
-  if (s.warp) {
-    if (s.vpt == 1) GDN_NORM(1, true);
-    if (s.vpt == 2) GDN_NORM(2, true);
-    GDN_NORM(4, true);
-  }
-  if (s.vpt == 1) GDN_NORM(1, false);
-  if (s.vpt == 2) GDN_NORM(2, false);
-  GDN_NORM(4, false);
+  if constexpr (BACK) {
+    const size_t smem = s.warp && a.partial ? (size_t)(s.threads / 32) * a.C * sizeof(float) : 0;
+    auto by_rows = [&](auto pieces) {
+      constexpr int V = decltype(pieces)::value;
+      const size_t bytes = (size_t)NormAhead<E, V>::BYTES * s.threads;
+      const cudaError_t e =
+          cudaFuncSetAttribute(norm_bwd_rows_kernel<E, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, NormAhead<E, V>::BYTES * 512);
+      return e != cudaSuccess ? e : launch_chained(norm_bwd_rows_kernel<E, V>, grid, block, bytes, st, a);
+    };
+    if (!s.warp) return s.vpt == 2 ? by_rows(std::integral_constant<int, 2>()) : by_rows(std::integral_constant<int, 4>());
+    if (s.vpt == 1) return launch_chained(norm_bwd_kernel<E, 1>, grid, block, smem, st, a);
+    if (s.vpt == 2) return launch_chained(norm_bwd_kernel<E, 2>, grid, block, smem, st, a);
+    return launch_chained(norm_bwd_kernel<E, 4>, grid, block, smem, st, a);
+  } else {
+#define GDN_NORM(V, W) return launch_chained(norm_fwd_kernel<E, V, W>, grid, block, 0, st, a)
+    if (s.warp) {
+      if (s.vpt == 1) GDN_NORM(1, true);
+      if (s.vpt == 2) GDN_NORM(2, true);
+      GDN_NORM(4, true);
+    }
+    if (s.vpt == 1) GDN_NORM(1, false);
+    if (s.vpt == 2) GDN_NORM(2, false);
+    GDN_NORM(4, false);
 #undef GDN_NORM
+  }
 }
 
 template <bool BACK> static cudaError_t norm_by_type(int dtype, const NormArgs& a, const NormShape& s, cudaStream_t st) {

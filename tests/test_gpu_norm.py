@@ -150,6 +150,13 @@ def test_backward(T, C, dtype):
     backward(T, C, dtype, seed=C)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("T,C,kw", [(2600, 1096, {}), (1900, 2048, dict(same="dy")), (1300, 4104, dict(same="dres")), (700, 8192, dict(along=False)),
+                                    (650, 12296, dict(pad=8)), (500, 16384, {})])
+def test_backward_of_more_rows_than_ctas(T, C, kw, dtype):
+    backward(T, C, dtype, seed=T, **kw)
+
+
 @pytest.mark.parametrize("T,C", [(4, 64), (3, 2048), (2, 77)])
 @pytest.mark.parametrize("kw", [dict(pad=8), dict(pad=3), dict(shift=8), dict(shift=1), dict(along=False), dict(want_dw=False), dict(same="dy"),
                                 dict(same="dres")])
