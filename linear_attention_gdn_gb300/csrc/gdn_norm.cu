@@ -260,7 +260,7 @@ template <typename E, int VPT> __global__ void __launch_bounds__(128) norm_bwd_k
 // and not to registers, so that three CTAs of 256 threads fit (65,536 rows of 4,096 BF16 values 333 us, 95% of a plain copy's
 // rate; two 363; with one row ahead in registers 365).  A thread's copies are its own to read: no barrier but for the sums.  Its
 // 8 VPT values are words of 16 bytes a whole CTA's width apart: the copies pass the L1, and would fetch sectors twice (30,517
-// FP32 rows: 300 us; words in pairs 485; without rows ahead 416).
+// FP32 rows: 304 us; words in pairs 485; without rows ahead 406).
 template <typename E, int VPT> struct NormAhead {
   static constexpr int U = 16 / (int)sizeof(E), N = 8 * VPT / U;   // values of a word, words of a thread's row
   static constexpr int ROWS = N == 2 ? 3 : 8 / N;
