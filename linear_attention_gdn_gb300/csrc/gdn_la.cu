@@ -790,7 +790,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
         const float* src = a.init + ((int64_t)(a.init_segments ? p.segment : p.doc) * a.HV + h) * (D * D);
         if (a.init_t) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) S[j] = make_float2(times * la_load<FOLLOWS>(src + (col + 2 * j) * D + row), times * la_load<FOLLOWS>(src + (col + 2 * j + 1) * D + row));
+          for (int j = 0; j < 32; ++j)
+            S[j] = make_float2(times * la_load<FOLLOWS>(src + (col + 2 * j) * D + row),
+                               times * la_load<FOLLOWS>(src + (col + 2 * j + 1) * D + row));
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
