@@ -354,3 +354,40 @@ def test_a_wrong_device_copy_is_reported_by_the_backward():
                        None, d["dO"], None, *out, None, err, ws)
         assert gdn.gdn_device_status(err) == 1
     check(x, run(x, d))   # and nothing is left behind
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_all_gradients_are_there_when_the_call_has_ended(in_place):
+    """The walks run side by side, but what comes behind them, on this stream or one that waits for it, sees all three; also
+    from a graph, which writes the states' gradients in place if so wished."""
+    x = make([900, 3, 140, 2], 1, 5, seed=41)
+    d = on_gpu(x)
+    want = run(x, d)
+    prob = problem(x, d)
+    ws = torch.empty(gdn.gdn_la_workspace_bytes(prob, x["cu"])[1], dtype=torch.uint8, device="cuda")
+    out = {m: torch.empty_like(want[m]) for m in ("dq", "dk", "dv", "ds_in")}
+    incoming = out["ds_in"] if in_place else d["ds_out"]
+    side = torch.cuda.Stream()
+
+    def call():
+        gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], d["dO"], incoming, out["dq"],
+                       out["dk"], out["dv"], out["ds_in"], d["err"], ws)
+
+    graph = torch.cuda.CUDAGraph()
+    out["ds_in"].copy_(d["ds_out"])
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call()
+    for go in (call, graph.replay) * 4:
+        for m in ("dq", "dk", "dv", "ds_in"):
+            out[m].fill_(float("nan"))
+        out["ds_in"].copy_(d["ds_out"])
+        go()
+        here = {m: t.clone() for m, t in out.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            there = {m: t.clone() for m, t in out.items()}
+        torch.cuda.current_stream().wait_stream(side)
+        for m in out:
+            assert torch.equal(here[m], want[m]) and torch.equal(there[m], want[m]), m
+    assert gdn.gdn_device_status(d["err"]) == 0
