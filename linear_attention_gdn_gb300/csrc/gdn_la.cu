@@ -69,9 +69,11 @@ struct LaPlace {
   int t0, t1;              // the document's tokens
 };
 
-// The segment of place `want` by one warp; false if there is none, or if the documents up to it are not in order.  If `check`,
-// the whole list is walked, and *sound tells whether it is in order and as long as the host counted it.  Up to 32 documents
-// give their segments by falling length, so that no long one begins when the others end (12 prompts of up to 4,096 tokens).
+// The segment of place `want` by one warp; false if there is none, if the documents up to it are not in order, or if its
+// document's segments do not all have numbers below the host's count (which is all that there is memory for; a place below it
+// alone says nothing of its segment's number where places go by length).  If `check`, the whole list is walked, and *sound
+// tells whether it is in order and as long as the host counted it.  Up to 32 documents give their segments by falling length,
+// so that no long one begins when the others end (12 prompts of up to 4,096 tokens).
 template <bool L2> __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool check, LaPlace* out, bool* sound) {
   const int lane = threadIdx.x & 31;
   int before = 0;
@@ -125,7 +127,7 @@ template <bool L2> __device__ __forceinline__ bool la_find(const LaSegments& s, 
       out->t0 = __shfl_sync(~0u, a, l);
       out->t1 = __shfl_sync(~0u, b, l);
       there = true;
-      found = good;
+      found = good && out->segment - out->index + out->count <= s.total;
       if (!check) break;
     }
     before += __shfl_sync(~0u, sums(n), 31);
@@ -326,8 +328,9 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     bool sound;
     const bool found = la_find<FOLLOWS>(a.seg, want, number == 0, &p, &sound);   // (all heads find the same)
     if (!sound && lane == 0) atomicCAS(a.err, 0, GDN_ERR_INVALID_ARG);
-    // without output: the segment that is last in the walk adds to none
-    const bool go = found && (OUT || (REV ? p.index > 0 : p.index + 1 < p.count));
+    // without output: the segment that is last in the walk adds to none; without states of segments: a document has one, or
+    // it is not the host's
+    const bool go = found && (OUT ? a.init_segments || p.count == 1 : REV ? p.index > 0 : p.index + 1 < p.count);
     if (lane == 0) {
       place_s = p;
       go_s = go;

@@ -26,7 +26,7 @@ struct LaWalk {
   int HV, gx, gy, gz;     // value heads to a head of x, y, z
   float p_scale, row_scale, state_scale;
   const float* init;      // states to start from, FP32 [.][HV][128][128], or null: zero
-  int init_segments;      // one a segment (else one a document)
+  int init_segments;      // one a segment (else one a document, which then has one segment)
   int init_t;             // stored [z][y] (else [y][z])
   float* sums;            // [segments][HV][y][z]: what each segment adds, for the carry (walks without output);
                           // [chunks][output heads][32][128 rows][4]: heads' sums (walks that sum)
