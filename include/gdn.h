@@ -454,8 +454,9 @@ gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
  *              It may be s_in.
  *   ds_out, ds_in   the gradients of s_out (NULL: zero) and s_in (NULL: not wanted; may be ds_out).
  *   dev_err    a device int, zero at first (gdn_device_status(dev_err) reads it, the call never clears it):
- *              GDN_ERR_INVALID_ARG where the device copy of cu_seqlens has other bounds than the host's, whose documents are
- *              then left out, GDN_ERR_TIMEOUT for a bounded wait that ran out.
+ *              GDN_ERR_INVALID_ARG where the device copy of cu_seqlens is not the host's (documents then go by the device's
+ *              bounds or are left out, and nothing but the outputs and the workspace is written), GDN_ERR_TIMEOUT for a
+ *              bounded wait that ran out.
  * The forward needs nothing saved for the backward but its inputs: the backward walks the documents again.  Sums and
  * states are FP32; the state keeps FP32's exactness, and is rounded to BF16 once, where it meets the rows.
  * Heads with decays down to -0.7 are held up to 2^65 times larger or smaller on the way: in them, products (q . k) v and states

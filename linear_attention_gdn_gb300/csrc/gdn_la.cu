@@ -72,12 +72,13 @@ struct LaPlace {
 // The segment of place `want` by one warp; false if there is none, if the documents up to it are not in order, or if its
 // document's segments do not all have numbers below the host's count (which is all that there is memory for; a place below it
 // alone says nothing of its segment's number where places go by length).  If `check`, the whole list is walked, and *sound
-// tells whether it is in order and as long as the host counted it.  Up to 32 documents give their segments by falling length,
+// tells whether it is in order and the host's.  Up to 32 documents give their segments by falling length,
 // so that no long one begins when the others end (12 prompts of up to 4,096 tokens).
 template <bool L2> __device__ __forceinline__ bool la_find(const LaSegments& s, int want, bool check, LaPlace* out, bool* sound) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   bool found = false, good = true, there = false;
+  uint64_t bounds = 0;   // of this lane's documents
 #pragma unroll 1
   for (int d0 = 0; d0 < s.N; d0 += 32) {
     int d = d0 + lane;
@@ -85,6 +86,7 @@ template <bool L2> __device__ __forceinline__ bool la_find(const LaSegments& s, 
     if (d < s.N) {
       a = la_load<L2>(s.cu + d);
       b = la_load<L2>(s.cu + d + 1);
+      if (check) bounds += la_bound(d, b);
       if (a < 0 || b < a || b > s.T || (d == 0 && a != 0) || (d == s.N - 1 && b != s.T)) good = false, b = a = 0;
       n = max(1, ((b - a + LA_CH - 1) / LA_CH + s.len - 1) / s.len);
     }
@@ -132,7 +134,12 @@ template <bool L2> __device__ __forceinline__ bool la_find(const LaSegments& s, 
     }
     before += __shfl_sync(~0u, sums(n), 31);
   }
-  *sound = good && (!check || before == s.total);
+  if (check) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) bounds += __shfl_xor_sync(~0u, bounds, o);
+    good = good && bounds == s.bounds;
+  }
+  *sound = good;
   return found;
 }
 

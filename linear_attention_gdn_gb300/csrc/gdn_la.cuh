@@ -10,11 +10,21 @@ namespace gdn {
 
 constexpr int LA_CH = 128;   // tokens of a chunk
 
+// A bound's part of a sum that tells two tables apart: the bits of (number, bound) mixed by shifts and odd factors
+// (splitmix64), so that two tables that differ have the same sum once in 2^64.
+__host__ __device__ __forceinline__ uint64_t la_bound(int d, int bound) {
+  uint64_t x = ((uint64_t)(uint32_t)d << 32 | (uint32_t)bound) + 0x9e3779b97f4a7c15ull;
+  x = (x ^ x >> 30) * 0xbf58476d1ce4e5b9ull;
+  x = (x ^ x >> 27) * 0x94d049bb133111ebull;
+  return x ^ x >> 31;
+}
+
 // How the segments of all documents are numbered: document d has max(1, ceil(chunks / len)) of them, in order.
 struct LaSegments {
   const int* cu;   // [N+1] on the device
   int N, len, total;   // chunks of a segment; segments as counted from the host's copy
   int64_t T;
+  uint64_t bounds;     // la_bound of the host's cu[1 .. N], summed
 };
 
 // One walk: out_r = sum over the tokens c that r sees of p_scale a^|r-c| (x_r . y_c) z_c  +  row_scale a^.. Z^T x_r, with

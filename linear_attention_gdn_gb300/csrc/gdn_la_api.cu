@@ -17,6 +17,7 @@ constexpr double LA_BEGIN = 2.2;   // of a walk, in chunks
 struct LaPlan {
   int len, total;   // chunks of a segment, segments
   bool split;       // some document has more than one
+  uint64_t bounds;  // of the table, as the kernels compare it
 };
 
 static int chunks_of(const int32_t* cu, int d) { return (int)(((int64_t)cu[d + 1] - cu[d] + LA_CH - 1) / LA_CH); }
@@ -40,10 +41,12 @@ static gdn_status la_plan(const gdn_la_problem* p, const int32_t* cu, LaPlan* pl
   if (cu[0] != 0 || cu[p->N] != p->T) return GDN_ERR_INVALID_ARG;
   int64_t all = 0;
   int most = 1;
+  plan->bounds = 0;
   for (int d = 0; d < p->N; ++d) {
     if (cu[d + 1] < cu[d]) return GDN_ERR_INVALID_ARG;
     all += chunks_of(cu, d);
     most = std::max(most, chunks_of(cu, d));
+    plan->bounds += la_bound(d, cu[d + 1]);
   }
   const double sms = sm_count(), work = (double)all * p->HV;
   plan->len = p->segment > 0 ? std::min(p->segment, most) : most;
@@ -105,7 +108,7 @@ struct LaCall {
   LaCall(const gdn_la_problem* prob, const LaPlan& pl, const float* decay, const int32_t* cu, int32_t* err, cudaStream_t st)
       : p(prob), plan(pl), s(st) {
     memset(&w, 0, sizeof w);
-    w.seg = {cu, p->N, pl.len, pl.total, p->T};
+    w.seg = {cu, p->N, pl.len, pl.total, p->T, pl.bounds};
     w.decay = decay;
     w.HV = p->HV;
     w.err = err;

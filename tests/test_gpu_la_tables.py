@@ -75,6 +75,16 @@ def test_documents_longer_than_the_hosts_longest_are_left_out(lengths, wrong, H,
 
 
 @pytest.mark.parametrize("H,HV", [(2, 2), (1, 4)])
+@pytest.mark.parametrize("lengths,wrong,segment", [
+    ([100, 60], [0, 60, 160], 0), ([100, 60], [0, 99, 160], 0), ([1, 1, 1], [0, 2, 2, 3], 0), ([100, 0, 60], [0, 100, 101, 160], 0),
+    ([60, 100], [0, 100, 160], 0), ([500, 500], [0, 490, 1000], 2), ([3] * 50, [0] + [3 * i - (i == 49) for i in range(1, 50)] + [150], 0),
+    ([3] * 40, [0] + [3 * i + (i == 1) - (i == 2) for i in range(1, 40)] + [120], 1)])
+def test_other_bounds_of_as_many_segments_are_reported(lengths, wrong, segment, H, HV):
+    assert wrong_call(lengths, wrong, H, HV, segment, True) == [1, 1]
+    assert wrong_call(lengths, [0] + np.cumsum(lengths).tolist(), H, HV, segment, True) == [0, 0]
+
+
+@pytest.mark.parametrize("H,HV", [(2, 2), (1, 4)])
 def test_nothing_is_left_behind(H, HV):
     wrong_call([1000, 1000], [0, 0, 2000], H, HV, 3, True)
     x = make([300, 140], H, HV, seed=3)
