@@ -314,11 +314,6 @@ __global__ void __launch_bounds__(LA_THREADS, 1) la_walk_kernel(const __grid_con
     for (int i = OUT ? 0 : 1; i < (OUT ? 4 : 3); ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[i]) : "memory");
   }
   if (!FOLLOWS || !a.follows) previous_kernel_done();   // (else the kernels before it, but one, have ended; what is read comes from L2)
-  if (LEADS && a.clear) {   // for the walks behind
-    for (int64_t i = (int64_t)blockIdx.x * LA_THREADS + tid; i < a.clear; i += (int64_t)gridDim.x * LA_THREADS) a.counts[i] = 0;
-    __threadfence();
-    __syncthreads();
-  }
   if (LEADS && a.leads) dependents_may_launch();
   // SUM: in the order in which CTAs begin, so that what a head waits for has begun before it, whatever runs side by side
   int number = blockIdx.x;

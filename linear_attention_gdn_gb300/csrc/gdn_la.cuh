@@ -45,11 +45,11 @@ struct LaWalk {
   int64_t out_token;      // elements
   // Walks that sum: over the `group` value heads of an output head
   int group;
-  int* counts;            // [chunks][output heads]: heads that have been added
-  int* ticket;            // numbers the CTAs as they begin
-  int64_t clear;          // walks that lead: of counts on, so many are cleared
+  int* counts;            // [chunks][output heads]: heads that have been added; zero before the call's first kernel
+  int* ticket;            // numbers the CTAs as they begin; the same
   // Walks that need nothing of one another fill the SMs that the one before leaves: `leads`: the next kernel may begin when
-  // all CTAs of this one run, and all before it has ended; `follows`: begins then, and does not end before it.
+  // all CTAs of this one run, and all before it has ended; `follows`: begins then, and does not end before it.  So a walk
+  // that follows reads only what was complete before the one that leads went on, never what that one writes.
   int leads, follows;
   int* err;
 };

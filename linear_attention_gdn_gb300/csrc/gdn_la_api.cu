@@ -243,6 +243,9 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
   float *wstates = states + values, *part = wstates + values;
   LaCall c(p, plan, decay, cu_dev, dev_err, stream);
   const float *w_start = ds_out, *s_start = s_in;
+  // The counts of heads and the tickets, zero before the first kernel of this call: a walk that follows another does not wait
+  // for it, so nothing it reads may come from there, or from anything but what had ended before that one went on.
+  if (p->HV > p->H && p->T > 0) c.check(cudaMemsetAsync(c.counts(part), 0, 2 * (la_counts(p) + 1) * sizeof(int), stream));
   if (plan.split) {   // the states that segments start from
     c.tensors(tk, tq, td);
     c.scales(p->scale, 1.f, p->scale);
@@ -259,7 +262,6 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
   // 48 heads on 16: 1,800 us, one after the other 1,913; a ragged pack of 7 244 and 286); but dk's reads the gradients of the
   // states before dv's writes over them.
   const bool in_place = ds_in && ds_in == ds_out && !plan.split;
-  const int64_t cleared = p->HV > p->H ? 2 * (la_counts(p) + 1) : 0;
   auto dk_walk = [&] {   // by dv's states, seen from the other side
     c.tensors(tv, td, tq);
     c.scales(p->scale, 1.f, p->scale);
@@ -277,16 +279,12 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
     return c.ok ? GDN_OK : GDN_ERR_CUDA;
   }
   if (in_place) {
-    if (cleared) c.check(cudaMemsetAsync(c.counts(part), 0, cleared * sizeof(int), stream));
     dk_walk();
     c.w.leads = 1;
     dv_walk();
   } else {
-    c.w.counts = c.counts(part);
-    c.w.clear = cleared;
     c.w.leads = 1;
     dv_walk();
-    c.w.clear = 0;
     c.w.leads = 0;
     c.w.follows = 1;
     dk_walk();

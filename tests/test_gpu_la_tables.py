@@ -1,5 +1,6 @@
 """The linear attention where the device's cu_seqlens are in order and end where the host's do, but cut the tokens otherwise:
-nothing outside the outputs and the workspace is written, and nothing is left behind for the next call."""
+nothing outside the outputs and the workspace is written, and nothing is left behind for the next call; and what the workspace
+held before a call is of no account."""
 import numpy as np
 import pytest
 import torch
@@ -89,3 +90,36 @@ def test_nothing_is_left_behind(H, HV):
     wrong_call([1000, 1000], [0, 0, 2000], H, HV, 3, True)
     x = make([300, 140], H, HV, seed=3)
     check(x, run(x, on_gpu(x), 1))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("segment", [0, 1])
+def test_the_workspace_may_hold_anything(segment, in_place):
+    """Counts of heads and tickets are cleared ahead of all walks of a call: a call, a captured one and its replays behind one
+    another give the same bits, whatever the workspace held before each."""
+    x = make([130, 0, 500, 60], 2, 10, seed=8)
+    d = on_gpu(x)
+    want = run(x, d, segment)
+    prob = gdn.la_problem(len(x["q"]), 4, 2, 10, SCALE, segment)
+    ws = torch.empty(gdn.gdn_la_workspace_bytes(prob, x["cu"])[1], dtype=torch.uint8, device="cuda")
+    out = {m: torch.empty_like(want[m]) for m in ("dq", "dk", "dv", "ds_in")}
+    incoming = out["ds_in"] if in_place else d["ds_out"]
+
+    def call():
+        gdn.gdn_la_bwd(prob, d["q"], d["k"], d["v"], d["decay"], d["cu_dev"], x["cu"], d["s_in"], d["dO"], incoming, out["dq"], out["dk"],
+                       out["dv"], out["ds_in"], d["err"], ws)
+
+    graph = torch.cuda.CUDAGraph()
+    out["ds_in"].copy_(d["ds_out"])
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        call()
+    for go, held in ((call, 0), (graph.replay, 0), (graph.replay, 1), (call, 3), (call, 127), (graph.replay, 255), (graph.replay, 128)):
+        for m in ("dq", "dk", "dv"):
+            out[m].fill_(float("nan"))
+        out["ds_in"].copy_(d["ds_out"])
+        ws.fill_(held)
+        go()
+        for m in out:
+            assert torch.equal(out[m], want[m]), (m, held)
+    assert gdn.gdn_device_status(d["err"]) == 0
