@@ -116,7 +116,8 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;"); }
+// what this thread has stored to shared memory before is seen by MMAs and bulk copies behind (the compiler keeps it before, too)
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // TMEM allocation (one full warp executes these)
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
