@@ -559,20 +559,21 @@ def gdn_rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, orig
     return freq, m.value
 
 
-def gdn_la_workspace_bytes(prob, cu_seqlens_host):
-    """(forward's, backward's) bytes of workspace of the linear attention."""
-    cu, cup = _cu_host(cu_seqlens_host)
-    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
-    _check(lib.gdn_la_workspace_bytes(ctypes.byref(prob), cup, ctypes.byref(f), ctypes.byref(b)), "gdn_la_workspace_bytes")
-    return f.value, b.value
-
-
 def _documents(prob, cu_seqlens_host, where):
     """The host's cu_seqlens as the library reads it, and its address."""
     cu = np.ascontiguousarray(np.asarray(cu_seqlens_host, dtype=np.int32))
     if cu.ndim != 1 or cu.size < prob.N + 1:
         raise ValueError(f"{where}: cu_seqlens_host has {cu.size} entries for {prob.N} documents")
     return cu, cu.__array_interface__["data"][0]
+
+
+def gdn_la_workspace_bytes(prob, cu_seqlens_host):
+    """(forward's, backward's) bytes of workspace of the linear attention."""
+    cu, at = _documents(prob, cu_seqlens_host, "gdn_la_workspace_bytes")
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib.gdn_la_workspace_bytes(ctypes.byref(prob), ctypes.cast(at, ctypes.POINTER(ctypes.c_int32)), ctypes.byref(f),
+                                      ctypes.byref(b)), "gdn_la_workspace_bytes")
+    return f.value, b.value
 
 
 def _bytes(workspace, ws_bytes):

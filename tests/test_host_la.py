@@ -66,6 +66,18 @@ def test_la_workspace():
         gdn.gdn_la_fwd(one, *[P] * 5, CU[:2], P, P, P, P, P, 0, stream=0)
 
 
+@pytest.mark.parametrize("cu", [[0, 5], [0], [], [[0, 3, 5]], 5])
+def test_la_tables_too_short_for_the_documents(cu):
+    """No entry point reads past the table that it is given."""
+    p = gdn.la_problem(**LA)
+    with pytest.raises(ValueError):
+        gdn.gdn_la_workspace_bytes(p, cu)
+    for call in (fwd, bwd):
+        f, *a = call(p, cu=cu)
+        with pytest.raises(ValueError):
+            f(*a, stream=0)
+
+
 def test_la_cuts_long_documents_only_where_heads_are_few():
     many = gdn.la_problem(8192 * 8, 8, 16, 48)
     assert gdn.gdn_la_workspace_bytes(many, np.arange(9) * 8192)[0] == 0
