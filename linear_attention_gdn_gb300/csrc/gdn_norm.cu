@@ -556,8 +556,10 @@ template <typename E, bool BACK> static cudaError_t norm_run(const NormArgs& a, 
       GDN_NORM(4, true);
     }
     if (s.vpt == 1) GDN_NORM(1, false);
-    if (s.vpt == 2) GDN_NORM(2, false);
-    GDN_NORM(4, false);
+    if constexpr (sizeof(E) == 4) {   // (16-bit rows have threads enough for 2)
+      if (s.vpt == 4) GDN_NORM(4, false);
+    }
+    GDN_NORM(2, false);
 #undef GDN_NORM
   }
 }
