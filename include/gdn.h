@@ -533,6 +533,8 @@ gdn_status gdn_add_norm_bwd(const gdn_norm_problem *prob, const void *h, const f
  * itself.  A request keeps a state to every `block` tokens: block j's slot holds the state after the last token taken of
  * j block .. (j+1) block - 1, so earlier blocks are what others with the same beginning can start from.  With `block` as long
  * as the longest context a request has one slot.
+ * A slot stands in one request's row, and goes back with it.  A request that begins as another did takes a slot from the end of
+ * the free list for itself, between two steps, copies the state of the other's block there, and has it in its own row.
  *   lengths      [N] tokens that each request takes now; -1: it has ended, its blocks go back
  *   context      [N] tokens it has taken before;  context_out [N]: after this step (0 where it has ended)
  *   block_table  [N][max_blocks] slots of its blocks: ceil(context / block) are read, the new ones written behind them

@@ -1,5 +1,5 @@
 """A generation step of a model with both kinds of layers in one captured graph: the step's tables, the norm with the residual's
-addition, the rule's step and the linear attention's on their pools."""
+addition, the rule's step and the linear attention's on their pools.  And requests that begin as others did."""
 import numpy as np
 import pytest
 import torch
@@ -107,3 +107,33 @@ def test_a_captured_step_of_both_layers():
         written = {slot_out[t] for t in range(n)}
         rest = [i for i in range(SLOTS) if i not in written]
         assert torch.equal(got["linear"][rest], before["linear"][rest])
+
+
+def test_a_request_begins_with_a_copy_of_anothers_block():
+    """A slot stands in one request's row, with which it goes back.  A request that begins as another did has a copy of its block's
+    state in a slot of its own; in the end every slot is free once."""
+    block, rows, slots = 8, 4, 10
+    i = lambda *a: torch.tensor(a, dtype=i32, device="cuda")  # noqa: E731
+    lengths, ctx, table = i(20, 0), i(0, 0), torch.full((2, rows), -1, dtype=i32, device="cuda")
+    free, count, err = torch.arange(slots, dtype=i32, device="cuda"), i(slots), i(0)
+    pool = torch.randn(slots, 4, device="cuda")
+    cu, pos, slot_in, slot_out = i(0, 0, 0), torch.zeros(20, dtype=i32, device="cuda"), i(0, 0), torch.zeros(20, dtype=i32, device="cuda")
+
+    def step():
+        gdn.gdn_step_tables(gdn.tables_problem(2, 20, block, rows, slots), lengths, ctx, ctx, table, free, count, count, cu, pos, slot_in,
+                            slot_out, err)
+        held = [int(x) for n in range(2) for x in table[n, :-(-int(ctx[n]) // block)]]
+        assert sorted(held + free[:int(count)].tolist()) == list(range(slots))
+
+    step()
+    count -= 1   # a slot of its own, between two steps
+    slot = free[count.long()]
+    pool[slot.long()] = pool[table[0, :1].long()]
+    table[1, :1] = slot
+    ctx[1] = 8
+    lengths.copy_(i(-1, 6))
+    step()
+    assert slot_in.tolist() == [-1, int(slot)] and pos[:6].tolist() == list(range(8, 14)) and int(ctx[0]) == 0
+    lengths.copy_(i(0, -1))
+    step()
+    assert int(count) == slots and gdn.gdn_device_status(err) == 0
