@@ -465,6 +465,8 @@ gdn_status gdn_rope_frequencies(int32_t rot, double base, int32_t scaling, doubl
  * documents, and rows outside cu_seqlens' range, reach none.
  * Results are the same bits from run to run; dq and dk are sums over the value heads of a group in order.
  * Outputs do not overlap inputs, but for the states as said.  T below 2^30 (else GDN_ERR_UNSUPPORTED).
+ * The kernels of gdn_la_*, gdn_add_norm_* and gdn_step_tables are launched as gdn_step's are: to the caller the stream is in order.
+ * Every CTA looks for its document in the device's table: past a thousand documents of a few tokens that is most of the time.
  * gdn_la_workspace_bytes: what the forward and the backward need (16-byte aligned; 0: nothing).
  *     The backward of groups (HV > H) takes 128 KiB to each begun chunk of 128 tokens of a document and q/k head; documents
  *     that are cut, 64 KiB (the backward 128) to a segment and value head.
@@ -509,8 +511,9 @@ gdn_status gdn_la_step(const gdn_step_problem *prob, const void *q, const void *
  * Backward, of y (what reads y8 takes its gradient to be z's): with h as the forward left it (h_stride), dy (y_stride) and
  * dres (r_stride), the gradient that reaches h along the stream (NULL: none), dx (x_stride) is the gradient of x and of r, and
  * dw [C] FP32 (NULL: not wanted) the weights', summed over the rows in a fixed order.  dx may be dy or dres (same stride).
- * Sums in FP32.  Any C up to 2^20 (else GDN_ERR_UNSUPPORTED), any alignment of at least the element's; the fast kernels take
- * C a multiple of 8 up to 16384 with strides and pointers in whole 16 bytes, the others are several times slower.
+ * Sums in FP32: rows whose squares add up to more than its range (4,096 values of 3 10^17) come out as zeros.  Any C up to 2^20
+ * (else GDN_ERR_UNSUPPORTED), any alignment of at least the element's; the fast kernels take C a multiple of 8 up to 16384 with
+ * strides and pointers in whole 16 bytes, the others are several times slower.
  * gdn_add_norm_workspace_bytes: the backward's scratch (16-byte aligned; not needed without dw).
  */
 typedef struct {

@@ -259,7 +259,7 @@ gdn_status gdn_la_bwd(const gdn_la_problem* p, const void* q, const void* k, con
     }
   }
   // The three walks need nothing of one another, so each begins as the one before runs out of work (8 documents of 8,192 tokens,
-  // 48 heads on 16: 1,800 us, one after the other 1,913; a ragged pack of 7 244 and 286); but dk's reads the gradients of the
+  // 48 heads on 16: 1,790 us, one after the other 1,911; a ragged pack of 7 225 and 281); but dk's reads the gradients of the
   // states before dv's writes over them.
   const bool in_place = ds_in && ds_in == ds_out && !plan.split;
   auto dk_walk = [&] {   // by dv's states, seen from the other side

@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(32) la_step_kernel(const LaStepArgs a) {
 }
 
 template <typename E> static cudaError_t launch_la_step(const LaStepArgs& a, int64_t heads, cudaStream_t s) {
-  // few heads: 16 columns a warp (one token of 48 heads 2.86 us, by 8 columns 3.19; of 144 5.85 and 4.05)
+  // few heads: 16 row lanes, 8 columns a warp (one token of 48 heads 2.86 us, by 8 row lanes and 16 columns 3.19; of 144 5.85
+  // and 4.05)
   if (heads <= sm_count() / 2)
     return launch_chained(la_step_kernel<E, 16, true>, dim3((unsigned)heads * LaStepLayout<16>::PARTS), dim3(32), 0, s, a);
   const dim3 grid((unsigned)heads * LaStepLayout<8>::PARTS);
